@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_size_t, c_uint32, c_uint64, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libdspark.so")
@@ -40,11 +40,15 @@ DSPARK_MAX_SCHED_KEYS = 65536
 DSPARK_MAX_VOCAB = 2097152
 DSPARK_STS_MAX_SAMPLES = 8388607
 DSPARK_STS_MAX_TABLE = 16384
+DSPARK_FP8_BLOCK = 128
+DSPARK_MAX_TOP = 32
 
 EXPORTED = ("dspark_workspace_size", "dspark_workspace_init", "dspark_read_error", "dspark_draft_sample",
             "dspark_schedule", "dspark_verify", "dspark_status_string", "dspark_version", "dspark_launch_count",
             "dspark_last_cuda_error", "dspark_schedule_noalloc", "dspark_sts_fit_workspace_size", "dspark_sts_fit",
-            "dspark_pack_rows", "dspark_draft_and_schedule")
+            "dspark_pack_rows", "dspark_draft_and_schedule", "dspark_quant_fp8", "dspark_matmul_fp8_workspace_size",
+            "dspark_matmul_fp8", "dspark_token_logprobs_workspace_size", "dspark_token_logprobs",
+            "dspark_token_logprobs_grad")
 
 
 class dspark_dims(ctypes.Structure):
@@ -88,6 +92,34 @@ class dspark_sts_fit_args(ctypes.Structure):
                 ("grid_index", c_void_p), ("ece", c_void_p)]
 
 
+class dspark_quant_fp8_args(ctypes.Structure):
+    _fields_ = [("M", c_int32), ("K", c_int32), ("dtype", c_int32), ("block_rows", c_int32), ("x", c_void_p),
+                ("ldx", c_int64), ("codes", c_void_p), ("ldq", c_int64), ("scale", c_void_p)]
+
+
+class dspark_matmul_fp8_args(ctypes.Structure):
+    _fields_ = [("M", c_int32), ("N", c_int32), ("K", c_int32), ("out_dtype", c_int32), ("a", c_void_p),
+                ("lda", c_int64), ("a_scale", c_void_p), ("w", c_void_p), ("ldw", c_int64), ("w_scale", c_void_p),
+                ("out", c_void_p), ("ldo", c_int64), ("n_rows", c_void_p)]
+
+
+class dspark_logit_rows(ctypes.Structure):
+    _fields_ = [("N", c_int32), ("V", c_int32), ("dtype", c_int32), ("tok_cols", c_int32), ("n_req", c_int32),
+                ("logits", c_void_p), ("ld", c_int64), ("tokens", c_void_p), ("temp", c_void_p), ("mask", c_void_p),
+                ("mask_ld", c_int64), ("mark_req", c_void_p), ("mark_pos", c_void_p), ("n_rows", c_void_p)]
+
+
+class dspark_token_logprobs_args(ctypes.Structure):
+    _fields_ = [("rows", dspark_logit_rows), ("top", c_int32), ("logprob", c_void_p), ("entropy", c_void_p),
+                ("rank", c_void_p), ("row_stat", c_void_p), ("top_id", c_void_p), ("top_logprob", c_void_p)]
+
+
+class dspark_token_logprobs_grad_args(ctypes.Structure):
+    _fields_ = [("rows", dspark_logit_rows), ("top", c_int32), ("row_stat", c_void_p), ("entropy", c_void_p),
+                ("top_id", c_void_p), ("g_logprob", c_void_p), ("g_entropy", c_void_p), ("g_top", c_void_p),
+                ("grad", c_void_p), ("ldg", c_int64)]
+
+
 _lib = None
 
 
@@ -112,9 +144,17 @@ def load() -> ctypes.CDLL:
     lib.dspark_sts_fit_workspace_size.argtypes = [c_int32, c_int32, c_int32, c_int32, POINTER(c_size_t)]
     lib.dspark_sts_fit.argtypes = [POINTER(dspark_sts_fit_args), c_void_p, c_size_t, c_void_p]
     lib.dspark_pack_rows.argtypes = [POINTER(dspark_pack_args), c_void_p, c_void_p]
+    lib.dspark_quant_fp8.argtypes = [POINTER(dspark_quant_fp8_args), c_void_p]
+    lib.dspark_matmul_fp8_workspace_size.argtypes = [c_int32, c_int32, c_int32, POINTER(c_size_t)]
+    lib.dspark_matmul_fp8.argtypes = [POINTER(dspark_matmul_fp8_args), c_void_p, c_size_t, c_void_p]
+    lib.dspark_token_logprobs_workspace_size.argtypes = [c_int32, c_int32, c_int32, POINTER(c_size_t)]
+    lib.dspark_token_logprobs.argtypes = [POINTER(dspark_token_logprobs_args), c_void_p, c_size_t, c_void_p]
+    lib.dspark_token_logprobs_grad.argtypes = [POINTER(dspark_token_logprobs_grad_args), c_void_p, c_void_p]
     for f in ("dspark_workspace_size", "dspark_workspace_init", "dspark_read_error", "dspark_draft_sample",
               "dspark_schedule", "dspark_verify", "dspark_schedule_noalloc", "dspark_sts_fit_workspace_size",
-              "dspark_sts_fit", "dspark_pack_rows", "dspark_draft_and_schedule"):
+              "dspark_sts_fit", "dspark_pack_rows", "dspark_draft_and_schedule", "dspark_quant_fp8",
+              "dspark_matmul_fp8_workspace_size", "dspark_matmul_fp8", "dspark_token_logprobs_workspace_size",
+              "dspark_token_logprobs", "dspark_token_logprobs_grad"):
         getattr(lib, f).restype = c_int32
     lib.dspark_status_string.argtypes = [c_int32]
     lib.dspark_status_string.restype = c_char_p
@@ -197,3 +237,32 @@ def dspark_sts_fit(args: dspark_sts_fit_args, workspace: int, nbytes: int, strea
 
 def dspark_pack_rows(args: dspark_pack_args, workspace: int, stream: int) -> int:
     return load().dspark_pack_rows(ctypes.byref(args), c_void_p(workspace) if workspace else None, c_void_p(stream))
+
+
+def dspark_quant_fp8(args: dspark_quant_fp8_args, stream: int) -> int:
+    return load().dspark_quant_fp8(ctypes.byref(args), c_void_p(stream))
+
+
+def dspark_matmul_fp8_workspace_size(M: int, N: int, K: int) -> tuple[int, int]:
+    n = c_size_t(0)
+    st = load().dspark_matmul_fp8_workspace_size(M, N, K, ctypes.byref(n))
+    return st, n.value
+
+
+def dspark_matmul_fp8(args: dspark_matmul_fp8_args, workspace: int, nbytes: int, stream: int) -> int:
+    return load().dspark_matmul_fp8(ctypes.byref(args), c_void_p(workspace), nbytes, c_void_p(stream))
+
+
+def dspark_token_logprobs_workspace_size(N: int, V: int, top: int) -> tuple[int, int]:
+    n = c_size_t(0)
+    st = load().dspark_token_logprobs_workspace_size(N, V, top, ctypes.byref(n))
+    return st, n.value
+
+
+def dspark_token_logprobs(args: dspark_token_logprobs_args, workspace: int, nbytes: int, stream: int) -> int:
+    return load().dspark_token_logprobs(ctypes.byref(args), c_void_p(workspace), nbytes, c_void_p(stream))
+
+
+def dspark_token_logprobs_grad(args: dspark_token_logprobs_grad_args, workspace: int, stream: int) -> int:
+    return load().dspark_token_logprobs_grad(ctypes.byref(args), c_void_p(workspace) if workspace else None,
+                                             c_void_p(stream))

@@ -291,4 +291,97 @@ dspark_status dspark_sts_fit(const dspark_sts_fit_args* a, void* workspace, size
   return cuda_status(launch_sts_fit(*a, static_cast<uint8_t*>(workspace), L, (cudaStream_t)stream));
 }
 
+static bool dtype_ok(int32_t dt) { return dt == DSPARK_BF16 || dt == DSPARK_F32; }
+
+// a workspace of at least `need` bytes
+static bool ws_ok(const void* ws, size_t bytes, size_t need) {
+  return ws && ((uintptr_t)ws & 255u) == 0 && bytes >= need;
+}
+
+// rows of `cols` elements `ld` apart whose last element's offset fits 63 bits in bytes
+static bool rows_ok(int64_t rows, int64_t cols, int64_t ld) {
+  if (rows <= 1) return true;
+  return ld >= cols && ld <= (int64_t)1 << 40 && rows <= ((int64_t)1 << 60) / (4 * ld);
+}
+
+static bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+dspark_status dspark_quant_fp8(const dspark_quant_fp8_args* a, void* stream) {
+  if (!a || a->M < 0 || a->K < 1 || !dtype_ok(a->dtype) || (a->block_rows != 1 && a->block_rows != DSPARK_FP8_BLOCK))
+    return DSPARK_INVALID_ARG;
+  if (a->M == 0) return DSPARK_OK;
+  if (!a->x || !a->codes || !a->scale || !rows_ok(a->M, a->K, a->ldx) || !rows_ok(a->M, a->K, a->ldq))
+    return DSPARK_INVALID_ARG;
+  if (!aligned_to(a->x, elem_size(a->dtype)) || !aligned_to(a->scale, 4)) return DSPARK_INVALID_ARG;
+  return cuda_status(launch_quant_fp8(*a, (cudaStream_t)stream));
+}
+
+dspark_status dspark_matmul_fp8_workspace_size(int32_t M, int32_t N, int32_t K, size_t* bytes) {
+  if (!bytes || M < 0 || N < 0 || K < 1) return DSPARK_INVALID_ARG;
+  *bytes = align_up(matmul_fp8_ws(M, N, K), 256);
+  return DSPARK_OK;
+}
+
+dspark_status dspark_matmul_fp8(const dspark_matmul_fp8_args* a, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  if (!a || a->M < 0 || a->N < 0 || a->K < 1 || !dtype_ok(a->out_dtype)) return DSPARK_INVALID_ARG;
+  if (a->M == 0 || a->N == 0) return DSPARK_OK;
+  if (!a->a || !a->a_scale || !a->w || !a->w_scale || !a->out) return DSPARK_INVALID_ARG;
+  if (!rows_ok(a->M, a->K, a->lda) || !rows_ok(a->N, a->K, a->ldw) || !rows_ok(a->M, a->N, a->ldo))
+    return DSPARK_INVALID_ARG;
+  if (!aligned16(a->a) || !aligned16(a->w) || (a->M > 1 && a->lda % 16) || (a->N > 1 && a->ldw % 16))
+    return DSPARK_INVALID_ARG;
+  if (!aligned_to(a->out, elem_size(a->out_dtype)) || !aligned_to(a->a_scale, 4) || !aligned_to(a->w_scale, 4))
+    return DSPARK_INVALID_ARG;
+  if (!ws_ok(workspace, workspace_bytes, matmul_fp8_ws(a->M, a->N, a->K))) return DSPARK_INVALID_ARG;
+  const cudaError_t e = launch_matmul_fp8(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream);
+  if (e == cudaErrorNotSupported) return DSPARK_UNSUPPORTED;
+  return cuda_status(e);
+}
+
+static dspark_status check_logit_rows(const dspark_logit_rows& r) {
+  if (r.N < 0 || r.V < 1 || r.V > DSPARK_MAX_VOCAB || !dtype_ok(r.dtype)) return DSPARK_INVALID_ARG;
+  if (r.N == 0) return DSPARK_OK;
+  if (!r.logits || !r.tokens || !rows_ok(r.N, r.V, r.ld) || !aligned_to(r.logits, elem_size(r.dtype)))
+    return DSPARK_INVALID_ARG;
+  if ((r.mark_req != nullptr) != (r.mark_pos != nullptr)) return DSPARK_INVALID_ARG;
+  if (r.mark_req && (r.n_req < 0 || r.tok_cols < 0)) return DSPARK_INVALID_ARG;
+  if (r.mask && (!aligned_to(r.mask, 4) || !rows_ok(r.N, ((int64_t)r.V + 31) / 32, r.mask_ld)))
+    return DSPARK_INVALID_ARG;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_token_logprobs_workspace_size(int32_t N, int32_t V, int32_t top, size_t* bytes) {
+  if (!bytes || N < 0 || V < 1 || V > DSPARK_MAX_VOCAB || top < 0) return DSPARK_INVALID_ARG;
+  if (top > DSPARK_MAX_TOP) return DSPARK_UNSUPPORTED;
+  *bytes = align_up(token_logprobs_ws(N, V, top), 256);
+  return DSPARK_OK;
+}
+
+dspark_status dspark_token_logprobs(const dspark_token_logprobs_args* a, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (!a || a->top < 0) return DSPARK_INVALID_ARG;
+  if (a->top > DSPARK_MAX_TOP) return DSPARK_UNSUPPORTED;
+  const dspark_status st = check_logit_rows(a->rows);
+  if (st != DSPARK_OK || a->rows.N == 0) return st;
+  if (a->top > 0 && (!a->top_id || !a->top_logprob)) return DSPARK_INVALID_ARG;
+  if (!ws_ok(workspace, workspace_bytes, token_logprobs_ws(a->rows.N, a->rows.V, a->top))) return DSPARK_INVALID_ARG;
+  const cudaError_t e = launch_token_logprobs(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream);
+  return cuda_status(e);
+}
+
+dspark_status dspark_token_logprobs_grad(const dspark_token_logprobs_grad_args* a, void* workspace, void* stream) {
+  if (!a || a->top < 0) return DSPARK_INVALID_ARG;
+  if (a->top > DSPARK_MAX_TOP) return DSPARK_UNSUPPORTED;
+  const dspark_status st = check_logit_rows(a->rows);
+  if (st != DSPARK_OK || a->rows.N == 0) return st;
+  if (!a->row_stat || !a->grad || (a->g_entropy && !a->entropy) || (a->top > 0 && (!a->top_id || !a->g_top)))
+    return DSPARK_INVALID_ARG;
+  if (!rows_ok(a->rows.N, a->rows.V, a->ldg) || !aligned_to(a->grad, elem_size(a->rows.dtype)))
+    return DSPARK_INVALID_ARG;
+  if (a->grad == a->rows.logits && a->rows.N > 1 && a->ldg != a->rows.ld) return DSPARK_INVALID_ARG;
+  if (workspace && ((uintptr_t)workspace & 255u)) return DSPARK_INVALID_ARG;
+  return cuda_status(launch_token_logprobs_grad(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream));
+}
+
 }  // extern "C"

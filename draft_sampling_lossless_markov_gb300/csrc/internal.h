@@ -125,6 +125,15 @@ cudaError_t launch_rnn_step(const dspark_draft_args& a, int j, const float* P, c
 // Verify-batch packing (pack.cu).
 cudaError_t launch_pack_rows(const dspark_pack_args& a, WsHeader* hdr, cudaStream_t s);
 
+// The vocabulary projection and the answers around verify (quant_fp8.cu,
+// matmul_fp8.cu, token_logprobs.cu); *_ws: bytes of workspace.
+cudaError_t launch_quant_fp8(const dspark_quant_fp8_args& a, cudaStream_t s);
+size_t matmul_fp8_ws(int M, int N, int K);
+cudaError_t launch_matmul_fp8(const dspark_matmul_fp8_args& a, uint8_t* ws, cudaStream_t s);
+size_t token_logprobs_ws(int N, int V, int top);
+cudaError_t launch_token_logprobs(const dspark_token_logprobs_args& a, uint8_t* ws, cudaStream_t s);
+cudaError_t launch_token_logprobs_grad(const dspark_token_logprobs_grad_args& a, uint8_t* ws, cudaStream_t s);
+
 // STS fitting (sts_fit.cu): its own workspace, after a WsHeader.
 struct StsLayout {
   size_t hp = 0;         // [gamma * n_bins * n_grid] u64 fixed-point prediction sums

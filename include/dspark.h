@@ -446,6 +446,179 @@ DSPARK_API dspark_status dspark_sts_fit_workspace_size(int32_t N, int32_t gamma,
 DSPARK_API dspark_status dspark_sts_fit(const dspark_sts_fit_args* args, void* workspace, size_t workspace_bytes,
                                         void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Around dspark_verify: the vocabulary projection and the answers
+ * ---------------------------------------------------------------------------
+ * dspark_verify reads target_logits and returns tokens.  The calls below are
+ * the two ends of that step in a serving or training program: the product that
+ * makes the logits from the target's last hidden rows (dspark_quant_fp8,
+ * dspark_matmul_fp8), and what is answered or learnt from them
+ * (dspark_token_logprobs, dspark_token_logprobs_grad).  The pages have no
+ * counterpart to them; they follow this library's conventions (device
+ * pointers, caller's buffers and workspace, one stream, no allocation).
+ * Matrices are row-major with a stride between rows, so a column range of a
+ * wider buffer is a valid argument. */
+#define DSPARK_FP8_BLOCK 128 /* columns (and weight rows) that share one scale */
+#define DSPARK_MAX_TOP 32    /* top alternatives of dspark_token_logprobs */
+
+/* dspark_quant_fp8: x [M, K] (dtype, row stride ldx elements) to e4m3 codes
+ * [M, K] (row stride ldq bytes, ldq >= K) and fp32 scales
+ * [ceil(M / block_rows), ceil(K / 128)], dense.  A block is block_rows x 128
+ * elements, block_rows 1 (activations) or 128 (weights); blocks at the edges
+ * are smaller.  Per block
+ *     amax = max(|x|, 2^-100), scale = amax / 448,
+ *     code = e4m3(x * (448 / amax)),  both quotients and the product in fp32,
+ * the code rounded to nearest, ties to even.  A NaN or an infinity in a block
+ * takes no part in amax and becomes the NaN code.  Bytes of a row past K are not
+ * written. */
+typedef struct {
+  int32_t M;
+  int32_t K;
+  int32_t dtype;
+  int32_t block_rows;
+  const void* x;
+  int64_t ldx;
+  void* codes;
+  int64_t ldq;
+  float* scale;
+} dspark_quant_fp8_args;
+
+DSPARK_API dspark_status dspark_quant_fp8(const dspark_quant_fp8_args* args, void* stream);
+
+/* dspark_matmul_fp8: out[m, n] = sum_b a_scale[m, b] w_scale[n / 128, b]
+ *                               sum_{k in block b} a[m, k] w[n, k]
+ * over the blocks b of 128 columns (the last may be shorter), for e4m3 codes
+ * a [M, K] and w [N, K] with scales a_scale [M, ceil(K / 128)] and
+ * w_scale [ceil(N / 128), ceil(K / 128)], the layouts dspark_quant_fp8 writes
+ * with block_rows 1 and 128.  Sums are fp32; out [M, N] (out_dtype, row stride
+ * ldo elements) is rounded once.  a, w 16-byte aligned, lda and ldw (bytes)
+ * multiples of 16 and >= K; out aligned to its element.  n_rows (device, may be
+ * NULL) holds a row count: rows of out from min(M, *n_rows) on are not
+ * written, so a packed batch whose size is known on the GPU only
+ * (dspark_schedule's n_verify) needs no host round trip.  out must not overlap
+ * an input.  M = 0 or N = 0 does nothing; K >= 1.  The sum over k is formed in an
+ * order that depends on the sizes only: equal calls give equal bits.  A
+ * workspace of dspark_matmul_fp8_workspace_size(M, N, K) bytes, initialised by
+ * dspark_workspace_init, is needed.  Needs sm_103, else DSPARK_UNSUPPORTED. */
+typedef struct {
+  int32_t M;
+  int32_t N;
+  int32_t K;
+  int32_t out_dtype;
+  const void* a;
+  int64_t lda;
+  const float* a_scale;
+  const void* w;
+  int64_t ldw;
+  const float* w_scale;
+  void* out;
+  int64_t ldo;
+  const int32_t* n_rows;
+} dspark_matmul_fp8_args;
+
+DSPARK_API dspark_status dspark_matmul_fp8_workspace_size(int32_t M, int32_t N, int32_t K, size_t* bytes);
+DSPARK_API dspark_status dspark_matmul_fp8(const dspark_matmul_fp8_args* args, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* The rows dspark_token_logprobs and its gradient work on: logits [N, V]
+ * (dtype, row stride ld elements >= V, aligned to the element).
+ * Row i's law is p(v) = softmax(logits[i, v] / T) over its candidates: the v
+ * with logit > -inf whose mask bit is set (mask [N, mask_ld] u32, bit v % 32 of
+ * word v / 32, mask_ld >= ceil(V / 32); NULL: all).  Logits of masked places are
+ * not looked at (they may be NaN).  T = temp[i] where that is finite and > 0;
+ * anything else, and temp = NULL, means T = 1 (a greedy request's answers
+ * come from the untempered law).  tokens [N]: the given token of each row, -1
+ * for none.
+ * With markers (mark_req, mark_pos [N], both or neither) row i belongs to
+ * request mark_req[i]: its token is tokens[mark_req[i] * tok_cols +
+ * mark_pos[i]] of tokens [n_req, tok_cols] and its temperature temp[mark_req[i]]
+ * of temp [n_req].  With dspark_schedule's markers and dspark_verify's out_tok
+ * [B, gamma + 1] row (r, j) is given the token emitted at place j, -1 past the
+ * last one.  A row whose mark_req is -1 has no token and T = 1.
+ * n_rows (device, may be NULL): rows from min(N, *n_rows) on are skipped,
+ * their outputs not written.
+ * A token outside [-1, V) or a marker outside its range counts as none and is
+ * reported in the workspace error word (DSPARK_BAD_INPUT, detail = row). */
+typedef struct {
+  int32_t N;
+  int32_t V;
+  int32_t dtype;
+  int32_t tok_cols;
+  int32_t n_req;
+  const void* logits;
+  int64_t ld;
+  const int32_t* tokens;
+  const float* temp;
+  const uint32_t* mask;
+  int64_t mask_ld;
+  const int32_t* mark_req;
+  const int32_t* mark_pos;
+  const int32_t* n_rows;
+} dspark_logit_rows;
+
+/* dspark_token_logprobs: per row, in fp32 and natural logarithms,
+ *     logprob [N]       ln p(token); 0 where there is no token
+ *     entropy [N]       -sum p ln p
+ *     rank [N] i32      candidates ahead of the token in the order (logit
+ *                       descending, id ascending); -1 where there is no token
+ *                       or the token is no candidate
+ *     top_id, top_logprob [N, top]  the first `top` candidates in that order;
+ *                       (-1, -inf) past the last candidate
+ *     row_stat [N, 2]   (m, S): the largest candidate logit and
+ *                       sum exp((logit - m) / T), what the gradient needs
+ * Each output may be NULL (top_id and top_logprob only when top = 0).
+ * A token that is no candidate has logprob -inf.  A row with no candidate has
+ * logprob -inf (0 without a token), entropy 0 and row_stat (-inf, 0).  A row
+ * with a NaN or +inf logit among its candidates has NaN logprob (0 without a
+ * token), entropy, S and top_logprob, rank -1 and top_id -1.
+ * Equal calls give equal bits.  The workspace: dspark_token_logprobs_workspace_size(N, V, top)
+ * bytes, initialised by dspark_workspace_init, kept to one stream at a time. */
+typedef struct {
+  dspark_logit_rows rows;
+  int32_t top; /* 0..DSPARK_MAX_TOP */
+  float* logprob;
+  float* entropy;
+  int32_t* rank;
+  float* row_stat;
+  int32_t* top_id;
+  float* top_logprob;
+} dspark_token_logprobs_args;
+
+DSPARK_API dspark_status dspark_token_logprobs_workspace_size(int32_t N, int32_t V, int32_t top, size_t* bytes);
+DSPARK_API dspark_status dspark_token_logprobs(const dspark_token_logprobs_args* args, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
+/* dspark_token_logprobs_grad: the gradient by the logits of
+ *     sum_i g_logprob[i] logprob[i] + g_entropy[i] entropy[i] + sum_k g_top[i, k] top_logprob[i, k]:
+ *     d(v) = (1 / T) (g_logprob [v = token] + sum_k g_top[k] [v = top_id[k]]
+ *                     - p(v) (G + g_entropy (ln p(v) + entropy))),
+ *     G = g_logprob + sum_k g_top[k]
+ * at candidates, 0 at every other place of the row and over a row without
+ * candidates.  Terms without a token, with top_id -1, or of a token that is no
+ * candidate are left out.  row_stat [N, 2] and, with g_entropy, entropy [N], and,
+ * with g_top, top_id [N, top] are dspark_token_logprobs's outputs for the same
+ * rows; g_logprob [N], g_entropy [N], g_top [N, top] may each be NULL (no such
+ * term).  top <= DSPARK_MAX_TOP.  grad [N, V] (rows.dtype, row stride ldg)
+ * may be the logits themselves (same address and stride), and must not overlap
+ * them otherwise.  A row whose S is NaN gets NaN at its candidates.  The
+ * workspace is that of dspark_token_logprobs (only the error word is used; may
+ * be any initialised dspark workspace). */
+typedef struct {
+  dspark_logit_rows rows;
+  int32_t top;
+  const float* row_stat;
+  const float* entropy;
+  const int32_t* top_id;
+  const float* g_logprob;
+  const float* g_entropy;
+  const float* g_top;
+  void* grad;
+  int64_t ldg;
+} dspark_token_logprobs_grad_args;
+
+DSPARK_API dspark_status dspark_token_logprobs_grad(const dspark_token_logprobs_grad_args* args, void* workspace,
+                                                    void* stream);
+
 /* Number of CUDA kernels this library has enqueued since it was loaded (a
  * host-side counter, incremented at launch time; a captured CUDA graph counts
  * its kernels once, at capture).  For accounting only: no library behaviour
