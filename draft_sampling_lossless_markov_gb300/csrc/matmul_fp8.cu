@@ -36,7 +36,7 @@ namespace dspark {
 
 namespace {
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr long long kWaitLimit = 4000000000ll;  // cycles: about two seconds
 constexpr int kKb = DSPARK_FP8_BLOCK;  // columns of a block: one 128-byte swizzled row of shared memory
 
 struct MmParams {
@@ -47,6 +47,7 @@ struct MmParams {
   int64_t ldo;
   const int32_t* n_rows;
   int tma_out;  // the output's rows are 16-byte aligned: stores by TMA
+  int a_vec;    // a_scale is 16-byte aligned
   WsHeader* hdr;
 };
 
@@ -63,36 +64,49 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------------------
-// wide: 256 x BN tiles by CTA pairs
+// wide: 256 x (128 NH) tiles by CTA pairs
 // ---------------------------------------------------------------------------
-constexpr int kEpiWarps = 8;
-constexpr int kWideThreads = 32 * (kEpiWarps + 2);
-
-template <int BN>
+// Warps of a CTA: 8 NH epilogue warps (warpgroup g reads 64 columns of TMEM),
+// then one each for loads, MMA and scales.
+//
+// A tile's columns are made as NH parts of 128, each with its own TMEM buffers:
+// a buffer goes MMA -> commit -> read out -> release, and the commit and the
+// release cross the pair (some 350 cycles each), so four smaller buffers keep the
+// tensor cores busier than two of 256 columns.  Part h takes rows 64 h .. 64 h + 63
+// of each CTA's rows of w: its columns 0-63 are the first CTA's, 64-127 the
+// second's, so a warpgroup's 64 columns lie in one scale block.
+template <int NH>
 struct Wide {
-  static constexpr uint32_t kA = 128 * kKb;         // bytes of a per CTA and stage
-  static constexpr uint32_t kB = BN / 2 * kKb;      // bytes of w per CTA and stage
+  static constexpr int BN = 128 * NH;
+  static constexpr int kEpiWarps = 8 * NH;
+  static constexpr int kThreads = 32 * (kEpiWarps + 3);
+  static constexpr uint32_t kA = 128 * kKb;       // bytes of a per CTA and stage
+  static constexpr uint32_t kB = BN / 2 * kKb;    // bytes of w per CTA and stage
   static constexpr uint32_t kStage = kA + kB;
-  static constexpr uint32_t kStg = kEpiWarps * 8192;  // output staging: two 4 KB buffers a warp
-  static constexpr int kStages = BN == 256 ? 5 : 6;
-  static constexpr int kBufs = 512 / BN;            // TMEM accumulators
-  static constexpr uint32_t kSmem = kStages * kStage + kStg + 1024;
+  static constexpr int kStages = NH == 2 ? 5 : 7;
+  static constexpr int kBufs = 4 / NH;            // TMEM buffers of 128 columns per part
+  static constexpr uint32_t kStg = kEpiWarps * 2048;  // output staging: 32 rows x 64 bytes a warp
+  static constexpr int kSlots = 4;                // scale ring: slots of 4 blocks
+  static constexpr uint32_t kSlot = 4 * 2 * 128 * 4;  // [4 blocks][2 column blocks][128 rows] fp32
+  static constexpr uint32_t kSmem = kStages * kStage + kStg + kSlots * kSlot + 1024;
 };
 
-template <int BN, typename TO>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+template <int NH, typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 1)
     k_fp8_wide(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                const __grid_constant__ CUtensorMap tmO, const MmParams p) {
-  using W = Wide<BN>;
-  constexpr int NS = W::kStages, NB = W::kBufs;
+  using W = Wide<NH>;
+  constexpr int NS = W::kStages, NB = W::kBufs, BN = W::BN, EW = W::kEpiWarps;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the same offset in both CTAs: the descriptors of a pair name one place for both
   uint8_t* sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t full[NS], empty[NS], tfull[NB], tempty[NB];
+  uint8_t* stg_all = sm + NS * W::kStage;
+  float* ring = reinterpret_cast<float*>(stg_all + W::kStg);
+  __shared__ uint64_t full[NS], empty[NS], tfull[NH * NB], tempty[NH * NB], sfull[W::kSlots], sempty[W::kSlots];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s, never_s;
   volatile int* abort_flag = &abort_s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp-uniform
   const uint32_t rank = ptx::cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
@@ -100,9 +114,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       ptx::mbar_init(&full[i], 1);
       ptx::mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < NH * NB; ++i) {
       ptx::mbar_init(&tfull[i], 1);
-      ptx::mbar_init(&tempty[i], 2 * kEpiWarps);
+      ptx::mbar_init(&tempty[i], 2 * 8);
+    }
+    for (int i = 0; i < W::kSlots; ++i) {
+      ptx::mbar_init(&sfull[i], 32);
+      ptx::mbar_init(&sempty[i], EW);
     }
     ptx::fence_mbar_init();
     abort_s = never_s = 0;
@@ -110,7 +128,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     ptx::prefetch_map(&tmW);
     ptx::prefetch_map(&tmO);
   }
-  if (warp == kEpiWarps + 1) {
+  if (warp == EW + 1) {
     ptx::tmem_alloc_pair(&tmem_slot, 512);
     ptx::tmem_relinquish_pair();
   }
@@ -118,168 +136,222 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   __syncthreads();
   ptx::cluster_sync();
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   auto fail = [&](int what) {
     if (p.hdr) report_error(p.hdr, DSPARK_TIMEOUT, what);
     *abort_flag = 1;
   };
   const int M = rows_of(p);
   const int mt = (M + 255) / 256;
-  const int64_t tiles = (int64_t)mt * ((p.N + BN - 1) / BN);
+  const int tiles = mt * ((p.N + BN - 1) / BN);
+  const int nblk = (p.N + kKb - 1) / kKb;
 
-  if (warp == kEpiWarps) {
+  if (warp == EW) {
     if (lane == 0) {
       // loads: this CTA's rows of a and its half of w's rows, signalled to the first CTA
       const uint64_t pol_a = ptx::policy_evict_last(), pol_w = ptx::policy_evict_normal();
-      uint32_t bar0[NS];
-      for (int i = 0; i < NS; ++i) bar0[i] = ptx::map_to_rank(&full[i], 0);
-      uint32_t it = 0;
+      const uint32_t bar0 = ptx::map_to_rank(&full[0], 0);
+      uint32_t s = 0, ph = 1, n = 0;
       bool ok = true;
-      for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        const int m0 = (int)(t % mt) * 256 + (int)rank * 128, n0 = (int)(t / mt) * BN + (int)rank * (BN / 2);
-        for (int b = 0; b < p.kb; ++b, ++it) {
-          const uint32_t s = it % NS;
-          if (!ptx::mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const int m0 = (t % mt) * 256 + (int)rank * 128, n0 = (t / mt) * BN + (int)rank * (BN / 2);
+        for (int b = 0; b < p.kb; ++b) {
+          if (!ptx::mbar_wait_cycles(&empty[s], ph, abort_flag, kWaitLimit)) {
             fail(1);
             ok = false;
             break;
           }
           uint8_t* dst = sm + s * W::kStage;
           if (rank == 0) ptx::mbar_expect_tx(&full[s], 2 * W::kStage);
-          ptx::tma_load_2d_pair(dst, &tmA, bar0[s], b * kKb, m0, pol_a);
-          ptx::tma_load_2d_pair(dst + W::kA, &tmW, bar0[s], b * kKb, n0, pol_w);
+          ptx::tma_load_2d_pair(dst, &tmA, bar0 + s * 8, b * kKb, m0, pol_a);
+          ptx::tma_load_2d_pair(dst + W::kA, &tmW, bar0 + s * 8, b * kKb, n0, pol_w);
+          ++n;
+          if (++s == NS) s = 0, ph ^= 1;
         }
       }
       // nothing of the pair may be in flight when the CTAs leave: the last
       // commits have arrived here, or (after a failure) at least the loads
-      for (uint32_t j = it > NS ? it - NS : 0; j < it; ++j)
+      for (uint32_t j = n > NS ? n - NS : 0; j < n; ++j)
         if (ok || rank == 0)
-          ptx::mbar_wait(ok ? &empty[j % NS] : &full[j % NS], (j / NS) & 1, &never_s, kWaitLimitNs);
+          ptx::mbar_wait_cycles(ok ? &empty[j % NS] : &full[j % NS], (j / NS) & 1, &never_s, kWaitLimit);
     }
     __syncwarp();
-  } else if (warp == kEpiWarps + 1) {
-    if (rank == 0 && lane == 0) {
-      constexpr uint32_t idesc = ptx::idesc_e4m3_f32(256, BN);
-      uint32_t it = 0;
+  } else if (warp == EW + 1) {
+    if (rank == 0) {
+      constexpr uint32_t idesc = ptx::idesc_e4m3_f32(256, 128);
+      // K-major, 128B swizzle: 8-row atoms 1024 bytes apart, 32 columns are 32 bytes
+      const uint64_t da0 = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
+      const uint64_t db0 = ptx::smem_desc_sw128(ptx::smem_u32(sm + W::kA), 16, 1024);
+      uint32_t s = 0, ph = 0, q = 0, tph = 1;
       bool ok = true;
-      for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        for (int b = 0; b < p.kb; ++b, ++it) {
-          const uint32_t s = it % NS, a = it % NB;
-          if (!ptx::mbar_wait(&full[s], (it / NS) & 1, abort_flag, kWaitLimitNs) ||
-              !ptx::mbar_wait(&tempty[a], ((it / NB) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
-            fail(2);
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t sa = ptx::smem_u32(sm + s * W::kStage), sb = sa + W::kA;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        for (int b = 0; b < p.kb && ok; ++b) {
+          ok = ptx::mbar_wait_cycles(&full[s], ph, abort_flag, kWaitLimit);
+          const uint64_t da = da0 + s * (W::kStage >> 4), db = db0 + s * (W::kStage >> 4);
 #pragma unroll
-          for (int k = 0; k < kKb / 32; ++k)
-            // K-major, 128B swizzle: 8-row atoms 1024 bytes apart, 32 columns are 32 bytes
-            ptx::tc_mma_fp8_pair(tmem + a * BN, ptx::smem_desc_sw128(sa + k * 32, 16, 1024),
-                                 ptx::smem_desc_sw128(sb + k * 32, 16, 1024), idesc, k ? 1u : 0u);
-          ptx::tc_commit_pair(&empty[s]);
-          ptx::tc_commit_pair(&tfull[a]);
+          for (int h = 0; h < NH; ++h) {
+            ok = ok && ptx::mbar_wait_cycles(&tempty[h * NB + q], tph, abort_flag, kWaitLimit);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+              const uint32_t d = tmem + (h * NB + q) * 128;
+              const uint64_t dbh = db + h * (64 * kKb / 16);
+              ptx::tc_mma_fp8_pair<0>(d, da, dbh, idesc);
+              ptx::tc_mma_fp8_pair<1>(d, da + 2, dbh + 2, idesc);
+              ptx::tc_mma_fp8_pair<1>(d, da + 4, dbh + 4, idesc);
+              ptx::tc_mma_fp8_pair<1>(d, da + 6, dbh + 6, idesc);
+              ptx::tc_commit_pair(&tfull[h * NB + q]);
+              if (h == NH - 1) ptx::tc_commit_pair(&empty[s]);
+            }
+            __syncwarp();
+          }
+          if (!ok && lane == 0) fail(2);
+          if (++s == NS) s = 0, ph ^= 1;
+          if (++q == NB) q = 0, tph ^= 1;
         }
       }
     }
-    __syncwarp();
-  } else {
-    constexpr int NC = BN / 2;  // columns of this warp
-    constexpr int CH = 128 / (int)sizeof(TO);  // columns of a 128-byte staging row
-    const int half = warp >> 2, quarter = warp & 3;
-    uint8_t* stg = sm + NS * W::kStage + warp * 8192;
-    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * NC);
-    uint32_t te[NB];
-    for (int i = 0; i < NB; ++i) te[i] = ptx::map_to_rank(&tempty[i], 0);
-    const int nblk = (p.N + kKb - 1) / kKb;
-    uint32_t it = 0, stores = 0;
+  } else if (warp == EW + 2) {
+    // scales: a_scale[row, b] w_scale[column block, b] of four blocks b at a time, four rows a lane
+    uint32_t slot = 0, ph = 1;
     bool ok = true;
-    for (int64_t t = pair; t < tiles && ok; t += pairs) {
-      const int row0 = (int)(t % mt) * 256 + (int)rank * 128 + quarter * 32;
-      const int col0 = (int)(t / mt) * BN + half * NC;
-      const float* as = p.a_scale + (int64_t)min(row0 + lane, M - 1) * p.kb;
-      const float* wsc = p.w_scale + (int64_t)min(col0 / kKb, nblk - 1) * p.kb;
-      uint64_t acc[NC / 2];
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int m0 = (t % mt) * 256 + (int)rank * 128, nb = (t / mt) * NH;
+      const float* w0 = p.w_scale + (int64_t)min(nb, nblk - 1) * p.kb;
+      const float* w1 = p.w_scale + (int64_t)min(nb + NH - 1, nblk - 1) * p.kb;
+      for (int b = 0; b < p.kb; b += 4) {
+        float sa[4][4], sw[2][4];
+        const int nb4 = min(4, p.kb - b);
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) acc[i] = 0;
-      float scale = as[0] * wsc[0];
+        for (int r = 0; r < 4; ++r) {
+          const float* ap = p.a_scale + (int64_t)min(m0 + r * 32 + lane, M - 1) * p.kb + b;
+          if (nb4 == 4 && (p.kb & 3) == 0 && p.a_vec) {
+            const float4 f = *reinterpret_cast<const float4*>(ap);
+            sa[r][0] = f.x, sa[r][1] = f.y, sa[r][2] = f.z, sa[r][3] = f.w;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sa[r][j] = j < nb4 ? ap[j] : 0.f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sw[0][j] = j < nb4 ? w0[b + j] : 0.f;
+          sw[1][j] = j < nb4 ? w1[b + j] : 0.f;
+        }
+        const bool got = ptx::mbar_wait_cycles(&sempty[slot], ph, abort_flag, kWaitLimit);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) fail(7);
+          ok = false;
+          break;
+        }
+        float* d = ring + slot * (W::kSlot / 4) + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d[(j * 2 + c) * 128 + r * 32] = sa[r][j] * sw[c][j];
+        ptx::mbar_arrive(&sfull[slot]);
+        if (++slot == W::kSlots) slot = 0, ph ^= 1;
+      }
+    }
+  } else {
+    constexpr int CH = 64 / (int)sizeof(TO);  // columns of a 64-byte staging row
+    const int g = warp >> 2, quarter = warp & 3, part = g >> 1, side = g & 1;
+    uint8_t* stg = stg_all + warp * 2048;
+    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * NB * 128 + side * 64);
+    const uint32_t te = ptx::map_to_rank(&tempty[part * NB], 0);
+    const float* sc = ring + side * 128 + quarter * 32 + lane;
+    uint32_t it = 0, slot = 0, sph = 0;
+    bool ok = true, staged = false;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int row0 = (t % mt) * 256 + (int)rank * 128 + quarter * 32;
+      const int col0 = (t / mt) * BN + side * (BN / 2) + part * 64;
+      uint64_t acc[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc[i] = 0;
       for (int b = 0; b < p.kb; ++b, ++it) {
-        const uint32_t a = it % NB;
-        const float next = b + 1 < p.kb ? as[b + 1] * wsc[b + 1] : 0.f;
-        const bool got = ptx::mbar_wait(&tfull[a], (it / NB) & 1, abort_flag, kWaitLimitNs);
+        const uint32_t q = it % NB;
+        bool got = true;
+        if ((b & 3) == 0) got = ptx::mbar_wait_cycles(&sfull[slot], sph, abort_flag, kWaitLimit);
+        const float scale = sc[slot * (W::kSlot / 4) + (b & 3) * 256];
+        got = got && ptx::mbar_wait_cycles(&tfull[part * NB + q], (it / NB) & 1, abort_flag, kWaitLimit);
         if (!__all_sync(0xffffffffu, got)) {
           if (lane == 0) fail(3);
           ok = false;
           break;
         }
+        if ((b & 3) == 3 || b + 1 == p.kb) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sempty[slot]);
+          if (++slot == W::kSlots) slot = 0, sph ^= 1;
+        }
         ptx::tc_fence_after();
         const uint64_t s2 = ptx::pack2(scale, scale);
-        float v[2][16];
-        ptx::tmem_ld16(taddr + a * BN, v[0]);
 #pragma unroll
-        for (int c = 0; c < NC / 16; ++c) {
-          ptx::tmem_ld_wait16(v[c & 1]);
-          if (c + 1 < NC / 16) {
-            ptx::tmem_ld16(taddr + a * BN + (c + 1) * 16, v[(c + 1) & 1]);
-          } else {
+        for (int c = 0; c < 4; ++c) {
+          float v[16];
+          ptx::tmem_ld16(taddr + q * 128 + c * 16, v);
+          ptx::tmem_ld_wait16(v);
+          if (c == 3) {
             ptx::tc_fence_before();
-            if (lane == 0) ptx::mbar_arrive_remote(te[a]);
+            if (lane == 0) ptx::mbar_arrive_remote(te + q * 8);
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc[c * 8 + i] = ptx::fma2(ptx::pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s2, acc[c * 8 + i]);
+          for (int i = 0; i < 8; ++i) acc[c * 8 + i] = ptx::fma2(ptx::pack2(v[2 * i], v[2 * i + 1]), s2, acc[c * 8 + i]);
         }
-        scale = next;
       }
       if (!ok) break;
-      // 32 rows x 128 bytes at a time through this warp's swizzled staging buffers
+      // 32 rows x 64 bytes at a time through this warp's swizzled staging buffer
 #pragma unroll
-      for (int c = 0; c < NC / CH; ++c) {
-        uint8_t* buf = stg + (stores & 1) * 4096;
+      for (int c = 0; c < 64 / CH; ++c) {
         const int col = col0 + c * CH;
-        if (stores >= 2) {
-          if (lane == 0) ptx::bulk_wait_read1();
+        if (col >= p.N || row0 >= M) break;
+        if (staged) {
+          if (lane == 0) ptx::bulk_wait_read0();
           __syncwarp();
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint4 q;
+        for (int u = 0; u < 4; ++u) {
+          uint4 v;
           if (sizeof(TO) == 2) {
             const uint64_t* x = acc + c * (CH / 2) + u * 4;
             const float2 f0 = ptx::unpack2(x[0]), f1 = ptx::unpack2(x[1]), f2 = ptx::unpack2(x[2]),
                          f3 = ptx::unpack2(x[3]);
-            q = make_uint4(pack_bf16(f0.x, f0.y), pack_bf16(f1.x, f1.y), pack_bf16(f2.x, f2.y), pack_bf16(f3.x, f3.y));
+            v = make_uint4(pack_bf16(f0.x, f0.y), pack_bf16(f1.x, f1.y), pack_bf16(f2.x, f2.y), pack_bf16(f3.x, f3.y));
           } else {
             const uint64_t* x = acc + c * (CH / 2) + u * 2;
-            q = make_uint4((uint32_t)x[0], (uint32_t)(x[0] >> 32), (uint32_t)x[1], (uint32_t)(x[1] >> 32));
+            v = make_uint4((uint32_t)x[0], (uint32_t)(x[0] >> 32), (uint32_t)x[1], (uint32_t)(x[1] >> 32));
           }
-          *reinterpret_cast<uint4*>(buf + lane * 128 + ((u ^ (lane & 7)) << 4)) = q;
+          // 64B swizzle: 16-byte unit u of row r at u ^ ((r / 2) % 4)
+          *reinterpret_cast<uint4*>(stg + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = v;
         }
-        if (col < p.N && row0 < M) {
-          if (p.tma_out && (row0 + 32 <= M || M == p.M)) {
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::tma_store_2d(&tmO, buf, col, row0);
-          } else {
-            __syncwarp();
-            TO* o = static_cast<TO*>(p.out) + col;
-            for (int r = 0; r < min(32, M - row0); ++r) {
-              const uint32_t w32 =
-                  *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-              TO* dst = o + (int64_t)(row0 + r) * p.ldo;
-              if (sizeof(TO) == 4) {
-                if (col + lane < p.N) reinterpret_cast<uint32_t*>(dst)[lane] = w32;
-              } else {
-                if (col + 2 * lane < p.N) reinterpret_cast<uint16_t*>(dst)[2 * lane] = (uint16_t)w32;
-                if (col + 2 * lane + 1 < p.N) reinterpret_cast<uint16_t*>(dst)[2 * lane + 1] = (uint16_t)(w32 >> 16);
-              }
+        if (p.tma_out && (row0 + 32 <= M || M == p.M)) {
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::tma_store_2d(&tmO, stg, col, row0);
+            ptx::bulk_commit();
+          }
+          staged = true;
+        } else {
+          __syncwarp();
+          // half a warp a row, four bytes a lane
+          const int l = lane & 15;
+          for (int r = lane >> 4; r < min(32, M - row0); r += 2) {
+            const uint32_t w32 =
+                *reinterpret_cast<const uint32_t*>(stg + r * 64 + (((l >> 2) ^ ((r >> 1) & 3)) << 4) + (l & 3) * 4);
+            TO* dst = static_cast<TO*>(p.out) + (int64_t)(row0 + r) * p.ldo + col;
+            if (sizeof(TO) == 4) {
+              if (col + l < p.N) reinterpret_cast<uint32_t*>(dst)[l] = w32;
+            } else {
+              if (col + 2 * l < p.N) reinterpret_cast<uint16_t*>(dst)[2 * l] = (uint16_t)w32;
+              if (col + 2 * l + 1 < p.N) reinterpret_cast<uint16_t*>(dst)[2 * l + 1] = (uint16_t)(w32 >> 16);
             }
           }
+          __syncwarp();
         }
-        if (lane == 0) ptx::bulk_commit();
-        ++stores;
-        __syncwarp();
       }
     }
     if (lane == 0) ptx::bulk_wait0();
@@ -287,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();
-  if (warp == kEpiWarps + 1) {
+  if (warp == EW + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem, 512);
   }
@@ -321,7 +393,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s, never_s;
   volatile int* abort_flag = &abort_s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp-uniform
   const int rank = split > 1 ? (int)ptx::cluster_rank() : 0;
   const int cl = blockIdx.x / split, cls = gridDim.x / split;
   float* red = reinterpret_cast<float*>(sm + stages * C::kStage);
@@ -346,7 +418,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   auto fail = [&](int what) {
     if (p.hdr) report_error(p.hdr, DSPARK_TIMEOUT, what);
     *abort_flag = 1;
@@ -364,7 +436,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       for (int64_t t = cl; t < tiles && ok; t += cls) {
         const int m0 = (int)(t % mt) * NT, n0 = (int)(t / mt) * 128;
         for (int b = b0; b < b1; ++b) {
-          if (!ptx::mbar_wait(&empty[s], ph ^ 1, abort_flag, kWaitLimitNs)) {
+          if (!ptx::mbar_wait_cycles(&empty[s], ph ^ 1, abort_flag, kWaitLimit)) {
             fail(4);
             ok = false;
             break;
@@ -379,36 +451,38 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       }
       // nothing may be in flight when the CTA leaves
       for (uint32_t j = n > (uint32_t)stages ? n - stages : 0; j < n; ++j)
-        ptx::mbar_wait(&full[j % stages], (j / stages) & 1, &never_s, kWaitLimitNs);
+        ptx::mbar_wait_cycles(&full[j % stages], (j / stages) & 1, &never_s, kWaitLimit);
     }
     __syncwarp();
   } else if (warp == 5) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, NT);
-      uint32_t s = 0, ph = 0, it = 0;
-      bool ok = true;
-      for (int64_t t = cl; t < tiles && ok; t += cls) {
-        for (int b = b0; b < b1; ++b, ++it) {
-          const uint32_t a = it % NB;
-          if (!ptx::mbar_wait(&full[s], ph, abort_flag, kWaitLimitNs) ||
-              !ptx::mbar_wait(&tempty[a], ((it / NB) & 1) ^ 1, abort_flag, kWaitLimitNs)) {
-            fail(5);
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t sw = ptx::smem_u32(sm + s * C::kStage), sa = sw + C::kW;
-#pragma unroll
-          for (int k = 0; k < kKb / 32; ++k)
-            ptx::tc_mma_fp8(tmem + a * NT, ptx::smem_desc_sw128(sw + k * 32, 16, 1024),
-                            ptx::smem_desc_sw128(sa + k * 32, 16, 1024), idesc, k ? 1u : 0u);
-          ptx::tc_commit(&empty[s]);
-          ptx::tc_commit(&tfull[a]);
-          if (++s == (uint32_t)stages) s = 0, ph ^= 1;
+    constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, NT);
+    const uint64_t dw0 = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
+    uint32_t s = 0, ph = 0, q = 0, tph = 1;
+    bool ok = true;
+    for (int64_t t = cl; t < tiles && ok; t += cls) {
+      for (int b = b0; b < b1; ++b) {
+        ok = ptx::mbar_wait_cycles(&full[s], ph, abort_flag, kWaitLimit) &&
+             ptx::mbar_wait_cycles(&tempty[q], tph, abort_flag, kWaitLimit);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) fail(5);
+          break;
         }
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint64_t dw = dw0 + s * (C::kStage >> 4), da = dw + (C::kW >> 4);
+          ptx::tc_mma_fp8<0>(tmem + q * NT, dw, da, idesc);
+          ptx::tc_mma_fp8<1>(tmem + q * NT, dw + 2, da + 2, idesc);
+          ptx::tc_mma_fp8<1>(tmem + q * NT, dw + 4, da + 4, idesc);
+          ptx::tc_mma_fp8<1>(tmem + q * NT, dw + 6, da + 6, idesc);
+          ptx::tc_commit(&empty[s]);
+          ptx::tc_commit(&tfull[q]);
+        }
+        __syncwarp();
+        if (++s == (uint32_t)stages) s = 0, ph ^= 1;
+        if (++q == NB) q = 0, tph ^= 1;
       }
     }
-    __syncwarp();
   }
   uint32_t it = 0;
   bool ok = true;
@@ -430,7 +504,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
           const int c = j * 32 + lane;
           sc[j] = c < nm ? ws * p.a_scale[(int64_t)(m0 + c) * p.kb + b] : 0.f;
         }
-        const bool got = ptx::mbar_wait(&tfull[a], (it / NB) & 1, abort_flag, kWaitLimitNs);
+        const bool got = ptx::mbar_wait_cycles(&tfull[a], (it / NB) & 1, abort_flag, kWaitLimit);
         if (!__all_sync(0xffffffffu, got)) {
           if (lane == 0) fail(6);
           ok = false;
@@ -528,16 +602,16 @@ cudaError_t device(Dev* out) {
     if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     d.sm103 = major == 10 && minor == 3;
     if (d.sm103) {
-      const void* f = (const void*)k_fp8_wide<256, __nv_bfloat16>;
-      if ((e = ensure_smem_limit(f, (int)Wide<256>::kSmem)) != cudaSuccess) return e;
+      const void* f = (const void*)k_fp8_wide<2, __nv_bfloat16>;
+      if ((e = ensure_smem_limit(f, (int)Wide<2>::kSmem)) != cudaSuccess) return e;
       cudaLaunchConfig_t c = {};
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;
       at[0].val.clusterDim.x = 2;
       at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
       c.gridDim = dim3((unsigned)(d.sms / 2 * 2));
-      c.blockDim = dim3(kWideThreads);
-      c.dynamicSmemBytes = Wide<256>::kSmem;
+      c.blockDim = dim3(Wide<2>::kThreads);
+      c.dynamicSmemBytes = Wide<2>::kSmem;
       c.attrs = at;
       c.numAttrs = 1;
       if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, f, &c)) != cudaSuccess) return e;
@@ -550,21 +624,23 @@ cudaError_t device(Dev* out) {
   return cudaSuccess;
 }
 
-template <int BN, typename TO>
+template <int NH, typename TO>
 cudaError_t run_wide(const dspark_matmul_fp8_args& a, const MmParams& p, const Dev& d, cudaStream_t s) {
+  using W = Wide<NH>;
   CUtensorMap tmA, tmW, tmO = {};
   if (!tensor_map_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, a.K, a.M, a.lda, kKb, 128) ||
-      !tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.ldw, kKb, BN / 2))
+      !tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.ldw, kKb, W::BN / 2))
     return cudaErrorInvalidValue;
   if (p.tma_out &&
       !tensor_map_2d(&tmO, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.out,
-                     a.N, a.M, a.ldo * (int64_t)sizeof(TO), 128 / sizeof(TO), 32))
+                     a.N, a.M, a.ldo * (int64_t)sizeof(TO), 64 / (int)sizeof(TO), 32, (int)sizeof(TO)))
     return cudaErrorInvalidValue;
-  const void* f = (const void*)k_fp8_wide<BN, TO>;
-  if (const cudaError_t e = ensure_smem_limit(f, (int)Wide<BN>::kSmem); e != cudaSuccess) return e;
-  const int64_t tiles = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + BN - 1) / BN);
+  const int64_t tiles = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + W::BN - 1) / W::BN);
+  if (tiles > INT32_MAX - d.pairs) return cudaErrorNotSupported;
+  const void* f = (const void*)k_fp8_wide<NH, TO>;
+  if (const cudaError_t e = ensure_smem_limit(f, (int)W::kSmem); e != cudaSuccess) return e;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, d.pairs);
-  k_fp8_wide<BN, TO><<<grid, kWideThreads, Wide<BN>::kSmem, s>>>(tmA, tmW, tmO, p);
+  k_fp8_wide<NH, TO><<<grid, W::kThreads, W::kSmem, s>>>(tmA, tmW, tmO, p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -610,7 +686,7 @@ cudaError_t run(const dspark_matmul_fp8_args& a, const MmParams& p, const Dev& d
   const int64_t mt = ((int64_t)a.M + 255) / 256;
   // the tile width that finishes first: waves of pairs times the width
   const auto cost = [&](int bn) { return (mt * ((a.N + bn - 1) / bn) + d.pairs - 1) / d.pairs * bn; };
-  return cost(128) < cost(256) ? run_wide<128, TO>(a, p, d, s) : run_wide<256, TO>(a, p, d, s);
+  return cost(128) < cost(256) ? run_wide<1, TO>(a, p, d, s) : run_wide<2, TO>(a, p, d, s);
 }
 
 }  // namespace
@@ -632,6 +708,7 @@ cudaError_t launch_matmul_fp8(const dspark_matmul_fp8_args& a, uint8_t* ws, cuda
   p.ldo = a.ldo;
   p.n_rows = a.n_rows;
   p.tma_out = ((uintptr_t)a.out % 16) == 0 && (a.M == 1 || (a.ldo * esize) % 16 == 0);
+  p.a_vec = ((uintptr_t)a.a_scale % 16) == 0;
   p.hdr = reinterpret_cast<WsHeader*>(ws);
   return a.out_dtype == DSPARK_BF16 ? run<__nv_bfloat16>(a, p, d, s) : run<float>(a, p, d, s);
 }

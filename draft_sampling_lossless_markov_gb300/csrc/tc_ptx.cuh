@@ -60,6 +60,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The same with the limit in SM cycles and read first after 256 polls: the
+// cycle counter is local to the SM, where the wall clock is a slow read that a
+// wait of a few hundred nanoseconds would pay in full.
+__device__ __forceinline__ bool mbar_wait_cycles(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                 long long limit) {
+  long long t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0u) {
+      if (*abort) return false;
+      const long long t = clock64();
+      if (t0 == 0)
+        t0 = t;
+      else if (t - t0 > limit)
+        return false;
+    }
+  }
+}
+
 // ---- L2 cache policies ----
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;
@@ -266,7 +285,7 @@ __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
   return a;
 }
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
   float4 v;
@@ -305,24 +324,27 @@ __device__ __forceinline__ void tmem_relinquish_pair() {
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// D[tmem] (+)= A[smem desc] x B[smem desc], kind::f8f6f4 (e4m3 inputs, fp32 accumulate)
-__device__ __forceinline__ void tc_mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// D[tmem] (+)= A[smem desc] x B[smem desc], kind::f8f6f4 (e4m3 inputs, fp32 accumulate); kAcc 0 starts a new sum.
+// Issue these from a warp-uniform loop under elect_one(): issued by one thread
+// of a divergent branch, an instruction takes some 180 cycles whatever its
+// size, under elect_one() 45 to 130 (its execution time).
+template <int kAcc>
+__device__ __forceinline__ void tc_mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(kAcc)
       : "memory");
 }
 // the same over a CTA pair: A's rows, B's rows and D's lanes are halved over the two CTAs
-__device__ __forceinline__ void tc_mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate) {
+template <int kAcc>
+__device__ __forceinline__ void tc_mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(kAcc)
       : "memory");
 }
 // arrive once on `bar`'s place in both CTAs of the pair when every MMA issued so far has completed

@@ -28,21 +28,20 @@ inline TensorMapEncodeFn tensor_map_encode_fn() {
 }
 
 // A [rows, cols] matrix with `stride` bytes between rows, copied in boxes of
-// box_cols x box_rows (128 bytes a row) with the 128-byte swizzle; reads
-// outside the matrix give zeros, writes there are dropped.  A single row needs no
-// stride of its own.
+// box_cols x box_rows, 128 or 64 bytes a row with the swizzle of that width;
+// reads outside the matrix give zeros, writes there are dropped.  A single row
+// needs no stride of its own.
 inline bool tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int64_t cols, int64_t rows,
-                          int64_t stride, int box_cols, int box_rows) {
+                          int64_t stride, int box_cols, int box_rows, int esize = 1) {
   const TensorMapEncodeFn fn = tensor_map_encode_fn();
   if (!fn) return false;
-  const int esize = 128 / box_cols;
   if (rows == 1) stride = (cols * esize + 15) / 16 * 16;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)stride};
   const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   const cuuint32_t es[2] = {1, 1};
   return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            box_cols * esize == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
