@@ -67,7 +67,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // wide: 256 x (128 NH) tiles by CTA pairs
 // ---------------------------------------------------------------------------
 // Warps of a CTA: 8 NH epilogue warps (warpgroup g reads 64 columns of TMEM),
-// then one each for loads, MMA and scales.
+// then one each for loads and scales and NH for the MMAs.
 //
 // A tile's columns are made as NH parts of 128, each with its own TMEM buffers:
 // a buffer goes MMA -> commit -> read out -> release, and the commit and the
@@ -79,13 +79,13 @@ template <int NH>
 struct Wide {
   static constexpr int BN = 128 * NH;
   static constexpr int kEpiWarps = 8 * NH;
-  static constexpr int kThreads = 32 * (kEpiWarps + 3);
+  static constexpr int kThreads = 32 * (kEpiWarps + 2 + NH);
   static constexpr uint32_t kA = 128 * kKb;       // bytes of a per CTA and stage
   static constexpr uint32_t kB = BN / 2 * kKb;    // bytes of w per CTA and stage
   static constexpr uint32_t kStage = kA + kB;
-  static constexpr int kStages = NH == 2 ? 5 : 7;
+  static constexpr int kStages = NH == 2 ? 4 : 6;
   static constexpr int kBufs = 4 / NH;            // TMEM buffers of 128 columns per part
-  static constexpr uint32_t kStg = kEpiWarps * 2048;  // output staging: 32 rows x 64 bytes a warp
+  static constexpr uint32_t kStg = kEpiWarps * 4096;  // output staging: 32 rows x 128 bytes a warp
   static constexpr int kSlots = 4;                // scale ring: slots of 4 blocks
   static constexpr uint32_t kSlot = 4 * 2 * 128 * 4;  // [4 blocks][2 column blocks][128 rows] fp32
   static constexpr uint32_t kSmem = kStages * kStage + kStg + kSlots * kSlot + 1024;
@@ -112,7 +112,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       ptx::mbar_init(&full[i], 1);
-      ptx::mbar_init(&empty[i], 1);
+      ptx::mbar_init(&empty[i], NH);
     }
     for (int i = 0; i < NH * NB; ++i) {
       ptx::mbar_init(&tfull[i], 1);
@@ -128,7 +128,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
     ptx::prefetch_map(&tmW);
     ptx::prefetch_map(&tmO);
   }
-  if (warp == EW + 1) {
+  if (warp == EW + 2) {
     ptx::tmem_alloc_pair(&tmem_slot, 512);
     ptx::tmem_relinquish_pair();
   }
@@ -176,43 +176,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
           ptx::mbar_wait_cycles(ok ? &empty[j % NS] : &full[j % NS], (j / NS) & 1, &never_s, kWaitLimit);
     }
     __syncwarp();
-  } else if (warp == EW + 1) {
+  } else if (warp > EW + 1) {
+    // one MMA warp per part: its waits (some 80 cycles each even when they
+    // are over) run beside the other's
     if (rank == 0) {
+      const int h = warp - (EW + 2);
       constexpr uint32_t idesc = ptx::idesc_e4m3_f32(256, 128);
       // K-major, 128B swizzle: 8-row atoms 1024 bytes apart, 32 columns are 32 bytes
       const uint64_t da0 = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
-      const uint64_t db0 = ptx::smem_desc_sw128(ptx::smem_u32(sm + W::kA), 16, 1024);
+      const uint64_t db0 = ptx::smem_desc_sw128(ptx::smem_u32(sm + W::kA + h * (64 * kKb)), 16, 1024);
+      const uint32_t d0 = tmem + h * NB * 128;
       uint32_t s = 0, ph = 0, q = 0, tph = 1;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        for (int b = 0; b < p.kb && ok; ++b) {
-          ok = ptx::mbar_wait_cycles(&full[s], ph, abort_flag, kWaitLimit);
-          const uint64_t da = da0 + s * (W::kStage >> 4), db = db0 + s * (W::kStage >> 4);
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            ok = ok && ptx::mbar_wait_cycles(&tempty[h * NB + q], tph, abort_flag, kWaitLimit);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-              const uint32_t d = tmem + (h * NB + q) * 128;
-              const uint64_t dbh = db + h * (64 * kKb / 16);
-              ptx::tc_mma_fp8_pair<0>(d, da, dbh, idesc);
-              ptx::tc_mma_fp8_pair<1>(d, da + 2, dbh + 2, idesc);
-              ptx::tc_mma_fp8_pair<1>(d, da + 4, dbh + 4, idesc);
-              ptx::tc_mma_fp8_pair<1>(d, da + 6, dbh + 6, idesc);
-              ptx::tc_commit_pair(&tfull[h * NB + q]);
-              if (h == NH - 1) ptx::tc_commit_pair(&empty[s]);
-            }
-            __syncwarp();
+      for (int t = pair; t < tiles; t += pairs) {
+        for (int b = 0; b < p.kb; ++b) {
+          // after a wait that gave up the loop runs on (its results are void): every later wait ends at once
+          if (!ptx::mbar_wait_cycles(&full[s], ph, abort_flag, kWaitLimit) ||
+              !ptx::mbar_wait_cycles(&tempty[h * NB + q], tph, abort_flag, kWaitLimit))
+            fail(2);
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint64_t da = da0 + s * (W::kStage >> 4), db = db0 + s * (W::kStage >> 4);
+            const uint32_t d = d0 + q * 128;
+            ptx::tc_mma_fp8_pair<0>(d, da, db, idesc);
+            ptx::tc_mma_fp8_pair<1>(d, da + 2, db + 2, idesc);
+            ptx::tc_mma_fp8_pair<1>(d, da + 4, db + 4, idesc);
+            ptx::tc_mma_fp8_pair<1>(d, da + 6, db + 6, idesc);
+            ptx::tc_commit_pair(&tfull[h * NB + q]);
+            ptx::tc_commit_pair(&empty[s]);
           }
-          if (!ok && lane == 0) fail(2);
+          __syncwarp();
           if (++s == NS) s = 0, ph ^= 1;
           if (++q == NB) q = 0, tph ^= 1;
         }
       }
     }
-  } else if (warp == EW + 2) {
+    __syncwarp();
+  } else if (warp == EW + 1) {
     // scales: a_scale[row, b] w_scale[column block, b] of four blocks b at a time, four rows a lane
     uint32_t slot = 0, ph = 1;
     bool ok = true;
@@ -257,38 +256,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
       }
     }
   } else {
-    constexpr int CH = 64 / (int)sizeof(TO);  // columns of a 64-byte staging row
+    constexpr int CH = 128 / (int)sizeof(TO);  // columns of a 128-byte staging row
     const int g = warp >> 2, quarter = warp & 3, part = g >> 1, side = g & 1;
-    uint8_t* stg = stg_all + warp * 2048;
+    uint8_t* stg = stg_all + warp * 4096;
     const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * NB * 128 + side * 64);
     const uint32_t te = ptx::map_to_rank(&tempty[part * NB], 0);
     const float* sc = ring + side * 128 + quarter * 32 + lane;
-    uint32_t it = 0, slot = 0, sph = 0;
-    bool ok = true, staged = false;
-    for (int t = pair; t < tiles && ok; t += pairs) {
+    uint32_t q = 0, tph = 0, slot = 0, sph = 0;
+    bool staged = false;
+    for (int t = pair; t < tiles; t += pairs) {
       const int row0 = (t % mt) * 256 + (int)rank * 128 + quarter * 32;
       const int col0 = (t / mt) * BN + side * (BN / 2) + part * 64;
       uint64_t acc[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[i] = 0;
-      for (int b = 0; b < p.kb; ++b, ++it) {
-        const uint32_t q = it % NB;
+      for (int b = 0; b < p.kb; ++b) {
         bool got = true;
         if ((b & 3) == 0) got = ptx::mbar_wait_cycles(&sfull[slot], sph, abort_flag, kWaitLimit);
         const float scale = sc[slot * (W::kSlot / 4) + (b & 3) * 256];
-        got = got && ptx::mbar_wait_cycles(&tfull[part * NB + q], (it / NB) & 1, abort_flag, kWaitLimit);
-        if (!__all_sync(0xffffffffu, got)) {
-          if (lane == 0) fail(3);
-          ok = false;
-          break;
-        }
-        if ((b & 3) == 3 || b + 1 == p.kb) {
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sempty[slot]);
-          if (++slot == W::kSlots) slot = 0, sph ^= 1;
-        }
-        ptx::tc_fence_after();
         const uint64_t s2 = ptx::pack2(scale, scale);
+        got = ptx::mbar_wait_cycles(&tfull[part * NB + q], tph, abort_flag, kWaitLimit) && got;
+        if (!got) fail(3);  // the loop runs on: every later wait ends at once
+        __syncwarp();
+        ptx::tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float v[16];
@@ -301,9 +291,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[c * 8 + i] = ptx::fma2(ptx::pack2(v[2 * i], v[2 * i + 1]), s2, acc[c * 8 + i]);
         }
+        if (++q == NB) q = 0, tph ^= 1;
+        if ((b & 3) == 3 || b + 1 == p.kb) {
+          if (lane == 0) ptx::mbar_arrive(&sempty[slot]);
+          if (++slot == W::kSlots) slot = 0, sph ^= 1;
+        }
       }
-      if (!ok) break;
-      // 32 rows x 64 bytes at a time through this warp's swizzled staging buffer
+      // 32 rows x 128 bytes at a time through this warp's swizzled staging buffer
 #pragma unroll
       for (int c = 0; c < 64 / CH; ++c) {
         const int col = col0 + c * CH;
@@ -313,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
           __syncwarp();
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
           uint4 v;
           if (sizeof(TO) == 2) {
             const uint64_t* x = acc + c * (CH / 2) + u * 4;
@@ -324,8 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
             const uint64_t* x = acc + c * (CH / 2) + u * 2;
             v = make_uint4((uint32_t)x[0], (uint32_t)(x[0] >> 32), (uint32_t)x[1], (uint32_t)(x[1] >> 32));
           }
-          // 64B swizzle: 16-byte unit u of row r at u ^ ((r / 2) % 4)
-          *reinterpret_cast<uint4*>(stg + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = v;
+          // 128B swizzle: 16-byte unit u of row r at u ^ (r % 8)
+          *reinterpret_cast<uint4*>(stg + lane * 128 + ((u ^ (lane & 7)) << 4)) = v;
         }
         if (p.tma_out && (row0 + 32 <= M || M == p.M)) {
           ptx::fence_proxy_async_smem();
@@ -337,17 +331,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
           staged = true;
         } else {
           __syncwarp();
-          // half a warp a row, four bytes a lane
-          const int l = lane & 15;
-          for (int r = lane >> 4; r < min(32, M - row0); r += 2) {
+          // a row at a time, four bytes a lane
+          TO* dst = static_cast<TO*>(p.out) + (int64_t)row0 * p.ldo + col;
+          const int rows = min(32, M - row0);
+#pragma unroll 8
+          for (int r = 0; r < 32; ++r) {
             const uint32_t w32 =
-                *reinterpret_cast<const uint32_t*>(stg + r * 64 + (((l >> 2) ^ ((r >> 1) & 3)) << 4) + (l & 3) * 4);
-            TO* dst = static_cast<TO*>(p.out) + (int64_t)(row0 + r) * p.ldo + col;
-            if (sizeof(TO) == 4) {
-              if (col + l < p.N) reinterpret_cast<uint32_t*>(dst)[l] = w32;
-            } else {
-              if (col + 2 * l < p.N) reinterpret_cast<uint16_t*>(dst)[2 * l] = (uint16_t)w32;
-              if (col + 2 * l + 1 < p.N) reinterpret_cast<uint16_t*>(dst)[2 * l + 1] = (uint16_t)(w32 >> 16);
+                *reinterpret_cast<const uint32_t*>(stg + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+            if (r < rows) {
+              TO* o = dst + (int64_t)r * p.ldo;
+              if (sizeof(TO) == 4) {
+                if (col + lane < p.N) reinterpret_cast<uint32_t*>(o)[lane] = w32;
+              } else {
+                if (col + 2 * lane < p.N) reinterpret_cast<uint16_t*>(o)[2 * lane] = (uint16_t)w32;
+                if (col + 2 * lane + 1 < p.N) reinterpret_cast<uint16_t*>(o)[2 * lane + 1] = (uint16_t)(w32 >> 16);
+              }
             }
           }
           __syncwarp();
@@ -359,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();
-  if (warp == EW + 1) {
+  if (warp == EW + 2) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem, 512);
   }
@@ -579,9 +577,35 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 // ---------------------------------------------------------------------------
 struct Dev {
   int sms = 0;
-  int pairs = 0;  // CTA pairs of the wide kernel that run at the same time
+  int pairs = 0;  // clusters of two CTAs of the wide kernel that run at the same time
   bool sm103 = false;
 };
+
+void cluster_config(cudaLaunchConfig_t* c, cudaLaunchAttribute* at, unsigned cluster, unsigned grid, unsigned threads,
+                    unsigned smem, cudaStream_t s) {
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = cluster;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  c->gridDim = dim3(grid);
+  c->blockDim = dim3(threads);
+  c->dynamicSmemBytes = smem;
+  c->stream = s;
+  c->attrs = at;
+  c->numAttrs = cluster > 1 ? 1 : 0;
+}
+
+// pairs of the wide kernel that fit the device at once
+cudaError_t count_pairs(int sms, int* n) {
+  using W = Wide<2>;
+  const void* f = (const void*)k_fp8_wide<2, __nv_bfloat16>;
+  if (const cudaError_t e = ensure_smem_limit(f, (int)W::kSmem); e != cudaSuccess) return e;
+  cudaLaunchConfig_t c = {};
+  cudaLaunchAttribute at[1];
+  cluster_config(&c, at, 2, (unsigned)(sms / 2 * 2), W::kThreads, W::kSmem, nullptr);
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, f, &c);
+  *n = std::max(1, std::min(*n, sms / 2));
+  return e;
+}
 
 // properties of the current device, looked up once each
 cudaError_t device(Dev* out) {
@@ -602,20 +626,7 @@ cudaError_t device(Dev* out) {
     if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     d.sm103 = major == 10 && minor == 3;
     if (d.sm103) {
-      const void* f = (const void*)k_fp8_wide<2, __nv_bfloat16>;
-      if ((e = ensure_smem_limit(f, (int)Wide<2>::kSmem)) != cudaSuccess) return e;
-      cudaLaunchConfig_t c = {};
-      cudaLaunchAttribute at[1];
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = 2;
-      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-      c.gridDim = dim3((unsigned)(d.sms / 2 * 2));
-      c.blockDim = dim3(Wide<2>::kThreads);
-      c.dynamicSmemBytes = Wide<2>::kSmem;
-      c.attrs = at;
-      c.numAttrs = 1;
-      if ((e = cudaOccupancyMaxActiveClusters(&d.pairs, f, &c)) != cudaSuccess) return e;
-      d.pairs = std::max(1, std::min(d.pairs, d.sms / 2));
+      if ((e = count_pairs(d.sms, &d.pairs)) != cudaSuccess) return e;
     }
     cache[dev] = d;
     have[dev] = true;
@@ -633,7 +644,7 @@ cudaError_t run_wide(const dspark_matmul_fp8_args& a, const MmParams& p, const D
     return cudaErrorInvalidValue;
   if (p.tma_out &&
       !tensor_map_2d(&tmO, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.out,
-                     a.N, a.M, a.ldo * (int64_t)sizeof(TO), 64 / (int)sizeof(TO), 32, (int)sizeof(TO)))
+                     a.N, a.M, a.ldo * (int64_t)sizeof(TO), 128 / (int)sizeof(TO), 32, (int)sizeof(TO)))
     return cudaErrorInvalidValue;
   const int64_t tiles = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + W::BN - 1) / W::BN);
   if (tiles > INT32_MAX - d.pairs) return cudaErrorNotSupported;
@@ -663,15 +674,8 @@ cudaError_t run_narrow(const dspark_matmul_fp8_args& a, const MmParams& p, const
   if (const cudaError_t e = ensure_smem_limit(f, (int)smem); e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  c.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, d.sms)));
-  c.blockDim = dim3(kNarrowThreads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  c.attrs = at;
-  c.numAttrs = split > 1 ? 1 : 0;
+  cluster_config(&c, at, (unsigned)split, (unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, d.sms)),
+                 kNarrowThreads, smem, s);
   const cudaError_t e = cudaLaunchKernelEx(&c, k_fp8_narrow<NT, TO>, tmA, tmW, p, split, stages, mt);
   if (e != cudaSuccess) return e;
   count_launches(1);
@@ -683,10 +687,13 @@ cudaError_t run(const dspark_matmul_fp8_args& a, const MmParams& p, const Dev& d
   if (a.M <= 16) return run_narrow<16, TO>(a, p, d, s);
   if (a.M <= 32) return run_narrow<32, TO>(a, p, d, s);
   if (a.M <= 64) return run_narrow<64, TO>(a, p, d, s);
+  // waves of pairs times a tile's columns; a column of a 128-column tile costs
+  // 1.25 of a 256-column tile's (2048 x 4096 x 151936: 1.10 against 0.88 ms), which
+  // pays where the wider tiles leave pairs idle (512 x 4096 x 4096: 13.7 against
+  // 19.8 us)
   const int64_t mt = ((int64_t)a.M + 255) / 256;
-  // the tile width that finishes first: waves of pairs times the width
-  const auto cost = [&](int bn) { return (mt * ((a.N + bn - 1) / bn) + d.pairs - 1) / d.pairs * bn; };
-  return cost(128) < cost(256) ? run_wide<1, TO>(a, p, d, s) : run_wide<2, TO>(a, p, d, s);
+  const auto cost = [&](int bn) { return (double)((mt * ((a.N + bn - 1) / bn) + d.pairs - 1) / d.pairs * bn); };
+  return 1.25 * cost(128) < cost(256) ? run_wide<1, TO>(a, p, d, s) : run_wide<2, TO>(a, p, d, s);
 }
 
 }  // namespace

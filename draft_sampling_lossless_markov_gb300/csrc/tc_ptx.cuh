@@ -347,7 +347,7 @@ __device__ __forceinline__ void tc_mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc
       "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(kAcc)
       : "memory");
 }
-// arrive once on `bar`'s place in both CTAs of the pair when every MMA issued so far has completed
+// arrive once on `bar`'s place in both CTAs of the pair (a cluster of two) when every MMA issued so far has completed
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
