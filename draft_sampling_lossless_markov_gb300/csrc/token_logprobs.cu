@@ -115,16 +115,9 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 1.0 where a > b, 0.0 elsewhere
+// 0xFFFF in each half where a > b
 __device__ __forceinline__ uint32_t gt_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+  return __hgt2_mask(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -156,9 +149,10 @@ struct Vec8<__nv_bfloat16> {
       *w[i] = (*w[i] & keep) | (0xFF80FF80u & ~keep);
     }
   }
-  // the largest element (NaN is passed over)
+  // the largest element (NaN is passed over), of each half and of both
+  __device__ __forceinline__ uint32_t max2() const { return max_bf16x2(max_bf16x2(a.x, a.y), max_bf16x2(a.z, a.w)); }
   __device__ __forceinline__ float max() const {
-    const uint32_t x = max_bf16x2(max_bf16x2(a.x, a.y), max_bf16x2(a.z, a.w));
+    const uint32_t x = max2();
     return fmaxf(bf_lo(x), bf_hi(x));
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -273,20 +267,23 @@ struct SumsBase {
     S2 = ptx::add2(S2, ptx::pack2(e, 0.f));
     A2 = ptx::add2(A2, ptx::pack2(e * t, 0.f));
   }
+  // what the sums are about the largest element
   __device__ __forceinline__ Stat stat() {
     raise(largest);
     const float2 s = ptx::unpack2(S2), a = ptx::unpack2(A2);
     return Stat{m, s.x + s.y, a.x + a.y};
   }
 };
+// add() takes a vector and says whether one of its elements reaches `want`
 template <typename T>
 struct Sums;
 template <>
 struct Sums<float> : SumsBase {
-  float x_hi, x_lo, n = 0.f;
+  float x_hi, x_lo, n = 0.f, want = INFINITY;
   int total = 0;
   __device__ __forceinline__ Sums(float c_, float hi, float lo) : SumsBase(c_), x_hi(hi), x_lo(lo) {}
-  __device__ __forceinline__ float add(const Vec8<float>& v, bool before) {
+  __device__ __forceinline__ void set_want(float x) { want = x; }
+  __device__ __forceinline__ bool add(const Vec8<float>& v, bool before) {
     float x[8];
     v.get(x);
     const float cm = v.max();
@@ -300,14 +297,7 @@ struct Sums<float> : SumsBase {
       n += x[e] > xr ? 1.f : 0.f;
       n += x[e + 1] > xr ? 1.f : 0.f;
     }
-    return cm;
-  }
-  // elements equal to the token's in front of it in its own vector
-  __device__ __forceinline__ void ties_before(const Vec8<float>& v, float xt, int place) {
-    float x[8];
-    v.get(x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) total += x[e] == xt && e < place;
+    return cm >= want;
   }
   __device__ __forceinline__ void add_one(float x, bool before) {
     if (x > limit) raise(x);
@@ -319,7 +309,8 @@ struct Sums<float> : SumsBase {
     total += (int)n;
     n = 0.f;
   }
-  __device__ __forceinline__ int count() const { return total; }
+  __device__ __forceinline__ float top() const { return largest; }
+  __device__ __forceinline__ void finish() {}
 };
 template <>
 struct Sums<__nv_bfloat16> : SumsBase {
@@ -327,28 +318,30 @@ struct Sums<__nv_bfloat16> : SumsBase {
   // below m that its t is at most -200 and its term 0.  There is no such bf16
   // for m < -1e38 (a thread that has met no candidate, or rows of the lowest
   // value): those vectors take the clamp on t.
-  uint32_t floor2 = 0, hi2, lo2, n2 = 0;
+  uint32_t floor2 = 0, limit2 = 0xFF80FF80u, largest2 = 0xFF7FFF7Fu, want2 = 0x7F807F80u, hi2, lo2, n2 = 0;
   float x_hi, x_lo;
   int total = 0;
-  __device__ __forceinline__ Sums(float c_, float hi, float lo) : SumsBase(c_), x_hi(hi), x_lo(lo) {
-    hi2 = (__float_as_uint(hi) >> 16) * 0x10001u;
-    lo2 = (__float_as_uint(lo) >> 16) * 0x10001u;
-  }
-  __device__ __forceinline__ void set_floor() {
-    // rounded down, then one more: strictly below m whatever its size
-    const float f = m - 6.25f * gap;
+  // bf16 at or below a float, in both halves
+  static __device__ __forceinline__ uint32_t down2(float f) {
     const uint32_t b = __float_as_uint(f);
-    const uint32_t t = (b & 0x80000000u) ? (b + 0xFFFFu) & 0xFFFF0000u : b & 0xFFFF0000u;
-    floor2 = (bits_below(t, 0x10000u) >> 16) * 0x10001u;
+    return (((b & 0x80000000u) ? b + 0xFFFFu : b) >> 16) * 0x10001u;
   }
-  __device__ __forceinline__ float add(const Vec8<__nv_bfloat16>& v, bool before) {
+  __device__ __forceinline__ Sums(float c_, float hi, float lo) : SumsBase(c_), x_hi(hi), x_lo(lo) {
+    hi2 = down2(hi);
+    lo2 = down2(lo);
+  }
+  __device__ __forceinline__ void set_want(float x) { want2 = down2(value_below<__nv_bfloat16>(x)); }
+  __device__ __forceinline__ void raise_to(float cm) {
+    raise(cm);
+    limit2 = down2(limit);
+    // one more below: strictly below m whatever its size
+    floor2 = down2(value_below<__nv_bfloat16>(__uint_as_float(down2(m - 6.25f * gap) << 16)));
+  }
+  __device__ __forceinline__ bool add(const Vec8<__nv_bfloat16>& v, bool before) {
     const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
-    const float cm = v.max();
-    if (cm > limit) {
-      raise(cm);
-      set_floor();
-    }
-    largest = fmaxf(largest, cm);
+    const uint32_t cm2 = v.max2();
+    if (gt_bf16x2(cm2, limit2)) raise_to(fmaxf(bf_lo(cm2), bf_hi(cm2)));
+    largest2 = max_bf16x2(largest2, cm2);
     const uint64_t nm = ptx::pack2(-m, -m);
     const uint32_t xr = before ? lo2 : hi2;
     if (m > -1e38f) {
@@ -365,31 +358,26 @@ struct Sums<__nv_bfloat16> : SumsBase {
 #pragma unroll
       for (int i = 0; i < 4; ++i) pair(bf_lo(w[i]), bf_hi(w[i]), nm);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) n2 = add_bf16x2(n2, gt_bf16x2(w[i], xr));
-    return cm;
-  }
-  __device__ __forceinline__ void ties_before(const Vec8<__nv_bfloat16>& v, float xt, int place) {
-    float x[8];
-    v.get(x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) total += x[e] == xt && e < place;
+    // masks are -1 in a half; their plain sum keeps both counts (see flush)
+    n2 += gt_bf16x2(w[0], xr) + gt_bf16x2(w[1], xr);
+    n2 += gt_bf16x2(w[2], xr) + gt_bf16x2(w[3], xr);
+    return gt_bf16x2(cm2, want2) != 0;
   }
   __device__ __forceinline__ void add_one(float x, bool before) {
-    if (x > limit) {
-      raise(x);
-      set_floor();
-    }
-    largest = fmaxf(largest, x);
+    if (x > limit) raise_to(x);
+    largest2 = max_bf16x2(largest2, (__float_as_uint(x) >> 16) * 0x10001u);
     single(x);
     total += x > (before ? x_lo : x_hi);
   }
-  // the counts are exact up to 256 in a bf16: a chunk adds at most 16 a half
+  // with L masks in the low halves and H in the high ones n2 is 65535 L - 65536 H = 65536 (L - H) - L
   __device__ __forceinline__ void flush() {
-    total += (int)(bf_lo(n2) + bf_hi(n2));
+    const int L = (int)((0u - n2) & 0xFFFFu);
+    const int diff = (int)(n2 + (uint32_t)L) >> 16;
+    total += 2 * L - diff;
     n2 = 0;
   }
-  __device__ __forceinline__ int count() const { return total; }
+  __device__ __forceinline__ float top() const { return fmaxf(bf_lo(largest2), bf_hi(largest2)); }
+  __device__ __forceinline__ void finish() { largest = top(); }
 };
 
 // (logit, id) as one number, larger for what comes first in the order (logit
@@ -467,7 +455,7 @@ struct TopSearch {
   }
 };
 
-template <typename T, bool kTop>
+template <typename T, bool kTop, bool kMask>
 __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_args p, WsHeader* hdr, int split) {
   constexpr bool kF32 = std::is_same<T, float>::value;
   constexpr int U = kF32 ? 2 : 4;  // vectors of a thread and chunk
@@ -490,6 +478,12 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
   const float xt = given ? to_f32(row[meta.tok]) : -INFINITY;
   const bool has = given && !(xt == -INFINITY);
   const int tok_vec = has ? (meta.tok < shp.head ? -1 : (meta.tok - shp.head) / 8) : -1;
+  // equal elements in front of the token in its own vector
+  int ties = 0;
+  if (has && tok_vec >= 0 && tok_vec < shp.nv && rank == 0 && tid < 8) {
+    const int v = shp.head + 8 * tok_vec + tid;
+    ties = v < meta.tok && mask_bit(mask, v) && to_f32(row[v]) == xt;
+  }
   Sums<T> sum(c, has ? xt : INFINITY, has ? value_below<T>(xt) : INFINITY);
 
   TopSearch top{reinterpret_cast<TopShared*>(dyn), p.top};
@@ -503,12 +497,8 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
   }
 
   const auto load = [&](Vec8<T>& raw, int j) {
-    if (j < v1) {
-      raw.load(base + 8 * (int64_t)j);
-      if (mask) raw.mask(mask8(mask, shp.head + 8 * j));
-    } else {
-      raw.fill_neg_inf();
-    }
+    raw.load(base + 8 * (int64_t)j);
+    if (kMask) raw.mask(mask8(mask, shp.head + 8 * j));
   };
   const auto offer8 = [&](const Vec8<T>& raw, int j, uint64_t thr) {
     float x[8];
@@ -558,32 +548,36 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
   };
 
   int chunk = 0, since = v0;
-  for (int j0 = v0; j0 < v1; j0 += U * LT, ++chunk) {
+  uint64_t thr = 0;
+  // U vectors of a thread; full: all of them exist
+  const auto step = [&](int j0, auto full) {
+    constexpr bool kFull = decltype(full)::value;
     Vec8<T> raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load(raw[u], j0 + u * LT + tid);
-    uint64_t thr = 0;
-    float thr_x = INFINITY;
-    if (kTop && chunk > 0) {
-      thr = top.s->thr;
-      thr_x = thr ? key_logit(thr) : -INFINITY;
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * LT;
+      if (kFull || j < v1)
+        load(raw[u], j);
+      else
+        raw[u].fill_neg_inf();
     }
-    float best = -INFINITY;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * LT + tid;
-      const float cm = sum.add(raw[u], j < tok_vec);
-      if (j == tok_vec) sum.ties_before(raw[u], xt, meta.tok - shp.head - 8 * j);
-      if (kTop) {
-        best = fmaxf(best, cm);
-        if (cm >= thr_x && cm > -INFINITY) offer8(raw[u], j, thr);
-      }
+      const int j = j0 + u * LT;
+      const bool in = sum.add(raw[u], j < tok_vec);
+      if (kTop && in) offer8(raw[u], j, thr);
     }
     sum.flush();
+  };
+  for (int j0 = v0; j0 < v1; j0 += U * LT, ++chunk) {
+    if (j0 + U * LT <= v1)
+      step(j0 + tid, std::true_type{});
+    else
+      step(j0 + tid, std::false_type{});
     if (kTop) {
       if (chunk == 0) {
         // a first threshold: LW j-th largest thread maxima are at least K elements
-        float jth = -INFINITY;
+        float best = sum.top(), jth = -INFINITY;
         for (int n = (p.top + LW - 1) / LW; n > 0; --n) {
           jth = warp_max(best);
           const unsigned at = __ballot_sync(0xffffffffu, best == jth);
@@ -594,21 +588,25 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
         float lo = sh.jth[0];
 #pragma unroll
         for (int w = 1; w < LW; ++w) lo = fminf(lo, sh.jth[w]);
-        // the key below every key of that logit
-        thr = lo > -INFINITY ? order_key(lo, 0x7FFFFFFF) : 0;
+        // the key below every key of that logit (of the lowest value, where threads met nothing)
+        thr = order_key(lo, 0x7FFFFFFF);
         if (tid == 0) top.s->thr = thr;
         for (int u = 0; u < U; ++u) {
           const int j = j0 + u * LT + tid;
-          Vec8<T> again;
-          load(again, j);
-          const float cm = again.max();
-          if (cm >= lo && cm > -INFINITY) offer8(again, j, thr);
+          if (j < v1) {
+            Vec8<T> again;
+            load(again, j);
+            if (again.max() >= lo) offer8(again, j, thr);
+          }
         }
+        sum.set_want(lo);
       }
       // a tighter threshold each time the elements seen have doubled, where a whole chunk is left for it
       if ((chunk & (chunk + 1)) == 0 && j0 + 2 * U * LT <= v1) {
         absorb(since, min(v1, j0 + U * LT));
         since = j0 + U * LT;
+        thr = top.s->thr;
+        sum.set_want(key_logit(thr));
       }
     }
   }
@@ -625,8 +623,9 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
   }
 
   // warp, CTA, cluster
+  sum.finish();
   Stat st = sum.stat();
-  int ahead = sum.count();
+  int ahead = sum.total + ties;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const Stat b{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.S, o),
@@ -850,11 +849,14 @@ cudaError_t launch_token_logprobs(const dspark_token_logprobs_args& a, uint8_t* 
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
   const int N = a.rows.N, split = row_split(N, a.rows.V);
   const bool bf16 = a.rows.dtype == DSPARK_BF16;
-  if (a.top > 0)
-    return bf16 ? launch_rows(k_logprobs<__nv_bfloat16, true>, a, hdr, N, split, sizeof(TopShared), s)
-                : launch_rows(k_logprobs<float, true>, a, hdr, N, split, sizeof(TopShared), s);
-  return bf16 ? launch_rows(k_logprobs<__nv_bfloat16, false>, a, hdr, N, split, 0, s)
-              : launch_rows(k_logprobs<float, false>, a, hdr, N, split, 0, s);
+  const unsigned smem = a.top > 0 ? sizeof(TopShared) : 0;
+#define DSPARK_LP(T, TOP, MASK) launch_rows(k_logprobs<T, TOP, MASK>, a, hdr, N, split, smem, s)
+#define DSPARK_LP_T(T)                                                                    \
+  (a.top > 0 ? (a.rows.mask ? DSPARK_LP(T, true, true) : DSPARK_LP(T, true, false))      \
+             : (a.rows.mask ? DSPARK_LP(T, false, true) : DSPARK_LP(T, false, false)))
+  return bf16 ? DSPARK_LP_T(__nv_bfloat16) : DSPARK_LP_T(float);
+#undef DSPARK_LP_T
+#undef DSPARK_LP
 }
 
 cudaError_t launch_token_logprobs_grad(const dspark_token_logprobs_grad_args& a, uint8_t* ws, cudaStream_t s) {
