@@ -104,6 +104,13 @@ __device__ __forceinline__ RowShape row_shape(const T* row, int V) {
   return s;
 }
 
+// the largest of a warp's values (NaN is passed over)
+__device__ __forceinline__ float warp_largest(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // bf16 pairs
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -129,6 +136,21 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// the largest value of the type below x (finite or +inf)
+__device__ __forceinline__ uint32_t bits_below(uint32_t b, uint32_t ulp) {
+  return (b & 0x80000000u) ? b + ulp : b == 0 ? 0x80000000u + ulp : b - ulp;
+}
+template <typename T>
+__device__ __forceinline__ float value_below(float x) {
+  return __uint_as_float(bits_below(__float_as_uint(x + 0.f), std::is_same<T, float>::value ? 1u : 0x10000u));
+}
+
+// the lowest value of the type
+template <typename T>
+__device__ __forceinline__ float lowest() {
+  return std::is_same<T, float>::value ? kLowest : __uint_as_float(0xFF7F0000u);
+}
+
 // eight elements as loaded
 template <typename T>
 struct Vec8;
@@ -136,7 +158,6 @@ template <>
 struct Vec8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void fill_neg_inf() { a = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
   // -inf where the bit is clear
   __device__ __forceinline__ void mask(uint32_t bits) {
     const uint32_t r = bits | (bits << 15);  // bit 2 i, and bit 2 i + 1 sixteen places above it
@@ -148,6 +169,18 @@ struct Vec8<__nv_bfloat16> {
       asm("prmt.b32 %0, %1, 0, 0xAA88;" : "=r"(keep) : "r"(r << (7 - 2 * i)));
       *w[i] = (*w[i] & keep) | (0xFF80FF80u & ~keep);
     }
+  }
+  // element e as a bit place of reach(): word e / 2 in bits 0-3, half e % 2 in bit 4
+  static __device__ __forceinline__ int element(int place) { return 2 * (place & 3) + (place >> 4); }
+  __device__ __forceinline__ float at(int place) const {
+    const uint32_t lo = (place & 1) ? a.y : a.x, hi = (place & 1) ? a.w : a.z, w = (place & 2) ? hi : lo;
+    return (place & 16) ? bf_hi(w) : bf_lo(w);
+  }
+  // a bit for each element at or above x, a bf16 value above -inf
+  __device__ __forceinline__ uint32_t reach(float x) const {
+    const uint32_t below2 = (bits_below(__float_as_uint(x + 0.f), 0x10000u) >> 16) * 0x10001u;
+    return (gt_bf16x2(a.x, below2) & 0x00010001u) | (gt_bf16x2(a.y, below2) & 0x00020002u) |
+           (gt_bf16x2(a.z, below2) & 0x00040004u) | (gt_bf16x2(a.w, below2) & 0x00080008u);
   }
   // the largest element (NaN is passed over), of each half and of both
   __device__ __forceinline__ uint32_t max2() const { return max_bf16x2(max_bf16x2(a.x, a.y), max_bf16x2(a.z, a.w)); }
@@ -185,12 +218,22 @@ struct Vec8<float> {
     a = __ldcs(reinterpret_cast<const float4*>(p));
     b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
-  __device__ __forceinline__ void fill_neg_inf() { a = b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
   __device__ __forceinline__ void mask(uint32_t bits) {
     float* x[8] = {&a.x, &a.y, &a.z, &a.w, &b.x, &b.y, &b.z, &b.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (!((bits >> e) & 1u)) *x[e] = -INFINITY;
+  }
+  static __device__ __forceinline__ int element(int place) { return place; }
+  __device__ __forceinline__ float at(int place) const {
+    const float4 q = (place & 4) ? b : a;
+    const float lo = (place & 1) ? q.y : q.x, hi = (place & 1) ? q.w : q.z;
+    return (place & 2) ? hi : lo;
+  }
+  // a bit for each element at or above x
+  __device__ __forceinline__ uint32_t reach(float x) const {
+    return (a.x >= x) | (a.y >= x) << 1 | (a.z >= x) << 2 | (a.w >= x) << 3 | (b.x >= x) << 4 | (b.y >= x) << 5 |
+           (b.z >= x) << 6 | (b.w >= x) << 7;
   }
   __device__ __forceinline__ float max() const {
     return fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
@@ -226,15 +269,6 @@ __device__ __forceinline__ void stat_merge(Stat& a, const Stat& b, float c) {
   a.m = m;
 }
 
-// the largest value of the type below x (finite or +inf)
-__device__ __forceinline__ uint32_t bits_below(uint32_t b, uint32_t ulp) {
-  return (b & 0x80000000u) ? b + ulp : b == 0 ? 0x80000000u + ulp : b - ulp;
-}
-template <typename T>
-__device__ __forceinline__ float value_below(float x) {
-  return __uint_as_float(bits_below(__float_as_uint(x + 0.f), std::is_same<T, float>::value ? 1u : 0x10000u));
-}
-
 // A thread's share of a row: running sums about m, the largest element, and the
 // count of elements above the token.  Sums are pairs of fp32.  They are about
 // an m of the thread's own that rises only when an element passes it by more
@@ -242,7 +276,7 @@ __device__ __forceinline__ float value_below(float x) {
 // element, some lane of a warp does in most steps (145 against 115 us for
 // 2048 x 151936 bf16).
 struct SumsBase {
-  float c, m = kLowest, limit = kLowest, largest = kLowest, gap;
+  float c, m = kLowest, limit = kLowest, largest = -INFINITY, gap;
   uint64_t c2, S2 = 0, A2 = 0;
   __device__ __forceinline__ SumsBase(float c_) : c(c_), gap(32.f / c_), c2(ptx::pack2(c_, c_)) {}
   __device__ __forceinline__ void raise(float cm) {
@@ -269,26 +303,24 @@ struct SumsBase {
   }
   // what the sums are about the largest element
   __device__ __forceinline__ Stat stat() {
-    raise(largest);
+    raise(fmaxf(largest, kLowest));
     const float2 s = ptx::unpack2(S2), a = ptx::unpack2(A2);
     return Stat{m, s.x + s.y, a.x + a.y};
   }
 };
-// add() takes a vector and says whether one of its elements reaches `want`
 template <typename T>
 struct Sums;
 template <>
 struct Sums<float> : SumsBase {
-  float x_hi, x_lo, n = 0.f, want = INFINITY;
+  float x_hi, x_lo, n = 0.f, chunk = -INFINITY;
   int total = 0;
   __device__ __forceinline__ Sums(float c_, float hi, float lo) : SumsBase(c_), x_hi(hi), x_lo(lo) {}
-  __device__ __forceinline__ void set_want(float x) { want = x; }
-  __device__ __forceinline__ bool add(const Vec8<float>& v, bool before) {
+  __device__ __forceinline__ void add(const Vec8<float>& v, bool before) {
     float x[8];
     v.get(x);
     const float cm = v.max();
     if (cm > limit) raise(cm);
-    largest = fmaxf(largest, cm);
+    chunk = fmaxf(chunk, cm);
     const uint64_t nm = ptx::pack2(-m, -m);
     const float xr = before ? x_lo : x_hi;
 #pragma unroll
@@ -297,7 +329,6 @@ struct Sums<float> : SumsBase {
       n += x[e] > xr ? 1.f : 0.f;
       n += x[e + 1] > xr ? 1.f : 0.f;
     }
-    return cm >= want;
   }
   __device__ __forceinline__ void add_one(float x, bool before) {
     if (x > limit) raise(x);
@@ -305,12 +336,15 @@ struct Sums<float> : SumsBase {
     single(x);
     total += x > (before ? x_lo : x_hi);
   }
-  __device__ __forceinline__ void flush() {
+  // ends a chunk; its largest element
+  __device__ __forceinline__ float flush() {
+    const float cm = chunk;
     total += (int)n;
     n = 0.f;
+    largest = fmaxf(largest, cm);
+    chunk = -INFINITY;
+    return cm;
   }
-  __device__ __forceinline__ float top() const { return largest; }
-  __device__ __forceinline__ void finish() {}
 };
 template <>
 struct Sums<__nv_bfloat16> : SumsBase {
@@ -318,10 +352,10 @@ struct Sums<__nv_bfloat16> : SumsBase {
   // below m that its t is at most -200 and its term 0.  There is no such bf16
   // for m < -1e38 (a thread that has met no candidate, or rows of the lowest
   // value): those vectors take the clamp on t.
-  uint32_t floor2 = 0, limit2 = 0xFF80FF80u, largest2 = 0xFF7FFF7Fu, want2 = 0x7F807F80u, hi2, lo2, n2 = 0;
+  uint32_t floor2 = 0, limit2 = 0xFF80FF80u, chunk2 = 0xFF80FF80u, hi2, lo2, n2 = 0;
   float x_hi, x_lo;
   int total = 0;
-  // bf16 at or below a float, in both halves
+  // the bf16 at or below a float, in both halves
   static __device__ __forceinline__ uint32_t down2(float f) {
     const uint32_t b = __float_as_uint(f);
     return (((b & 0x80000000u) ? b + 0xFFFFu : b) >> 16) * 0x10001u;
@@ -330,18 +364,17 @@ struct Sums<__nv_bfloat16> : SumsBase {
     hi2 = down2(hi);
     lo2 = down2(lo);
   }
-  __device__ __forceinline__ void set_want(float x) { want2 = down2(value_below<__nv_bfloat16>(x)); }
   __device__ __forceinline__ void raise_to(float cm) {
     raise(cm);
     limit2 = down2(limit);
     // one more below: strictly below m whatever its size
     floor2 = down2(value_below<__nv_bfloat16>(__uint_as_float(down2(m - 6.25f * gap) << 16)));
   }
-  __device__ __forceinline__ bool add(const Vec8<__nv_bfloat16>& v, bool before) {
+  __device__ __forceinline__ void add(const Vec8<__nv_bfloat16>& v, bool before) {
     const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
     const uint32_t cm2 = v.max2();
     if (gt_bf16x2(cm2, limit2)) raise_to(fmaxf(bf_lo(cm2), bf_hi(cm2)));
-    largest2 = max_bf16x2(largest2, cm2);
+    chunk2 = max_bf16x2(chunk2, cm2);
     const uint64_t nm = ptx::pack2(-m, -m);
     const uint32_t xr = before ? lo2 : hi2;
     if (m > -1e38f) {
@@ -361,23 +394,24 @@ struct Sums<__nv_bfloat16> : SumsBase {
     // masks are -1 in a half; their plain sum keeps both counts (see flush)
     n2 += gt_bf16x2(w[0], xr) + gt_bf16x2(w[1], xr);
     n2 += gt_bf16x2(w[2], xr) + gt_bf16x2(w[3], xr);
-    return gt_bf16x2(cm2, want2) != 0;
   }
   __device__ __forceinline__ void add_one(float x, bool before) {
     if (x > limit) raise_to(x);
-    largest2 = max_bf16x2(largest2, (__float_as_uint(x) >> 16) * 0x10001u);
+    largest = fmaxf(largest, x);
     single(x);
     total += x > (before ? x_lo : x_hi);
   }
   // with L masks in the low halves and H in the high ones n2 is 65535 L - 65536 H = 65536 (L - H) - L
-  __device__ __forceinline__ void flush() {
+  __device__ __forceinline__ float flush() {
     const int L = (int)((0u - n2) & 0xFFFFu);
     const int diff = (int)(n2 + (uint32_t)L) >> 16;
     total += 2 * L - diff;
     n2 = 0;
+    const float cm = fmaxf(bf_lo(chunk2), bf_hi(chunk2));
+    largest = fmaxf(largest, cm);
+    chunk2 = 0xFF80FF80u;
+    return cm;
   }
-  __device__ __forceinline__ float top() const { return fmaxf(bf_lo(largest2), bf_hi(largest2)); }
-  __device__ __forceinline__ void finish() { largest = top(); }
 };
 
 // (logit, id) as one number, larger for what comes first in the order (logit
@@ -398,50 +432,51 @@ constexpr int kCap = 2048;  // candidate buffer: one vector a thread always fits
 struct LpShared {
   Stat st[LW];
   int cnt[LW];
-  float jth[LW];
   // the CTA's results, read by rank 0 of the cluster
   Stat part;
   int part_cnt;
 };
+// The first K candidates of a CTA's part of the row, with next to no work in
+// the pass over it: every thread writes down the largest element of each group
+// of its vectors.  K elements reach the smallest of the warps' (K / 8)-th largest
+// threads, so only groups that reach it hold candidates; they (some 2 K of up
+// to 4096) are read again.  (Offering elements to a running threshold in the
+// pass itself cost 49 us more than no alternatives at 2048 x 151936 bf16,
+// against XX here.)
+constexpr int kGroups = 16;  // of a thread
 struct TopShared {
-  uint64_t list[32];   // the best so far, descending, 0 past the last
-  uint64_t buf[kCap];  // candidates since
-  uint64_t thr;        // keys up to this one are out
+  uint64_t list[32];   // descending, 0 past the last
+  uint64_t buf[kCap];  // candidates not yet in the list
+  uint64_t thr;        // the cluster's lower bound
   int n;               // candidates met (those past kCap were dropped)
+  int picked;
+  float jth[LW];
+  float group[kGroups][LT];    // largest element
+  uint16_t pick[kGroups * LT]; // groups to read again
 };
-
-// The top-K search of a CTA.  Keys above the threshold go to the buffer; from
-// time to time the buffer is taken into the list, whose K-th key is the next
-// threshold.
 struct TopSearch {
   TopShared* s;
-  int k;
-  __device__ __forceinline__ void offer(float x, int v, uint64_t thr) const {
-    const uint64_t key = order_key(x, v);
-    if (x > -INFINITY && key > thr) {
-      const int at = atomicAdd(&s->n, 1);
-      if (at < kCap) s->buf[at] = key;
-    }
+  // a key that belongs to the buffer
+  __device__ __forceinline__ void offer(uint64_t key) const {
+    const int at = atomicAdd(&s->n, 1);
+    if (at < kCap) s->buf[at] = key;
   }
-  // the list from list and n keys of the buffer: a key's place is the number of
-  // larger ones (keys differ).  All threads, after a barrier; ends with one.
-  __device__ __forceinline__ void take(int n) const {
+  // the list from `listed` keys of the list and n of the buffer: a key's place
+  // is the number of larger ones (keys differ).  All threads, after a barrier;
+  // ends with one.
+  __device__ __forceinline__ void take(int listed, int n) const {
     constexpr int kMine = (kCap + 32 + LT - 1) / LT;
-    const int m = n + 32;
     uint64_t key[kMine];
     int place[kMine];
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
       const int at = threadIdx.x + q * LT;
-      key[q] = at < 32 ? s->list[at] : at < m ? s->buf[at - 32] : 0;
+      key[q] = at < listed ? s->list[at] : at < listed + n ? s->buf[at - listed] : 0;
       place[q] = 0;
-      if (q * LT < m) {
-        if (key[q]) {
+      if (key[q]) {
+        for (int o = 0; o < listed; ++o) place[q] += s->list[o] > key[q];
 #pragma unroll 8
-          for (int o = 0; o < 32; ++o) place[q] += s->list[o] > key[q];
-#pragma unroll 8
-          for (int o = 0; o < n; ++o) place[q] += s->buf[o] > key[q];
-        }
+        for (int o = 0; o < n; ++o) place[q] += s->buf[o] > key[q];
       }
     }
     __syncthreads();
@@ -450,28 +485,42 @@ struct TopSearch {
       if (key[q] && place[q] < 32) s->list[place[q]] = key[q];
     if (threadIdx.x == 0) s->n = 0;
     __syncthreads();
-    if (threadIdx.x == 0) s->thr = max(s->thr, s->list[k - 1]);
-    __syncthreads();
   }
 };
 
-template <typename T, bool kTop, bool kMask>
+template <typename T, bool kMask>
 __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_args p, WsHeader* hdr, int split) {
-  constexpr bool kF32 = std::is_same<T, float>::value;
-  constexpr int U = kF32 ? 2 : 4;  // vectors of a thread and chunk
+  constexpr int U = std::is_same<T, float>::value ? 2 : 4;  // vectors of a thread and chunk
   const dspark_logit_rows& r = p.rows;
   const int i = blockIdx.x / split, rank = blockIdx.x % split;
   if (r.n_rows && i >= *r.n_rows) return;  // the whole cluster
   __shared__ LpShared sh;
-  extern __shared__ __align__(16) uint8_t dyn[];
+  extern __shared__ __align__(16) uint8_t dyn[];  // a TopShared where alternatives are asked for
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const RowMeta meta = row_meta(r, i, hdr, tid == 0 && rank == 0);
   const T* row = static_cast<const T*>(r.logits) + (int64_t)i * r.ld;
-  const uint32_t* mask = r.mask ? r.mask + (int64_t)i * r.mask_ld : nullptr;
-  const float c = log2_scale(meta.T);
+  const uint32_t* mask = kMask ? r.mask + (int64_t)i * r.mask_ld : nullptr;
   const RowShape shp = row_shape(row, r.V);
   const int v0 = (int)((int64_t)shp.nv * rank / split), v1 = (int)((int64_t)shp.nv * (rank + 1) / split);
   const T* base = row + shp.head;
+  const auto load = [&](Vec8<T>& raw, int j) {
+    raw.load(base + 8 * (int64_t)j);
+    if (kMask) raw.mask(mask8(mask, shp.head + 8 * j));
+  };
+  // U vectors of every thread; the first ones are under way while the row's token and temperature are read
+  Vec8<T> raw[U];
+  const auto load_chunk = [&](int j0) {
+    if (j0 + U * LT <= v1) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load(raw[u], j0 + u * LT + tid);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j0 + u * LT + tid < v1) load(raw[u], j0 + u * LT + tid);
+    }
+  };
+  load_chunk(v0);
+  const RowMeta meta = row_meta(r, i, hdr, tid == 0 && rank == 0);
+  const float c = log2_scale(meta.T);
 
   // rank: x > x_hi counts from the token's vector on, x > x_lo (x >= x_token) before it
   const bool given = meta.tok >= 0 && mask_bit(mask, meta.tok);
@@ -486,145 +535,56 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
   }
   Sums<T> sum(c, has ? xt : INFINITY, has ? value_below<T>(xt) : INFINITY);
 
-  TopSearch top{reinterpret_cast<TopShared*>(dyn), p.top};
-  if (kTop) {
-    if (tid < 32) top.s->list[tid] = 0;
-    if (tid == 0) {
-      top.s->thr = 0;
-      top.s->n = 0;
-    }
-    __syncthreads();
-  }
-
-  const auto load = [&](Vec8<T>& raw, int j) {
-    raw.load(base + 8 * (int64_t)j);
-    if (kMask) raw.mask(mask8(mask, shp.head + 8 * j));
-  };
-  const auto offer8 = [&](const Vec8<T>& raw, int j, uint64_t thr) {
-    float x[8];
-    raw.get(x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top.offer(x[e], shp.head + 8 * j + e, thr);
-  };
-  // the buffer into the list; where more came than it holds, vectors from .. to again
-  // with a threshold raised after each vector of a thread
-  const auto absorb = [&](int from, int to) {
-    __syncthreads();
-    const int n = top.s->n;
-    if (n <= kCap) {
-      if (n > 0)
-        top.take(n);
-      else
-        __syncthreads();
-      return;
-    }
-    top.take(kCap);
-    for (int j0 = from; j0 < to; j0 += LT) {
-      const int j = j0 + tid;
-      const uint64_t thr = top.s->thr;
-      if (j < to) {
-        Vec8<T> raw;
-        load(raw, j);
-        if (raw.max() >= key_logit(thr)) {
-          // what the list already holds is not offered again
-          float x[8];
-          raw.get(x);
-          for (int e = 0; e < 8; ++e) {
-            const int v = shp.head + 8 * j + e;
-            const uint64_t key = order_key(x[e], v);
-            bool in = key > thr;
-            for (int o = 0; in && o < 32; ++o) in = top.s->list[o] != key;
-            if (in) top.offer(x[e], v, thr);
-          }
-        }
-      }
-      __syncthreads();
-      const int more = top.s->n;
-      if (more > 0)
-        top.take(more);
-      else
-        __syncthreads();
-    }
-  };
-
-  int chunk = 0, since = v0;
-  uint64_t thr = 0;
-  // U vectors of a thread; full: all of them exist
-  const auto step = [&](int j0, auto full) {
-    constexpr bool kFull = decltype(full)::value;
-    Vec8<T> raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * LT;
-      if (kFull || j < v1)
-        load(raw[u], j);
-      else
-        raw[u].fill_neg_inf();
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * LT;
-      const bool in = sum.add(raw[u], j < tok_vec);
-      if (kTop && in) offer8(raw[u], j, thr);
-    }
-    sum.flush();
-  };
+  const TopSearch top{reinterpret_cast<TopShared*>(dyn)};
+  // a group: 2^gshift chunks of a thread
+  int gshift = 0;
+  while ((v1 - v0 + ((U * LT) << gshift) - 1) / ((U * LT) << gshift) > kGroups) ++gshift;
+  float gmax = -INFINITY;
+  int chunk = 0;
   for (int j0 = v0; j0 < v1; j0 += U * LT, ++chunk) {
-    if (j0 + U * LT <= v1)
-      step(j0 + tid, std::true_type{});
-    else
-      step(j0 + tid, std::false_type{});
-    if (kTop) {
-      if (chunk == 0) {
-        // a first threshold: LW j-th largest thread maxima are at least K elements
-        float best = sum.top(), jth = -INFINITY;
-        for (int n = (p.top + LW - 1) / LW; n > 0; --n) {
-          jth = warp_max(best);
-          const unsigned at = __ballot_sync(0xffffffffu, best == jth);
-          if (lane == __ffs(at) - 1) best = -INFINITY;
-        }
-        if (lane == 0) sh.jth[warp] = jth;
-        __syncthreads();
-        float lo = sh.jth[0];
+    const int j = j0 + tid;
+    if (j0 > v0) load_chunk(j0);
+    if (j0 + U * LT <= v1) {
 #pragma unroll
-        for (int w = 1; w < LW; ++w) lo = fminf(lo, sh.jth[w]);
-        // the key below every key of that logit (of the lowest value, where threads met nothing)
-        thr = order_key(lo, 0x7FFFFFFF);
-        if (tid == 0) top.s->thr = thr;
-        for (int u = 0; u < U; ++u) {
-          const int j = j0 + u * LT + tid;
-          if (j < v1) {
-            Vec8<T> again;
-            load(again, j);
-            if (again.max() >= lo) offer8(again, j, thr);
-          }
-        }
-        sum.set_want(lo);
-      }
-      // a tighter threshold each time the elements seen have doubled, where a whole chunk is left for it
-      if ((chunk & (chunk + 1)) == 0 && j0 + 2 * U * LT <= v1) {
-        absorb(since, min(v1, j0 + U * LT));
-        since = j0 + U * LT;
-        thr = top.s->thr;
-        sum.set_want(key_logit(thr));
+      for (int u = 0; u < U; ++u) sum.add(raw[u], j + u * LT < tok_vec);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j + u * LT < v1) sum.add(raw[u], j + u * LT < tok_vec);
+    }
+    const float cm = sum.flush();
+    if (p.top > 0) {
+      gmax = fmaxf(gmax, cm);
+      if (((chunk + 1) & ((1 << gshift) - 1)) == 0 || j0 + U * LT >= v1) {
+        top.s->group[chunk >> gshift][tid] = gmax;
+        gmax = -INFINITY;
       }
     }
   }
-  if (kTop && since < v1) absorb(since, v1);
+  const int groups = (chunk + (1 << gshift) - 1) >> gshift;
   // the elements outside the vectors, one a thread
-  if (rank == 0 && shp.n_edge() > 0) {
-    if (tid < shp.n_edge()) {
-      const int v = shp.edge(tid);
-      const float x = mask_bit(mask, v) ? to_f32(row[v]) : -INFINITY;
-      sum.add_one(x, v < meta.tok);
-      if (kTop) top.offer(x, v, top.s->thr);
-    }
-    if (kTop) absorb(0, 0);
+  const bool edge = rank == 0 && tid < shp.n_edge();
+  const int edge_v = edge ? shp.edge(tid) : 0;
+  float edge_x = -INFINITY;
+  if (edge) {
+    if (mask_bit(mask, edge_v)) edge_x = to_f32(row[edge_v]);
+    sum.add_one(edge_x, edge_v < meta.tok);
   }
 
-  // warp, CTA, cluster
-  sum.finish();
+  // warp, CTA
   Stat st = sum.stat();
+  float mine = sum.largest;
+  if (p.top > 0) {
+    float best = mine, jth = -INFINITY;
+    for (int n = (p.top + LW - 1) / LW; n > 0; --n) {
+      jth = warp_largest(best);
+      const unsigned at = __ballot_sync(0xffffffffu, best == jth);
+      if (lane == __ffs(at) - 1) best = -INFINITY;
+    }
+    if (lane == 0) top.s->jth[warp] = jth;
+    if (tid < 32) top.s->list[tid] = 0;
+    if (tid == 0) top.s->n = top.s->picked = 0;
+  }
   int ahead = sum.total + ties;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -645,10 +605,67 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
     stat_merge(st, sh.st[w], c);
     ahead += sh.cnt[w];
   }
+
+  if (p.top > 0) {
+    float kth = top.s->jth[0];
+#pragma unroll
+    for (int w = 1; w < LW; ++w) kth = fminf(kth, top.s->jth[w]);
+    kth = fmaxf(kth, lowest<T>());
+    if (mine >= kth) {
+      for (int g = 0; g < groups; ++g)
+        if (top.s->group[g][tid] >= kth) top.s->pick[atomicAdd(&top.s->picked, 1)] = (uint16_t)(g * LT + tid);
+      if (edge_x >= kth) top.offer(order_key(edge_x, edge_v));
+    }
+    __syncthreads();
+    const int each = U << gshift, items = top.s->picked * each;  // vectors of a group, of all
+    for (int it = tid; it < items; it += LT) {
+      const int g = top.s->pick[it / each];
+      const int j = v0 + ((g / LT) * each + it % each) * LT + g % LT;
+      if (j < v1) {
+        Vec8<T> again;
+        load(again, j);
+        for (uint32_t bits = again.reach(kth); bits; bits &= bits - 1) {
+          const int at = __ffs(bits) - 1;
+          top.offer(order_key(again.at(at), shp.head + 8 * j + Vec8<T>::element(at)));
+        }
+      }
+    }
+    __syncthreads();
+    const int n = top.s->n;
+    if (n <= kCap) {
+      top.take(0, n);
+    } else {
+      // more ties with the bound than the buffer holds: the row in steps of a
+      // vector a thread, each against the list so far
+      __syncthreads();
+      if (tid == 0) top.s->n = 0;
+      __syncthreads();
+      if (edge && edge_x >= kth) top.offer(order_key(edge_x, edge_v));
+      __syncthreads();
+      top.take(0, top.s->n);
+      for (int j0 = v0; j0 < v1; j0 += LT) {
+        const int j = j0 + tid;
+        const uint64_t last = top.s->list[p.top - 1];
+        if (j < v1) {
+          Vec8<T> again;
+          load(again, j);
+          for (uint32_t bits = again.reach(kth); bits; bits &= bits - 1) {
+            const int at = __ffs(bits) - 1;
+            const uint64_t key = order_key(again.at(at), shp.head + 8 * j + Vec8<T>::element(at));
+            if (key > last) top.offer(key);
+          }
+        }
+        __syncthreads();
+        top.take(32, top.s->n);
+      }
+    }
+  }
+
   if (split > 1) {
     if (tid == 0) {
       sh.part = st;
       sh.part_cnt = ahead;
+      if (p.top > 0) top.s->thr = top.s->list[p.top - 1];
     }
     __syncwarp();
     ptx::cluster_sync();
@@ -661,25 +678,23 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
           stat_merge(st, b, c);
           ahead += __float_as_int(ptx::ld_cluster_f32(ptx::map_to_rank(&sh.part_cnt, q)));
         }
-      if (kTop) {
+      if (p.top > 0) {
         // the other CTAs' lists are candidates; no key below some CTA's K-th can matter
-        if (tid > 0 && tid < split)
-          atomicMax(reinterpret_cast<unsigned long long*>(&top.s->thr),
-                    (unsigned long long)ptx::ld_cluster_u64(ptx::map_to_rank(&top.s->list[p.top - 1], tid)));
         uint64_t key[kMaxSplit * 32 / LT];
 #pragma unroll
         for (int q = 0; q < kMaxSplit * 32 / LT; ++q) {
           const int o = tid + q * LT;
           key[q] = o >= 32 && o < 32 * split ? ptx::ld_cluster_u64(ptx::map_to_rank(&top.s->list[o & 31], o >> 5)) : 0;
+          if ((o & 31) == p.top - 1)
+            atomicMax(reinterpret_cast<unsigned long long*>(&top.s->thr), (unsigned long long)key[q]);
         }
         __syncthreads();
         const uint64_t thr = top.s->thr;
 #pragma unroll
         for (int q = 0; q < kMaxSplit * 32 / LT; ++q)
-          if (key[q] && key[q] >= thr) top.s->buf[atomicAdd(&top.s->n, 1)] = key[q];
+          if (key[q] && key[q] >= thr) top.offer(key[q]);
         __syncthreads();
-        const int n = top.s->n;
-        if (n > 0) top.take(n);
+        top.take(32, top.s->n);
       }
       __syncwarp();
     }
@@ -698,7 +713,7 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
         p.row_stat[2 * (int64_t)i + 1] = st.S;
       }
     }
-    if (kTop && lane < p.top) {
+    if (lane < p.top) {
       const uint64_t key = top.s->list[lane];
       const bool found = key != 0 && !bad;
       p.top_id[(int64_t)i * p.top + lane] = found ? key_id(key) : -1;
@@ -798,10 +813,12 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs_grad(const dspark_token_logp
   }
 }
 
-// CTAs a row is split over
+// CTAs a row is split over: as many as leave every CTA a place at once (four an
+// SM).  A cluster of 16 pays only for very few rows: 32 x 151936 bf16 8.8 us
+// against 7.7 with 8; 100 rows 12.8 us with 4 against 16.6 with 2 and 17.0 with 8.
 int row_split(int64_t N, int64_t V) {
   int split = 1;
-  while (split < kMaxSplit && N * split * 2 <= 608 && V >= 4096 * split) split *= 2;
+  while (split < kMaxSplit && N * split * 2 <= (split == 8 ? 256 : 608) && V >= 4096 * split) split *= 2;
   return split;
 }
 
@@ -850,13 +867,11 @@ cudaError_t launch_token_logprobs(const dspark_token_logprobs_args& a, uint8_t* 
   const int N = a.rows.N, split = row_split(N, a.rows.V);
   const bool bf16 = a.rows.dtype == DSPARK_BF16;
   const unsigned smem = a.top > 0 ? sizeof(TopShared) : 0;
-#define DSPARK_LP(T, TOP, MASK) launch_rows(k_logprobs<T, TOP, MASK>, a, hdr, N, split, smem, s)
-#define DSPARK_LP_T(T)                                                                    \
-  (a.top > 0 ? (a.rows.mask ? DSPARK_LP(T, true, true) : DSPARK_LP(T, true, false))      \
-             : (a.rows.mask ? DSPARK_LP(T, false, true) : DSPARK_LP(T, false, false)))
-  return bf16 ? DSPARK_LP_T(__nv_bfloat16) : DSPARK_LP_T(float);
-#undef DSPARK_LP_T
-#undef DSPARK_LP
+  if (a.rows.mask)
+    return bf16 ? launch_rows(k_logprobs<__nv_bfloat16, true>, a, hdr, N, split, smem, s)
+                : launch_rows(k_logprobs<float, true>, a, hdr, N, split, smem, s);
+  return bf16 ? launch_rows(k_logprobs<__nv_bfloat16, false>, a, hdr, N, split, smem, s)
+              : launch_rows(k_logprobs<float, false>, a, hdr, N, split, smem, s);
 }
 
 cudaError_t launch_token_logprobs_grad(const dspark_token_logprobs_grad_args& a, uint8_t* ws, cudaStream_t s) {
