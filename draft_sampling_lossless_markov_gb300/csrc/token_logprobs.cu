@@ -158,6 +158,8 @@ template <>
 struct Vec8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load_shared(const uint8_t* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void fill_neg_inf() { a = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
   // -inf where the bit is clear
   __device__ __forceinline__ void mask(uint32_t bits) {
     const uint32_t r = bits | (bits << 15);  // bit 2 i, and bit 2 i + 1 sixteen places above it
@@ -218,6 +220,11 @@ struct Vec8<float> {
     a = __ldcs(reinterpret_cast<const float4*>(p));
     b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
+  __device__ __forceinline__ void load_shared(const uint8_t* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 16);
+  }
+  __device__ __forceinline__ void fill_neg_inf() { a = b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
   __device__ __forceinline__ void mask(uint32_t bits) {
     float* x[8] = {&a.x, &a.y, &a.z, &a.w, &b.x, &b.y, &b.z, &b.w};
 #pragma unroll
@@ -269,148 +276,159 @@ __device__ __forceinline__ void stat_merge(Stat& a, const Stat& b, float c) {
   a.m = m;
 }
 
-// A thread's share of a row: running sums about m, the largest element, and the
-// count of elements above the token.  Sums are pairs of fp32.  They are about
-// an m of the thread's own that rises only when an element passes it by more
-// than 32 in t (the sums stay below 2^64 then): rising with every new largest
-// element, some lane of a warp does in most steps (145 against 115 us for
-// 2048 x 151936 bf16).
+// A thread's share of a row: sums of 2^t and t 2^t with t = x c - r about a
+// reference r of its own, the largest element, and the count of elements above
+// the token.  Sums are pairs of fp32.
+//
+// r is the rounded product of an element and c, so t needs one FMA and r's
+// rounding cancels where the sums are moved to the largest element (stat).  r
+// rises only when an element passes it by more than 32 (the sums stay below
+// 2^64): rising with every new largest element, some lane of a warp does in
+// most steps.  A product above 1e7, whose rounding could move t by more than 1,
+// makes the thread `wild`: its sums are void and formed again from (x - largest) c.
 struct SumsBase {
-  float c, m = kLowest, limit = kLowest, largest = -INFINITY, gap;
+  float c, gap, r = 0.f, limit = -INFINITY, largest = -INFINITY;
   uint64_t c2, S2 = 0, A2 = 0;
+  int total = 0;
+  bool wild = false;
   __device__ __forceinline__ SumsBase(float c_) : c(c_), gap(32.f / c_), c2(ptx::pack2(c_, c_)) {}
-  __device__ __forceinline__ void raise(float cm) {
-    const float d = shifted(m, cm, c), f = ptx::ex2(d);
+  __device__ __forceinline__ void move(float d) {  // the reference by -d
+    const float f = ptx::ex2(d);
     const uint64_t d2 = ptx::pack2(d, d), f2 = ptx::pack2(f, f);
     A2 = ptx::mul2(f2, ptx::fma2(d2, S2, A2));
     S2 = ptx::mul2(f2, S2);
-    m = cm;
-    limit = m + gap;
   }
-  // two elements; the clamp on t
-  __device__ __forceinline__ void pair(float a, float b, uint64_t nm) {
-    const float2 t = ptx::unpack2(ptx::mul2(ptx::add2(ptx::pack2(a, b), nm), c2));
-    const float t0 = ptx::max_nan(t.x, -200.f), t1 = ptx::max_nan(t.y, -200.f);
-    const uint64_t e2 = ptx::pack2(ptx::ex2(t0), ptx::ex2(t1));
-    S2 = ptx::add2(S2, e2);
-    A2 = ptx::fma2(e2, ptx::pack2(t0, t1), A2);
+  __device__ __forceinline__ void raise(float x) {
+    const float to = x * c;
+    move(fminf(fmaxf(r - to, -200.f), 0.f));  // (above 0 only the first time, with nothing to move)
+    r = to;
+    limit = x + gap;
+    wild |= fabsf(to) > 1e7f || fabsf(x) > 1e38f;
   }
-  // one element
   __device__ __forceinline__ void single(float x) {
-    const float t = shifted(x, m, c), e = ptx::ex2(t);
+    const float t = ptx::max_nan(fmaf(x, c, -r), -200.f), e = ptx::ex2(t);
+    S2 = ptx::add2(S2, ptx::pack2(e, 0.f));
+    A2 = ptx::add2(A2, ptx::pack2(e * t, 0.f));
+    largest = fmaxf(largest, x);
+  }
+  // one element of a wild thread
+  __device__ __forceinline__ void again(float x) {
+    const float t = shifted(x, largest, c), e = ptx::ex2(t);
     S2 = ptx::add2(S2, ptx::pack2(e, 0.f));
     A2 = ptx::add2(A2, ptx::pack2(e * t, 0.f));
   }
-  // what the sums are about the largest element
+  // the sums about the largest element
   __device__ __forceinline__ Stat stat() {
-    raise(fmaxf(largest, kLowest));
+    if (largest > -INFINITY && !wild) move(fmaf(-c, largest, r));
     const float2 s = ptx::unpack2(S2), a = ptx::unpack2(A2);
-    return Stat{m, s.x + s.y, a.x + a.y};
+    return Stat{fmaxf(largest, kLowest), s.x + s.y, a.x + a.y};
   }
 };
 template <typename T>
 struct Sums;
 template <>
 struct Sums<float> : SumsBase {
-  float x_hi, x_lo, n = 0.f, chunk = -INFINITY;
-  int total = 0;
+  float x_hi, x_lo, n = 0.f;
   __device__ __forceinline__ Sums(float c_, float hi, float lo) : SumsBase(c_), x_hi(hi), x_lo(lo) {}
-  __device__ __forceinline__ void add(const Vec8<float>& v, bool before) {
-    float x[8];
-    v.get(x);
-    const float cm = v.max();
-    if (cm > limit) raise(cm);
-    chunk = fmaxf(chunk, cm);
-    const uint64_t nm = ptx::pack2(-m, -m);
-    const float xr = before ? x_lo : x_hi;
+  // U vectors; before(u): vector u lies in front of the token's.  Returns their largest element
+  template <int U, typename F>
+  __device__ __forceinline__ float add(const Vec8<float> (&v)[U], F before) {
+    float cm = v[0].max();
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      pair(x[e], x[e + 1], nm);
-      n += x[e] > xr ? 1.f : 0.f;
-      n += x[e + 1] > xr ? 1.f : 0.f;
+    for (int u = 1; u < U; ++u) cm = fmaxf(cm, v[u].max());
+    if (cm > limit) raise(cm);
+    const uint64_t nr = ptx::pack2(-r, -r);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[8];
+      v[u].get(x);
+      const float xr = before(u) ? x_lo : x_hi;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 t = ptx::unpack2(ptx::fma2(ptx::pack2(x[e], x[e + 1]), c2, nr));
+        const float t0 = ptx::max_nan(t.x, -200.f), t1 = ptx::max_nan(t.y, -200.f);
+        const uint64_t e2 = ptx::pack2(ptx::ex2(t0), ptx::ex2(t1));
+        S2 = ptx::add2(S2, e2);
+        A2 = ptx::fma2(e2, ptx::pack2(t0, t1), A2);
+        n += x[e] > xr ? 1.f : 0.f;
+        n += x[e + 1] > xr ? 1.f : 0.f;
+      }
     }
+    largest = fmaxf(largest, cm);
+    return cm;
   }
   __device__ __forceinline__ void add_one(float x, bool before) {
     if (x > limit) raise(x);
-    largest = fmaxf(largest, x);
     single(x);
     total += x > (before ? x_lo : x_hi);
   }
-  // ends a chunk; its largest element
-  __device__ __forceinline__ float flush() {
-    const float cm = chunk;
-    total += (int)n;
-    n = 0.f;
-    largest = fmaxf(largest, cm);
-    chunk = -INFINITY;
-    return cm;
-  }
+  __device__ __forceinline__ void flush() { total += (int)n; }  // n: below 2^24
 };
 template <>
 struct Sums<__nv_bfloat16> : SumsBase {
-  // The clamp acts on pairs before they are widened: floor is a bf16 so far
-  // below m that its t is at most -200 and its term 0.  There is no such bf16
-  // for m < -1e38 (a thread that has met no candidate, or rows of the lowest
-  // value): those vectors take the clamp on t.
-  uint32_t floor2 = 0, limit2 = 0xFF80FF80u, chunk2 = 0xFF80FF80u, hi2, lo2, n2 = 0;
+  // The clamp acts on pairs before they are widened: floor is a bf16 whose t is
+  // at most -200, its term 0.
+  uint32_t floor2, limit2 = 0xFF80FF80u, hi2, lo2, n2 = 0;
   float x_hi, x_lo;
-  int total = 0;
   // the bf16 at or below a float, in both halves
   static __device__ __forceinline__ uint32_t down2(float f) {
     const uint32_t b = __float_as_uint(f);
     return (((b & 0x80000000u) ? b + 0xFFFFu : b) >> 16) * 0x10001u;
   }
+  // one below the bf16 at or below f: strictly below it whatever its size
+  static __device__ __forceinline__ uint32_t under2(float f) {
+    return down2(value_below<__nv_bfloat16>(__uint_as_float(down2(f) << 16)));
+  }
   __device__ __forceinline__ Sums(float c_, float hi, float lo) : SumsBase(c_), x_hi(hi), x_lo(lo) {
     hi2 = down2(hi);
     lo2 = down2(lo);
+    floor2 = under2(-6.25f * gap);
   }
-  __device__ __forceinline__ void raise_to(float cm) {
-    raise(cm);
+  __device__ __forceinline__ void raise(float x) {
+    SumsBase::raise(x);
     limit2 = down2(limit);
-    // one more below: strictly below m whatever its size
-    floor2 = down2(value_below<__nv_bfloat16>(__uint_as_float(down2(m - 6.25f * gap) << 16)));
+    floor2 = under2(x - 6.25f * gap);
   }
-  __device__ __forceinline__ void add(const Vec8<__nv_bfloat16>& v, bool before) {
-    const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
-    const uint32_t cm2 = v.max2();
-    if (gt_bf16x2(cm2, limit2)) raise_to(fmaxf(bf_lo(cm2), bf_hi(cm2)));
-    chunk2 = max_bf16x2(chunk2, cm2);
-    const uint64_t nm = ptx::pack2(-m, -m);
-    const uint32_t xr = before ? lo2 : hi2;
-    if (m > -1e38f) {
+  template <int U, typename F>
+  __device__ __forceinline__ float add(const Vec8<__nv_bfloat16> (&v)[U], F before) {
+    uint32_t cm2 = v[0].max2();
+#pragma unroll
+    for (int u = 1; u < U; ++u) cm2 = max_bf16x2(cm2, v[u].max2());
+    const float cm = fmaxf(bf_lo(cm2), bf_hi(cm2));
+    if (cm > limit) raise(cm);
+    const uint64_t nr = ptx::pack2(-r, -r);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t w[4] = {v[u].a.x, v[u].a.y, v[u].a.z, v[u].a.w};
+      const uint32_t xr = before(u) ? lo2 : hi2;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t x = max_nan_bf16x2(w[i], floor2);
-        const uint64_t t2 = ptx::mul2(ptx::add2(ptx::pack2(bf_lo(x), bf_hi(x)), nm), c2);
+        const uint64_t t2 = ptx::fma2(ptx::pack2(bf_lo(x), bf_hi(x)), c2, nr);
         const float2 t = ptx::unpack2(t2);
         const uint64_t e2 = ptx::pack2(ptx::ex2(t.x), ptx::ex2(t.y));
         S2 = ptx::add2(S2, e2);
         A2 = ptx::fma2(e2, t2, A2);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) pair(bf_lo(w[i]), bf_hi(w[i]), nm);
+      // masks are -1 in a half; their plain sum keeps both counts (see flush)
+      n2 += gt_bf16x2(w[0], xr) + gt_bf16x2(w[1], xr);
+      n2 += gt_bf16x2(w[2], xr) + gt_bf16x2(w[3], xr);
     }
-    // masks are -1 in a half; their plain sum keeps both counts (see flush)
-    n2 += gt_bf16x2(w[0], xr) + gt_bf16x2(w[1], xr);
-    n2 += gt_bf16x2(w[2], xr) + gt_bf16x2(w[3], xr);
+    largest = fmaxf(largest, cm);
+    return cm;
   }
   __device__ __forceinline__ void add_one(float x, bool before) {
-    if (x > limit) raise_to(x);
-    largest = fmaxf(largest, x);
+    if (x > limit) raise(x);
     single(x);
     total += x > (before ? x_lo : x_hi);
   }
-  // with L masks in the low halves and H in the high ones n2 is 65535 L - 65536 H = 65536 (L - H) - L
-  __device__ __forceinline__ float flush() {
+  // with L masks in the low halves and H in the high ones (below 2^15 each: a
+  // thread meets at most DSPARK_MAX_VOCAB / (2 LT) + 1 of either) n2 is
+  // 65535 L - 65536 H = 65536 (L - H) - L
+  __device__ __forceinline__ void flush() {
     const int L = (int)((0u - n2) & 0xFFFFu);
     const int diff = (int)(n2 + (uint32_t)L) >> 16;
     total += 2 * L - diff;
-    n2 = 0;
-    const float cm = fmaxf(bf_lo(chunk2), bf_hi(chunk2));
-    largest = fmaxf(largest, cm);
-    chunk2 = 0xFF80FF80u;
-    return cm;
   }
 };
 
@@ -442,24 +460,28 @@ struct LpShared {
 // threads, so only groups that reach it hold candidates; they (some 2 K of up
 // to 4096) are read again.  (Offering elements to a running threshold in the
 // pass itself cost 49 us more than no alternatives at 2048 x 151936 bf16,
-// against XX here.)
+// against 18 here.)
 constexpr int kGroups = 16;  // of a thread
 struct TopShared {
   uint64_t list[32];   // descending, 0 past the last
-  uint64_t buf[kCap];  // candidates not yet in the list
   uint64_t thr;        // the cluster's lower bound
   int n;               // candidates met (those past kCap were dropped)
   int picked;
   float jth[LW];
-  float group[kGroups][LT];    // largest element
-  uint16_t pick[kGroups * LT]; // groups to read again
+  float group[kGroups][LT];  // largest element
+};
+// the place of the ring after the pass
+struct TopBuffer {
+  uint64_t key[kCap];           // candidates not yet in the list
+  uint16_t pick[kGroups * LT];  // groups to read again
 };
 struct TopSearch {
   TopShared* s;
+  TopBuffer* b;
   // a key that belongs to the buffer
   __device__ __forceinline__ void offer(uint64_t key) const {
     const int at = atomicAdd(&s->n, 1);
-    if (at < kCap) s->buf[at] = key;
+    if (at < kCap) b->key[at] = key;
   }
   // the list from `listed` keys of the list and n of the buffer: a key's place
   // is the number of larger ones (keys differ).  All threads, after a barrier;
@@ -471,12 +493,12 @@ struct TopSearch {
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
       const int at = threadIdx.x + q * LT;
-      key[q] = at < listed ? s->list[at] : at < listed + n ? s->buf[at - listed] : 0;
+      key[q] = at < listed ? s->list[at] : at < listed + n ? b->key[at - listed] : 0;
       place[q] = 0;
       if (key[q]) {
         for (int o = 0; o < listed; ++o) place[q] += s->list[o] > key[q];
 #pragma unroll 8
-        for (int o = 0; o < n; ++o) place[q] += s->buf[o] > key[q];
+        for (int o = 0; o < n; ++o) place[q] += b->key[o] > key[q];
       }
     }
     __syncthreads();
@@ -488,14 +510,28 @@ struct TopSearch {
   }
 };
 
+constexpr int kChunkBytes = 16384;  // of the ring; U vectors of a thread
+constexpr int kMaxStages = 3, kTopStages = 2;  // four CTAs an SM either way
+constexpr long long kWaitLimit = 4000000000ll;  // cycles: about two seconds
+template <typename T>
+constexpr int chunk_vectors() {
+  return kChunkBytes / (LT * 8 * (int)sizeof(T));
+}
+static_assert(sizeof(TopBuffer) <= kTopStages * kChunkBytes, "the buffer takes the ring's place");
+
 template <typename T, bool kMask>
 __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_args p, WsHeader* hdr, int split) {
-  constexpr int U = std::is_same<T, float>::value ? 2 : 4;  // vectors of a thread and chunk
+  constexpr int U = chunk_vectors<T>();
+  constexpr int kVec = 8 * sizeof(T);
   const dspark_logit_rows& r = p.rows;
   const int i = blockIdx.x / split, rank = blockIdx.x % split;
   if (r.n_rows && i >= *r.n_rows) return;  // the whole cluster
   __shared__ LpShared sh;
-  extern __shared__ __align__(16) uint8_t dyn[];  // a TopShared where alternatives are asked for
+  // a ring of chunks; with alternatives a TopShared after it and a TopBuffer in its place later
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
+  __shared__ int abort_s, never_s;
+  const int stages = p.top > 0 ? kTopStages : kMaxStages;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* row = static_cast<const T*>(r.logits) + (int64_t)i * r.ld;
   const uint32_t* mask = kMask ? r.mask + (int64_t)i * r.mask_ld : nullptr;
@@ -506,19 +542,26 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
     raw.load(base + 8 * (int64_t)j);
     if (kMask) raw.mask(mask8(mask, shp.head + 8 * j));
   };
-  // U vectors of every thread; the first ones are under way while the row's token and temperature are read
-  Vec8<T> raw[U];
-  const auto load_chunk = [&](int j0) {
-    if (j0 + U * LT <= v1) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) load(raw[u], j0 + u * LT + tid);
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j0 + u * LT + tid < v1) load(raw[u], j0 + u * LT + tid);
-    }
+  // one thread keeps the ring filled by bulk copies; the first chunks are under
+  // way while the row's token and temperature are read
+  const int chunks = (v1 - v0 + U * LT - 1) / (U * LT);
+  const uint64_t policy = ptx::policy_evict_first();
+  const auto fill = [&](int ch) {
+    const int j0 = v0 + ch * U * LT, s = ch % stages;
+    const uint32_t bytes = (uint32_t)min(U * LT, v1 - j0) * kVec;
+    ptx::mbar_expect_tx(&full[s], bytes);
+    ptx::bulk_load(dyn + s * kChunkBytes, base + 8 * (int64_t)j0, bytes, &full[s], policy);
   };
-  load_chunk(v0);
+  if (tid == 0) {
+    for (int q = 0; q < stages; ++q) {
+      ptx::mbar_init(&full[q], 1);
+      ptx::mbar_init(&empty[q], LW);
+    }
+    ptx::fence_mbar_init();
+    abort_s = never_s = 0;
+    for (int ch = 0; ch < min(chunks, stages); ++ch) fill(ch);
+  }
+  __syncthreads();
   const RowMeta meta = row_meta(r, i, hdr, tid == 0 && rank == 0);
   const float c = log2_scale(meta.T);
 
@@ -535,33 +578,73 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
   }
   Sums<T> sum(c, has ? xt : INFINITY, has ? value_below<T>(xt) : INFINITY);
 
-  const TopSearch top{reinterpret_cast<TopShared*>(dyn)};
+  const TopSearch top{reinterpret_cast<TopShared*>(dyn + kTopStages * kChunkBytes), reinterpret_cast<TopBuffer*>(dyn)};
   // a group: 2^gshift chunks of a thread
   int gshift = 0;
-  while ((v1 - v0 + ((U * LT) << gshift) - 1) / ((U * LT) << gshift) > kGroups) ++gshift;
+  while ((chunks + (1 << gshift) - 1) >> gshift > kGroups) ++gshift;
   float gmax = -INFINITY;
-  int chunk = 0;
-  for (int j0 = v0; j0 < v1; j0 += U * LT, ++chunk) {
-    const int j = j0 + tid;
-    if (j0 > v0) load_chunk(j0);
-    if (j0 + U * LT <= v1) {
+  int stage = 0;
+  uint32_t parity = 0;
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    // refill the place of the chunk before this one
+    if (tid == 0 && chunk > 0 && chunk - 1 + stages < chunks) {
+      const int q = stage == 0 ? stages - 1 : stage - 1;
+      if (!ptx::mbar_wait_cycles(&empty[q], stage == 0 ? parity ^ 1 : parity, &abort_s, kWaitLimit)) {
+        if (hdr) report_error(hdr, DSPARK_TIMEOUT, i);
+        abort_s = 1;
+      }
+      fill(chunk - 1 + stages);
+    }
+    __syncwarp();
+    if (!ptx::mbar_wait_cycles(&full[stage], parity, &abort_s, kWaitLimit)) {
+      if (hdr) report_error(hdr, DSPARK_TIMEOUT, i);
+      abort_s = 1;
+    }
+    const int j = v0 + chunk * U * LT + tid;
+    const uint8_t* at = dyn + stage * kChunkBytes + tid * kVec;
+    Vec8<T> raw[U];
+    if (chunk + 1 < chunks || v0 + chunks * U * LT == v1) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) sum.add(raw[u], j + u * LT < tok_vec);
+      for (int u = 0; u < U; ++u) {
+        raw[u].load_shared(at + u * LT * kVec);
+        if (kMask) raw[u].mask(mask8(mask, shp.head + 8 * (j + u * LT)));
+      }
     } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j + u * LT < v1) sum.add(raw[u], j + u * LT < tok_vec);
+      for (int u = 0; u < U; ++u) {
+        if (j + u * LT < v1) {
+          raw[u].load_shared(at + u * LT * kVec);
+          if (kMask) raw[u].mask(mask8(mask, shp.head + 8 * (j + u * LT)));
+        } else {
+          raw[u].fill_neg_inf();
+        }
+      }
     }
-    const float cm = sum.flush();
+    // only the token's own chunk has vectors on both sides
+    const int j0 = v0 + chunk * U * LT;
+    float cm;
+    if (tok_vec < j0 || tok_vec >= j0 + U * LT)
+      cm = sum.add(raw, [&](int) { return tok_vec > j0; });
+    else
+      cm = sum.add(raw, [&](int u) { return j + u * LT < tok_vec; });
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&empty[stage]);
+    if (++stage == stages) stage = 0, parity ^= 1;
     if (p.top > 0) {
       gmax = fmaxf(gmax, cm);
-      if (((chunk + 1) & ((1 << gshift) - 1)) == 0 || j0 + U * LT >= v1) {
+      if (((chunk + 1) & ((1 << gshift) - 1)) == 0 || chunk + 1 == chunks) {
         top.s->group[chunk >> gshift][tid] = gmax;
         gmax = -INFINITY;
       }
     }
   }
-  const int groups = (chunk + (1 << gshift) - 1) >> gshift;
+  // after a failure: no copy may be in flight when the CTA leaves
+  if (tid == 0 && *(volatile int*)&abort_s)
+    for (int ch = max(0, chunks - stages); ch < chunks; ++ch)
+      ptx::mbar_wait_cycles(&full[ch % stages], (ch / stages) & 1, &never_s, kWaitLimit);
+  __syncwarp();
+  const int groups = (chunks + (1 << gshift) - 1) >> gshift;
+  sum.flush();
   // the elements outside the vectors, one a thread
   const bool edge = rank == 0 && tid < shp.n_edge();
   const int edge_v = edge ? shp.edge(tid) : 0;
@@ -572,6 +655,18 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
   }
 
   // warp, CTA
+  if (sum.wild) {
+    sum.S2 = sum.A2 = 0;
+    for (int j = v0 + tid; j < v1; j += LT) {
+      Vec8<T> raw;
+      float x[8];
+      load(raw, j);
+      raw.get(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum.again(x[e]);
+    }
+    if (edge) sum.again(edge_x);
+  }
   Stat st = sum.stat();
   float mine = sum.largest;
   if (p.top > 0) {
@@ -613,13 +708,13 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
     kth = fmaxf(kth, lowest<T>());
     if (mine >= kth) {
       for (int g = 0; g < groups; ++g)
-        if (top.s->group[g][tid] >= kth) top.s->pick[atomicAdd(&top.s->picked, 1)] = (uint16_t)(g * LT + tid);
+        if (top.s->group[g][tid] >= kth) top.b->pick[atomicAdd(&top.s->picked, 1)] = (uint16_t)(g * LT + tid);
       if (edge_x >= kth) top.offer(order_key(edge_x, edge_v));
     }
     __syncthreads();
     const int each = U << gshift, items = top.s->picked * each;  // vectors of a group, of all
     for (int it = tid; it < items; it += LT) {
-      const int g = top.s->pick[it / each];
+      const int g = top.b->pick[it / each];
       const int j = v0 + ((g / LT) * each + it % each) * LT + g % LT;
       if (j < v1) {
         Vec8<T> again;
@@ -850,6 +945,8 @@ cudaError_t launch_rows(K kernel, const A& a, WsHeader* hdr, int N, int split, u
   c.stream = s;
   c.attrs = at;
   c.numAttrs = split > 1 ? 1 : 0;
+  if (smem > 0)
+    if (const cudaError_t e = ensure_smem_limit((const void*)kernel, (int)smem); e != cudaSuccess) return e;
   if (split > 8)
     if (const cudaError_t e = allow_large_cluster((const void*)kernel); e != cudaSuccess) return e;
   const cudaError_t e = cudaLaunchKernelEx(&c, kernel, a, hdr, split);
@@ -866,7 +963,7 @@ cudaError_t launch_token_logprobs(const dspark_token_logprobs_args& a, uint8_t* 
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
   const int N = a.rows.N, split = row_split(N, a.rows.V);
   const bool bf16 = a.rows.dtype == DSPARK_BF16;
-  const unsigned smem = a.top > 0 ? sizeof(TopShared) : 0;
+  const unsigned smem = a.top > 0 ? kTopStages * kChunkBytes + sizeof(TopShared) : kMaxStages * kChunkBytes;
   if (a.rows.mask)
     return bf16 ? launch_rows(k_logprobs<__nv_bfloat16, true>, a, hdr, N, split, smem, s)
                 : launch_rows(k_logprobs<float, true>, a, hdr, N, split, smem, s);
