@@ -240,7 +240,7 @@ def dspark_pack_rows(args: dspark_pack_args, workspace: int, stream: int) -> int
 
 
 def dspark_quant_fp8(args: dspark_quant_fp8_args, stream: int) -> int:
-    return load().dspark_quant_fp8(ctypes.byref(args), c_void_p(stream))
+    return load().dspark_quant_fp8(ctypes.byref(args), stream)
 
 
 def dspark_matmul_fp8_workspace_size(M: int, N: int, K: int) -> tuple[int, int]:
@@ -250,7 +250,7 @@ def dspark_matmul_fp8_workspace_size(M: int, N: int, K: int) -> tuple[int, int]:
 
 
 def dspark_matmul_fp8(args: dspark_matmul_fp8_args, workspace: int, nbytes: int, stream: int) -> int:
-    return load().dspark_matmul_fp8(ctypes.byref(args), c_void_p(workspace), nbytes, c_void_p(stream))
+    return load().dspark_matmul_fp8(ctypes.byref(args), workspace, nbytes, stream)
 
 
 def dspark_token_logprobs_workspace_size(N: int, V: int, top: int) -> tuple[int, int]:
@@ -260,9 +260,8 @@ def dspark_token_logprobs_workspace_size(N: int, V: int, top: int) -> tuple[int,
 
 
 def dspark_token_logprobs(args: dspark_token_logprobs_args, workspace: int, nbytes: int, stream: int) -> int:
-    return load().dspark_token_logprobs(ctypes.byref(args), c_void_p(workspace), nbytes, c_void_p(stream))
+    return load().dspark_token_logprobs(ctypes.byref(args), workspace, nbytes, stream)
 
 
 def dspark_token_logprobs_grad(args: dspark_token_logprobs_grad_args, workspace: int, stream: int) -> int:
-    return load().dspark_token_logprobs_grad(ctypes.byref(args), c_void_p(workspace) if workspace else None,
-                                             c_void_p(stream))
+    return load().dspark_token_logprobs_grad(ctypes.byref(args), workspace, stream)

@@ -45,8 +45,14 @@ def _ptr(t: Optional[torch.Tensor], dtype=None) -> Optional[int]:
     return t.data_ptr()
 
 
+# the address of the current stream without a Stream object around it (3 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -262,20 +268,38 @@ def pack_rows(src, mark_req, mark_pos, n_rows, dst, ws: Optional[Workspace] = No
 # ---------------------------------------------------------------------------
 # The vocabulary projection and the answers around verify
 # ---------------------------------------------------------------------------
-def _rows(t: torch.Tensor, what: str, dtype=None) -> tuple:
+def _rows(t: torch.Tensor, what: str, dtype) -> tuple:
     """(address, row stride in elements) of a 2-D CUDA tensor whose rows are dense."""
     if not t.is_cuda:
         raise ValueError("dspark tensors must live on a CUDA device")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be a 2-D tensor with dense rows")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1]))
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D tensor with dense rows")
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what} must be a 2-D tensor with dense rows")
+    return t.data_ptr(), ld if rows > 1 else max(ld, cols)
 
 
-def _shape(t: Optional[torch.Tensor], shape: tuple, what: str):
-    if t is not None and tuple(t.shape) != shape:
+def _dense(t: Optional[torch.Tensor], shape: tuple, what: str, dtype) -> Optional[int]:
+    """The address of a dense CUDA tensor of this shape and type; None for None."""
+    if t is None:
+        return None
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: dspark tensors must be contiguous and live on a CUDA device")
+    return t.data_ptr()
+
+
+def _io_dtype(t: torch.Tensor, what: str) -> int:
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
+    return dt
 
 
 _FP8 = torch.float8_e4m3fn
@@ -289,9 +313,8 @@ def fp8_codes(rows: int, cols: int, device="cuda") -> torch.Tensor:
 def quant_fp8(x, block_rows: int = 1, out: Optional[tuple] = None, stream=None) -> tuple:
     """dspark_quant_fp8: x [M, K] (bf16 or f32, dense rows) to (codes [M, K] e4m3, scale
     [ceil(M / block_rows), ceil(K / 128)] f32); block_rows 1 for activations, 128 for weights."""
-    px, ldx = _rows(x, "x")
-    if x.dtype not in _DT:
-        raise TypeError(f"x: expected bfloat16 or float32, got {x.dtype}")
+    dt = _io_dtype(x, "x")
+    px, ldx = _rows(x, "x", x.dtype)
     M, K = x.shape
     if block_rows not in (1, 128):
         raise ValueError("block_rows is 1 or 128")
@@ -299,12 +322,10 @@ def quant_fp8(x, block_rows: int = 1, out: Optional[tuple] = None, stream=None) 
     if out is None:
         out = fp8_codes(M, K, x.device), torch.empty(shape, dtype=torch.float32, device=x.device)
     codes, scale = out
-    _shape(codes, (M, K), "codes")
-    _shape(scale, shape, "scale")
-    a = capi.dspark_quant_fp8_args()
-    a.M, a.K, a.dtype, a.block_rows, a.x, a.ldx = M, K, _DT[x.dtype], block_rows, px, ldx
-    a.codes, a.ldq = _rows(codes, "codes", _FP8)
-    a.scale = _ptr(scale, torch.float32)
+    pq, ldq = _rows(codes, "codes", _FP8)
+    if codes.shape != x.shape:
+        raise ValueError(f"codes: expected shape {(M, K)}, got {tuple(codes.shape)}")
+    a = capi.dspark_quant_fp8_args(M, K, dt, block_rows, px, ldx, pq, ldq, _dense(scale, shape, "scale", torch.float32))
     _check("dspark_quant_fp8", capi.dspark_quant_fp8(a, _stream(stream)))
     return out
 
@@ -321,52 +342,47 @@ def matmul_fp8_workspace(M: int, N: int, K: int, device="cuda", stream=None) -> 
 def matmul_fp8(ws: Workspace, a, a_scale, w, w_scale, out=None, out_dtype=torch.bfloat16, n_rows=None, stream=None):
     """dspark_matmul_fp8: out [M, N] = (a a_scale) (w w_scale)^T for e4m3 a [M, K] and w [N, K] with a scale for each
     block of 128 (quant_fp8 with block_rows 1 and 128); n_rows [1] i32 bounds the rows computed."""
-    c = capi.dspark_matmul_fp8_args()
-    c.a, c.lda = _rows(a, "a", _FP8)
-    c.w, c.ldw = _rows(w, "w", _FP8)
     (M, K), N = a.shape, w.shape[0]
-    kb = -(-K // 128)
-    _shape(w, (N, K), "w")
-    _shape(a_scale, (M, kb), "a_scale")
-    _shape(w_scale, (-(-N // 128), kb), "w_scale")
+    pa, lda = _rows(a, "a", _FP8)
+    pw, ldw = _rows(w, "w", _FP8)
+    if w.shape[1] != K:
+        raise ValueError(f"w: expected shape {(N, K)}, got {tuple(w.shape)}")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
-    _shape(out, (M, N), "out")
-    if out.dtype not in _DT:
-        raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
-    c.M, c.N, c.K, c.out_dtype = M, N, K, _DT[out.dtype]
-    c.a_scale, c.w_scale = _ptr(a_scale, torch.float32), _ptr(w_scale, torch.float32)
-    c.out, c.ldo = _rows(out, "out")
-    c.n_rows = _ptr(n_rows, torch.int32)
+    dt = _io_dtype(out, "out")
+    po, ldo = _rows(out, "out", out.dtype)
+    if out.shape != (M, N):
+        raise ValueError(f"out: expected shape {(M, N)}, got {tuple(out.shape)}")
+    kb, f32 = -(-K // 128), torch.float32
+    c = capi.dspark_matmul_fp8_args(M, N, K, dt, pa, lda, _dense(a_scale, (M, kb), "a_scale", f32), pw, ldw,
+                                    _dense(w_scale, (-(-N // 128), kb), "w_scale", f32), po, ldo,
+                                    _dense(n_rows, (1,), "n_rows", torch.int32))
     _check("dspark_matmul_fp8", capi.dspark_matmul_fp8(c, ws.ptr, ws.nbytes, _stream(stream)))
     return out
 
 
-def _logit_rows(r: capi.dspark_logit_rows, logits, tokens, temp, mask, mark_req, mark_pos, n_rows):
+def _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows) -> capi.dspark_logit_rows:
+    dt = _io_dtype(logits, "logits")
+    p, ld = _rows(logits, "logits", logits.dtype)
     N, V = logits.shape
-    if logits.dtype not in _DT:
-        raise TypeError(f"logits: expected bfloat16 or float32, got {logits.dtype}")
-    r.N, r.V, r.dtype = N, V, _DT[logits.dtype]
-    r.logits, r.ld = _rows(logits, "logits")
-    if (mark_req is None) != (mark_pos is None):
-        raise ValueError("mark_req and mark_pos go together")
-    if mark_req is not None:
+    i32, f32 = torch.int32, torch.float32
+    if mark_req is None and mark_pos is None:
+        n_req = cols = 0
+        pt, pT = _dense(tokens, (N,), "tokens", i32), _dense(temp, (N,), "temp", f32)
+    else:
+        if mark_req is None or mark_pos is None:
+            raise ValueError("mark_req and mark_pos go together")
         if tokens.dim() != 2:
             raise ValueError("tokens [n_req, tok_cols] is needed with markers")
-        r.n_req, r.tok_cols = tokens.shape
-        _shape(mark_req, (N,), "mark_req")
-        _shape(mark_pos, (N,), "mark_pos")
-        _shape(temp, (tokens.shape[0],), "temp")
-    else:
-        _shape(tokens, (N,), "tokens")
-        _shape(temp, (N,), "temp")
-    r.tokens, r.temp = _ptr(tokens, torch.int32), _ptr(temp, torch.float32)
-    r.mark_req, r.mark_pos = _ptr(mark_req, torch.int32), _ptr(mark_pos, torch.int32)
+        n_req, cols = tokens.shape
+        pt, pT = _dense(tokens, (n_req, cols), "tokens", i32), _dense(temp, (n_req,), "temp", f32)
+    pm = ldm = 0
     if mask is not None:
+        pm, ldm = _rows(mask, "mask", i32)
         if mask.shape[0] != N or mask.shape[1] < -(-V // 32):
             raise ValueError("mask: expected [N, >= ceil(V / 32)] words")
-        r.mask, r.mask_ld = _rows(mask, "mask", torch.int32)
-    r.n_rows = _ptr(n_rows, torch.int32)
+    return capi.dspark_logit_rows(N, V, dt, cols, n_req, p, ld, pt, pT, pm, ldm, _dense(mark_req, (N,), "mark_req", i32),
+                                  _dense(mark_pos, (N,), "mark_pos", i32), _dense(n_rows, (1,), "n_rows", i32))
 
 
 def token_logprobs_workspace(N: int, V: int, top: int, device="cuda", stream=None) -> Workspace:
@@ -385,23 +401,18 @@ def token_logprobs(ws: Workspace, logits, tokens, temp=None, top: int = 0, mask=
     tokens [n_req, tok_cols] and temp [n_req]; mask [N, >= ceil(V / 32)] i32 holds a bit a place.
     Returns dict(logprob, entropy, rank, row_stat, top_id, top_logprob); an `out` may leave keys out (top_id and
     top_logprob only when top is 0)."""
-    a = capi.dspark_token_logprobs_args()
-    _logit_rows(a.rows, logits, tokens, temp, mask, mark_req, mark_pos, n_rows)
-    N = logits.shape[0]
-    a.top = top
+    rows = _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows)
+    N = rows.N
+    f32, i32 = torch.float32, torch.int32
     if out is None:
-        dev = logits.device
-        f32 = dict(dtype=torch.float32, device=dev)
-        i32 = dict(dtype=torch.int32, device=dev)
-        out = dict(logprob=torch.empty(N, **f32), entropy=torch.empty(N, **f32), rank=torch.empty(N, **i32),
-                   row_stat=torch.empty((N, 2), **f32), top_id=torch.empty((N, top), **i32),
-                   top_logprob=torch.empty((N, top), **f32))
-    for k, dt, shape in (("logprob", torch.float32, (N,)), ("entropy", torch.float32, (N,)),
-                         ("rank", torch.int32, (N,)), ("row_stat", torch.float32, (N, 2)),
-                         ("top_id", torch.int32, (N, top)), ("top_logprob", torch.float32, (N, top))):
-        t = out.get(k)
-        _shape(t, shape, k)
-        setattr(a, k, _ptr(t, dt))
+        new = lambda shape, dt: torch.empty(shape, dtype=dt, device=logits.device)  # noqa: E731
+        out = dict(logprob=new(N, f32), entropy=new(N, f32), rank=new(N, i32), row_stat=new((N, 2), f32),
+                   top_id=new((N, top), i32), top_logprob=new((N, top), f32))
+    get = out.get
+    a = capi.dspark_token_logprobs_args(
+        rows, top, _dense(get("logprob"), (N,), "logprob", f32), _dense(get("entropy"), (N,), "entropy", f32),
+        _dense(get("rank"), (N,), "rank", i32), _dense(get("row_stat"), (N, 2), "row_stat", f32),
+        _dense(get("top_id"), (N, top), "top_id", i32), _dense(get("top_logprob"), (N, top), "top_logprob", f32))
     _check("dspark_token_logprobs", capi.dspark_token_logprobs(a, ws.ptr, ws.nbytes, _stream(stream)))
     return out
 
@@ -411,30 +422,28 @@ def token_logprobs_grad(ws: Optional[Workspace], logits, tokens, row_stat, entro
                         out=None, stream=None):
     """dspark_token_logprobs_grad: the gradient by the logits of sum(g_logprob logprob) + sum(g_entropy entropy) +
     sum(g_top top_logprob), from token_logprobs's row_stat, entropy and top_id.  out may be logits itself."""
-    a = capi.dspark_token_logprobs_grad_args()
-    _logit_rows(a.rows, logits, tokens, temp, mask, mark_req, mark_pos, n_rows)
+    rows = _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows)
     N, V = logits.shape
-    a.top = g_top.shape[1] if g_top is not None else 0
-    _shape(row_stat, (N, 2), "row_stat")
-    _shape(g_logprob, (N,), "g_logprob")
-    _shape(g_entropy, (N,), "g_entropy")
-    if g_entropy is not None:
-        if entropy is None:
-            raise ValueError("g_entropy needs entropy")
-        _shape(entropy, (N,), "entropy")
+    f32 = torch.float32
+    top = 0
     if g_top is not None:
         if top_id is None:
             raise ValueError("g_top needs top_id")
-        _shape(g_top, (N, a.top), "g_top")
-        _shape(top_id, (N, a.top), "top_id")
+        if g_top.dim() != 2:
+            raise ValueError("g_top: expected [N, top]")
+        top = g_top.shape[1]
+    if g_entropy is not None and entropy is None:
+        raise ValueError("g_entropy needs entropy")
     if out is None:
         out = torch.empty((N, V), dtype=logits.dtype, device=logits.device)
-    _shape(out, (N, V), "out")
-    f32 = torch.float32
-    a.row_stat, a.entropy = _ptr(row_stat, f32), _ptr(entropy, f32) if g_entropy is not None else None
-    a.top_id = _ptr(top_id, torch.int32) if a.top else None
-    a.g_logprob, a.g_entropy, a.g_top = _ptr(g_logprob, f32), _ptr(g_entropy, f32), _ptr(g_top, f32) if a.top else None
-    a.grad, a.ldg = _rows(out, "out", logits.dtype)
+    po, ldo = _rows(out, "out", logits.dtype)
+    if out.shape != logits.shape:
+        raise ValueError(f"out: expected shape {(N, V)}, got {tuple(out.shape)}")
+    a = capi.dspark_token_logprobs_grad_args(
+        rows, top, _dense(row_stat, (N, 2), "row_stat", f32),
+        _dense(entropy, (N,), "entropy", f32) if g_entropy is not None else None,
+        _dense(top_id, (N, top), "top_id", torch.int32) if top else None, _dense(g_logprob, (N,), "g_logprob", f32),
+        _dense(g_entropy, (N,), "g_entropy", f32), _dense(g_top, (N, top), "g_top", f32) if top else None, po, ldo)
     _check("dspark_token_logprobs_grad",
            capi.dspark_token_logprobs_grad(a, ws.ptr if ws is not None else 0, _stream(stream)))
     return out
