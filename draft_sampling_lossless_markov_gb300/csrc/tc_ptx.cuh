@@ -274,9 +274,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // every thread of every CTA of the cluster; orders shared-memory accesses across it
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 // the shared::cluster address of `p`'s place in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {

@@ -276,6 +276,18 @@ __device__ __forceinline__ void stat_merge(Stat& a, const Stat& b, float c) {
   a.m = m;
 }
 
+// over each n lanes of a warp (the same in all of them: a + b is b + a here)
+template <int n>
+__device__ __forceinline__ void merge_lanes(Stat& st, int& count, float c) {
+#pragma unroll
+  for (int o = n / 2; o > 0; o >>= 1) {
+    const Stat b{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.S, o),
+                 __shfl_xor_sync(0xffffffffu, st.A, o)};
+    stat_merge(st, b, c);
+    count += __shfl_xor_sync(0xffffffffu, count, o);
+  }
+}
+
 // A thread's share of a row: sums of 2^t and t 2^t with t = x c - r about a
 // reference r of its own, the largest element, and the count of elements above
 // the token.  Sums are pairs of fp32.
@@ -487,24 +499,40 @@ struct TopSearch {
   // is the number of larger ones (keys differ).  All threads, after a barrier;
   // ends with one.
   __device__ __forceinline__ void take(int listed, int n) const {
-    constexpr int kMine = (kCap + 32 + LT - 1) / LT;
-    uint64_t key[kMine];
-    int place[kMine];
+    const int m = listed + n;
+    if (m <= LT) {
+      // 2^sh threads count for one key
+      const int sh = m <= LT / 8 ? 3 : m <= LT / 4 ? 2 : m <= LT / 2 ? 1 : 0;
+      const int at = threadIdx.x >> sh, from = threadIdx.x & ((1 << sh) - 1);
+      const uint64_t key = at < listed ? s->list[at] : at < m ? b->key[at - listed] : 0;
+      int place = 0;
+#pragma unroll 4
+      for (int o = from; o < listed; o += 1 << sh) place += s->list[o] > key;
+#pragma unroll 4
+      for (int o = from; o < n; o += 1 << sh) place += b->key[o] > key;
+      for (int d = 1; d < (1 << sh); d <<= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
+      __syncthreads();
+      if (key && from == 0 && place < 32) s->list[place] = key;
+    } else {
+      constexpr int kMine = (kCap + 32 + LT - 1) / LT;
+      uint64_t key[kMine];
+      int place[kMine];
 #pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-      const int at = threadIdx.x + q * LT;
-      key[q] = at < listed ? s->list[at] : at < listed + n ? b->key[at - listed] : 0;
-      place[q] = 0;
-      if (key[q]) {
-        for (int o = 0; o < listed; ++o) place[q] += s->list[o] > key[q];
-#pragma unroll 8
-        for (int o = 0; o < n; ++o) place[q] += b->key[o] > key[q];
+      for (int q = 0; q < kMine; ++q) {
+        const int at = threadIdx.x + q * LT;
+        key[q] = at < listed ? s->list[at] : at < m ? b->key[at - listed] : 0;
+        place[q] = 0;
+        if (key[q]) {
+          for (int o = 0; o < listed; ++o) place[q] += s->list[o] > key[q];
+#pragma unroll 4
+          for (int o = 0; o < n; ++o) place[q] += b->key[o] > key[q];
+        }
       }
-    }
-    __syncthreads();
+      __syncthreads();
 #pragma unroll
-    for (int q = 0; q < kMine; ++q)
-      if (key[q] && place[q] < 32) s->list[place[q]] = key[q];
+      for (int q = 0; q < kMine; ++q)
+        if (key[q] && place[q] < 32) s->list[place[q]] = key[q];
+    }
     if (threadIdx.x == 0) s->n = 0;
     __syncthreads();
   }
@@ -681,24 +709,16 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
     if (tid == 0) top.s->n = top.s->picked = 0;
   }
   int ahead = sum.total + ties;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Stat b{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.S, o),
-                 __shfl_xor_sync(0xffffffffu, st.A, o)};
-    stat_merge(st, b, c);
-    ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
-  }
+  merge_lanes<32>(st, ahead, c);
   if (lane == 0) {
     sh.st[warp] = st;
     sh.cnt[warp] = ahead;
   }
   __syncthreads();
-  st = sh.st[0];
-  ahead = sh.cnt[0];
-#pragma unroll
-  for (int w = 1; w < LW; ++w) {
-    stat_merge(st, sh.st[w], c);
-    ahead += sh.cnt[w];
+  if (warp == 0) {
+    st = sh.st[lane % LW];
+    ahead = sh.cnt[lane % LW];
+    merge_lanes<LW>(st, ahead, c);
   }
 
   if (p.top > 0) {
@@ -712,10 +732,11 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
       if (edge_x >= kth) top.offer(order_key(edge_x, edge_v));
     }
     __syncthreads();
-    const int each = U << gshift, items = top.s->picked * each;  // vectors of a group, of all
+    // 2^esh vectors a group
+    const int esh = (U == 4 ? 2 : 1) + gshift, items = top.s->picked << esh;
     for (int it = tid; it < items; it += LT) {
-      const int g = top.b->pick[it / each];
-      const int j = v0 + ((g / LT) * each + it % each) * LT + g % LT;
+      const int g = top.b->pick[it >> esh];
+      const int j = v0 + (((g / LT) << esh) + (it & ((1 << esh) - 1))) * LT + g % LT;
       if (j < v1) {
         Vec8<T> again;
         load(again, j);
@@ -765,14 +786,20 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
     __syncwarp();
     ptx::cluster_sync();
     if (rank == 0) {
-      if (warp == 0)
-        for (int q = 1; q < split; ++q) {
-          const Stat b{ptx::ld_cluster_f32(ptx::map_to_rank(&sh.part.m, q)),
-                       ptx::ld_cluster_f32(ptx::map_to_rank(&sh.part.S, q)),
-                       ptx::ld_cluster_f32(ptx::map_to_rank(&sh.part.A, q))};
-          stat_merge(st, b, c);
-          ahead += __float_as_int(ptx::ld_cluster_f32(ptx::map_to_rank(&sh.part_cnt, q)));
+      if (warp == 0) {
+        // a lane each reads a CTA's part (both halves of the warp the same)
+        const int q = lane % kMaxSplit;
+        st = Stat{kLowest, 0.f, 0.f};
+        ahead = 0;
+        if (q < split) {
+          st = Stat{ptx::ld_cluster_f32(ptx::map_to_rank(&sh.part.m, q)),
+                    ptx::ld_cluster_f32(ptx::map_to_rank(&sh.part.S, q)),
+                    ptx::ld_cluster_f32(ptx::map_to_rank(&sh.part.A, q))};
+          ahead = __float_as_int(ptx::ld_cluster_f32(ptx::map_to_rank(&sh.part_cnt, q)));
         }
+        __syncwarp();
+        merge_lanes<kMaxSplit>(st, ahead, c);
+      }
       if (p.top > 0) {
         // the other CTAs' lists are candidates; no key below some CTA's K-th can matter
         uint64_t key[kMaxSplit * 32 / LT];
@@ -793,7 +820,7 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
       }
       __syncwarp();
     }
-    ptx::cluster_sync();
+    ptx::cluster_arrive();  // the others' shared memory has been read
   }
   if (warp == 0 && rank == 0) {
     const bool empty = st.S == 0.f, bad = isnan(st.S);
@@ -815,6 +842,10 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
       p.top_logprob[(int64_t)i * p.top + lane] =
           bad ? NAN : found ? __fdiv_rn(key_logit(key) - st.m, meta.T) - logS : -INFINITY;
     }
+  }
+  if (split > 1) {
+    __syncwarp();
+    ptx::cluster_wait();
   }
 }
 
