@@ -11,13 +11,17 @@
 // Two kernels, chosen by M:
 //   k_fp8_wide    rows of a on the TMEM lanes.  A CTA pair (cta_group::2) makes a
 //                 256 x BN tile: each CTA stages its 128 rows of a and half of the
-//                 BN rows of w.  A lane's scale is one register and a tile column
-//                 block's scale is uniform, so the promotion is one packed FMA for
-//                 two elements.
-//   k_fp8_narrow  rows of w on the lanes, up to 64 rows of a on the columns:
-//                 a weight-bandwidth kernel.  A cluster of S CTAs splits the
-//                 blocks of K and adds its parts through distributed shared memory
-//                 in rank order (no atomics: equal calls give equal bits).
+//                 BN rows of w.  A row's scale is one number a lane, so the
+//                 promotion is one packed FMA for two elements.  2048 x 4096 x 151936
+//                 to bf16: 0.89 ms, 2.87 PFLOP/s at full clocks (1.12 ms where the
+//                 power cap holds them at 1.6 GHz); bounded by the round trip of a
+//                 TMEM buffer (MMA, commit, read-out, release) and then by power.
+//   k_fp8_narrow  rows of w on the lanes, up to 64 rows of a on the columns: bounded
+//                 by reading w (1 row x 2560 x 151936: 62 us, 0.92 of measured HBM;
+//                 64 x 7168 x 129280 to fp32: 151 us, 0.94).  A cluster of S CTAs
+//                 splits the blocks of K and adds its parts through distributed
+//                 shared memory in rank order (no atomics: equal calls give equal
+//                 bits): 8 x 2560 x 2560 6.6 us.
 //
 // Every wait is bounded; one that gives up reports DSPARK_TIMEOUT.
 #include <cuda.h>
@@ -80,6 +84,8 @@ struct Wide {
   static constexpr int BN = 128 * NH;
   static constexpr int kEpiWarps = 8 * NH;
   static constexpr int kThreads = 32 * (kEpiWarps + 2 + NH);
+  // registers of the epilogue warps and of the last warpgroup (NH = 2)
+  static constexpr int kRegsHigh = 104, kRegsLow = 64;
   static constexpr uint32_t kA = 128 * kKb;       // bytes of a per CTA and stage
   static constexpr uint32_t kB = BN / 2 * kKb;    // bytes of w per CTA and stage
   static constexpr uint32_t kStage = kA + kB;
@@ -146,35 +152,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
   const int tiles = mt * ((p.N + BN - 1) / BN);
   const int nblk = (p.N + kKb - 1) / kKb;
 
+  // the epilogue warps' accumulators need more than an even share of the
+  // registers: with 96 each they spill (1.03 against 0.89 ms for 2048 x 4096 x 151936)
+  if (NH == 2) {
+    if (warp >= EW)
+      ptx::reg_dec<W::kRegsLow>();
+    else
+      ptx::reg_inc<W::kRegsHigh>();
+  }
   if (warp == EW) {
-    if (lane == 0) {
-      // loads: this CTA's rows of a and its half of w's rows, signalled to the first CTA
-      const uint64_t pol_a = ptx::policy_evict_last(), pol_w = ptx::policy_evict_normal();
-      const uint32_t bar0 = ptx::map_to_rank(&full[0], 0);
-      uint32_t s = 0, ph = 1, n = 0;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        const int m0 = (t % mt) * 256 + (int)rank * 128, n0 = (t / mt) * BN + (int)rank * (BN / 2);
-        for (int b = 0; b < p.kb; ++b) {
-          if (!ptx::mbar_wait_cycles(&empty[s], ph, abort_flag, kWaitLimit)) {
-            fail(1);
-            ok = false;
-            break;
-          }
+    // loads: this CTA's rows of a and its half of w's rows, signalled to the
+    // first CTA.  The whole warp runs the loop and one elected lane issues, as
+    // for the MMAs: from one thread of a divergent branch the loads alone took
+    // longer than the tensor cores.
+    const uint64_t pol_a = ptx::policy_evict_last(), pol_w = ptx::policy_evict_normal();
+    const uint32_t bar0 = ptx::map_to_rank(&full[0], 0);
+    uint32_t s = 0, ph = 1, n = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int m0 = (t % mt) * 256 + (int)rank * 128, n0 = (t / mt) * BN + (int)rank * (BN / 2);
+      for (int b = 0; b < p.kb; ++b) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(&empty[s], ph, abort_flag, kWaitLimit));
+        if (!ok) {
+          if (lane == 0) fail(1);
+          break;
+        }
+        if (ptx::elect_one()) {
           uint8_t* dst = sm + s * W::kStage;
           if (rank == 0) ptx::mbar_expect_tx(&full[s], 2 * W::kStage);
           ptx::tma_load_2d_pair(dst, &tmA, bar0 + s * 8, b * kKb, m0, pol_a);
           ptx::tma_load_2d_pair(dst + W::kA, &tmW, bar0 + s * 8, b * kKb, n0, pol_w);
-          ++n;
-          if (++s == NS) s = 0, ph ^= 1;
         }
+        __syncwarp();
+        ++n;
+        if (++s == NS) s = 0, ph ^= 1;
       }
-      // nothing of the pair may be in flight when the CTAs leave: the last
-      // commits have arrived here, or (after a failure) at least the loads
-      for (uint32_t j = n > NS ? n - NS : 0; j < n; ++j)
-        if (ok || rank == 0)
-          ptx::mbar_wait_cycles(ok ? &empty[j % NS] : &full[j % NS], (j / NS) & 1, &never_s, kWaitLimit);
     }
+    // nothing of the pair may be in flight when the CTAs leave: the last
+    // commits have arrived here, or (after a failure) at least the loads
+    for (uint32_t j = n > NS ? n - NS : 0; j < n; ++j)
+      if (ok || rank == 0)
+        ptx::mbar_wait_cycles(ok ? &empty[j % NS] : &full[j % NS], (j / NS) & 1, &never_s, kWaitLimit);
     __syncwarp();
   } else if (warp > EW + 1) {
     // one MMA warp per part: its waits (some 80 cycles each even when they
@@ -279,17 +297,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
         if (!got) fail(3);  // the loop runs on: every later wait ends at once
         __syncwarp();
         ptx::tc_fence_after();
+        // 16 columns arrive while the 16 before them are added
+        float v[2][16];
+        ptx::tmem_ld16(taddr + q * 128, v[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float v[16];
-          ptx::tmem_ld16(taddr + q * 128 + c * 16, v);
-          ptx::tmem_ld_wait16(v);
-          if (c == 3) {
+          ptx::tmem_ld_wait16(v[c & 1]);
+          if (c < 3) {
+            ptx::tmem_ld16(taddr + q * 128 + (c + 1) * 16, v[(c + 1) & 1]);
+          } else {
             ptx::tc_fence_before();
             if (lane == 0) ptx::mbar_arrive_remote(te + q * 8);
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[c * 8 + i] = ptx::fma2(ptx::pack2(v[2 * i], v[2 * i + 1]), s2, acc[c * 8 + i]);
+          for (int i = 0; i < 8; ++i)
+            acc[c * 8 + i] = ptx::fma2(ptx::pack2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s2, acc[c * 8 + i]);
         }
         if (++q == NB) q = 0, tph ^= 1;
         if ((b & 3) == 3 || b + 1 == p.kb) {
@@ -366,24 +388,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
 // ---------------------------------------------------------------------------
 // narrow: 128 rows of w on the lanes, NT rows of a on the columns, a cluster over K
 // ---------------------------------------------------------------------------
-constexpr int kNarrowThreads = 192;  // 4 epilogue warps, loads, MMA
-
 template <int NT>
 struct Narrow {
+  static constexpr int kCols32 = NT < 32 ? NT : 32;     // columns of an epilogue warp
+  static constexpr int kEpiWarps = 4 * (NT / kCols32);
+  static constexpr int kThreads = 32 * (kEpiWarps + 2);  // and loads, MMA
   static constexpr uint32_t kW = 128 * kKb;
   static constexpr uint32_t kA = NT * kKb;
   static constexpr uint32_t kStage = kW + kA;
   static constexpr int kBufs = 4;
-  static constexpr uint32_t kCols = NT * kBufs < 32 ? 32 : NT * kBufs;
+  static constexpr uint32_t kTmemCols = NT * kBufs;
   static constexpr uint32_t kRed = NT * 128 * 4;  // a tile's sums, one float each
 };
 
 template <int NT, typename TO>
-__global__ void __launch_bounds__(kNarrowThreads, 1)
+__global__ void __launch_bounds__(Narrow<NT>::kThreads, 1)
     k_fp8_narrow(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, const MmParams p,
                  int split, int stages, int m_tiles) {
   using C = Narrow<NT>;
-  constexpr int NB = C::kBufs;
+  constexpr int NB = C::kBufs, EW = C::kEpiWarps, NC = C::kCols32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   constexpr int kMaxStages = 12;
@@ -402,15 +425,15 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     }
     for (int i = 0; i < NB; ++i) {
       ptx::mbar_init(&tfull[i], 1);
-      ptx::mbar_init(&tempty[i], 4);
+      ptx::mbar_init(&tempty[i], EW);
     }
     ptx::fence_mbar_init();
     abort_s = never_s = 0;
     ptx::prefetch_map(&tmA);
     ptx::prefetch_map(&tmW);
   }
-  if (warp == 5) {
-    ptx::tmem_alloc(&tmem_slot, C::kCols);
+  if (warp == EW + 1) {
+    ptx::tmem_alloc(&tmem_slot, C::kTmemCols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -426,33 +449,34 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   const int64_t tiles = (int64_t)mt * ((p.N + 127) / 128);
   const int b0 = (int)((int64_t)p.kb * rank / split), b1 = (int)((int64_t)p.kb * (rank + 1) / split);
 
-  if (warp == 4) {
-    if (lane == 0) {
-      const uint64_t pol_a = ptx::policy_evict_last(), pol_w = ptx::policy_evict_first();
-      uint32_t s = 0, ph = 0, n = 0;
-      bool ok = true;
-      for (int64_t t = cl; t < tiles && ok; t += cls) {
-        const int m0 = (int)(t % mt) * NT, n0 = (int)(t / mt) * 128;
-        for (int b = b0; b < b1; ++b) {
-          if (!ptx::mbar_wait_cycles(&empty[s], ph ^ 1, abort_flag, kWaitLimit)) {
-            fail(4);
-            ok = false;
-            break;
-          }
+  if (warp == EW) {
+    const uint64_t pol_a = ptx::policy_evict_last(), pol_w = ptx::policy_evict_first();
+    uint32_t s = 0, ph = 1, n = 0;
+    bool ok = true;
+    for (int64_t t = cl; t < tiles && ok; t += cls) {
+      const int m0 = (int)(t % mt) * NT, n0 = (int)(t / mt) * 128;
+      for (int b = b0; b < b1; ++b) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(&empty[s], ph, abort_flag, kWaitLimit));
+        if (!ok) {
+          if (lane == 0) fail(4);
+          break;
+        }
+        if (ptx::elect_one()) {
           uint8_t* dst = sm + s * C::kStage;
           ptx::mbar_expect_tx(&full[s], C::kStage);
           ptx::tma_load_2d(dst, &tmW, &full[s], b * kKb, n0, pol_w);
           ptx::tma_load_2d(dst + C::kW, &tmA, &full[s], b * kKb, m0, pol_a);
-          ++n;
-          if (++s == (uint32_t)stages) s = 0, ph ^= 1;
         }
+        __syncwarp();
+        ++n;
+        if (++s == (uint32_t)stages) s = 0, ph ^= 1;
       }
-      // nothing may be in flight when the CTA leaves
-      for (uint32_t j = n > (uint32_t)stages ? n - stages : 0; j < n; ++j)
-        ptx::mbar_wait_cycles(&full[j % stages], (j / stages) & 1, &never_s, kWaitLimit);
     }
+    // nothing may be in flight when the CTA leaves
+    for (uint32_t j = n > (uint32_t)stages ? n - stages : 0; j < n; ++j)
+      ptx::mbar_wait_cycles(&full[j % stages], (j / stages) & 1, &never_s, kWaitLimit);
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == EW + 1) {
     constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, NT);
     const uint64_t dw0 = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
     uint32_t s = 0, ph = 0, q = 0, tph = 1;
@@ -482,68 +506,68 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       }
     }
   }
-  uint32_t it = 0;
+  uint32_t q = 0, tph = 0;
   bool ok = true;
+  const int quarter = warp & 3, c0 = (warp >> 2) * NC;  // lanes and columns of an epilogue warp
   for (int64_t t = cl; t < tiles; t += cls) {
     const int m0 = (int)(t % mt) * NT, n0 = (int)(t / mt) * 128;
     const int nm = min(NT, M - m0);
-    if (warp < 4) {
+    if (warp < EW) {
       const float* wsc = p.w_scale + (int64_t)(n0 / kKb) * p.kb;
-      float acc[NT];
+      // lane l holds the scale of column c0 + l, the next block's on its way
+      const bool mine = lane < NC && c0 + lane < nm;
+      const float* asc = p.a_scale + (int64_t)(m0 + (mine ? c0 + lane : 0)) * p.kb;
+      float acc[NC];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i] = 0.f;
-      for (int b = b0; b < b1 && ok; ++b, ++it) {
-        const uint32_t a = it % NB;
-        const float ws = wsc[b];
-        // lane l holds the scales of columns l and l + 32
-        float sc[(NT + 31) / 32];
-#pragma unroll
-        for (int j = 0; j < (NT + 31) / 32; ++j) {
-          const int c = j * 32 + lane;
-          sc[j] = c < nm ? ws * p.a_scale[(int64_t)(m0 + c) * p.kb + b] : 0.f;
+      for (int i = 0; i < NC; ++i) acc[i] = 0.f;
+      float sa = mine && b0 < b1 ? asc[b0] : 0.f, sw = b0 < b1 ? wsc[b0] : 0.f;
+      for (int b = b0; b < b1 && ok; ++b) {
+        const float sc = sa * sw;
+        if (b + 1 < b1) {
+          sa = mine ? asc[b + 1] : 0.f;
+          sw = wsc[b + 1];
         }
-        const bool got = ptx::mbar_wait_cycles(&tfull[a], (it / NB) & 1, abort_flag, kWaitLimit);
+        const bool got = ptx::mbar_wait_cycles(&tfull[q], tph, abort_flag, kWaitLimit);
         if (!__all_sync(0xffffffffu, got)) {
           if (lane == 0) fail(6);
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t ta = tmem + ((uint32_t)(warp * 32) << 16) + a * NT;
+        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + q * NT + c0;
 #pragma unroll
-        for (int c = 0; c < NT / 16; ++c) {
+        for (int c = 0; c < NC / 16; ++c) {
           float v[16];
           ptx::tmem_ld16(ta + c * 16, v);
           ptx::tmem_ld_wait16(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int col = c * 16 + i;
-            acc[col] = fmaf(v[i], __shfl_sync(0xffffffffu, sc[col / 32], col & 31), acc[col]);
-          }
+          for (int i = 0; i < 16; ++i)
+            acc[c * 16 + i] = fmaf(v[i], __shfl_sync(0xffffffffu, sc, c * 16 + i), acc[c * 16 + i]);
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&tempty[a]);
+        if (lane == 0) ptx::mbar_arrive(&tempty[q]);
+        if (++q == NB) q = 0, tph ^= 1;
       }
       if (split == 1) {
-        const int n = n0 + warp * 32 + lane;
+        const int n = n0 + quarter * 32 + lane;
         if (ok && n < p.N) {
-          TO* o = static_cast<TO*>(p.out) + (int64_t)m0 * p.ldo + n;
+          TO* o = static_cast<TO*>(p.out) + (int64_t)(m0 + c0) * p.ldo + n;
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            if (i < nm) store_out(o + (int64_t)i * p.ldo, acc[i]);
+          for (int i = 0; i < NC; ++i)
+            if (c0 + i < nm) store_out(o + (int64_t)i * p.ldo, acc[i]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (i < nm) red[i * 128 + warp * 32 + lane] = acc[i];
+        for (int i = 0; i < NC; ++i)
+          if (c0 + i < nm) red[(c0 + i) * 128 + quarter * 32 + lane] = acc[i];
       }
     }
     if (split > 1) {
       // every CTA adds the parts of its share of the tile's rows in rank order
       __syncwarp();
       ptx::cluster_sync();
-      for (int u = threadIdx.x; u < nm * 32; u += kNarrowThreads) {
+      for (int u = threadIdx.x; u < nm * 32; u += C::kThreads) {
         if ((u / 32) % split != rank) continue;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int r = 0; r < split; ++r) {
@@ -566,9 +590,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == EW + 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, C::kCols);
+    ptx::tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
@@ -607,6 +631,20 @@ cudaError_t count_pairs(int sms, int* n) {
   return e;
 }
 
+// The wide kernel's warps trade registers among themselves: what the epilogue
+// warps ask for has to be there, or they would wait for ever.
+cudaError_t check_registers() {
+  using W = Wide<2>;
+  const void* kernels[] = {(const void*)k_fp8_wide<2, __nv_bfloat16>, (const void*)k_fp8_wide<2, float>};
+  for (const void* f : kernels) {
+    cudaFuncAttributes at;
+    if (const cudaError_t e = cudaFuncGetAttributes(&at, f); e != cudaSuccess) return e;
+    const int rest = W::kThreads / 32 - W::kEpiWarps;
+    if (at.numRegs * W::kThreads < 32 * (W::kEpiWarps * W::kRegsHigh + rest * W::kRegsLow)) return cudaErrorNotSupported;
+  }
+  return cudaSuccess;
+}
+
 // properties of the current device, looked up once each
 cudaError_t device(Dev* out) {
   constexpr int kMaxDev = 64;
@@ -627,6 +665,7 @@ cudaError_t device(Dev* out) {
     d.sm103 = major == 10 && minor == 3;
     if (d.sm103) {
       if ((e = count_pairs(d.sms, &d.pairs)) != cudaSuccess) return e;
+      if ((e = check_registers()) != cudaSuccess) return e;
     }
     cache[dev] = d;
     have[dev] = true;
@@ -668,14 +707,14 @@ cudaError_t run_narrow(const dspark_matmul_fp8_args& a, const MmParams& p, const
   int split = 1;
   while (split < 8 && tiles * split * 2 <= d.sms && p.kb >= split * 4) split *= 2;
   // a deep ring where one CTA has an SM to itself for many blocks
-  const int stages = split > 1 ? 4 : NT <= 16 ? 11 : NT <= 32 ? 9 : 8;
+  const int stages = split > 1 ? 4 : NT <= 16 ? 11 : NT <= 32 ? 9 : NT <= 64 ? 8 : 6;
   const uint32_t smem = stages * C::kStage + (split > 1 ? C::kRed : 0) + 1024;
   const void* f = (const void*)k_fp8_narrow<NT, TO>;
   if (const cudaError_t e = ensure_smem_limit(f, (int)smem); e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   cudaLaunchAttribute at[1];
   cluster_config(&c, at, (unsigned)split, (unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, d.sms)),
-                 kNarrowThreads, smem, s);
+                 C::kThreads, smem, s);
   const cudaError_t e = cudaLaunchKernelEx(&c, k_fp8_narrow<NT, TO>, tmA, tmW, p, split, stages, mt);
   if (e != cudaSuccess) return e;
   count_launches(1);

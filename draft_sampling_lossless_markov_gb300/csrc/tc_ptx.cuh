@@ -267,6 +267,16 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          | ((uint32_t)(M >> 4) << 24);              // M / 16
 }
 
+// ---- registers of a warpgroup (all its warps make the call) ----
+template <int n>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
+}
+template <int n>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
+}
+
 // ---- clusters and CTA pairs ----
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
