@@ -313,7 +313,9 @@ dspark_status dspark_quant_fp8(const dspark_quant_fp8_args* a, void* stream) {
   if (!a->x || !a->codes || !a->scale || !rows_ok(a->M, a->K, a->ldx) || !rows_ok(a->M, a->K, a->ldq))
     return DSPARK_INVALID_ARG;
   if (!aligned_to(a->x, elem_size(a->dtype)) || !aligned_to(a->scale, 4)) return DSPARK_INVALID_ARG;
-  return cuda_status(launch_quant_fp8(*a, (cudaStream_t)stream));
+  const cudaError_t e = launch_quant_fp8(*a, (cudaStream_t)stream);
+  if (e == cudaErrorNotSupported) return DSPARK_UNSUPPORTED;
+  return cuda_status(e);
 }
 
 dspark_status dspark_matmul_fp8_workspace_size(int32_t M, int32_t N, int32_t K, size_t* bytes) {

@@ -695,6 +695,16 @@ cudaError_t run_wide(const dspark_matmul_fp8_args& a, const MmParams& p, const D
   return cudaGetLastError();
 }
 
+// CTAs of a cluster over K: up to one CTA an SM (a little more where two fit
+// one: 20 tiles of 2560 x 2560 take 5.7 us in clusters of 8 and 5.9 in clusters of 4,
+// 32 tiles of 1024 x 4096 4.6 us with 4 and 5.4 with 8), each with a block at least
+int narrow_split(int64_t tiles, int kb, int nt, int sms) {
+  const int most = nt <= 32 ? sms + sms / 16 : sms;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= most && kb >= split * 2) split *= 2;
+  return split;
+}
+
 template <int NT, typename TO>
 cudaError_t run_narrow(const dspark_matmul_fp8_args& a, const MmParams& p, const Dev& d, cudaStream_t s) {
   using C = Narrow<NT>;
@@ -704,8 +714,7 @@ cudaError_t run_narrow(const dspark_matmul_fp8_args& a, const MmParams& p, const
     return cudaErrorInvalidValue;
   const int mt = (a.M + NT - 1) / NT;
   const int64_t tiles = (int64_t)mt * (((int64_t)a.N + 127) / 128);
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= d.sms && p.kb >= split * 4) split *= 2;
+  const int split = narrow_split(tiles, p.kb, NT, d.sms);
   // a deep ring where one CTA has an SM to itself for many blocks
   const int stages = split > 1 ? 4 : NT <= 16 ? 11 : NT <= 32 ? 9 : NT <= 64 ? 8 : 6;
   const uint32_t smem = stages * C::kStage + (split > 1 ? C::kRed : 0) + 1024;
@@ -726,10 +735,15 @@ cudaError_t run(const dspark_matmul_fp8_args& a, const MmParams& p, const Dev& d
   if (a.M <= 16) return run_narrow<16, TO>(a, p, d, s);
   if (a.M <= 32) return run_narrow<32, TO>(a, p, d, s);
   if (a.M <= 64) return run_narrow<64, TO>(a, p, d, s);
+  // few tiles and a long K: four CTAs or more a tile (128 x 4096 x 1024: 8.5 against
+  // 11.2 us, 128 x 7168 x 2048: 11.5 against 17.1; not 128 x 2560 x 2560, 10.4
+  // against 8.6, whose tiles leave room for two)
+  if (a.M <= 256 && p.kb >= 16 && ((a.M + 63) / 64) * (((int64_t)a.N + 127) / 128) * 4 <= d.sms)
+    return run_narrow<64, TO>(a, p, d, s);
   // waves of pairs times a tile's columns; a column of a 128-column tile costs
-  // 1.25 of a 256-column tile's (2048 x 4096 x 151936: 1.10 against 0.88 ms), which
-  // pays where the wider tiles leave pairs idle (512 x 4096 x 4096: 13.7 against
-  // 19.8 us)
+  // 1.25 of a 256-column tile's (2048 x 4096 x 151936: 1.06 against 0.89 ms), which
+  // pays where the wider tiles leave pairs idle (512 x 4096 x 4096: 14.3 against
+  // 24.8 us)
   const int64_t mt = ((int64_t)a.M + 255) / 256;
   const auto cost = [&](int bn) { return (double)((mt * ((a.N + bn - 1) / bn) + d.pairs - 1) / d.pairs * bn); };
   return 1.25 * cost(128) < cost(256) ? run_wide<1, TO>(a, p, d, s) : run_wide<2, TO>(a, p, d, s);

@@ -540,3 +540,61 @@ def test_grad_strided_misaligned_and_row_count(dt):
         _check_grad(out, np64(z), tok, temp, fwd, g, None, slice(0, n))
         assert bool((store[:, :c0 // 2] == -7).all()) and bool((store[:, c0 // 2 + V:] == -7).all())
         assert bool((store[n:] == -7).all())
+
+
+# --------------------------------------------------------------------------- cases of single paths
+def test_quant_of_fp32_rounds_the_exact_quotient():
+    # products that fp32 puts on the wrong side of the middle between two codes: x one
+    # float from middle * amax / 448, both sides of every middle, blocks of two amax
+    mids = (O.e4m3_values()[:126] + O.e4m3_values()[1:127]) / 2
+    for amax in (3.0, 0.1, 7.7e-20, 5.3e30):
+        base = (mids * (amax / 448)).astype(np.float32)
+        rows = [base, np.nextafter(base, np.float32(0)), np.nextafter(base, np.float32(np.inf)), -base]
+        x = np.concatenate([np.stack(rows), np.full((4, 2), amax, np.float32)], 1)
+        assert x.shape[1] == 128
+        t = torch.from_numpy(x).cuda()
+        for block_rows in (1, 128):
+            codes, _ = T.quant_fp8(t, block_rows)
+            a = np.abs(x.astype(np.float64)).max()
+            want = O.e4m3_round(x.astype(np.float64) * 448.0 / a)
+            frac = x.astype(np.float64) * 448.0 / a
+            tie = np.isin(np.abs(frac), mids)  # fp64 itself cannot tell: either neighbour
+            got = O.e4m3_decode(codes_np(codes))
+            np.testing.assert_array_equal(got[~tie], want[~tie])
+
+
+def test_quant_many_rows_and_non_finite_in_some():
+    # enough blocks for the wide form of the row kernel; non-finite elements in a few of them
+    x = torch.randn(20000, 1700, device="cuda")
+    at = torch.randint(0, x.numel(), (500,), device="cuda")
+    x.view(-1)[at] = float("nan")
+    x.view(-1)[at[:200]] = float("inf")
+    for dt in (BF16, F32):
+        y = x.to(dt)
+        codes, scale = T.quant_fp8(y, 1)
+        rows = torch.unique(at // 1700)[:60]
+        _check_quant(y[rows], 1, codes[rows], scale[rows])
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_logprobs_more_ties_than_the_candidate_buffer(dt):
+    # rows where thousands of places tie with the K-th: the lowest ids win
+    V = 30000
+    z = torch.zeros(4, V, device="cuda", dtype=dt)
+    z[1, ::2] = 1.0
+    z[2, 5000:] = 2.0
+    z[2, 29000] = 3.0
+    z[3] = torch.arange(V, device="cuda").to(dt) // 4096
+    tok, temp = np.array([17, 29998, 29000, 0]), np.ones(4, np.float32)
+    for top in (1, 20, 32):
+        _check_logprobs(_run(z, tok, temp, top), np64(z), tok, temp, top)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 900, 7168), (200, 640, 4096), (64, 384, 8192), (33, 2560, 2560)])
+def test_matmul_split_over_k(M, N, K):
+    a, sa, w, sw = _random_operands(M, N, K, M)
+    ws = T.matmul_fp8_workspace(M, N, K)
+    for dt in (BF16, F32):
+        out = T.matmul_fp8(ws, a, sa, w, sw, out_dtype=dt)
+        check_no_error(ws)
+        _check_matmul(out, a, sa, w, sw)
