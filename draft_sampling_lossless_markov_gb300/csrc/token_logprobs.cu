@@ -31,8 +31,7 @@ namespace dspark {
 
 namespace {
 
-constexpr int LT = 256;  // threads
-constexpr int LW = LT / 32;
+constexpr int GT = 256;  // threads of the gradient kernel
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMaxTemp = 1e35f;
 constexpr int kMaxSplit = 16;
@@ -308,11 +307,10 @@ __device__ __forceinline__ float key_logit(uint64_t k) {
 }
 __device__ __forceinline__ int key_id(uint64_t k) { return 0x7FFFFFFF - (int)(uint32_t)k; }
 
-constexpr int kCap = 2048;  // candidate buffer: one vector a thread always fits
-
+template <int LT>
 struct LpShared {
-  Stat st[LW];
-  int cnt[LW];
+  Stat st[LT / 32];
+  int cnt[LT / 32];
   // the CTA's results, read by rank 0 of the cluster
   Stat part;
   int part_cnt;
@@ -325,22 +323,27 @@ struct LpShared {
 // pass itself cost 49 us more than no alternatives at 2048 x 151936 bf16,
 // against 18 here.)
 constexpr int kGroups = 16;  // of a thread
+template <int LT>
 struct TopShared {
   uint64_t list[32];   // descending, 0 past the last
   uint64_t thr;        // the cluster's lower bound
   int n;               // candidates met (those past kCap were dropped)
   int picked;
-  float jth[LW];
+  float jth[LT / 32];
   float group[kGroups][LT];  // largest element
 };
 // the place of the ring after the pass
+template <int LT>
 struct TopBuffer {
+  static constexpr int kCap = LT * 8;  // one vector a thread always fits
   uint64_t key[kCap];           // candidates not yet in the list
   uint16_t pick[kGroups * LT];  // groups to read again
 };
+template <int LT>
 struct TopSearch {
-  TopShared* s;
-  TopBuffer* b;
+  static constexpr int kCap = TopBuffer<LT>::kCap;
+  TopShared<LT>* s;
+  TopBuffer<LT>* b;
   // a key that belongs to the buffer
   __device__ __forceinline__ void offer(uint64_t key) const {
     const int at = atomicAdd(&s->n, 1);
@@ -349,7 +352,7 @@ struct TopSearch {
   // the list from `listed` keys of the list and n of the buffer: a key's place
   // is the number of larger ones (keys differ).  All threads, after a barrier;
   // ends with one.
-  __device__ __forceinline__ void take(int listed, int n) const {
+  __device__ __noinline__ void take(int listed, int n) const {
     const int m = listed + n;
     if (m <= LT) {
       // 2^sh threads count for one key
@@ -389,23 +392,29 @@ struct TopSearch {
   }
 };
 
-constexpr int kChunkBytes = 16384;  // of the ring; U vectors of a thread
-constexpr int kMaxStages = 3, kTopStages = 2;  // four CTAs an SM either way
+// A CTA's ring: chunks of U vectors of a thread (16 KB with 256 threads, 8 KB with 128)
+constexpr int kMaxStages = 3, kTopStages = 2;  // 1024 threads an SM either way
+template <int LT>
+constexpr int kChunkBytes = 64 * LT;
 constexpr long long kWaitLimit = 4000000000ll;  // cycles: about two seconds
 template <typename T>
 constexpr int chunk_vectors() {
-  return kChunkBytes / (LT * 8 * (int)sizeof(T));
+  return 64 / (8 * (int)sizeof(T));
 }
-static_assert(sizeof(TopBuffer) <= kTopStages * kChunkBytes, "the buffer takes the ring's place");
+static_assert(sizeof(TopBuffer<128>) <= kTopStages * kChunkBytes<128> &&
+                  sizeof(TopBuffer<256>) <= kTopStages * kChunkBytes<256>,
+              "the buffer takes the ring's place");
 
-template <typename T, bool kMask>
-__global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_args p, WsHeader* hdr, int split) {
-  constexpr int U = chunk_vectors<T>();
+template <typename T, bool kMask, int LT>
+__global__ void __launch_bounds__(LT, 1024 / LT)
+    k_logprobs(const dspark_token_logprobs_args p, WsHeader* hdr, int split) {
+  constexpr int U = chunk_vectors<T>(), LW = LT / 32, CB = kChunkBytes<LT>;
+  constexpr int kKeys = (kMaxSplit * 32 + LT - 1) / LT;
   constexpr int kVec = 8 * sizeof(T);
   const dspark_logit_rows& r = p.rows;
   const int i = blockIdx.x / split, rank = blockIdx.x % split;
   if (r.n_rows && i >= *r.n_rows) return;  // the whole cluster
-  __shared__ LpShared sh;
+  __shared__ LpShared<LT> sh;
   // a ring of chunks; with alternatives a TopShared after it and a TopBuffer in its place later
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
@@ -429,7 +438,7 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
     const int j0 = v0 + ch * U * LT, s = ch % stages;
     const uint32_t bytes = (uint32_t)min(U * LT, v1 - j0) * kVec;
     ptx::mbar_expect_tx(&full[s], bytes);
-    ptx::bulk_load(dyn + s * kChunkBytes, base + 8 * (int64_t)j0, bytes, &full[s], policy);
+    ptx::bulk_load(dyn + s * CB, base + 8 * (int64_t)j0, bytes, &full[s], policy);
   };
   if (tid == 0) {
     for (int q = 0; q < stages; ++q) {
@@ -457,7 +466,8 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
   }
   Sums<T> sum(c, has ? xt : INFINITY, has ? value_below<T>(xt) : INFINITY);
 
-  const TopSearch top{reinterpret_cast<TopShared*>(dyn + kTopStages * kChunkBytes), reinterpret_cast<TopBuffer*>(dyn)};
+  constexpr int kCap = TopBuffer<LT>::kCap;
+  const TopSearch<LT> top{reinterpret_cast<TopShared<LT>*>(dyn + kTopStages * CB), reinterpret_cast<TopBuffer<LT>*>(dyn)};
   // a group: 2^gshift chunks of a thread
   int gshift = 0;
   while ((chunks + (1 << gshift) - 1) >> gshift > kGroups) ++gshift;
@@ -480,32 +490,34 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
       abort_s = 1;
     }
     const int j = v0 + chunk * U * LT + tid;
-    const uint8_t* at = dyn + stage * kChunkBytes + tid * kVec;
-    Vec8<T> raw[U];
-    if (chunk + 1 < chunks || v0 + chunks * U * LT == v1) {
+    const uint8_t* at = dyn + stage * CB + tid * kVec;
+    const int j0 = v0 + chunk * U * LT;
+    float cm = -INFINITY;
+    if (j0 + U * LT <= v1) {
+      Vec8<T> raw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         raw[u].load_shared(at + u * LT * kVec);
         if (kMask) raw[u].mask(mask8(mask, shp.head + 8 * (j + u * LT)));
       }
+      // only the token's own chunk has vectors on both sides
+      if (tok_vec < j0 || tok_vec >= j0 + U * LT)
+        cm = sum.add(raw, [&](int) { return tok_vec > j0; });
+      else
+        cm = sum.add(raw, [&](int u) { return j + u * LT < tok_vec; });
     } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
+#pragma unroll 1
+      for (int u = 0; j0 + u * LT < v1; ++u) {
+        Vec8<T> raw[1];
         if (j + u * LT < v1) {
-          raw[u].load_shared(at + u * LT * kVec);
-          if (kMask) raw[u].mask(mask8(mask, shp.head + 8 * (j + u * LT)));
+          raw[0].load_shared(at + u * LT * kVec);
+          if (kMask) raw[0].mask(mask8(mask, shp.head + 8 * (j + u * LT)));
         } else {
-          raw[u].fill_neg_inf();
+          raw[0].fill_neg_inf();
         }
+        cm = fmaxf(cm, sum.add(raw, [&](int) { return j + u * LT < tok_vec; }));
       }
     }
-    // only the token's own chunk has vectors on both sides
-    const int j0 = v0 + chunk * U * LT;
-    float cm;
-    if (tok_vec < j0 || tok_vec >= j0 + U * LT)
-      cm = sum.add(raw, [&](int) { return tok_vec > j0; });
-    else
-      cm = sum.add(raw, [&](int u) { return j + u * LT < tok_vec; });
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&empty[stage]);
     if (++stage == stages) stage = 0, parity ^= 1;
@@ -653,9 +665,9 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
       }
       if (p.top > 0) {
         // the other CTAs' lists are candidates; no key below some CTA's K-th can matter
-        uint64_t key[kMaxSplit * 32 / LT];
+        uint64_t key[kKeys];
 #pragma unroll
-        for (int q = 0; q < kMaxSplit * 32 / LT; ++q) {
+        for (int q = 0; q < kKeys; ++q) {
           const int o = tid + q * LT;
           key[q] = o >= 32 && o < 32 * split ? ptx::ld_cluster_u64(ptx::map_to_rank(&top.s->list[o & 31], o >> 5)) : 0;
           if ((o & 31) == p.top - 1)
@@ -664,14 +676,14 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
         __syncthreads();
         const uint64_t thr = top.s->thr;
 #pragma unroll
-        for (int q = 0; q < kMaxSplit * 32 / LT; ++q)
+        for (int q = 0; q < kKeys; ++q)
           if (key[q] && key[q] >= thr) top.offer(key[q]);
         __syncthreads();
         top.take(32, top.s->n);
       }
       __syncwarp();
     }
-    ptx::cluster_arrive();  // the others' shared memory has been read
+    ptx::cluster_arrive_relaxed();  // the others' shared memory has been read
   }
   if (warp == 0 && rank == 0) {
     const bool empty = st.S == 0.f, bad = isnan(st.S);
@@ -704,7 +716,7 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs(const dspark_token_logprobs_
 // gradient
 // ---------------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(LT, 4) k_logprobs_grad(const dspark_token_logprobs_grad_args p, WsHeader* hdr,
+__global__ void __launch_bounds__(GT, 4) k_logprobs_grad(const dspark_token_logprobs_grad_args p, WsHeader* hdr,
                                                          int split) {
   constexpr int U = std::is_same<T, float>::value ? 2 : 4;
   const dspark_logit_rows& r = p.rows;
@@ -749,16 +761,16 @@ __global__ void __launch_bounds__(LT, 4) k_logprobs_grad(const dspark_token_logp
   const T* base = row + shp.head;
   T* obase = out + shp.head;
   const bool vec = ((uintptr_t)obase & 15u) == 0;
-  for (int j0 = v0; j0 < v1; j0 += U * LT) {
+  for (int j0 = v0; j0 < v1; j0 += U * GT) {
     Vec8<T> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * LT + tid;
+      const int j = j0 + u * GT + tid;
       if (j < v1) raw[u].load(base + 8 * (int64_t)j);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * LT + tid;
+      const int j = j0 + u * GT + tid;
       if (j >= v1) continue;
       float x[8];
       if (mask) raw[u].mask(mask8(mask, shp.head + 8 * j));
@@ -815,14 +827,15 @@ cudaError_t allow_large_cluster(const void* kernel) {
 }
 
 template <typename K, typename A>
-cudaError_t launch_rows(K kernel, const A& a, WsHeader* hdr, int N, int split, unsigned smem, cudaStream_t s) {
+cudaError_t launch_rows(K kernel, const A& a, WsHeader* hdr, int N, int split, int threads, unsigned smem,
+                        cudaStream_t s) {
   cudaLaunchConfig_t c = {};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)split;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   c.gridDim = dim3((unsigned)N * (unsigned)split);
-  c.blockDim = dim3(LT);
+  c.blockDim = dim3((unsigned)threads);
   c.dynamicSmemBytes = smem;
   c.stream = s;
   c.attrs = at;
@@ -837,6 +850,13 @@ cudaError_t launch_rows(K kernel, const A& a, WsHeader* hdr, int N, int split, u
   return cudaGetLastError();
 }
 
+template <typename T, int LT>
+cudaError_t launch_logprobs(const dspark_token_logprobs_args& a, WsHeader* hdr, int split, cudaStream_t s) {
+  const unsigned smem = a.top > 0 ? kTopStages * kChunkBytes<LT> + sizeof(TopShared<LT>) : kMaxStages * kChunkBytes<LT>;
+  return a.rows.mask ? launch_rows(k_logprobs<T, true, LT>, a, hdr, a.rows.N, split, LT, smem, s)
+                     : launch_rows(k_logprobs<T, false, LT>, a, hdr, a.rows.N, split, LT, smem, s);
+}
+
 }  // namespace
 
 size_t token_logprobs_ws(int, int, int) { return sizeof(WsHeader); }
@@ -845,19 +865,19 @@ cudaError_t launch_token_logprobs(const dspark_token_logprobs_args& a, uint8_t* 
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
   const int N = a.rows.N, split = row_split(N, a.rows.V);
   const bool bf16 = a.rows.dtype == DSPARK_BF16;
-  const unsigned smem = a.top > 0 ? kTopStages * kChunkBytes + sizeof(TopShared) : kMaxStages * kChunkBytes;
-  if (a.rows.mask)
-    return bf16 ? launch_rows(k_logprobs<__nv_bfloat16, true>, a, hdr, N, split, smem, s)
-                : launch_rows(k_logprobs<float, true>, a, hdr, N, split, smem, s);
-  return bf16 ? launch_rows(k_logprobs<__nv_bfloat16, false>, a, hdr, N, split, smem, s)
-              : launch_rows(k_logprobs<float, false>, a, hdr, N, split, smem, s);
+  // many rows: CTAs of 128 threads, eight an SM, so that more rows cover a
+  // row's end (4096 x 30000 bf16, 8 alternatives: 66 against 82 us; 2048 x 151936 123
+  // against 127; but 1300 x 100000 64.4 against 62.7)
+  if (N >= 2048)
+    return bf16 ? launch_logprobs<__nv_bfloat16, 128>(a, hdr, 1, s) : launch_logprobs<float, 128>(a, hdr, 1, s);
+  return bf16 ? launch_logprobs<__nv_bfloat16, 256>(a, hdr, split, s) : launch_logprobs<float, 256>(a, hdr, split, s);
 }
 
 cudaError_t launch_token_logprobs_grad(const dspark_token_logprobs_grad_args& a, uint8_t* ws, cudaStream_t s) {
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
   const int N = a.rows.N, split = row_split(N, a.rows.V);
-  return a.rows.dtype == DSPARK_BF16 ? launch_rows(k_logprobs_grad<__nv_bfloat16>, a, hdr, N, split, 0, s)
-                                     : launch_rows(k_logprobs_grad<float>, a, hdr, N, split, 0, s);
+  return a.rows.dtype == DSPARK_BF16 ? launch_rows(k_logprobs_grad<__nv_bfloat16>, a, hdr, N, split, GT, 0, s)
+                                     : launch_rows(k_logprobs_grad<float>, a, hdr, N, split, GT, 0, s);
 }
 
 }  // namespace dspark
