@@ -130,6 +130,21 @@ dspark_status check_sched_args(const dspark_sched_args* a, int64_t max_keys) {
 
 using namespace dspark;
 
+// sizes whose tile counts and rounded-up lengths stay in 32 bits
+constexpr int32_t kMaxFp8Dim = 1 << 30;
+
+// A launcher's result as a status; nothing it throws (a table that cannot grow)
+// leaves the C entry.
+template <typename F>
+static dspark_status launched(F launch) {
+  try {
+    const cudaError_t e = launch();
+    return e == cudaErrorNotSupported ? DSPARK_UNSUPPORTED : cuda_status(e);
+  } catch (...) {
+    return cuda_status(cudaErrorMemoryAllocation);
+  }
+}
+
 extern "C" {
 
 const char* dspark_status_string(dspark_status s) {
@@ -313,9 +328,8 @@ dspark_status dspark_quant_fp8(const dspark_quant_fp8_args* a, void* stream) {
   if (!a->x || !a->codes || !a->scale || !rows_ok(a->M, a->K, a->ldx) || !rows_ok(a->M, a->K, a->ldq))
     return DSPARK_INVALID_ARG;
   if (!aligned_to(a->x, elem_size(a->dtype)) || !aligned_to(a->scale, 4)) return DSPARK_INVALID_ARG;
-  const cudaError_t e = launch_quant_fp8(*a, (cudaStream_t)stream);
-  if (e == cudaErrorNotSupported) return DSPARK_UNSUPPORTED;
-  return cuda_status(e);
+  if (a->M > kMaxFp8Dim || a->K > kMaxFp8Dim) return DSPARK_UNSUPPORTED;
+  return launched([&] { return launch_quant_fp8(*a, (cudaStream_t)stream); });
 }
 
 dspark_status dspark_matmul_fp8_workspace_size(int32_t M, int32_t N, int32_t K, size_t* bytes) {
@@ -336,9 +350,8 @@ dspark_status dspark_matmul_fp8(const dspark_matmul_fp8_args* a, void* workspace
   if (!aligned_to(a->out, elem_size(a->out_dtype)) || !aligned_to(a->a_scale, 4) || !aligned_to(a->w_scale, 4))
     return DSPARK_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, matmul_fp8_ws(a->M, a->N, a->K))) return DSPARK_INVALID_ARG;
-  const cudaError_t e = launch_matmul_fp8(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream);
-  if (e == cudaErrorNotSupported) return DSPARK_UNSUPPORTED;
-  return cuda_status(e);
+  if (a->M > kMaxFp8Dim || a->N > kMaxFp8Dim || a->K > kMaxFp8Dim) return DSPARK_UNSUPPORTED;
+  return launched([&] { return launch_matmul_fp8(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream); });
 }
 
 static dspark_status check_logit_rows(const dspark_logit_rows& r) {
@@ -368,8 +381,7 @@ dspark_status dspark_token_logprobs(const dspark_token_logprobs_args* a, void* w
   if (st != DSPARK_OK || a->rows.N == 0) return st;
   if (a->top > 0 && (!a->top_id || !a->top_logprob)) return DSPARK_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, token_logprobs_ws(a->rows.N, a->rows.V, a->top))) return DSPARK_INVALID_ARG;
-  const cudaError_t e = launch_token_logprobs(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream);
-  return cuda_status(e);
+  return launched([&] { return launch_token_logprobs(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream); });
 }
 
 dspark_status dspark_token_logprobs_grad(const dspark_token_logprobs_grad_args* a, void* workspace, void* stream) {
@@ -383,7 +395,7 @@ dspark_status dspark_token_logprobs_grad(const dspark_token_logprobs_grad_args* 
     return DSPARK_INVALID_ARG;
   if (a->grad == a->rows.logits && a->rows.N > 1 && a->ldg != a->rows.ld) return DSPARK_INVALID_ARG;
   if (workspace && ((uintptr_t)workspace & 255u)) return DSPARK_INVALID_ARG;
-  return cuda_status(launch_token_logprobs_grad(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream));
+  return launched([&] { return launch_token_logprobs_grad(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream); });
 }
 
 }  // extern "C"

@@ -716,7 +716,7 @@ cudaError_t run_narrow(const dspark_matmul_fp8_args& a, const MmParams& p, const
   const int64_t tiles = (int64_t)mt * (((int64_t)a.N + 127) / 128);
   const int split = narrow_split(tiles, p.kb, NT, d.sms);
   // a deep ring where one CTA has an SM to itself for many blocks
-  const int stages = split > 1 ? 4 : NT <= 16 ? 11 : NT <= 32 ? 9 : NT <= 64 ? 8 : 6;
+  const int stages = split > 1 ? 4 : NT <= 16 ? 11 : NT <= 32 ? 9 : 8;
   const uint32_t smem = stages * C::kStage + (split > 1 ? C::kRed : 0) + 1024;
   const void* f = (const void*)k_fp8_narrow<NT, TO>;
   if (const cudaError_t e = ensure_smem_limit(f, (int)smem); e != cudaSuccess) return e;

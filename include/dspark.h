@@ -457,7 +457,10 @@ DSPARK_API dspark_status dspark_sts_fit(const dspark_sts_fit_args* args, void* w
  * counterpart to them; they follow this library's conventions (device
  * pointers, caller's buffers and workspace, one stream, no allocation).
  * Matrices are row-major with a stride between rows, so a column range of a
- * wider buffer is a valid argument. */
+ * wider buffer is a valid argument.  Sizes above 2^30 return
+ * DSPARK_UNSUPPORTED.  As with dspark_schedule_noalloc, the first call of each
+ * entry point in a context can load device code: make it before a stream
+ * capture begins. */
 #define DSPARK_FP8_BLOCK 128 /* columns (and weight rows) that share one scale */
 #define DSPARK_MAX_TOP 32    /* top alternatives of dspark_token_logprobs */
 
