@@ -533,7 +533,7 @@ DSPARK_API dspark_status dspark_matmul_fp8(const dspark_matmul_fp8_args* args, v
  * word v / 32, mask_ld >= ceil(V / 32); NULL: all).  Logits of masked places are
  * not looked at (they may be NaN).  T = temp[i] where that is finite and > 0;
  * anything else, and temp = NULL, means T = 1 (a greedy request's answers
- * come from the untempered law).  tokens [N]: the given token of each row, -1
+ * come from the untempered law); above 1e35 it counts as 1e35.  tokens [N]: the given token of each row, -1
  * for none.
  * With markers (mark_req, mark_pos [N], both or neither) row i belongs to
  * request mark_req[i]: its token is tokens[mark_req[i] * tok_cols +

@@ -23,6 +23,7 @@ Modules:
   draft     Markov-head draft sampler + confidence head
   schedule  Sequential Temperature Scaling, Algorithm 1, flatten + markers
   verify    lossless rejection-sampling verification
+  vocab     block-scaled e4m3 quantisation and product; token log probabilities and their gradient
 
 Every function computes in fp64 unless its docstring says otherwise (the
 scheduler's survival products are fp32 by contract, because they are sort keys
