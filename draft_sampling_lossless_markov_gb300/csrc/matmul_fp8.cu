@@ -33,6 +33,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch.h"
 #include "tc_ptx.cuh"
 #include "tensor_map.h"
 
@@ -143,6 +144,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  ptx::launch_dependents();
+  ptx::grid_wait();
   auto fail = [&](int what) {
     if (p.hdr) report_error(p.hdr, DSPARK_TIMEOUT, what);
     *abort_flag = 1;
@@ -440,6 +443,8 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  ptx::launch_dependents();
+  ptx::grid_wait();
   auto fail = [&](int what) {
     if (p.hdr) report_error(p.hdr, DSPARK_TIMEOUT, what);
     *abort_flag = 1;
@@ -690,7 +695,9 @@ cudaError_t run_wide(const dspark_matmul_fp8_args& a, const MmParams& p, const D
   const void* f = (const void*)k_fp8_wide<NH, TO>;
   if (const cudaError_t e = ensure_smem_limit(f, (int)W::kSmem); e != cudaSuccess) return e;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, d.pairs);
-  k_fp8_wide<NH, TO><<<grid, W::kThreads, W::kSmem, s>>>(tmA, tmW, tmO, p);
+  if (const cudaError_t e = launch_overlapped(k_fp8_wide<NH, TO>, grid, W::kThreads, W::kSmem, 1, s, tmA, tmW, tmO, p);
+      e != cudaSuccess)
+    return e;
   count_launches(1);
   return cudaGetLastError();
 }
@@ -720,11 +727,9 @@ cudaError_t run_narrow(const dspark_matmul_fp8_args& a, const MmParams& p, const
   const uint32_t smem = stages * C::kStage + (split > 1 ? C::kRed : 0) + 1024;
   const void* f = (const void*)k_fp8_narrow<NT, TO>;
   if (const cudaError_t e = ensure_smem_limit(f, (int)smem); e != cudaSuccess) return e;
-  cudaLaunchConfig_t c = {};
-  cudaLaunchAttribute at[1];
-  cluster_config(&c, at, (unsigned)split, (unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, d.sms)),
-                 C::kThreads, smem, s);
-  const cudaError_t e = cudaLaunchKernelEx(&c, k_fp8_narrow<NT, TO>, tmA, tmW, p, split, stages, mt);
+  const unsigned grid = (unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, d.sms));
+  const cudaError_t e =
+      launch_overlapped(k_fp8_narrow<NT, TO>, grid, C::kThreads, smem, (unsigned)split, s, tmA, tmW, p, split, stages, mt);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();

@@ -16,6 +16,8 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch.h"
+#include "tc_ptx.cuh"
 #include "vec8.cuh"
 
 namespace dspark {
@@ -144,13 +146,16 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c0, int K, bool ve
   }
 }
 
+// (No __restrict__ in these kernels: their loads must stay behind the wait.)
+//
 // One block of 128 columns of one row per 16 lanes.  A CTA takes 16 QU blocks
 // that follow each other in the scales' order (row by row).  The divisions of a
 // group's QU blocks are made by QU of its lanes at once.
 template <int QU, typename T>
-__global__ void __launch_bounds__(QT, 4) k_quant_rows(const T* __restrict__ x, int64_t ldx, uint8_t* __restrict__ codes,
-                                                   int64_t ldq, float* __restrict__ scale, int64_t blocks, int K,
-                                                   uint32_t kb, bool vec) {
+__global__ void __launch_bounds__(QT, 4) k_quant_rows(const T* x, int64_t ldx, uint8_t* codes, int64_t ldq,
+                                                      float* scale, int64_t blocks, int K, uint32_t kb, bool vec) {
+  ptx::launch_dependents();
+  ptx::grid_wait();
   constexpr int G = QT / QL;
   const int l = threadIdx.x % QL;
   const int64_t first = (int64_t)blockIdx.x * (G * QU) + threadIdx.x / QL;
@@ -205,11 +210,12 @@ constexpr int block_threads() {
   return std::is_same<T, float>::value ? 512 : 256;
 }
 template <typename T>
-__global__ void __launch_bounds__(block_threads<T>(), 1024 / block_threads<T>()) k_quant_blocks(const T* __restrict__ x, int64_t ldx,
-                                                     uint8_t* __restrict__ codes, int64_t ldq,
-                                                     float* __restrict__ scale, int M, int K, int kb, bool vec) {
+__global__ void __launch_bounds__(block_threads<T>(), 1024 / block_threads<T>())
+    k_quant_blocks(const T* x, int64_t ldx, uint8_t* codes, int64_t ldq, float* scale, int M, int K, int kb, bool vec) {
   constexpr int BT = block_threads<T>(), BR = DSPARK_FP8_BLOCK * QL / BT;
   __shared__ uint32_t red[BT / 32], fin[BT / 32];
+  ptx::launch_dependents();
+  ptx::grid_wait();
   const int rb = blockIdx.x / kb, b = blockIdx.x - rb * kb;
   const int c0 = b * DSPARK_FP8_BLOCK + (threadIdx.x % QL) * 8;
   const int64_t r0 = (int64_t)rb * DSPARK_FP8_BLOCK + threadIdx.x / QL;
@@ -265,16 +271,13 @@ cudaError_t launch_t(const dspark_quant_fp8_args& a, cudaStream_t s) {
     const bool many = blocks >= 1 << 18;
     const int64_t each = QT / QL * (many ? 4 : 2), grid = (blocks + each - 1) / each;
     if (grid > INT32_MAX) return cudaErrorNotSupported;
-    if (many)
-      k_quant_rows<4, T><<<(unsigned)grid, QT, 0, s>>>(x, a.ldx, q, a.ldq, a.scale, blocks, a.K, (uint32_t)kb, vec);
-    else
-      k_quant_rows<2, T><<<(unsigned)grid, QT, 0, s>>>(x, a.ldx, q, a.ldq, a.scale, blocks, a.K, (uint32_t)kb, vec);
-  } else {
-    const int64_t grid = (((int64_t)a.M + DSPARK_FP8_BLOCK - 1) / DSPARK_FP8_BLOCK) * kb;
-    if (grid > INT32_MAX) return cudaErrorNotSupported;
-    k_quant_blocks<T><<<(unsigned)grid, block_threads<T>(), 0, s>>>(x, a.ldx, q, a.ldq, a.scale, a.M, a.K, (int)kb, vec);
+    return launch_overlapped(many ? k_quant_rows<4, T> : k_quant_rows<2, T>, (unsigned)grid, QT, 0, 1, s, x, a.ldx, q, a.ldq,
+                             a.scale, blocks, a.K, (uint32_t)kb, vec);
   }
-  return cudaGetLastError();
+  const int64_t grid = (((int64_t)a.M + DSPARK_FP8_BLOCK - 1) / DSPARK_FP8_BLOCK) * kb;
+  if (grid > INT32_MAX) return cudaErrorNotSupported;
+  return launch_overlapped(k_quant_blocks<T>, (unsigned)grid, block_threads<T>(), 0, 1, s, x, a.ldx, q, a.ldq, a.scale, a.M,
+                           a.K, (int)kb, vec);
 }
 
 }  // namespace

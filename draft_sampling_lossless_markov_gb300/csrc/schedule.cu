@@ -33,6 +33,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "sts_sigmoid.cuh"
+#include "tc_ptx.cuh"
 
 namespace dspark {
 
@@ -230,7 +231,10 @@ __global__ void __launch_bounds__(SCH_THREADS, 1) k_schedule(dspark_sched_args a
       s_first = ok;
     }
     __syncthreads();
-    if (!s_first) return;
+    if (!s_first) {
+      ptx::grid_wait();
+      return;
+    }
   }
   if (fused_keys) {
     sts_consts_init(sc, a.sts_temp, G, tab);
@@ -389,6 +393,8 @@ __global__ void __launch_bounds__(SCH_THREADS, 1) k_schedule(dspark_sched_args a
     a.offsets[B] = (int)nv;
     *a.n_verify = (int)nv;
   }
+  // a kernel set up behind this one waits for this grid alone: it ends after the draft's
+  if (dep) ptx::grid_wait();
 }
 
 // Up to kSmemSortMax slots the whole schedule runs out of shared memory.  A
@@ -639,7 +645,10 @@ __global__ void __launch_bounds__(SCH_THREADS, 1) k_schedule_smem(dspark_sched_a
       s_first = ok;
     }
     __syncthreads();
-    if (!s_first) return;
+    if (!s_first) {
+      ptx::grid_wait();
+      return;
+    }
   }
   const int R = sched_run_len(G);
   sts_consts_init(sc, a.sts_temp, G, tab);
@@ -838,6 +847,8 @@ __global__ void __launch_bounds__(SCH_THREADS, 1) k_schedule_smem(dspark_sched_a
     a.offsets[B] = (int)nv;
     *a.n_verify = (int)nv;
   }
+  // a kernel set up behind this one waits for this grid alone: it ends after the draft's
+  if (dep) ptx::grid_wait();
 }
 
 static size_t schedule_smem_bytes(int B, int G) {

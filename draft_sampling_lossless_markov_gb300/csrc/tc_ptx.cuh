@@ -23,6 +23,8 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // done so or exited).  It orders no memory: the dependent grid synchronises on
 // a flag of its own.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// The grids this one was launched behind have ended and what they wrote is visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- mbarrier ----
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {

@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch.h"
 #include "tc_ptx.cuh"
 #include "vec8.cuh"
 
@@ -44,31 +45,29 @@ struct RowMeta {
   float T;
 };
 
-// token and temperature of row i; reports what is outside its range
-__device__ __forceinline__ RowMeta row_meta(const dspark_logit_rows& r, int i, WsHeader* hdr, bool report) {
-  RowMeta m{-1, 1.f};
+// what the buffers hold for row i (loads that nothing waits for yet)
+struct RowRaw {
+  int tok;
+  float T;
+  bool bad;
+};
+__device__ __forceinline__ RowRaw row_raw(const dspark_logit_rows& r, int i) {
   int64_t at = i;
   int ti = i;
   if (r.mark_req) {
     const int q = r.mark_req[i], pos = r.mark_pos[i];
-    if (q == -1) return m;
-    if (q < 0 || q >= r.n_req || pos < 0 || pos >= r.tok_cols) {
-      if (report && hdr) report_error(hdr, DSPARK_BAD_INPUT, i);
-      return m;
-    }
+    if (q < 0 || q >= r.n_req || pos < 0 || pos >= r.tok_cols) return RowRaw{-1, 1.f, q != -1};
     at = (int64_t)q * r.tok_cols + pos;
     ti = q;
   }
-  const int t = r.tokens[at];
-  if (t >= 0 && t < r.V)
-    m.tok = t;
-  else if (t != -1 && report && hdr)
-    report_error(hdr, DSPARK_BAD_INPUT, i);
-  if (r.temp) {
-    const float T = r.temp[ti];
-    if (T > 0.f && T < INFINITY) m.T = fminf(T, kMaxTemp);
-  }
-  return m;
+  return RowRaw{r.tokens[at], r.temp ? r.temp[ti] : 1.f, false};
+}
+// its token and temperature; reports what is outside its range
+__device__ __forceinline__ RowMeta row_meta(const dspark_logit_rows& r, const RowRaw& raw, int i, WsHeader* hdr,
+                                            bool report) {
+  const bool in = raw.tok >= 0 && raw.tok < r.V;
+  if ((raw.bad || (!in && raw.tok != -1)) && report && hdr) report_error(hdr, DSPARK_BAD_INPUT, i);
+  return RowMeta{in ? raw.tok : -1, raw.T > 0.f && raw.T < INFINITY ? fminf(raw.T, kMaxTemp) : 1.f};
 }
 
 // log2(e) / T, finite for every T > 0 so that 0 * c is 0
@@ -413,6 +412,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
   constexpr int kVec = 8 * sizeof(T);
   const dspark_logit_rows& r = p.rows;
   const int i = blockIdx.x / split, rank = blockIdx.x % split;
+  ptx::grid_wait();
   if (r.n_rows && i >= *r.n_rows) return;  // the whole cluster
   __shared__ LpShared<LT> sh;
   // a ring of chunks; with alternatives a TopShared after it and a TopBuffer in its place later
@@ -430,6 +430,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
     raw.load(base + 8 * (int64_t)j);
     if (kMask) raw.mask(mask8(mask, shp.head + 8 * j));
   };
+  const RowRaw given_row = row_raw(r, i);  // on its way before the ring is set up
   // one thread keeps the ring filled by bulk copies; the first chunks are under
   // way while the row's token and temperature are read
   const int chunks = (v1 - v0 + U * LT - 1) / (U * LT);
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
     for (int ch = 0; ch < min(chunks, stages); ++ch) fill(ch);
   }
   __syncthreads();
-  const RowMeta meta = row_meta(r, i, hdr, tid == 0 && rank == 0);
+  const RowMeta meta = row_meta(r, given_row, i, hdr, tid == 0 && rank == 0);
   const float c = log2_scale(meta.T);
 
   // rank: x > x_hi counts from the token's vector on, x > x_lo (x >= x_token) before it
@@ -721,11 +722,12 @@ __global__ void __launch_bounds__(GT, 4) k_logprobs_grad(const dspark_token_logp
   constexpr int U = std::is_same<T, float>::value ? 2 : 4;
   const dspark_logit_rows& r = p.rows;
   const int i = blockIdx.x / split, rank = blockIdx.x % split;
+  ptx::grid_wait();
   if (r.n_rows && i >= *r.n_rows) return;  // the whole cluster
   __shared__ int pid[DSPARK_MAX_TOP + 1];
   __shared__ float pg[DSPARK_MAX_TOP + 1], px[DSPARK_MAX_TOP + 1];
   const int tid = threadIdx.x;
-  const RowMeta meta = row_meta(r, i, hdr, tid == 0 && rank == 0);
+  const RowMeta meta = row_meta(r, row_raw(r, i), i, hdr, tid == 0 && rank == 0);
   const T* row = static_cast<const T*>(r.logits) + (int64_t)i * r.ld;
   T* out = static_cast<T*>(p.grad) + (int64_t)i * p.ldg;
   const uint32_t* mask = r.mask ? r.mask + (int64_t)i * r.mask_ld : nullptr;
@@ -802,14 +804,19 @@ __global__ void __launch_bounds__(GT, 4) k_logprobs_grad(const dspark_token_logp
   }
 }
 
-// CTAs a row is split over: as many as leave every CTA a place at once (four an
-// SM).  A cluster of 16 pays only for very few rows: 32 x 151936 bf16 8.8 us
-// against 7.7 with 8; 100 rows 12.8 us with 4 against 16.6 with 2 and 17.0 with 8.
-int row_split(int64_t N, int64_t V) {
+// CTAs a row is split over: about as many as have a place at once, each with
+// `least` elements or more (8192, but 2048 where rows are very few: 1 x 100003 fp32 with
+// a mask 9.2 us, with 8192 10.2).  V = 151936 bf16, without alternatives: 16 rows 6.0 us
+// with 16 CTAs a row (8: 6.2), 32 rows 6.7 with 8 (16: 7.6), 64 rows 9.4 with 4 (8:
+// 10.8), 150 rows 14.4 with 2 (4: 17.9), 300 rows 21.9 with 1 (2: 22.9); 300 x 32000 with 8
+// alternatives 11.3 with 1 (2: 15.3).  The gradient keeps fewer bytes on their way
+// to a CTA and wants more of them: 64 rows 10.2 with 8 (4: 10.7), 300 rows 34.0 with 2 (1: 38.9).
+int row_split(int64_t N, int64_t V, int64_t most, int64_t least) {
   int split = 1;
-  while (split < kMaxSplit && N * split * 2 <= (split == 8 ? 256 : 608) && V >= 4096 * split) split *= 2;
+  while (split < kMaxSplit && N * split * 2 <= (split == 8 ? 256 : most) && V >= least * split * 2) split *= 2;
   return split;
 }
+constexpr int kMostLp = 400, kMostGrad = 608, kLeast = 2048;
 
 // Clusters of 16 CTAs: the attribute belongs to the kernel in a device's
 // context, so it is set once per (device, kernel).
@@ -829,22 +836,12 @@ cudaError_t allow_large_cluster(const void* kernel) {
 template <typename K, typename A>
 cudaError_t launch_rows(K kernel, const A& a, WsHeader* hdr, int N, int split, int threads, unsigned smem,
                         cudaStream_t s) {
-  cudaLaunchConfig_t c = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  c.gridDim = dim3((unsigned)N * (unsigned)split);
-  c.blockDim = dim3((unsigned)threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  c.attrs = at;
-  c.numAttrs = split > 1 ? 1 : 0;
   if (smem > 0)
     if (const cudaError_t e = ensure_smem_limit((const void*)kernel, (int)smem); e != cudaSuccess) return e;
   if (split > 8)
     if (const cudaError_t e = allow_large_cluster((const void*)kernel); e != cudaSuccess) return e;
-  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, a, hdr, split);
+  const cudaError_t e = launch_overlapped(kernel, (unsigned)N * (unsigned)split, (unsigned)threads, smem,
+                                          (unsigned)split, s, a, hdr, split);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
@@ -863,7 +860,7 @@ size_t token_logprobs_ws(int, int, int) { return sizeof(WsHeader); }
 
 cudaError_t launch_token_logprobs(const dspark_token_logprobs_args& a, uint8_t* ws, cudaStream_t s) {
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
-  const int N = a.rows.N, split = row_split(N, a.rows.V);
+  const int N = a.rows.N, split = row_split(N, a.rows.V, kMostLp, N <= 32 ? kLeast : 4 * kLeast);
   const bool bf16 = a.rows.dtype == DSPARK_BF16;
   // many rows: CTAs of 128 threads, eight an SM, so that more rows cover a
   // row's end (4096 x 30000 bf16, 8 alternatives: 66 against 82 us; 2048 x 151936 123
@@ -875,7 +872,7 @@ cudaError_t launch_token_logprobs(const dspark_token_logprobs_args& a, uint8_t* 
 
 cudaError_t launch_token_logprobs_grad(const dspark_token_logprobs_grad_args& a, uint8_t* ws, cudaStream_t s) {
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
-  const int N = a.rows.N, split = row_split(N, a.rows.V);
+  const int N = a.rows.N, split = row_split(N, a.rows.V, kMostGrad, kLeast);
   return a.rows.dtype == DSPARK_BF16 ? launch_rows(k_logprobs_grad<__nv_bfloat16>, a, hdr, N, split, GT, 0, s)
                                      : launch_rows(k_logprobs_grad<float>, a, hdr, N, split, GT, 0, s);
 }

@@ -14,6 +14,13 @@ namespace dspark {
 
 constexpr float kLowest = -3.402823466e+38f;
 
+// 16 bytes that are read once.  Volatile: the load stays behind a wait in front of it.
+__device__ __forceinline__ uint4 load16_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // bf16 pairs
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -60,7 +67,7 @@ struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = load16_once(p); }
   __device__ __forceinline__ void load_shared(const uint8_t* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void fill_neg_inf() { a = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
   // -inf where the bit is clear
@@ -120,8 +127,9 @@ template <>
 struct Vec8<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    const uint4 u = load16_once(p), w = load16_once(p + 4);
+    a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+    b = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
   }
   __device__ __forceinline__ void load_shared(const uint8_t* p) {
     a = *reinterpret_cast<const float4*>(p);

@@ -460,7 +460,11 @@ DSPARK_API dspark_status dspark_sts_fit(const dspark_sts_fit_args* args, void* w
  * wider buffer is a valid argument.  Sizes above 2^30 return
  * DSPARK_UNSUPPORTED.  As with dspark_schedule_noalloc, the first call of each
  * entry point in a context can load device code: make it before a stream
- * capture begins. */
+ * capture begins.
+ * Their kernels may be set up while the kernel before them in the stream
+ * drains (programmatic stream serialization), and wait for its end before they
+ * touch memory.  A caller's kernel that is itself launched with that attribute
+ * has to wait (griddepcontrol.wait) before it ends, as CUDA asks of such chains. */
 #define DSPARK_FP8_BLOCK 128 /* columns (and weight rows) that share one scale */
 #define DSPARK_MAX_TOP 32    /* top alternatives of dspark_token_logprobs */
 
