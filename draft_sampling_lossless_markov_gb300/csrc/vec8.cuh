@@ -67,7 +67,9 @@ struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
   uint4 a;
+  static constexpr int kAlign = 16;  // bytes, for load_aligned and store
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = load16_once(p); }
+  __device__ __forceinline__ void load_aligned(const __nv_bfloat16* p) { load(p); }
   __device__ __forceinline__ void load_shared(const uint8_t* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void fill_neg_inf() { a = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
   // -inf where the bit is clear
@@ -126,6 +128,12 @@ struct Vec8<__nv_bfloat16> {
 template <>
 struct Vec8<float> {
   float4 a, b;
+  static constexpr int kAlign = 32;
+  __device__ __forceinline__ void load_aligned(const float* p) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w), "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+                 : "l"(p));
+  }
   __device__ __forceinline__ void load(const float* p) {
     const uint4 u = load16_once(p), w = load16_once(p + 4);
     a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
@@ -162,8 +170,9 @@ struct Vec8<float> {
   }
   static __device__ __forceinline__ void store(float* p, const float (&d)[8], bool vec) {
     if (vec) {
-      __stcs(reinterpret_cast<float4*>(p), make_float4(d[0], d[1], d[2], d[3]));
-      __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(d[4], d[5], d[6], d[7]));
+      asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(d[0]), "f"(d[1]), "f"(d[2]),
+                   "f"(d[3]), "f"(d[4]), "f"(d[5]), "f"(d[6]), "f"(d[7]), "l"(p)
+                   : "memory");
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = d[i];
