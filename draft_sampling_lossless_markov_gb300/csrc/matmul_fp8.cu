@@ -395,11 +395,11 @@ template <int NT>
 struct Narrow {
   static constexpr int kCols32 = NT < 32 ? NT : 32;     // columns of an epilogue warp
   static constexpr int kEpiWarps = 4 * (NT / kCols32);
-  static constexpr int kThreads = 32 * (kEpiWarps + 2);  // and loads, MMA
+  static constexpr int kThreads = 32 * (kEpiWarps + 3);  // and loads, two for the MMAs
   static constexpr uint32_t kW = 128 * kKb;
   static constexpr uint32_t kA = NT * kKb;
   static constexpr uint32_t kStage = kW + kA;
-  static constexpr int kBufs = 4;
+  static constexpr int kBufs = 8;
   static constexpr uint32_t kTmemCols = NT * kBufs;
   static constexpr uint32_t kRed = NT * 128 * 4;  // a tile's sums, one float each
 };
@@ -481,31 +481,36 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads, 1)
     for (uint32_t j = n > (uint32_t)stages ? n - stages : 0; j < n; ++j)
       ptx::mbar_wait_cycles(&full[j % stages], (j / stages) & 1, &never_s, kWaitLimit);
     __syncwarp();
-  } else if (warp == EW + 1) {
+  } else if (warp > EW) {
+    // every other block each: a wait costs some 80 cycles even when it is over, and
+    // one warp's waits and issues for a block took longer than its load
+    const uint32_t other = warp - (EW + 1);
     constexpr uint32_t idesc = ptx::idesc_e4m3_f32(128, NT);
     const uint64_t dw0 = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
     uint32_t s = 0, ph = 0, q = 0, tph = 1;
     bool ok = true;
     for (int64_t t = cl; t < tiles && ok; t += cls) {
       for (int b = b0; b < b1; ++b) {
-        ok = ptx::mbar_wait_cycles(&full[s], ph, abort_flag, kWaitLimit) &&
-             ptx::mbar_wait_cycles(&tempty[q], tph, abort_flag, kWaitLimit);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (lane == 0) fail(5);
-          break;
+        if ((q & 1) == other) {
+          ok = ptx::mbar_wait_cycles(&full[s], ph, abort_flag, kWaitLimit) &&
+               ptx::mbar_wait_cycles(&tempty[q], tph, abort_flag, kWaitLimit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            if (lane == 0) fail(5);
+            break;
+          }
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint64_t dw = dw0 + s * (C::kStage >> 4), da = dw + (C::kW >> 4);
+            ptx::tc_mma_fp8<0>(tmem + q * NT, dw, da, idesc);
+            ptx::tc_mma_fp8<1>(tmem + q * NT, dw + 2, da + 2, idesc);
+            ptx::tc_mma_fp8<1>(tmem + q * NT, dw + 4, da + 4, idesc);
+            ptx::tc_mma_fp8<1>(tmem + q * NT, dw + 6, da + 6, idesc);
+            ptx::tc_commit(&empty[s]);
+            ptx::tc_commit(&tfull[q]);
+          }
+          __syncwarp();
         }
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          const uint64_t dw = dw0 + s * (C::kStage >> 4), da = dw + (C::kW >> 4);
-          ptx::tc_mma_fp8<0>(tmem + q * NT, dw, da, idesc);
-          ptx::tc_mma_fp8<1>(tmem + q * NT, dw + 2, da + 2, idesc);
-          ptx::tc_mma_fp8<1>(tmem + q * NT, dw + 4, da + 4, idesc);
-          ptx::tc_mma_fp8<1>(tmem + q * NT, dw + 6, da + 6, idesc);
-          ptx::tc_commit(&empty[s]);
-          ptx::tc_commit(&tfull[q]);
-        }
-        __syncwarp();
         if (++s == (uint32_t)stages) s = 0, ph ^= 1;
         if (++q == NB) q = 0, tph ^= 1;
       }
@@ -519,40 +524,51 @@ __global__ void __launch_bounds__(Narrow<NT>::kThreads, 1)
     const int nm = min(NT, M - m0);
     if (warp < EW) {
       const float* wsc = p.w_scale + (int64_t)(n0 / kKb) * p.kb;
-      // lane l holds the scale of column c0 + l, the next block's on its way
+      // lane l holds the scales of column c0 + l, four blocks' at a time, the next four on their way
       const bool mine = lane < NC && c0 + lane < nm;
       const float* asc = p.a_scale + (int64_t)(m0 + (mine ? c0 + lane : 0)) * p.kb;
       float acc[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) acc[i] = 0.f;
-      float sa = mine && b0 < b1 ? asc[b0] : 0.f, sw = b0 < b1 ? wsc[b0] : 0.f;
-      for (int b = b0; b < b1 && ok; ++b) {
-        const float sc = sa * sw;
-        if (b + 1 < b1) {
-          sa = mine ? asc[b + 1] : 0.f;
-          sw = wsc[b + 1];
-        }
-        const bool got = ptx::mbar_wait_cycles(&tfull[q], tph, abort_flag, kWaitLimit);
-        if (!__all_sync(0xffffffffu, got)) {
-          if (lane == 0) fail(6);
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + q * NT + c0;
+      float sa[4], sw[4];
+      const auto fetch = [&](int b) {
 #pragma unroll
-        for (int c = 0; c < NC / 16; ++c) {
-          float v[16];
-          ptx::tmem_ld16(ta + c * 16, v);
-          ptx::tmem_ld_wait16(v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[c * 16 + i] = fmaf(v[i], __shfl_sync(0xffffffffu, sc, c * 16 + i), acc[c * 16 + i]);
+        for (int j = 0; j < 4; ++j) {
+          sa[j] = mine && b + j < b1 ? asc[b + j] : 0.f;
+          sw[j] = b + j < b1 ? wsc[b + j] : 0.f;
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&tempty[q]);
-        if (++q == NB) q = 0, tph ^= 1;
+      };
+      fetch(b0);
+      for (int b = b0; b < b1 && ok; b += 4) {
+        float sc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[j] = sa[j] * sw[j];
+        fetch(b + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (b + j >= b1) break;
+          const bool got = ptx::mbar_wait_cycles(&tfull[q], tph, abort_flag, kWaitLimit);
+          if (!__all_sync(0xffffffffu, got)) {
+            if (lane == 0) fail(6);
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + q * NT + c0;
+#pragma unroll
+          for (int c = 0; c < NC / 16; ++c) {
+            float v[16];
+            ptx::tmem_ld16(ta + c * 16, v);
+            ptx::tmem_ld_wait16(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              acc[c * 16 + i] = fmaf(v[i], __shfl_sync(0xffffffffu, sc[j], c * 16 + i), acc[c * 16 + i]);
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&tempty[q]);
+          if (++q == NB) q = 0, tph ^= 1;
+        }
       }
       if (split == 1) {
         const int n = n0 + quarter * 32 + lane;
