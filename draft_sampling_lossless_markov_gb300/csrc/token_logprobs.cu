@@ -332,7 +332,7 @@ struct LpShared {
 };
 // The first K candidates of a CTA's part of the row, with next to no work in
 // the pass over it: every thread writes down the largest element of each group
-// of its vectors.  K elements reach the smallest of the warps' (K / 8)-th largest
+// of its vectors.  K elements reach the smallest of the w (full) warps' (K / w)-th largest
 // threads, so only groups that reach it hold candidates; they (some 2 K of up
 // to 4096) are read again.  (Offering elements to a running threshold in the
 // pass itself cost 49 us more than no alternatives at 2048 x 151936 bf16,
@@ -364,8 +364,69 @@ struct TopSearch {
     const int at = atomicAdd(&s->n, 1);
     if (at < kCap) b->key[at] = key;
   }
-  // the list from `listed` keys of the list and n of the buffer: a key's place
-  // is the number of larger ones (keys differ).  All threads, after a barrier;
+  // Many keys (a short row, or a mask that leaves a few warps' threads all the
+  // candidates): a bound from the keys themselves, made as the threads' was,
+  // keeps some 2 K of them.  600 x 151936 with 960 candidates, 20 alternatives: 61
+  // against 145 us.
+  __device__ __forceinline__ int thin(int listed, int n, int K) const {
+    constexpr int kMine = (kCap + LT - 1) / LT, LW = LT / 32;
+    const int m = listed + n, lane = threadIdx.x & 31;
+    uint64_t key[kMine], best = 0;
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const int at = threadIdx.x + q * LT;
+      key[q] = at < listed ? s->list[at] : at < m ? b->key[at - listed] : 0;
+      best = key[q] > best ? key[q] : best;
+    }
+    float mine = best ? key_logit(best) : -INFINITY, jth = -INFINITY;
+    for (int j = (K + LW - 1) / LW; j > 0; --j) {
+      jth = warp_largest(mine);
+      const unsigned at = __ballot_sync(0xffffffffu, mine == jth);
+      if (lane == __ffs(at) - 1) mine = -INFINITY;
+    }
+    if (lane == 0) s->jth[threadIdx.x >> 5] = jth;
+    __syncthreads();
+    if (threadIdx.x == 0) s->n = 0;
+    if (threadIdx.x < 32) s->list[threadIdx.x] = 0;
+    float kth = s->jth[0];
+#pragma unroll
+    for (int w = 1; w < LW; ++w) kth = fminf(kth, s->jth[w]);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kMine; ++q)
+      if (key[q] && key_logit(key[q]) >= kth) offer(key[q]);
+    __syncthreads();
+    return s->n;
+  }
+  // take with kMine keys a thread
+  template <int kMine>
+  __device__ __forceinline__ void place(int listed, int n) const {
+    const int m = listed + n;
+    uint64_t key[kMine];
+    int place[kMine];
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const int at = threadIdx.x + q * LT;
+      key[q] = at < listed ? s->list[at] : at < m ? b->key[at - listed] : 0;
+      place[q] = 0;
+    }
+#pragma unroll
+    for (int q0 = 0; q0 < kMine; q0 += 2) {
+      if (q0 * LT >= m) break;
+#pragma unroll 4
+      for (int o = 0; o < m; ++o) {
+        const uint64_t other = o < listed ? s->list[o] : b->key[o - listed];
+#pragma unroll
+        for (int q = q0; q < min(q0 + 2, kMine); ++q) place[q] += other > key[q];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kMine; ++q)
+      if (key[q] && place[q] < 32) s->list[place[q]] = key[q];
+  }
+  // the list from `listed` keys of the list and n of the buffer, 2 LT together: a
+  // key's place is the number of larger ones (keys differ).  All threads, after a barrier;
   // ends with one.
   __device__ __noinline__ void take(int listed, int n) const {
     const int m = listed + n;
@@ -383,27 +444,30 @@ struct TopSearch {
       __syncthreads();
       if (key && from == 0 && place < 32) s->list[place] = key;
     } else {
-      constexpr int kMine = (kCap + 32 + LT - 1) / LT;
-      uint64_t key[kMine];
-      int place[kMine];
-#pragma unroll
-      for (int q = 0; q < kMine; ++q) {
-        const int at = threadIdx.x + q * LT;
-        key[q] = at < listed ? s->list[at] : at < m ? b->key[at - listed] : 0;
-        place[q] = 0;
-        if (key[q]) {
-          for (int o = 0; o < listed; ++o) place[q] += s->list[o] > key[q];
-#pragma unroll 4
-          for (int o = 0; o < n; ++o) place[q] += b->key[o] > key[q];
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < kMine; ++q)
-        if (key[q] && place[q] < 32) s->list[place[q]] = key[q];
+      place<2>(listed, n);
     }
     if (threadIdx.x == 0) s->n = 0;
     __syncthreads();
+  }
+  // take for any number of keys
+  static __device__ __noinline__ void take_many(TopShared<LT>* s, TopBuffer<LT>* b, int listed, int n, int K) {
+    const TopSearch<LT> t{s, b};
+    if (listed + n <= kCap) {
+      n = t.thin(listed, n, K);
+      listed = 0;
+    }
+    if (listed + n <= 2 * LT)
+      t.place<2>(listed, n);
+    else
+      t.place<(kCap + 32 + LT - 1) / LT>(listed, n);
+    if (threadIdx.x == 0) s->n = 0;
+    __syncthreads();
+  }
+  __device__ __forceinline__ void take_any(int listed, int n, int K) const {
+    if (listed + n <= 2 * LT)
+      take(listed, n);
+    else
+      take_many(s, b, listed, n, K);
   }
 };
 
@@ -590,8 +654,10 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
   Stat st = sum.stat();
   float mine = sum.largest;
   if (kTop) {
-    float best = mine, jth = -INFINITY;
-    for (int n = (p.top + LW - 1) / LW; n > 0; --n) {
+    // by the warps whose threads all have elements (a short row leaves others empty)
+    const int full_warps = max(1, min(LW, (v1 - v0) / 32));
+    float best = mine, jth = INFINITY;
+    for (int n = warp < full_warps ? (p.top + full_warps - 1) / full_warps : 0; n > 0; --n) {
       jth = warp_largest(best);
       const unsigned at = __ballot_sync(0xffffffffu, best == jth);
       if (lane == __ffs(at) - 1) best = -INFINITY;
@@ -650,7 +716,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
     __syncthreads();
     const int n = top.s->n;
     if (n <= kCap) {
-      top.take(0, n);
+      top.take_any(0, n, p.top);
     } else {
       // more ties with the bound than the buffer holds: the row in steps of a
       // vector a thread, each against the list so far
@@ -659,7 +725,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
       __syncthreads();
       if (edge && edge_x >= kth) top.offer(order_key(edge_x, edge_v));
       __syncthreads();
-      top.take(0, top.s->n);
+      top.take_any(0, top.s->n, p.top);
       for (int j0 = v0; j0 < v1; j0 += LT) {
         const int j = j0 + tid;
         const uint64_t last = top.s->list[p.top - 1];
@@ -673,7 +739,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
           }
         }
         __syncthreads();
-        top.take(32, top.s->n);
+        top.take_any(32, top.s->n, p.top);
       }
     }
   }
@@ -717,7 +783,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
         for (int q = 0; q < kKeys; ++q)
           if (key[q] && key[q] >= thr) top.offer(key[q]);
         __syncthreads();
-        top.take(32, top.s->n);
+        top.take_any(32, top.s->n, p.top);
       }
       __syncwarp();
     }

@@ -47,12 +47,13 @@ def _ptr(t: Optional[torch.Tensor], dtype=None) -> Optional[int]:
 
 # the address of the current stream without a Stream object around it (3 us less a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -269,17 +270,18 @@ def pack_rows(src, mark_req, mark_pos, n_rows, dst, ws: Optional[Workspace] = No
 # The vocabulary projection and the answers around verify
 # ---------------------------------------------------------------------------
 def _rows(t: torch.Tensor, what: str, dtype) -> tuple:
-    """(address, row stride in elements) of a 2-D CUDA tensor whose rows are dense."""
+    """(address, row stride in elements, rows, columns) of a 2-D CUDA tensor whose rows are dense."""
     if not t.is_cuda:
         raise ValueError("dspark tensors must live on a CUDA device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} must be a 2-D tensor with dense rows")
-    (rows, cols), (ld, step) = t.shape, t.stride()
+    (rows, cols), (ld, step) = shape, t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what} must be a 2-D tensor with dense rows")
-    return t.data_ptr(), ld if rows > 1 else max(ld, cols)
+    return t.data_ptr(), ld if rows > 1 else max(ld, cols), rows, cols
 
 
 def _dense(t: Optional[torch.Tensor], shape: tuple, what: str, dtype) -> Optional[int]:
@@ -288,7 +290,7 @@ def _dense(t: Optional[torch.Tensor], shape: tuple, what: str, dtype) -> Optiona
         return None
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: dspark tensors must be contiguous and live on a CUDA device")
@@ -314,16 +316,15 @@ def quant_fp8(x, block_rows: int = 1, out: Optional[tuple] = None, stream=None) 
     """dspark_quant_fp8: x [M, K] (bf16 or f32, dense rows) to (codes [M, K] e4m3, scale
     [ceil(M / block_rows), ceil(K / 128)] f32); block_rows 1 for activations, 128 for weights."""
     dt = _io_dtype(x, "x")
-    px, ldx = _rows(x, "x", x.dtype)
-    M, K = x.shape
+    px, ldx, M, K = _rows(x, "x", x.dtype)
     if block_rows not in (1, 128):
         raise ValueError("block_rows is 1 or 128")
     shape = (-(-M // block_rows), -(-K // 128))
     if out is None:
         out = fp8_codes(M, K, x.device), torch.empty(shape, dtype=torch.float32, device=x.device)
     codes, scale = out
-    pq, ldq = _rows(codes, "codes", _FP8)
-    if codes.shape != x.shape:
+    pq, ldq, *got = _rows(codes, "codes", _FP8)
+    if got != [M, K]:
         raise ValueError(f"codes: expected shape {(M, K)}, got {tuple(codes.shape)}")
     a = capi.dspark_quant_fp8_args(M, K, dt, block_rows, px, ldx, pq, ldq, _dense(scale, shape, "scale", torch.float32))
     _check("dspark_quant_fp8", capi.dspark_quant_fp8(a, _stream(stream)))
@@ -342,16 +343,15 @@ def matmul_fp8_workspace(M: int, N: int, K: int, device="cuda", stream=None) -> 
 def matmul_fp8(ws: Workspace, a, a_scale, w, w_scale, out=None, out_dtype=torch.bfloat16, n_rows=None, stream=None):
     """dspark_matmul_fp8: out [M, N] = (a a_scale) (w w_scale)^T for e4m3 a [M, K] and w [N, K] with a scale for each
     block of 128 (quant_fp8 with block_rows 1 and 128); n_rows [1] i32 bounds the rows computed."""
-    (M, K), N = a.shape, w.shape[0]
-    pa, lda = _rows(a, "a", _FP8)
-    pw, ldw = _rows(w, "w", _FP8)
-    if w.shape[1] != K:
+    pa, lda, M, K = _rows(a, "a", _FP8)
+    pw, ldw, N, cols = _rows(w, "w", _FP8)
+    if cols != K:
         raise ValueError(f"w: expected shape {(N, K)}, got {tuple(w.shape)}")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
     dt = _io_dtype(out, "out")
-    po, ldo = _rows(out, "out", out.dtype)
-    if out.shape != (M, N):
+    po, ldo, *got = _rows(out, "out", out.dtype)
+    if got != [M, N]:
         raise ValueError(f"out: expected shape {(M, N)}, got {tuple(out.shape)}")
     kb, f32 = -(-K // 128), torch.float32
     c = capi.dspark_matmul_fp8_args(M, N, K, dt, pa, lda, _dense(a_scale, (M, kb), "a_scale", f32), pw, ldw,
@@ -363,8 +363,7 @@ def matmul_fp8(ws: Workspace, a, a_scale, w, w_scale, out=None, out_dtype=torch.
 
 def _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows) -> capi.dspark_logit_rows:
     dt = _io_dtype(logits, "logits")
-    p, ld = _rows(logits, "logits", logits.dtype)
-    N, V = logits.shape
+    p, ld, N, V = _rows(logits, "logits", logits.dtype)
     i32, f32 = torch.int32, torch.float32
     if mark_req is None and mark_pos is None:
         n_req = cols = 0
@@ -378,8 +377,8 @@ def _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows) -> capi.
         pt, pT = _dense(tokens, (n_req, cols), "tokens", i32), _dense(temp, (n_req,), "temp", f32)
     pm = ldm = 0
     if mask is not None:
-        pm, ldm = _rows(mask, "mask", i32)
-        if mask.shape[0] != N or mask.shape[1] < -(-V // 32):
+        pm, ldm, mask_rows, words = _rows(mask, "mask", i32)
+        if mask_rows != N or words < -(-V // 32):
             raise ValueError("mask: expected [N, >= ceil(V / 32)] words")
     return capi.dspark_logit_rows(N, V, dt, cols, n_req, p, ld, pt, pT, pm, ldm, _dense(mark_req, (N,), "mark_req", i32),
                                   _dense(mark_pos, (N,), "mark_pos", i32), _dense(n_rows, (1,), "n_rows", i32))
@@ -423,7 +422,7 @@ def token_logprobs_grad(ws: Optional[Workspace], logits, tokens, row_stat, entro
     """dspark_token_logprobs_grad: the gradient by the logits of sum(g_logprob logprob) + sum(g_entropy entropy) +
     sum(g_top top_logprob), from token_logprobs's row_stat, entropy and top_id.  out may be logits itself."""
     rows = _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows)
-    N, V = logits.shape
+    N, V = rows.N, rows.V
     f32 = torch.float32
     top = 0
     if g_top is not None:
@@ -436,8 +435,8 @@ def token_logprobs_grad(ws: Optional[Workspace], logits, tokens, row_stat, entro
         raise ValueError("g_entropy needs entropy")
     if out is None:
         out = torch.empty((N, V), dtype=logits.dtype, device=logits.device)
-    po, ldo = _rows(out, "out", logits.dtype)
-    if out.shape != logits.shape:
+    po, ldo, *got = _rows(out, "out", logits.dtype)
+    if got != [N, V]:
         raise ValueError(f"out: expected shape {(N, V)}, got {tuple(out.shape)}")
     a = capi.dspark_token_logprobs_grad_args(
         rows, top, _dense(row_stat, (N, 2), "row_stat", f32),
