@@ -908,8 +908,8 @@ __global__ void __launch_bounds__(GT, 4) k_logprobs_grad(const dspark_token_logp
 }
 
 // CTAs a row is split over: about as many as have a place at once, each with
-// `least` elements or more (8192, but 2048 where rows are very few: 1 x 100003 fp32 with
-// a mask 9.2 us, with 8192 10.2).  V = 151936 bf16, without alternatives: 16 rows 6.0 us
+// `least` elements or more (8192, but 4096 where rows are very few: 1 x 100003 fp32 with
+// a mask 9.2 us, with 8192 10.2; 32 x 4264 with 20 alternatives 7.5 us, with 2048 10.1).  V = 151936 bf16, without alternatives: 16 rows 6.0 us
 // with 16 CTAs a row (8: 6.2), 32 rows 6.7 with 8 (16: 7.6), 64 rows 9.4 with 4 (8:
 // 10.8), 150 rows 14.4 with 2 (4: 17.9), 300 rows 21.9 with 1 (2: 22.9); 300 x 32000 with 8
 // alternatives 11.3 with 1 (2: 15.3).  The gradient keeps fewer bytes on their way
@@ -969,12 +969,14 @@ size_t token_logprobs_ws(int, int, int) { return sizeof(WsHeader); }
 
 cudaError_t launch_token_logprobs(const dspark_token_logprobs_args& a, uint8_t* ws, cudaStream_t s) {
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
-  const int N = a.rows.N, split = row_split(N, a.rows.V, kMostLp, N <= 32 ? kLeast : 4 * kLeast);
+  const int N = a.rows.N, split = row_split(N, a.rows.V, kMostLp, N <= 32 ? 2 * kLeast : 4 * kLeast);
   const bool bf16 = a.rows.dtype == DSPARK_BF16;
-  // many rows: CTAs of 128 threads, eight an SM, so that more rows cover a
-  // row's end (4096 x 30000 bf16, 8 alternatives: 66 against 82 us; 2048 x 151936 123
-  // against 127; but 1300 x 100000 64.4 against 62.7)
-  if (N >= 2048)
+  // Many rows for their length: CTAs of 128 threads, eight an SM, so that more rows
+  // cover a row's start and end.  bf16, 128 against 256 threads: 500 x 14088 with 20
+  // alternatives 11.8 and 13.8 us, 2932 x 14088 35.8 and 52.2, 2047 x 64367 with 5 59.1 and
+  // 64.9, 2048 x 151936 with 8 114 and 118; but 1352 x 151936 75.9 and 70.2, 100 x 1280 with 20 8.6 and 6.9
+  const int64_t bytes = (int64_t)a.rows.V * (bf16 ? 2 : 4);
+  if (N >= 200 && N * (int64_t)200 >= bytes)
     return bf16 ? launch_logprobs<__nv_bfloat16, 128>(a, hdr, 1, s) : launch_logprobs<float, 128>(a, hdr, 1, s);
   return bf16 ? launch_logprobs<__nv_bfloat16, 256>(a, hdr, split, s) : launch_logprobs<float, 256>(a, hdr, split, s);
 }

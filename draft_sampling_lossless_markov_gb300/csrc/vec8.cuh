@@ -70,6 +70,7 @@ struct Vec8<__nv_bfloat16> {
   static constexpr int kAlign = 16;  // bytes, for load_aligned and store
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = load16_once(p); }
   __device__ __forceinline__ void load_aligned(const __nv_bfloat16* p) { load(p); }
+  __device__ __forceinline__ void set(const uint32_t* w) { a = make_uint4(w[0], w[1], w[2], w[3]); }
   __device__ __forceinline__ void load_shared(const uint8_t* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void fill_neg_inf() { a = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
   // -inf where the bit is clear
@@ -129,6 +130,10 @@ template <>
 struct Vec8<float> {
   float4 a, b;
   static constexpr int kAlign = 32;
+  __device__ __forceinline__ void set(const uint32_t* w) {
+    a = make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
+    b = make_float4(__uint_as_float(w[4]), __uint_as_float(w[5]), __uint_as_float(w[6]), __uint_as_float(w[7]));
+  }
   __device__ __forceinline__ void load_aligned(const float* p) {
     asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w), "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)

@@ -284,10 +284,10 @@ def _rows(t: torch.Tensor, what: str, dtype) -> tuple:
     return t.data_ptr(), ld if rows > 1 else max(ld, cols), rows, cols
 
 
-def _dense(t: Optional[torch.Tensor], shape: tuple, what: str, dtype) -> Optional[int]:
-    """The address of a dense CUDA tensor of this shape and type; None for None."""
+def _dense(t: Optional[torch.Tensor], shape: tuple, what: str, dtype) -> int:
+    """The address of a dense CUDA tensor of this shape and type; 0 for None."""
     if t is None:
-        return None
+        return 0
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
@@ -326,7 +326,7 @@ def quant_fp8(x, block_rows: int = 1, out: Optional[tuple] = None, stream=None) 
     pq, ldq, *got = _rows(codes, "codes", _FP8)
     if got != [M, K]:
         raise ValueError(f"codes: expected shape {(M, K)}, got {tuple(codes.shape)}")
-    a = capi.dspark_quant_fp8_args(M, K, dt, block_rows, px, ldx, pq, ldq, _dense(scale, shape, "scale", torch.float32))
+    a = capi.pack_quant_fp8(M, K, dt, block_rows, px, ldx, pq, ldq, _dense(scale, shape, "scale", torch.float32))
     _check("dspark_quant_fp8", capi.dspark_quant_fp8(a, _stream(stream)))
     return out
 
@@ -354,14 +354,15 @@ def matmul_fp8(ws: Workspace, a, a_scale, w, w_scale, out=None, out_dtype=torch.
     if got != [M, N]:
         raise ValueError(f"out: expected shape {(M, N)}, got {tuple(out.shape)}")
     kb, f32 = -(-K // 128), torch.float32
-    c = capi.dspark_matmul_fp8_args(M, N, K, dt, pa, lda, _dense(a_scale, (M, kb), "a_scale", f32), pw, ldw,
-                                    _dense(w_scale, (-(-N // 128), kb), "w_scale", f32), po, ldo,
-                                    _dense(n_rows, (1,), "n_rows", torch.int32))
+    c = capi.pack_matmul_fp8(M, N, K, dt, pa, lda, _dense(a_scale, (M, kb), "a_scale", f32), pw, ldw,
+                             _dense(w_scale, (-(-N // 128), kb), "w_scale", f32), po, ldo,
+                             _dense(n_rows, (1,), "n_rows", torch.int32))
     _check("dspark_matmul_fp8", capi.dspark_matmul_fp8(c, ws.ptr, ws.nbytes, _stream(stream)))
     return out
 
 
-def _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows) -> capi.dspark_logit_rows:
+def _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows) -> tuple:
+    """The values of a dspark_logit_rows."""
     dt = _io_dtype(logits, "logits")
     p, ld, N, V = _rows(logits, "logits", logits.dtype)
     i32, f32 = torch.int32, torch.float32
@@ -380,8 +381,8 @@ def _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows) -> capi.
         pm, ldm, mask_rows, words = _rows(mask, "mask", i32)
         if mask_rows != N or words < -(-V // 32):
             raise ValueError("mask: expected [N, >= ceil(V / 32)] words")
-    return capi.dspark_logit_rows(N, V, dt, cols, n_req, p, ld, pt, pT, pm, ldm, _dense(mark_req, (N,), "mark_req", i32),
-                                  _dense(mark_pos, (N,), "mark_pos", i32), _dense(n_rows, (1,), "n_rows", i32))
+    return (N, V, dt, cols, n_req, p, ld, pt, pT, pm, ldm, _dense(mark_req, (N,), "mark_req", i32),
+            _dense(mark_pos, (N,), "mark_pos", i32), _dense(n_rows, (1,), "n_rows", i32))
 
 
 def token_logprobs_workspace(N: int, V: int, top: int, device="cuda", stream=None) -> Workspace:
@@ -401,15 +402,15 @@ def token_logprobs(ws: Workspace, logits, tokens, temp=None, top: int = 0, mask=
     Returns dict(logprob, entropy, rank, row_stat, top_id, top_logprob); an `out` may leave keys out (top_id and
     top_logprob only when top is 0)."""
     rows = _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows)
-    N = rows.N
+    N = rows[0]
     f32, i32 = torch.float32, torch.int32
     if out is None:
         new = lambda shape, dt: torch.empty(shape, dtype=dt, device=logits.device)  # noqa: E731
         out = dict(logprob=new(N, f32), entropy=new(N, f32), rank=new(N, i32), row_stat=new((N, 2), f32),
                    top_id=new((N, top), i32), top_logprob=new((N, top), f32))
     get = out.get
-    a = capi.dspark_token_logprobs_args(
-        rows, top, _dense(get("logprob"), (N,), "logprob", f32), _dense(get("entropy"), (N,), "entropy", f32),
+    a = capi.pack_token_logprobs(
+        *rows, top, _dense(get("logprob"), (N,), "logprob", f32), _dense(get("entropy"), (N,), "entropy", f32),
         _dense(get("rank"), (N,), "rank", i32), _dense(get("row_stat"), (N, 2), "row_stat", f32),
         _dense(get("top_id"), (N, top), "top_id", i32), _dense(get("top_logprob"), (N, top), "top_logprob", f32))
     _check("dspark_token_logprobs", capi.dspark_token_logprobs(a, ws.ptr, ws.nbytes, _stream(stream)))
@@ -422,7 +423,7 @@ def token_logprobs_grad(ws: Optional[Workspace], logits, tokens, row_stat, entro
     """dspark_token_logprobs_grad: the gradient by the logits of sum(g_logprob logprob) + sum(g_entropy entropy) +
     sum(g_top top_logprob), from token_logprobs's row_stat, entropy and top_id.  out may be logits itself."""
     rows = _logit_rows(logits, tokens, temp, mask, mark_req, mark_pos, n_rows)
-    N, V = rows.N, rows.V
+    N, V = rows[:2]
     f32 = torch.float32
     top = 0
     if g_top is not None:
@@ -438,11 +439,11 @@ def token_logprobs_grad(ws: Optional[Workspace], logits, tokens, row_stat, entro
     po, ldo, *got = _rows(out, "out", logits.dtype)
     if got != [N, V]:
         raise ValueError(f"out: expected shape {(N, V)}, got {tuple(out.shape)}")
-    a = capi.dspark_token_logprobs_grad_args(
-        rows, top, _dense(row_stat, (N, 2), "row_stat", f32),
-        _dense(entropy, (N,), "entropy", f32) if g_entropy is not None else None,
-        _dense(top_id, (N, top), "top_id", torch.int32) if top else None, _dense(g_logprob, (N,), "g_logprob", f32),
-        _dense(g_entropy, (N,), "g_entropy", f32), _dense(g_top, (N, top), "g_top", f32) if top else None, po, ldo)
+    a = capi.pack_token_logprobs_grad(
+        *rows, top, _dense(row_stat, (N, 2), "row_stat", f32),
+        _dense(entropy, (N,), "entropy", f32) if g_entropy is not None else 0,
+        _dense(top_id, (N, top), "top_id", torch.int32) if top else 0, _dense(g_logprob, (N,), "g_logprob", f32),
+        _dense(g_entropy, (N,), "g_entropy", f32), _dense(g_top, (N, top), "g_top", f32) if top else 0, po, ldo)
     _check("dspark_token_logprobs_grad",
            capi.dspark_token_logprobs_grad(a, ws.ptr if ws is not None else 0, _stream(stream)))
     return out
