@@ -8,7 +8,9 @@
 // Both kernels read a row once in 16-byte vectors (the gradient also writes it
 // once) and are bounded by memory as long as the arithmetic stays below some
 // ten instructions an element; hence packed fp32 pairs and the approximate
-// base-2 exponential (2 ulp), with fp32 sums.  A cluster of CTAs splits a row
+// base-2 exponential (2 ulp), with fp32 sums.  2048 x 151936 bf16: 101 us (0.91 of the
+// measured copy rate; issue slots 68 % busy), with 8 alternatives 112 us (0.82), the
+// gradient 198 us (0.92); one row with 20 alternatives 8.6 us, all latency.  A cluster of CTAs splits a row
 // when there are few rows; the parts meet in distributed shared memory in rank
 // order (no atomics on results: equal calls give equal bits).
 //
@@ -332,12 +334,12 @@ struct LpShared {
 };
 // The first K candidates of a CTA's part of the row, with next to no work in
 // the pass over it: every thread writes down the largest element of each group
-// of its vectors.  K elements reach the smallest of the w (full) warps' (K / w)-th largest
-// threads, so only groups that reach it hold candidates; they (some 2 K of up
-// to 4096) are read again.  (Offering elements to a running threshold in the
-// pass itself cost 49 us more than no alternatives at 2048 x 151936 bf16,
-// against 18 here.)
-constexpr int kGroups = 16;  // of a thread
+// of its vectors.  K elements reach the smallest of the w full warps' (K / w)-th
+// largest threads, so only groups that reach it hold candidates; they (some 2 K of
+// up to 8192) are read again.  Offering elements to a running threshold in the pass
+// itself cost 49 us more than no alternatives at 2048 x 151936 bf16; this costs 11
+// (with half as many groups 12: 48 MB were read again).
+constexpr int kGroupBytes = 64;  // of a thread's groups: their largest elements, in the logits' type
 template <int LT>
 struct TopShared {
   uint64_t list[32];   // descending, 0 past the last
@@ -345,14 +347,14 @@ struct TopShared {
   int n;               // candidates met (those past kCap were dropped)
   int picked;
   float jth[LT / 32];
-  float group[kGroups][LT];  // largest element
+  uint32_t group[kGroupBytes / 4 * LT];
 };
 // the place of the ring after the pass
 template <int LT>
 struct TopBuffer {
   static constexpr int kCap = LT * 8;  // one vector a thread always fits
   uint64_t key[kCap];           // candidates not yet in the list
-  uint16_t pick[kGroups * LT];  // groups to read again
+  uint16_t pick[kGroupBytes / 2 * LT];  // groups to read again
 };
 template <int LT>
 struct TopSearch {
@@ -547,13 +549,13 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
   }
   Sums<T> sum(c, has ? xt : INFINITY, has ? value_below<T>(xt) : INFINITY);
 
-  constexpr int kCap = TopBuffer<LT>::kCap;
+  constexpr int kCap = TopBuffer<LT>::kCap, kGroups = kGroupBytes / (int)sizeof(T);
   const TopSearch<LT> top{reinterpret_cast<TopShared<LT>*>(dyn + kTopStages * CB), reinterpret_cast<TopBuffer<LT>*>(dyn)};
   // a group: 2^gshift chunks of a thread
   int gshift = 0;
   while ((chunks + (1 << gshift) - 1) >> gshift > kGroups) ++gshift;
   float gmax = -INFINITY;
-  float* group = &top.s->group[0][tid];
+  T* group = reinterpret_cast<T*>(top.s->group) + tid;
   int left = 1 << gshift;
   int stage = 0;
   uint32_t parity = 0;
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
     if (kTop) {
       gmax = fmaxf(gmax, cm);
       if (--left == 0) {
-        *group = gmax;
+        *group = from_f32<T>(gmax);
         group += LT;
         gmax = -INFINITY;
         left = 1 << gshift;
@@ -627,7 +629,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
       ptx::mbar_wait_cycles(&full[ch % stages], (ch / stages) & 1, &never_s, kWaitLimit);
   __syncwarp();
   const int groups = (chunks + (1 << gshift) - 1) >> gshift;
-  if (kTop && left < 1 << gshift) *group = gmax;
+  if (kTop && left < 1 << gshift) *group = from_f32<T>(gmax);
   sum.flush();
   // the elements outside the vectors, one a thread
   const bool edge = rank == 0 && tid < shp.n_edge();
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
     kth = fmaxf(kth, lowest<T>());
     if (mine >= kth) {
       for (int g = 0; g < groups; ++g)
-        if (top.s->group[g][tid] >= kth) top.b->pick[atomicAdd(&top.s->picked, 1)] = (uint16_t)(g * LT + tid);
+        if (to_f32(reinterpret_cast<const T*>(top.s->group)[g * LT + tid]) >= kth) top.b->pick[atomicAdd(&top.s->picked, 1)] = (uint16_t)(g * LT + tid);
       if (edge_x >= kth) top.offer(order_key(edge_x, edge_v));
     }
     __syncthreads();
@@ -909,9 +911,9 @@ __global__ void __launch_bounds__(GT, 4) k_logprobs_grad(const dspark_token_logp
 
 // CTAs a row is split over: about as many as have a place at once, each with
 // `least` elements or more (8192, but 4096 where rows are very few: 1 x 100003 fp32 with
-// a mask 9.2 us, with 8192 10.2; 32 x 4264 with 20 alternatives 7.5 us, with 2048 10.1).  V = 151936 bf16, without alternatives: 16 rows 6.0 us
-// with 16 CTAs a row (8: 6.2), 32 rows 6.7 with 8 (16: 7.6), 64 rows 9.4 with 4 (8:
-// 10.8), 150 rows 14.4 with 2 (4: 17.9), 300 rows 21.9 with 1 (2: 22.9); 300 x 32000 with 8
+// a mask 9.2 us, with 8192 10.2; 32 x 4264 with 20 alternatives 7.5 us, with 2048
+// 10.1).  V = 151936 bf16, without alternatives: 16 rows 6.0 us with 16 CTAs a row (8:
+// 6.2), 32 rows 6.7 with 8 (16: 7.6), 64 rows 9.4 with 4 (8: 10.8), 150 rows 14.4 with 2 (4: 17.9), 300 rows 21.9 with 1 (2: 22.9); 300 x 32000 with 8
 // alternatives 11.3 with 1 (2: 15.3).  The gradient keeps fewer bytes on their way
 // to a CTA and wants more of them: 64 rows 10.2 with 8 (4: 10.7), 300 rows 34.0 with 2 (1: 38.9).
 int row_split(int64_t N, int64_t V, int64_t most, int64_t least) {
