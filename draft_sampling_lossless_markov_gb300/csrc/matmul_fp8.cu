@@ -719,14 +719,60 @@ cudaError_t run_wide(const dspark_matmul_fp8_args& a, const MmParams& p, const D
   return cudaGetLastError();
 }
 
+template <int NT>
+uint32_t narrow_smem(int split, int* stages) {
+  using C = Narrow<NT>;
+  // a deep ring where one CTA has an SM to itself for many blocks
+  *stages = split > 1 ? 4 : NT <= 16 ? 11 : NT <= 32 ? 9 : 8;
+  return *stages * C::kStage + (split > 1 ? C::kRed : 0) + 1024;
+}
+
+// Clusters of 2, 4 and 8 CTAs of the narrow kernel that the device runs at the
+// same time (a cluster stays inside a group of SMs, so fewer than the SMs allow):
+// looked up once per device.
+struct Fit {
+  int n[3];
+};
+template <int NT, typename TO>
+cudaError_t clusters_fit(Fit* out) {
+  constexpr int kMaxDev = 64;
+  static Fit cache[kMaxDev];
+  static bool have[kMaxDev] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorNotSupported;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!have[dev]) {
+    const void* f = (const void*)k_fp8_narrow<NT, TO>;
+    for (int i = 0; i < 3; ++i) {
+      int stages;
+      const unsigned split = 2u << i, smem = narrow_smem<NT>((int)split, &stages);
+      if (const cudaError_t e = ensure_smem_limit(f, (int)smem); e != cudaSuccess) return e;
+      cudaLaunchConfig_t c = {};
+      cudaLaunchAttribute at[1];
+      cluster_config(&c, at, split, split, Narrow<NT>::kThreads, smem, nullptr);
+      if (const cudaError_t e = cudaOccupancyMaxActiveClusters(&cache[dev].n[i], f, &c); e != cudaSuccess) return e;
+    }
+    have[dev] = true;
+  }
+  *out = cache[dev];
+  return cudaSuccess;
+}
+
 // CTAs of a cluster over K: up to one CTA an SM (a little more where two fit
-// one: 20 tiles of 2560 x 2560 take 5.7 us in clusters of 8 and 5.9 in clusters of 4,
-// 32 tiles of 1024 x 4096 4.6 us with 4 and 5.4 with 8), each with a block at least
-int narrow_split(int64_t tiles, int kb, int nt, int sms) {
+// one: 20 tiles of 2560 x 2560 take 5.0 us in clusters of 8 and 5.3 in clusters of 4,
+// 32 tiles of 1024 x 4096 4.6 us with 4 and 5.4 with 8), each with a block at least,
+// all clusters at once (16 tiles of 64 rows, K = 4096: 7.2 us in clusters of 4 and 10.7
+// in clusters of 8, of which 16 do not fit; with up to 16 rows the 20 tiles above
+// are over the device's count too, but start soon enough)
+int narrow_split(int64_t tiles, int kb, int nt, int sms, const Fit& fit) {
   const int most = nt <= 32 ? sms + sms / 16 : sms;
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= most && kb >= split * 2) split *= 2;
-  return split;
+  for (int i = 2; i >= 0; --i) {
+    const int split = 2 << i;
+    if (kb >= split && tiles * split <= most && (nt <= 16 || tiles <= fit.n[i])) return split;
+  }
+  return 1;
 }
 
 template <int NT, typename TO>
@@ -738,10 +784,11 @@ cudaError_t run_narrow(const dspark_matmul_fp8_args& a, const MmParams& p, const
     return cudaErrorInvalidValue;
   const int mt = (a.M + NT - 1) / NT;
   const int64_t tiles = (int64_t)mt * (((int64_t)a.N + 127) / 128);
-  const int split = narrow_split(tiles, p.kb, NT, d.sms);
-  // a deep ring where one CTA has an SM to itself for many blocks
-  const int stages = split > 1 ? 4 : NT <= 16 ? 11 : NT <= 32 ? 9 : 8;
-  const uint32_t smem = stages * C::kStage + (split > 1 ? C::kRed : 0) + 1024;
+  Fit fit;
+  if (const cudaError_t e = clusters_fit<NT, TO>(&fit); e != cudaSuccess) return e;
+  const int split = narrow_split(tiles, p.kb, NT, d.sms, fit);
+  int stages;
+  const uint32_t smem = narrow_smem<NT>(split, &stages);
   const void* f = (const void*)k_fp8_narrow<NT, TO>;
   if (const cudaError_t e = ensure_smem_limit(f, (int)smem); e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, d.sms));
@@ -757,10 +804,11 @@ cudaError_t run(const dspark_matmul_fp8_args& a, const MmParams& p, const Dev& d
   if (a.M <= 16) return run_narrow<16, TO>(a, p, d, s);
   if (a.M <= 32) return run_narrow<32, TO>(a, p, d, s);
   if (a.M <= 64) return run_narrow<64, TO>(a, p, d, s);
-  // few tiles and a long K: four CTAs or more a tile (128 x 4096 x 1024: 8.5 against
-  // 11.2 us, 128 x 7168 x 2048: 11.5 against 17.1; not 128 x 2560 x 2560, 10.4
-  // against 8.6, whose tiles leave room for two)
-  if (a.M <= 256 && p.kb >= 16 && ((a.M + 63) / 64) * (((int64_t)a.N + 127) / 128) * 4 <= d.sms)
+  // few tiles and a long K: four CTAs or more a tile, or two where K is very long
+  // (128 x 4096 x 1024: 7.2 against 10.1 us, 512 x 4096 x 512 7.6 against 10.1, 128 x 7168 x 4096
+  // 14.4 against 16.1; not 128 x 2560 x 2560, 8.2 against 7.5)
+  const int64_t few = ((a.M + 63) / 64) * (((int64_t)a.N + 127) / 128);
+  if (a.M <= 512 && ((p.kb >= 16 && few * 4 <= d.sms) || (p.kb >= 48 && few * 2 <= d.sms)))
     return run_narrow<64, TO>(a, p, d, s);
   // waves of pairs times a tile's columns; a column of a 128-column tile costs
   // 1.25 of a 256-column tile's (2048 x 4096 x 151936: 1.06 against 0.89 ms), which
