@@ -72,7 +72,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // ---------------------------------------------------------------------------
 // wide: 256 x (128 NH) tiles by CTA pairs
 // ---------------------------------------------------------------------------
-// Warps of a CTA: 8 NH epilogue warps (warpgroup g reads 64 columns of TMEM),
+// Warps of a CTA: 8 NH epilogue warps (a warpgroup reads EC = 64 columns of TMEM;
+// 16 of 32 columns for one part to fp32 rows that TMA cannot store, whose stores are
+// many: 333 x 2050 x 10007 22.9 against 25.5 us, but 512 x 4096 x 4096 12.9 against 12.3),
 // then one each for loads and scales and NH for the MMAs.
 //
 // A tile's columns are made as NH parts of 128, each with its own TMEM buffers:
@@ -81,10 +83,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // tensor cores busier than two of 256 columns.  Part h takes rows 64 h .. 64 h + 63
 // of each CTA's rows of w: its columns 0-63 are the first CTA's, 64-127 the
 // second's, so a warpgroup's 64 columns lie in one scale block.
-template <int NH>
+template <int NH, int EC>
 struct Wide {
   static constexpr int BN = 128 * NH;
-  static constexpr int kEpiWarps = 8 * NH;
+  static constexpr int kEpiWarps = 4 * BN / EC;
   static constexpr int kThreads = 32 * (kEpiWarps + 2 + NH);
   // registers of the epilogue warps and of the last warpgroup (NH = 2)
   static constexpr int kRegsHigh = 104, kRegsLow = 64;
@@ -99,11 +101,11 @@ struct Wide {
   static constexpr uint32_t kSmem = kStages * kStage + kStg + kSlots * kSlot + 1024;
 };
 
-template <int NH, typename TO>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 1)
+template <int NH, int EC, typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH, EC>::kThreads, 1)
     k_fp8_wide(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                const __grid_constant__ CUtensorMap tmO, const MmParams p) {
-  using W = Wide<NH>;
+  using W = Wide<NH, EC>;
   constexpr int NS = W::kStages, NB = W::kBufs, BN = W::BN, EW = W::kEpiWarps;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the same offset in both CTAs: the descriptors of a pair name one place for both
@@ -124,7 +126,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
     }
     for (int i = 0; i < NH * NB; ++i) {
       ptx::mbar_init(&tfull[i], 1);
-      ptx::mbar_init(&tempty[i], 2 * 8);
+      ptx::mbar_init(&tempty[i], 2 * EW / NH);
     }
     for (int i = 0; i < W::kSlots; ++i) {
       ptx::mbar_init(&sfull[i], 32);
@@ -279,19 +281,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
     }
   } else {
     constexpr int CH = 128 / (int)sizeof(TO);  // columns of a 128-byte staging row
-    const int g = warp >> 2, quarter = warp & 3, part = g >> 1, side = g & 1;
+    constexpr int per_part = 128 / EC, per_side = 64 / EC;
+    const int g = warp >> 2, quarter = warp & 3;
+    const int part = g / per_part, side = g % per_part / per_side, sub = g % per_side * EC;
     uint8_t* stg = stg_all + warp * 4096;
-    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * NB * 128 + side * 64);
+    const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * NB * 128 + side * 64 + sub);
     const uint32_t te = ptx::map_to_rank(&tempty[part * NB], 0);
     const float* sc = ring + side * 128 + quarter * 32 + lane;
     uint32_t q = 0, tph = 0, slot = 0, sph = 0;
     bool staged = false;
     for (int t = pair; t < tiles; t += pairs) {
       const int row0 = (t % mt) * 256 + (int)rank * 128 + quarter * 32;
-      const int col0 = (t / mt) * BN + side * (BN / 2) + part * 64;
-      uint64_t acc[32];
+      const int col0 = (t / mt) * BN + side * (BN / 2) + part * 64 + sub;
+      uint64_t acc[EC / 2];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[i] = 0;
+      for (int i = 0; i < EC / 2; ++i) acc[i] = 0;
       for (int b = 0; b < p.kb; ++b) {
         bool got = true;
         if ((b & 3) == 0) got = ptx::mbar_wait_cycles(&sfull[slot], sph, abort_flag, kWaitLimit);
@@ -305,9 +309,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
         float v[2][16];
         ptx::tmem_ld16(taddr + q * 128, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < EC / 16; ++c) {
           ptx::tmem_ld_wait16(v[c & 1]);
-          if (c < 3) {
+          if (c + 1 < EC / 16) {
             ptx::tmem_ld16(taddr + q * 128 + (c + 1) * 16, v[(c + 1) & 1]);
           } else {
             ptx::tc_fence_before();
@@ -325,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH>::kThreads, 
       }
       // 32 rows x 128 bytes at a time through this warp's swizzled staging buffer
 #pragma unroll
-      for (int c = 0; c < 64 / CH; ++c) {
+      for (int c = 0; c < EC / CH; ++c) {
         const int col = col0 + c * CH;
         if (col >= p.N || row0 >= M) break;
         if (staged) {
@@ -642,8 +646,8 @@ void cluster_config(cudaLaunchConfig_t* c, cudaLaunchAttribute* at, unsigned clu
 
 // pairs of the wide kernel that fit the device at once
 cudaError_t count_pairs(int sms, int* n) {
-  using W = Wide<2>;
-  const void* f = (const void*)k_fp8_wide<2, __nv_bfloat16>;
+  using W = Wide<2, 64>;
+  const void* f = (const void*)k_fp8_wide<2, 64, __nv_bfloat16>;
   if (const cudaError_t e = ensure_smem_limit(f, (int)W::kSmem); e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   cudaLaunchAttribute at[1];
@@ -656,8 +660,8 @@ cudaError_t count_pairs(int sms, int* n) {
 // The wide kernel's warps trade registers among themselves: what the epilogue
 // warps ask for has to be there, or they would wait for ever.
 cudaError_t check_registers() {
-  using W = Wide<2>;
-  const void* kernels[] = {(const void*)k_fp8_wide<2, __nv_bfloat16>, (const void*)k_fp8_wide<2, float>};
+  using W = Wide<2, 64>;  // the same for both types
+  const void* kernels[] = {(const void*)k_fp8_wide<2, 64, __nv_bfloat16>, (const void*)k_fp8_wide<2, 64, float>};
   for (const void* f : kernels) {
     cudaFuncAttributes at;
     if (const cudaError_t e = cudaFuncGetAttributes(&at, f); e != cudaSuccess) return e;
@@ -696,9 +700,9 @@ cudaError_t device(Dev* out) {
   return cudaSuccess;
 }
 
-template <int NH, typename TO>
+template <int NH, int EC, typename TO>
 cudaError_t run_wide(const dspark_matmul_fp8_args& a, const MmParams& p, const Dev& d, cudaStream_t s) {
-  using W = Wide<NH>;
+  using W = Wide<NH, EC>;
   CUtensorMap tmA, tmW, tmO = {};
   if (!tensor_map_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, a.K, a.M, a.lda, kKb, 128) ||
       !tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.K, a.N, a.ldw, kKb, W::BN / 2))
@@ -709,10 +713,10 @@ cudaError_t run_wide(const dspark_matmul_fp8_args& a, const MmParams& p, const D
     return cudaErrorInvalidValue;
   const int64_t tiles = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + W::BN - 1) / W::BN);
   if (tiles > INT32_MAX - d.pairs) return cudaErrorNotSupported;
-  const void* f = (const void*)k_fp8_wide<NH, TO>;
+  const void* f = (const void*)k_fp8_wide<NH, EC, TO>;
   if (const cudaError_t e = ensure_smem_limit(f, (int)W::kSmem); e != cudaSuccess) return e;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, d.pairs);
-  if (const cudaError_t e = launch_overlapped(k_fp8_wide<NH, TO>, grid, W::kThreads, W::kSmem, 1, s, tmA, tmW, tmO, p);
+  if (const cudaError_t e = launch_overlapped(k_fp8_wide<NH, EC, TO>, grid, W::kThreads, W::kSmem, 1, s, tmA, tmW, tmO, p);
       e != cudaSuccess)
     return e;
   count_launches(1);
@@ -816,7 +820,10 @@ cudaError_t run(const dspark_matmul_fp8_args& a, const MmParams& p, const Dev& d
   // 24.8 us)
   const int64_t mt = ((int64_t)a.M + 255) / 256;
   const auto cost = [&](int bn) { return (double)((mt * ((a.N + bn - 1) / bn) + d.pairs - 1) / d.pairs * bn); };
-  return 1.25 * cost(128) < cost(256) ? run_wide<1, TO>(a, p, d, s) : run_wide<2, TO>(a, p, d, s);
+  if (1.25 * cost(128) >= cost(256)) return run_wide<2, 64, TO>(a, p, d, s);
+  if constexpr (sizeof(TO) == 4)
+    if (!p.tma_out) return run_wide<1, 32, TO>(a, p, d, s);
+  return run_wide<1, 64, TO>(a, p, d, s);
 }
 
 }  // namespace
