@@ -407,24 +407,35 @@ struct Narrow {
   static constexpr int kBufs = 8;
   static constexpr uint32_t kTmemCols = NT * kBufs;
   static constexpr uint32_t kRed = NT * 128 * 4;  // a tile's sums, one float each
+  // Stages of the ring: a deep one where a CTA has an SM to itself for many
+  // blocks, four in a cluster.  Even, like kBufs: the two MMA warps take every
+  // other block, and a parity wait only holds for a warp that has seen the phase
+  // before end.  With 9 stages a warp met every other phase of a stage and could
+  // take a block that had not arrived.
+  static constexpr int kDeepStages = NT <= 16 ? 12 : NT <= 32 ? 10 : 8, kSplitStages = 4;
+  static_assert(kDeepStages % 2 == 0 && kSplitStages % 2 == 0 && kBufs % 2 == 0,
+                "a stage and a buffer belong to one MMA warp");
+  static constexpr uint32_t smem(bool split) {
+    return (split ? kSplitStages * kStage + kRed : kDeepStages * kStage) + 1024;
+  }
 };
 
 template <int NT, typename TO>
 __global__ void __launch_bounds__(Narrow<NT>::kThreads, 1)
     k_fp8_narrow(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW, const MmParams p,
-                 int split, int stages, int m_tiles) {
+                 int split, int m_tiles) {
   using C = Narrow<NT>;
   constexpr int NB = C::kBufs, EW = C::kEpiWarps, NC = C::kCols32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-  constexpr int kMaxStages = 12;
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[NB], tempty[NB];
+  __shared__ uint64_t full[C::kDeepStages], empty[C::kDeepStages], tfull[NB], tempty[NB];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s, never_s;
   volatile int* abort_flag = &abort_s;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp-uniform
   const int rank = split > 1 ? (int)ptx::cluster_rank() : 0;
   const int cl = blockIdx.x / split, cls = gridDim.x / split;
+  const int stages = split > 1 ? C::kSplitStages : C::kDeepStages;
   float* red = reinterpret_cast<float*>(sm + stages * C::kStage);
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
@@ -723,14 +734,6 @@ cudaError_t run_wide(const dspark_matmul_fp8_args& a, const MmParams& p, const D
   return cudaGetLastError();
 }
 
-template <int NT>
-uint32_t narrow_smem(int split, int* stages) {
-  using C = Narrow<NT>;
-  // a deep ring where one CTA has an SM to itself for many blocks
-  *stages = split > 1 ? 4 : NT <= 16 ? 11 : NT <= 32 ? 9 : 8;
-  return *stages * C::kStage + (split > 1 ? C::kRed : 0) + 1024;
-}
-
 // Clusters of 2, 4 and 8 CTAs of the narrow kernel that the device runs at the
 // same time (a cluster stays inside a group of SMs, so fewer than the SMs allow):
 // looked up once per device.
@@ -750,8 +753,7 @@ cudaError_t clusters_fit(Fit* out) {
   if (!have[dev]) {
     const void* f = (const void*)k_fp8_narrow<NT, TO>;
     for (int i = 0; i < 3; ++i) {
-      int stages;
-      const unsigned split = 2u << i, smem = narrow_smem<NT>((int)split, &stages);
+      const unsigned split = 2u << i, smem = Narrow<NT>::smem(true);
       if (const cudaError_t e = ensure_smem_limit(f, (int)smem); e != cudaSuccess) return e;
       cudaLaunchConfig_t c = {};
       cudaLaunchAttribute at[1];
@@ -791,13 +793,12 @@ cudaError_t run_narrow(const dspark_matmul_fp8_args& a, const MmParams& p, const
   Fit fit;
   if (const cudaError_t e = clusters_fit<NT, TO>(&fit); e != cudaSuccess) return e;
   const int split = narrow_split(tiles, p.kb, NT, d.sms, fit);
-  int stages;
-  const uint32_t smem = narrow_smem<NT>(split, &stages);
+  const uint32_t smem = C::smem(split > 1);
   const void* f = (const void*)k_fp8_narrow<NT, TO>;
   if (const cudaError_t e = ensure_smem_limit(f, (int)smem); e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, d.sms));
   const cudaError_t e =
-      launch_overlapped(k_fp8_narrow<NT, TO>, grid, C::kThreads, smem, (unsigned)split, s, tmA, tmW, p, split, stages, mt);
+      launch_overlapped(k_fp8_narrow<NT, TO>, grid, C::kThreads, smem, (unsigned)split, s, tmA, tmW, p, split, mt);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();

@@ -1,0 +1,85 @@
+"""matmul_fp8 where every CTA makes several tiles of an output: its rings, buffers and scales go on from tile to
+tile.  Codes are whole numbers of at most 8 and scales 1 or 2, so every sum is a whole number below 2^24 (64 * 4 * K,
+K <= 4096 here gives at most 2^20): fp32 results are exact, bf16 ones the nearest to the exact value."""
+import numpy as np
+import pytest
+import torch
+
+from draft_sampling_lossless_markov_gb300 import torch_api as T
+from gpu_common import check_no_error, require_gpu
+from oracle import vocab as O
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _operands(M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(M * 31 + N + K)
+    kb = -(-K // 128)
+
+    def whole(rows):
+        q = T.fp8_codes(rows, K)
+        q.copy_(torch.randint(-8, 9, (rows, K), generator=g, device="cuda").to(torch.float8_e4m3fn))
+        return q
+
+    def scales(rows):
+        return torch.randint(0, 2, (rows, kb), generator=g, device="cuda").float().exp2()
+
+    return whole(M), scales(M), whole(N), scales(-(-N // 128))
+
+
+def _want(a, sa, w, sw):
+    """In fp64 on the GPU; a sample of its columns against the oracle."""
+    block = torch.arange(a.shape[1], device="cuda") // 128
+    x = a.double() * sa.double()[:, block]
+    y = torch.empty((a.shape[0], w.shape[0]), dtype=torch.float64, device="cuda")
+    for n in range(0, w.shape[0], 8192):
+        rows = torch.arange(n, min(n + 8192, w.shape[0]), device="cuda")
+        y[:, n:n + 8192] = x @ (w[n:n + 8192].double() * sw.double()[rows // 128][:, block]).T
+    codes = lambda t: t.contiguous().view(torch.uint8).cpu().numpy()  # noqa: E731
+    for n in (0, w.shape[0] // 256 * 128, w.shape[0] - 1 - (w.shape[0] - 1) % 128):
+        part = w[n:n + 128]
+        ref, _ = O.matmul(codes(a), sa.double().cpu().numpy(), codes(part), sw[n // 128:n // 128 + 1].double().cpu().numpy())
+        np.testing.assert_array_equal(y[:, n:n + 128].cpu().numpy(), ref)
+    return y
+
+
+def _check(M, N, K, dtype, c0, ld, times=3):
+    """A column range from c0 on of rows ld apart; equal calls give equal bits while other work shares the GPU."""
+    a, sa, w, sw = _operands(M, N, K)
+    want = _want(a, sa, w, sw).to(dtype)
+    ws = T.matmul_fp8_workspace(M, N, K)
+    store = torch.empty((M, ld), dtype=dtype, device="cuda")
+    out = store[:, c0:c0 + N]
+    other, side = torch.empty(1 << 26, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(times):
+        store.fill_(-7)
+        if i:
+            with torch.cuda.stream(side):
+                other.add_(1)
+        T.matmul_fp8(ws, a, sa, w, sw, out=out)
+        assert torch.equal(out, want), (i, (out != want).nonzero()[:4].tolist())
+        assert bool((store[:, :c0] == -7).all()) and bool((store[:, c0 + N:] == -7).all())
+    torch.cuda.synchronize()
+    check_no_error(ws)
+
+
+def _sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("K", [100, 1030, 2560])
+@pytest.mark.parametrize("M", [1, 16, 17, 24, 32, 33, 64])
+def test_few_rows(M, K, dtype):
+    # 2 SMs + 5 tiles of 128 columns: two or three a CTA; rows of an odd length, of 16-byte multiples
+    tiles = 2 * _sms() + 5
+    _check(M, tiles * 128 - 3, K, dtype, 1, tiles * 128 + 1, times=12 if 16 < M <= 32 else 3)
+    _check(M, tiles * 128, K, dtype, 0, tiles * 128, times=1)
