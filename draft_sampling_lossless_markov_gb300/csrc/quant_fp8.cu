@@ -1,11 +1,12 @@
 // Quantisation to e4m3 codes with one fp32 scale for each block of 128 columns
 // (and of 1 or 128 rows):
-//     amax = max(|x|, 2^-100), scale = amax / 448, code = e4m3(x * (448 / amax)).
+//     amax = max(|x|, 2^-100), scale = amax / 448, code = e4m3(x * 448 / amax),
+// the code that of the exact quotient (inv_rest, code_between).
 // A block's elements stay in registers between the maximum and the conversion,
 // so x is read once: 3 (bf16) or 5 (fp32) bytes an element, bounded by memory
 // as long as the arithmetic stays below some 15 (25) instructions an element.
-// 151936 x 2560 in 128 x 128 blocks: 169 us from bf16 and 290 us from fp32 (1.0 and
-// 0.99 of the measured copy rate); in rows 230 us (0.75) and 303 us (0.95).
+// 151936 x 2560 in 128 x 128 blocks: 172 us from bf16 and 295 us from fp32 (1.0 and
+// 0.97 of the measured copy rate); in rows 240 us (0.72) and 309 us (0.93).
 //
 // The maximum is taken on the bits of |x| (as whole numbers they order like the
 // values, with infinities and NaN above all), so a block is known to be finite
@@ -114,13 +115,22 @@ __device__ __forceinline__ uint32_t finite_amax_bits(const Vec8<T>& v) {
   return a;
 }
 
-// four products to codes; the conversion saturates at 448, which only the
+// four quotients to codes; the conversion saturates at 448, which only the
 // rounding of amax * (448 / amax) can pass
-__device__ __forceinline__ uint32_t codes4(uint64_t x01, uint64_t x23, uint64_t f2) {
-  const float2 a = ptx::unpack2(ptx::mul2(x01, f2)), b = ptx::unpack2(ptx::mul2(x23, f2));
+__device__ __forceinline__ uint32_t codes4(uint64_t q01, uint64_t q23) {
+  const float2 a = ptx::unpack2(q01), b = ptx::unpack2(q23);
   return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
          ((uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16);
 }
+
+// What 448 / a leaves past inv = fp32(448 / a), good to 2^-31 of inv: inv + rest
+// gives a bf16 x its quotient in one more FMA.  x 448 and (middle of two codes) a
+// are whole numbers below 2^13 on a common scale, so x 448 / a is such a middle or at
+// least 2^-13 of it away: the sum x rest + x inv, rounded once, is the middle itself
+// where the quotient is, and on the quotient's side of it elsewhere.  The product
+// x inv alone misses a middle for one code in some thousands; the rest costs 2048 x
+// 4096 in rows 6.5 against 6.25 us, 151936 x 2560 240 against 233.
+__device__ __forceinline__ float inv_rest(float a, float inv) { return fmaf(-a, inv, 448.f) * (1.f / 448.f) * inv; }
 
 // Which of two neighbouring codes (down the one nearer 0) x * 448 / a rounds to:
 // the sign of |x| 448 - middle a, both products as exact sums of two floats.
@@ -134,10 +144,10 @@ __device__ __forceinline__ uint32_t code_between(float x, float a, uint32_t down
   return d > 0.f || (d == 0.f && !(up & 1u)) ? up : down;
 }
 
-// a: the block's amax, inv: 448 / a.  Non-finite elements become the NaN code.
+// a: the block's amax, inv: 448 / a, rest: inv_rest (bf16).  Non-finite elements become the NaN code.
 template <typename T>
 __device__ __forceinline__ void store_codes(uint8_t* row, int c0, int K, bool vec, const Vec8<T>& v, float a, float inv,
-                                            bool finite) {
+                                            float rest, bool finite) {
   float x[8];
   v.get(x);
   if (!finite) {
@@ -155,8 +165,8 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c0, int K, bool ve
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint64_t x01 = ptx::pack2(x[4 * h], x[4 * h + 1]), x23 = ptx::pack2(x[4 * h + 2], x[4 * h + 3]);
-      w[h] = codes4(x01, x23, up2);
-      other[h] = codes4(x01, x23, down2);
+      w[h] = codes4(ptx::mul2(x01, up2), ptx::mul2(x23, up2));
+      other[h] = codes4(ptx::mul2(x01, down2), ptx::mul2(x23, down2));
     }
     if ((w[0] ^ other[0]) | (w[1] ^ other[1])) {
 #pragma unroll
@@ -167,10 +177,12 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c0, int K, bool ve
       }
     }
   } else {
-    const uint64_t inv2 = ptx::pack2(inv, inv);
+    const uint64_t inv2 = ptx::pack2(inv, inv), rest2 = ptx::pack2(rest, rest);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      w[h] = codes4(ptx::pack2(x[4 * h], x[4 * h + 1]), ptx::pack2(x[4 * h + 2], x[4 * h + 3]), inv2);
+    for (int h = 0; h < 2; ++h) {
+      const uint64_t x01 = ptx::pack2(x[4 * h], x[4 * h + 1]), x23 = ptx::pack2(x[4 * h + 2], x[4 * h + 3]);
+      w[h] = codes4(ptx::fma2(x01, inv2, ptx::mul2(x01, rest2)), ptx::fma2(x23, inv2, ptx::mul2(x23, rest2)));
+    }
   }
   if (vec && c0 + 8 <= K) {
     *reinterpret_cast<uint2*>(row + c0) = make_uint2(w[0], w[1]);
@@ -227,13 +239,14 @@ __global__ void __launch_bounds__(QT, 4) k_quant_rows(const Source<T, kVec> src,
     if (l == u) mine = m;
   }
   const float a = fmaxf(__uint_as_float(mine), kAmaxMin);
-  const float inv = __fdiv_rn(448.f, a);
+  const float inv = __fdiv_rn(448.f, a), rest = inv_rest(a, inv);
   if (l < QU && first + l * G < blocks) scale[first + l * G] = __fdiv_rn(a, 448.f);
 #pragma unroll
   for (int u = 0; u < QU; ++u) {
     const float au = __shfl_sync(0xffffffffu, a, u, QL), iu = __shfl_sync(0xffffffffu, inv, u, QL);
+    const float ru = std::is_same<T, float>::value ? 0.f : __shfl_sync(0xffffffffu, rest, u, QL);
     if (first + u * G < blocks)
-      store_codes(codes + rows[u] * ldq, c0[u], K, vec, v[u], au, iu, !((non_finite >> u) & 1u));
+      store_codes(codes + rows[u] * ldq, c0[u], K, vec, v[u], au, iu, ru, !((non_finite >> u) & 1u));
   }
 }
 
@@ -281,11 +294,11 @@ __global__ void __launch_bounds__(block_threads<T>(), 1024 / block_threads<T>())
 #pragma unroll
     for (int i = 1; i < BT / 32; ++i) m = max(m, fin[i]);
   }
-  const float a = fmaxf(__uint_as_float(m), kAmaxMin), inv = __fdiv_rn(448.f, a);
+  const float a = fmaxf(__uint_as_float(m), kAmaxMin), inv = __fdiv_rn(448.f, a), rest = inv_rest(a, inv);
 #pragma unroll
   for (int i = 0; i < BR; ++i) {
     const int64_t r = r0 + i * (BT / QL);
-    if (r < M) store_codes(codes + r * ldq, c0, K, vec, v[i], a, inv, finite);
+    if (r < M) store_codes(codes + r * ldq, c0, K, vec, v[i], a, inv, rest, finite);
   }
   if (threadIdx.x == 0) scale[blockIdx.x] = __fdiv_rn(a, 448.f);
 }

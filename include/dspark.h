@@ -474,13 +474,10 @@ DSPARK_API dspark_status dspark_sts_fit(const dspark_sts_fit_args* args, void* w
  * elements, block_rows 1 (activations) or 128 (weights); blocks at the edges
  * are smaller.  Per block
  *     amax = max(|x|, 2^-100), scale = amax / 448,
- *     code = e4m3(x * (448 / amax)),
- * the scale rounded to fp32 and the code to nearest, ties to even: from fp32 x
- * that of the exact quotient, from bf16 x that of the fp32 product of x and the
- * fp32 quotient (a product within 2^-23 of the middle between two codes may go
- * either way).  A NaN or an infinity in a block
- * takes no part in amax and becomes the NaN code.  Bytes of a row past K are not
- * written. */
+ *     code = e4m3(x * 448 / amax),
+ * the scale rounded to fp32 and the exact quotient to the nearest code, ties to
+ * the even one.  A NaN or an infinity in a block takes no part in amax and
+ * becomes the NaN code.  Bytes of a row past K are not written. */
 typedef struct {
   int32_t M;
   int32_t K;
