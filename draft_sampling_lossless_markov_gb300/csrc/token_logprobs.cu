@@ -157,7 +157,9 @@ __device__ __forceinline__ void merge_lanes(Stat& st, int& count, float c) {
 
 // A thread's share of a row: sums of 2^t and t 2^t with t = x c - r about a
 // reference r of its own, the largest element, and the count of elements above
-// the token.  Sums are pairs of fp32.
+// the token.  Sums are pairs of fp32; U vectors are summed by themselves first
+// (a vector, where U is 1): added one by one to a running sum of 2^24 times their
+// size, small terms would all be lost (a peaked row of 151936: S 3e-5 too small).
 //
 // r is the rounded product of an element and c, so t needs one FMA and r's
 // rounding cancels where the sums are moved to the largest element (stat).  r
@@ -190,11 +192,19 @@ struct SumsBase {
     A2 = ptx::add2(A2, ptx::pack2(e * t, 0.f));
     largest = fmaxf(largest, x);
   }
-  // one element of a wild thread
-  __device__ __forceinline__ void again(float x) {
-    const float t = shifted(x, largest, c), e = ptx::ex2(t);
-    S2 = ptx::add2(S2, ptx::pack2(e, 0.f));
-    A2 = ptx::add2(A2, ptx::pack2(e * t, 0.f));
+  // elements of a wild thread, into sums of their own
+  template <int n>
+  __device__ __forceinline__ void again(const float (&x)[n], float& s, float& a) const {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float t = shifted(x[i], largest, c), e = ptx::ex2(t);
+      s += e;
+      a = fmaf(e, t, a);
+    }
+  }
+  __device__ __forceinline__ void join(float s, float a) {
+    S2 = ptx::add2(S2, ptx::pack2(s, 0.f));
+    A2 = ptx::add2(A2, ptx::pack2(a, 0.f));
   }
   // the sums about the largest element
   __device__ __forceinline__ Stat stat() {
@@ -217,6 +227,7 @@ struct Sums<float> : SumsBase {
     for (int u = 1; u < U; ++u) cm = fmaxf(cm, v[u].max());
     if (cm > limit) raise(cm);
     const uint64_t nr = ptx::pack2(-r, -r);
+    uint64_t s2 = 0, a2 = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float x[8];
@@ -227,12 +238,14 @@ struct Sums<float> : SumsBase {
         const float2 t = ptx::unpack2(ptx::fma2(ptx::pack2(x[e], x[e + 1]), c2, nr));
         const float t0 = ptx::max_nan(t.x, -200.f), t1 = ptx::max_nan(t.y, -200.f);
         const uint64_t e2 = ptx::pack2(ptx::ex2(t0), ptx::ex2(t1));
-        S2 = ptx::add2(S2, e2);
-        A2 = ptx::fma2(e2, ptx::pack2(t0, t1), A2);
+        s2 = ptx::add2(s2, e2);
+        a2 = ptx::fma2(e2, ptx::pack2(t0, t1), a2);
         n += x[e] > xr ? 1.f : 0.f;
         n += x[e + 1] > xr ? 1.f : 0.f;
       }
     }
+    S2 = ptx::add2(S2, s2);
+    A2 = ptx::add2(A2, a2);
     largest = fmaxf(largest, cm);
     return cm;
   }
@@ -276,6 +289,7 @@ struct Sums<__nv_bfloat16> : SumsBase {
     const float cm = fmaxf(bf_lo(cm2), bf_hi(cm2));
     if (cm > limit) raise(cm);
     const uint64_t nr = ptx::pack2(-r, -r);
+    uint64_t s2 = 0, a2 = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t w[4] = {v[u].a.x, v[u].a.y, v[u].a.z, v[u].a.w};
@@ -286,13 +300,15 @@ struct Sums<__nv_bfloat16> : SumsBase {
         const uint64_t t2 = ptx::fma2(ptx::pack2(bf_lo(x), bf_hi(x)), c2, nr);
         const float2 t = ptx::unpack2(t2);
         const uint64_t e2 = ptx::pack2(ptx::ex2(t.x), ptx::ex2(t.y));
-        S2 = ptx::add2(S2, e2);
-        A2 = ptx::fma2(e2, t2, A2);
+        s2 = ptx::add2(s2, e2);
+        a2 = ptx::fma2(e2, t2, a2);
       }
       // masks are -1 in a half; their plain sum keeps both counts (see flush)
       n2 += gt_bf16x2(w[0], xr) + gt_bf16x2(w[1], xr);
       n2 += gt_bf16x2(w[2], xr) + gt_bf16x2(w[3], xr);
     }
+    S2 = ptx::add2(S2, s2);
+    A2 = ptx::add2(A2, a2);
     largest = fmaxf(largest, cm);
     return cm;
   }
@@ -643,15 +659,23 @@ __global__ void __launch_bounds__(LT, 1024 / LT)
   // warp, CTA
   if (sum.wild) {
     sum.S2 = sum.A2 = 0;
-    for (int j = v0 + tid; j < v1; j += LT) {
-      Vec8<T> raw;
-      float x[8];
-      load(raw, j);
-      raw.get(x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum.again(x[e]);
+    for (int j0 = v0 + tid; j0 < v1; j0 += U * LT) {
+      float s = 0.f, a = 0.f;
+#pragma unroll 1
+      for (int j = j0; j < min(j0 + U * LT, v1); j += LT) {
+        Vec8<T> raw;
+        float x[8];
+        load(raw, j);
+        raw.get(x);
+        sum.again(x, s, a);
+      }
+      sum.join(s, a);
     }
-    if (edge) sum.again(edge_x);
+    if (edge) {
+      float s = 0.f, a = 0.f;
+      sum.again({edge_x}, s, a);
+      sum.join(s, a);
+    }
   }
   Stat st = sum.stat();
   float mine = sum.largest;
