@@ -130,8 +130,8 @@ dspark_status check_sched_args(const dspark_sched_args* a, int64_t max_keys) {
 
 using namespace dspark;
 
-// sizes whose tile counts and rounded-up lengths stay in 32 bits
-constexpr int32_t kMaxFp8Dim = 1 << 30;
+// sizes of the vocabulary calls whose tile counts and rounded-up lengths stay in 32 bits
+constexpr int32_t kMaxVocabDim = 1 << 30;
 
 // A launcher's result as a status; nothing it throws (a table that cannot grow)
 // leaves the C entry.
@@ -328,12 +328,13 @@ dspark_status dspark_quant_fp8(const dspark_quant_fp8_args* a, void* stream) {
   if (!a->x || !a->codes || !a->scale || !rows_ok(a->M, a->K, a->ldx) || !rows_ok(a->M, a->K, a->ldq))
     return DSPARK_INVALID_ARG;
   if (!aligned_to(a->x, elem_size(a->dtype)) || !aligned_to(a->scale, 4)) return DSPARK_INVALID_ARG;
-  if (a->M > kMaxFp8Dim || a->K > kMaxFp8Dim) return DSPARK_UNSUPPORTED;
+  if (a->M > kMaxVocabDim || a->K > kMaxVocabDim) return DSPARK_UNSUPPORTED;
   return launched([&] { return launch_quant_fp8(*a, (cudaStream_t)stream); });
 }
 
 dspark_status dspark_matmul_fp8_workspace_size(int32_t M, int32_t N, int32_t K, size_t* bytes) {
   if (!bytes || M < 0 || N < 0 || K < 1) return DSPARK_INVALID_ARG;
+  if (M > kMaxVocabDim || N > kMaxVocabDim || K > kMaxVocabDim) return DSPARK_UNSUPPORTED;
   *bytes = align_up(matmul_fp8_ws(M, N, K), 256);
   return DSPARK_OK;
 }
@@ -350,7 +351,7 @@ dspark_status dspark_matmul_fp8(const dspark_matmul_fp8_args* a, void* workspace
   if (!aligned_to(a->out, elem_size(a->out_dtype)) || !aligned_to(a->a_scale, 4) || !aligned_to(a->w_scale, 4))
     return DSPARK_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, matmul_fp8_ws(a->M, a->N, a->K))) return DSPARK_INVALID_ARG;
-  if (a->M > kMaxFp8Dim || a->N > kMaxFp8Dim || a->K > kMaxFp8Dim) return DSPARK_UNSUPPORTED;
+  if (a->M > kMaxVocabDim || a->N > kMaxVocabDim || a->K > kMaxVocabDim) return DSPARK_UNSUPPORTED;
   return launched([&] { return launch_matmul_fp8(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream); });
 }
 
@@ -363,12 +364,13 @@ static dspark_status check_logit_rows(const dspark_logit_rows& r) {
   if (r.mark_req && (r.n_req < 0 || r.tok_cols < 0)) return DSPARK_INVALID_ARG;
   if (r.mask && (!aligned_to(r.mask, 4) || !rows_ok(r.N, ((int64_t)r.V + 31) / 32, r.mask_ld)))
     return DSPARK_INVALID_ARG;
+  if (r.N > kMaxVocabDim) return DSPARK_UNSUPPORTED;
   return DSPARK_OK;
 }
 
 dspark_status dspark_token_logprobs_workspace_size(int32_t N, int32_t V, int32_t top, size_t* bytes) {
   if (!bytes || N < 0 || V < 1 || V > DSPARK_MAX_VOCAB || top < 0) return DSPARK_INVALID_ARG;
-  if (top > DSPARK_MAX_TOP) return DSPARK_UNSUPPORTED;
+  if (top > DSPARK_MAX_TOP || N > kMaxVocabDim) return DSPARK_UNSUPPORTED;
   *bytes = align_up(token_logprobs_ws(N, V, top), 256);
   return DSPARK_OK;
 }

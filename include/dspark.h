@@ -458,7 +458,8 @@ DSPARK_API dspark_status dspark_sts_fit(const dspark_sts_fit_args* args, void* w
  * pointers, caller's buffers and workspace, one stream, no allocation).
  * Matrices are row-major with a stride between rows, so a column range of a
  * wider buffer is a valid argument.  Sizes above 2^30 return
- * DSPARK_UNSUPPORTED.  As with dspark_schedule_noalloc, the first call of each
+ * DSPARK_UNSUPPORTED, from the workspace size calls too; a vocabulary above
+ * DSPARK_MAX_VOCAB in the row calls is DSPARK_INVALID_ARG.  As with dspark_schedule_noalloc, the first call of each
  * entry point in a context can load device code: make it before a stream
  * capture begins.
  * Their kernels may be set up while the kernel before them in the stream
