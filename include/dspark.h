@@ -459,9 +459,9 @@ DSPARK_API dspark_status dspark_sts_fit(const dspark_sts_fit_args* args, void* w
  * Matrices are row-major with a stride between rows, so a column range of a
  * wider buffer is a valid argument.  Sizes above 2^30 return
  * DSPARK_UNSUPPORTED, from the workspace size calls too; a vocabulary above
- * DSPARK_MAX_VOCAB in the row calls is DSPARK_INVALID_ARG.  As with dspark_schedule_noalloc, the first call of each
- * entry point in a context can load device code: make it before a stream
- * capture begins.
+ * DSPARK_MAX_VOCAB in the row calls is DSPARK_INVALID_ARG.  The first call of each
+ * entry point in a context, and the first of each form that it picks by sizes
+ * and types, can load device code; a stream capture may begin with it.
  * Their kernels may be set up while the kernel before them in the stream
  * drains (programmatic stream serialization), and wait for its end before they
  * touch memory.  A caller's kernel that is itself launched with that attribute
