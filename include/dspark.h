@@ -605,8 +605,8 @@ DSPARK_API dspark_status dspark_token_logprobs(const dspark_token_logprobs_args*
  * candidates.  Terms without a token, with top_id -1, or of a token that is no
  * candidate are left out.  row_stat [N, 2] and, with g_entropy, entropy [N], and,
  * with g_top, top_id [N, top] are dspark_token_logprobs's outputs for the same
- * rows; g_logprob [N], g_entropy [N], g_top [N, top] may each be NULL (no such
- * term).  top <= DSPARK_MAX_TOP.  grad [N, V] (rows.dtype, row stride ldg)
+ * rows; g_logprob [N] and g_entropy [N] may each be NULL (no such term), g_top
+ * [N, top] and top_id only with top = 0.  top <= DSPARK_MAX_TOP.  grad [N, V] (rows.dtype, row stride ldg)
  * may be the logits themselves (same address and stride), and must not overlap
  * them otherwise.  A row whose S is NaN gets NaN at its candidates.  The
  * workspace is that of dspark_token_logprobs (only the error word is used; may
