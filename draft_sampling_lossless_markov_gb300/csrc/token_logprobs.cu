@@ -260,7 +260,7 @@ template <>
 struct Sums<__nv_bfloat16> : SumsBase {
   // The clamp acts on pairs before they are widened: floor is a bf16 whose t is
   // at most -200, its term 0.
-  uint32_t floor2, limit2 = 0xFF80FF80u, hi2, lo2, n2 = 0;
+  uint32_t floor2, hi2, lo2, n2 = 0;
   float x_hi, x_lo;
   // the bf16 at or below a float, in both halves
   static __device__ __forceinline__ uint32_t down2(float f) {
@@ -278,7 +278,6 @@ struct Sums<__nv_bfloat16> : SumsBase {
   }
   __device__ __forceinline__ void raise(float x) {
     SumsBase::raise(x);
-    limit2 = down2(limit);
     floor2 = under2(x - 6.25f * gap);
   }
   template <int U, typename F>
