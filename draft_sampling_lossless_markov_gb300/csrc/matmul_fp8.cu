@@ -766,17 +766,23 @@ cudaError_t clusters_fit(Fit* out) {
   return cudaSuccess;
 }
 
-// CTAs of a cluster over K: up to one CTA an SM (a little more where two fit
-// one: 20 tiles of 2560 x 2560 take 5.0 us in clusters of 8 and 5.3 in clusters of 4,
-// 32 tiles of 1024 x 4096 4.6 us with 4 and 5.4 with 8), each with a block at least,
-// all clusters at once (16 tiles of 64 rows, K = 4096: 7.2 us in clusters of 4 and 10.7
-// in clusters of 8, of which 16 do not fit; with up to 16 rows the 20 tiles above
-// are over the device's count too, but start soon enough)
+// CTAs of a cluster over K.  One CTA an SM: the largest cluster with which all run
+// at the same time and each has a block at least (16 tiles of 64 rows, K = 4096: 7.2 us
+// in clusters of 4 and 10.7 in clusters of 8, of which 15 fit).  With up to 16 rows two
+// CTAs fit an SM (36 clusters of 8 and 74 of 4 ran at once, though the device's count is
+// that of the other forms); that pays up to some 1.6 CTAs an SM, with two blocks or more
+// a CTA.  Larger against next smaller cluster, over K = 1024 to 8192 and 1 to 16 rows:
+// 20 tiles, 8 against 4: 5.5 and 5.5 us at K = 2560, 7.9 and 9.0 at 8192; 30 tiles: 5.6 to
+// 6.3 and 5.8 to 6.3 at 2560, 8.9 and 10.0 at 8192 (but 5.1 and 4.8 at 1024, a block a CTA);
+// 48 tiles, 4 against 2: 4.7 to 5.3 and 5.0 to 5.7 at 1024, 12.6 and 15.5 at 8192; past it 36 tiles,
+// 8 against 4: 6.3 to 7.3 and 6.0 to 6.5 at 2560.  Clusters of 2 gain nothing there: 84
+// tiles 5.9 against 5.4 undivided at 1024, 8.8 to 9.6 against 8.9 to 9.3 at 2560.
 int narrow_split(int64_t tiles, int kb, int nt, int sms, const Fit& fit) {
-  const int most = nt <= 32 ? sms + sms / 16 : sms;
   for (int i = 2; i >= 0; --i) {
     const int split = 2 << i;
-    if (kb >= split && tiles * split <= most && (nt <= 16 || tiles <= fit.n[i])) return split;
+    const int64_t ctas = tiles * split;
+    if (nt <= 16 ? ctas <= sms || (split > 2 && 5 * ctas <= 8 * sms && kb >= 2 * split) : ctas <= sms && tiles <= fit.n[i])
+      if (kb >= split) return split;
   }
   return 1;
 }

@@ -83,3 +83,11 @@ def test_few_rows(M, K, dtype):
     tiles = 2 * _sms() + 5
     _check(M, tiles * 128 - 3, K, dtype, 1, tiles * 128 + 1, times=12 if 16 < M <= 32 else 3)
     _check(M, tiles * 128, K, dtype, 0, tiles * 128, times=1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,tiles,K", [(1, 24, 2560), (16, 30, 2049), (8, 31, 4096), (3, 60, 1024), (16, 50, 1300),
+                                       (16, 61, 1024), (1, 77, 2560), (30, 15, 2560), (30, 36, 1024), (30, 76, 700)])
+def test_clusters_over_k(M, tiles, K, dtype):
+    # around where the size of the clusters that share a tile's K changes
+    _check(M, tiles * 128 - 1, K, dtype, 1, tiles * 128 + 3)
