@@ -52,7 +52,10 @@ struct MmParams {
   void* out;
   int64_t ldo;
   const int32_t* n_rows;
-  int tma_out;  // the output's rows are 16-byte aligned: stores by TMA
+  // stores by TMA: 0 none (the output's rows are not 16-byte aligned), 1 those that
+  // end inside a row, 2 a row's last one too.  A tensor's store writes whole 16-byte
+  // pieces, so it would pass a row end that is no multiple of 16 bytes.
+  int tma_out;
   int a_vec;    // a_scale is 16-byte aligned
   WsHeader* hdr;
 };
@@ -351,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH, EC>::kThrea
           // 128B swizzle: 16-byte unit u of row r at u ^ (r % 8)
           *reinterpret_cast<uint4*>(stg + lane * 128 + ((u ^ (lane & 7)) << 4)) = v;
         }
-        if (p.tma_out && (row0 + 32 <= M || M == p.M)) {
+        if ((p.tma_out == 2 || (p.tma_out == 1 && col + CH <= p.N)) && (row0 + 32 <= M || M == p.M)) {
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -851,7 +854,8 @@ cudaError_t launch_matmul_fp8(const dspark_matmul_fp8_args& a, uint8_t* ws, cuda
   p.out = a.out;
   p.ldo = a.ldo;
   p.n_rows = a.n_rows;
-  p.tma_out = ((uintptr_t)a.out % 16) == 0 && (a.M == 1 || (a.ldo * esize) % 16 == 0);
+  if (((uintptr_t)a.out % 16) == 0 && (a.M == 1 || (a.ldo * esize) % 16 == 0))
+    p.tma_out = ((int64_t)a.N * esize) % 16 == 0 ? 2 : 1;
   p.a_vec = ((uintptr_t)a.a_scale % 16) == 0;
   p.hdr = reinterpret_cast<WsHeader*>(ws);
   return a.out_dtype == DSPARK_BF16 ? run<__nv_bfloat16>(a, p, d, s) : run<float>(a, p, d, s);
