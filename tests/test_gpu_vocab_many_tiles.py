@@ -91,3 +91,41 @@ def test_few_rows(M, K, dtype):
 def test_clusters_over_k(M, tiles, K, dtype):
     # around where the size of the clusters that share a tile's K changes
     _check(M, tiles * 128 - 1, K, dtype, 1, tiles * 128 + 3)
+
+
+def _pairs():
+    return _sms() // 2
+
+
+@pytest.mark.parametrize("K", [100, 384, 700, 2050])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,wide", [(600, True), (1025, True), (256, True), (300, False), (513, False)])
+def test_many_rows(M, wide, K, dtype):
+    # two tiles or more a CTA pair, of 256 columns (where tiles are many) and of 128 (some 2.1 a pair); the last ones ragged
+    row_tiles = -(-M // 256)
+    n256 = -(-(2 * _pairs() + 5) // row_tiles) if wide else 0
+    N = n256 * 256 + 129 if wide else -(-(2 * _pairs() + 3) // row_tiles) * 128 - 41
+    _check(M, N, K, dtype, 1, N + 2)  # rows that TMA cannot store
+    ld = -(-N // 16) * 16
+    _check(M, N, K, dtype, 0, ld, times=2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(2048, 12288, 512), (777, 30011, 1030)])
+def test_many_tiles_a_pair(M, N, K, dtype):
+    _check(M, N, K, dtype, 0, -(-N // 16) * 16, times=2)
+
+
+@pytest.mark.parametrize("M,count", [(64, 20), (64, 64), (32, 1), (600, 300), (600, 599), (2048, 60), (2048, 0)])
+def test_row_count_on_the_device(M, count):
+    K, N = 700, (2 * _sms() + 5) * 128 - 3
+    a, sa, w, sw = _operands(M, N, K)
+    want = _want(a[:max(count, 1)], sa[:max(count, 1)], w, sw)[:count]
+    ws = T.matmul_fp8_workspace(M, N, K)
+    n = torch.tensor([count], dtype=torch.int32, device="cuda")
+    for dtype, ld in ((BF16, N + 3), (F32, N + 2), (F32, N)):
+        store = torch.full((M, ld), -7.0, dtype=dtype, device="cuda")
+        T.matmul_fp8(ws, a, sa, w, sw, out=store[:, :N], n_rows=n)
+        assert torch.equal(store[:count, :N], want.to(dtype))
+        assert bool((store[count:] == -7).all()) and bool((store[:, N:] == -7).all())
+    check_no_error(ws)
