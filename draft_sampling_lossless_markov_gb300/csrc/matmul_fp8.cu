@@ -411,17 +411,28 @@ struct Narrow {
   static constexpr uint32_t kTmemCols = NT * kBufs;
   static constexpr uint32_t kRed = NT * 128 * 4;  // a tile's sums, one float each
   // Stages of the ring: a deep one where a CTA has an SM to itself for many
-  // blocks, four in a cluster.  Even, like kBufs: the two MMA warps take every
+  // blocks, fewer in a cluster.  Even, like kBufs: the two MMA warps take every
   // other block, and a parity wait only holds for a warp that has seen the phase
   // before end.  With 9 stages a warp met every other phase of a stage and could
   // take a block that had not arrived.
-  static constexpr int kDeepStages = NT <= 16 ? 12 : NT <= 32 ? 10 : 8, kSplitStages = 4;
+  static constexpr int kDeepStages = NT <= 16 ? 12 : NT <= 32 ? 10 : 8, kSplitStages = NT <= 32 ? 4 : 6;
   static_assert(kDeepStages % 2 == 0 && kSplitStages % 2 == 0 && kBufs % 2 == 0,
                 "a stage and a buffer belong to one MMA warp");
   static constexpr uint32_t smem(bool split) {
     return (split ? kSplitStages * kStage + kRed : kDeepStages * kStage) + 1024;
   }
 };
+
+// Two clusters on the same SMs (of two streams, say) must never want more TMEM than
+// there is: each could hold it on one SM and wait for the other's on the next, for
+// ever.  Up to 32 rows two CTAs want 256 or 512 columns of the 512 and three do not fit
+// an SM's shared memory; a CTA of 64 rows wants all of them and leaves no shared
+// memory for another CTA.
+constexpr uint32_t kSmShared = 228 * 1024;
+static_assert(2 * Narrow<32>::kTmemCols <= 512 && 3 * Narrow<16>::smem(true) > kSmShared &&
+                  Narrow<64>::smem(true) + Narrow<16>::smem(true) > kSmShared &&
+                  Narrow<16>::smem(true) <= Narrow<32>::smem(true),
+              "TMEM of the clusters that share an SM");
 
 template <int NT, typename TO>
 __global__ void __launch_bounds__(Narrow<NT>::kThreads, 1)
