@@ -13,16 +13,17 @@
 //                 256 x BN tile: each CTA stages its 128 rows of a and half of the
 //                 BN rows of w.  A row's scale is one number a lane, so the
 //                 promotion is one packed FMA for two elements.  2048 x 4096 x 151936
-//                 to bf16: 0.89 ms, 2.87 PFLOP/s at full clocks (1.12 ms where the
-//                 power cap holds them at 1.6 GHz); bounded by the round trip of a
-//                 TMEM buffer (MMA, commit, read-out, release) and then by power.
+//                 to bf16: 0.86 ms, 2.97 PFLOP/s, for a call in 20 ms (2070 MHz); back to
+//                 back 0.96 to 0.98 ms, where the power cap holds the clock at 1.55 GHz.
+//                 Bounded by the round trip of a TMEM buffer (MMA, commit, read-out,
+//                 release; the tensor pipe is busy 63 % of the time) and then by power.
 //   k_fp8_narrow  rows of w on the lanes, up to 64 rows of a on the columns: bounded
-//                 by reading w (1 row x 2560 x 151936: 62 us, 0.92 of measured HBM;
-//                 64 x 7168 x 129280 to fp32: 149 us, 0.95; its 1010 tiles
+//                 by reading w (1 row x 2560 x 151936: 62 to 64 us, 0.90 to 0.92 of
+//                 measured HBM; 64 x 7168 x 129280 to fp32: 148 us, 0.96; its 1010 tiles
 //                 are 6.6 waves).  A cluster of S CTAs
 //                 splits the blocks of K and adds its parts through distributed
 //                 shared memory in rank order (no atomics: equal calls give equal
-//                 bits): 8 x 2560 x 2560 5.5 us.
+//                 bits): 8 x 2560 x 2560 5.4 us.
 //
 // Every wait is bounded; one that gives up reports DSPARK_TIMEOUT.
 #include <cuda.h>
@@ -162,7 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide<NH, EC>::kThrea
   const int nblk = (p.N + kKb - 1) / kKb;
 
   // the epilogue warps' accumulators need more than an even share of the
-  // registers: with 96 each they spill (1.03 against 0.89 ms for 2048 x 4096 x 151936)
+  // registers: with 96 each they spill (2048 x 4096 x 151936 1.03 ms, when this was 0.89)
   if (NH == 2) {
     if (warp >= EW)
       ptx::reg_dec<W::kRegsLow>();
@@ -836,7 +837,7 @@ cudaError_t run(const dspark_matmul_fp8_args& a, const MmParams& p, const Dev& d
   if (a.M <= 512 && ((p.kb >= 16 && few * 4 <= d.sms) || (p.kb >= 48 && few * 2 <= d.sms)))
     return run_narrow<64, TO>(a, p, d, s);
   // waves of pairs times a tile's columns; a column of a 128-column tile costs
-  // 1.25 of a 256-column tile's (2048 x 4096 x 151936: 1.06 against 0.89 ms), which
+  // 1.25 of a 256-column tile's (2048 x 4096 x 151936: 1.06 ms, when this was 0.89), which
   // pays where the wider tiles leave pairs idle (512 x 4096 x 4096: 14.3 against
   // 24.8 us)
   const int64_t mt = ((int64_t)a.M + 255) / 256;
