@@ -123,13 +123,19 @@ __device__ __forceinline__ uint32_t codes4(uint64_t q01, uint64_t q23) {
          ((uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16);
 }
 
-// What 448 / a leaves past inv = fp32(448 / a), good to 2^-31 of inv: inv + rest
-// gives a bf16 x its quotient in one more FMA.  x 448 and (middle of two codes) a
-// are whole numbers below 2^13 on a common scale, so x 448 / a is such a middle or at
-// least 2^-13 of it away: the sum x rest + x inv, rounded once, is the middle itself
-// where the quotient is, and on the quotient's side of it elsewhere.  The product
-// x inv alone misses a middle for one code in some thousands; the rest costs 2048 x
-// 4096 in rows 6.5 against 6.25 us, 151936 x 2560 240 against 233.
+// fp32(448 / a); from bf16 the float below it, so that what is left (below) is positive
+template <typename T>
+__device__ __forceinline__ float inv_of(float a) {
+  const float inv = __fdiv_rn(448.f, a);
+  return std::is_same<T, float>::value ? inv : __uint_as_float(__float_as_uint(inv) - 1u);
+}
+// What 448 / a leaves past inv, good to 2^-31 of inv: inv + rest gives a bf16 x its
+// quotient in one more FMA (and, of one sign, keeps that of a zero).  x 448 and (middle
+// of two codes) a are whole numbers below 2^13 on a common scale, so x 448 / a is such a
+// middle or at least 2^-13 of it away: the sum x rest + x inv, rounded once, is the
+// middle itself where the quotient is, and on the quotient's side of it elsewhere.
+// fp32(448 / a) x alone misses a middle for one code in some thousands; the rest costs
+// 2048 x 4096 in rows 6.5 against 6.25 us, 151936 x 2560 240 against 233.
 __device__ __forceinline__ float inv_rest(float a, float inv) { return fmaf(-a, inv, 448.f) * (1.f / 448.f) * inv; }
 
 // Which of two neighbouring codes (down the one nearer 0) x * 448 / a rounds to:
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(QT, 4) k_quant_rows(const Source<T, kVec> src,
     if (l == u) mine = m;
   }
   const float a = fmaxf(__uint_as_float(mine), kAmaxMin);
-  const float inv = __fdiv_rn(448.f, a), rest = inv_rest(a, inv);
+  const float inv = inv_of<T>(a), rest = inv_rest(a, inv);
   if (l < QU && first + l * G < blocks) scale[first + l * G] = __fdiv_rn(a, 448.f);
 #pragma unroll
   for (int u = 0; u < QU; ++u) {
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(block_threads<T>(), 1024 / block_threads<T>())
 #pragma unroll
     for (int i = 1; i < BT / 32; ++i) m = max(m, fin[i]);
   }
-  const float a = fmaxf(__uint_as_float(m), kAmaxMin), inv = __fdiv_rn(448.f, a), rest = inv_rest(a, inv);
+  const float a = fmaxf(__uint_as_float(m), kAmaxMin), inv = inv_of<T>(a), rest = inv_rest(a, inv);
 #pragma unroll
   for (int i = 0; i < BR; ++i) {
     const int64_t r = r0 + i * (BT / QL);
