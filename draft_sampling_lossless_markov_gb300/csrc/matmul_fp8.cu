@@ -14,7 +14,7 @@
 //                 BN rows of w.  A row's scale is one number a lane, so the
 //                 promotion is one packed FMA for two elements.  2048 x 4096 x 151936
 //                 to bf16: 0.86 ms, 2.97 PFLOP/s, for a call in 20 ms (2070 MHz); back to
-//                 back 0.96 to 0.98 ms, where the power cap holds the clock at 1.55 GHz.
+//                 back 0.96 to 1.01 ms, where the power cap holds the clock at 1.55 GHz.
 //                 Bounded by the round trip of a TMEM buffer (MMA, commit, read-out,
 //                 release; the tensor pipe is busy 63 % of the time) and then by power.
 //   k_fp8_narrow  rows of w on the lanes, up to 64 rows of a on the columns: bounded
