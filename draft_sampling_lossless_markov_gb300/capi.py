@@ -23,6 +23,7 @@ DSPARK_BAD_INPUT = 5
 
 DSPARK_BF16 = 0
 DSPARK_F32 = 1
+DSPARK_E4M3 = 2
 
 DSPARK_RESIDUAL_INVERSE_CDF = 0
 DSPARK_RESIDUAL_REJECTION = 1
@@ -43,13 +44,15 @@ DSPARK_STS_MAX_SAMPLES = 8388607
 DSPARK_STS_MAX_TABLE = 16384
 DSPARK_FP8_BLOCK = 128
 DSPARK_MAX_TOP = 32
+DSPARK_MAX_TREE = 64
 
 EXPORTED = ("dspark_workspace_size", "dspark_workspace_init", "dspark_read_error", "dspark_draft_sample",
             "dspark_schedule", "dspark_verify", "dspark_status_string", "dspark_version", "dspark_launch_count",
             "dspark_last_cuda_error", "dspark_schedule_noalloc", "dspark_sts_fit_workspace_size", "dspark_sts_fit",
             "dspark_pack_rows", "dspark_draft_and_schedule", "dspark_quant_fp8", "dspark_matmul_fp8_workspace_size",
             "dspark_matmul_fp8", "dspark_token_logprobs_workspace_size", "dspark_token_logprobs",
-            "dspark_token_logprobs_grad")
+            "dspark_token_logprobs_grad", "dspark_cache_write", "dspark_cache_read", "dspark_cache_move",
+            "dspark_tree_attention_workspace_size", "dspark_tree_attention")
 
 
 class dspark_dims(ctypes.Structure):
@@ -121,11 +124,38 @@ class dspark_token_logprobs_grad_args(ctypes.Structure):
                 ("grad", c_void_p), ("ldg", c_int64)]
 
 
+class dspark_kv_cache(ctypes.Structure):
+    _fields_ = [("n_pages", c_int32), ("page_size", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+                ("dtype", c_int32), ("n_req", c_int32), ("max_pages", c_int32), ("k", c_void_p), ("v", c_void_p),
+                ("k_scale", c_void_p), ("v_scale", c_void_p), ("table", c_void_p), ("table_ld", c_int64)]
+
+
+class dspark_cache_write_args(ctypes.Structure):
+    _fields_ = [("cache", dspark_kv_cache), ("N", c_int32), ("dtype", c_int32), ("k", c_void_p), ("ldk", c_int64),
+                ("v", c_void_p), ("ldv", c_int64), ("mark_req", c_void_p), ("mark_pos", c_void_p), ("base", c_void_p),
+                ("n_rows", c_void_p)]
+
+
+class dspark_cache_read_args(ctypes.Structure):
+    _fields_ = list(dspark_cache_write_args._fields_)
+
+
+class dspark_cache_move_args(ctypes.Structure):
+    _fields_ = [("cache", dspark_kv_cache), ("path_cols", c_int32), ("base", c_void_p), ("path", c_void_p),
+                ("path_ld", c_int64), ("n_path", c_void_p)]
+
+
+class dspark_tree_attention_args(ctypes.Structure):
+    _fields_ = [("cache", dspark_kv_cache), ("N", c_int32), ("n_q_heads", c_int32), ("max_tree", c_int32),
+                ("scale", c_float), ("q", c_void_p), ("ldq", c_int64), ("out", c_void_p), ("ldo", c_int64),
+                ("offsets", c_void_p), ("base", c_void_p), ("tree", c_void_p)]
+
+
 def _packer(kind):
     """A function from a struct's values, in the order of its fields (a nested struct's in its place), to its bytes.
-    The vocabulary calls take these as well: a third of the time a ctypes struct takes."""
+    The vocabulary and cache calls take these as well: a third of the time a ctypes struct takes."""
     def form(k):
-        return "".join({c_int32: "i", c_int64: "q", c_void_p: "P"}.get(t) or form(t) for _, t in k._fields_)
+        return "".join({c_int32: "i", c_int64: "q", c_void_p: "P", c_float: "f"}.get(t) or form(t) for _, t in k._fields_)
     s = struct.Struct("@" + form(kind))
     assert s.size == ctypes.sizeof(kind), kind
     return s.pack
@@ -135,6 +165,9 @@ pack_quant_fp8 = _packer(dspark_quant_fp8_args)
 pack_matmul_fp8 = _packer(dspark_matmul_fp8_args)
 pack_token_logprobs = _packer(dspark_token_logprobs_args)
 pack_token_logprobs_grad = _packer(dspark_token_logprobs_grad_args)
+pack_cache_write = pack_cache_read = _packer(dspark_cache_write_args)
+pack_cache_move = _packer(dspark_cache_move_args)
+pack_tree_attention = _packer(dspark_tree_attention_args)
 
 
 _lib = None
@@ -167,11 +200,16 @@ def load() -> ctypes.CDLL:
     lib.dspark_token_logprobs_workspace_size.argtypes = [c_int32, c_int32, c_int32, POINTER(c_size_t)]
     lib.dspark_token_logprobs.argtypes = [c_void_p, c_void_p, c_size_t, c_void_p]
     lib.dspark_token_logprobs_grad.argtypes = [c_void_p, c_void_p, c_void_p]
+    for f in (lib.dspark_cache_write, lib.dspark_cache_read, lib.dspark_cache_move):
+        f.argtypes = [c_void_p, c_void_p, c_void_p]
+    lib.dspark_tree_attention_workspace_size.argtypes = [c_int32] * 5 + [POINTER(c_size_t)]
+    lib.dspark_tree_attention.argtypes = [c_void_p, c_void_p, c_size_t, c_void_p]
     for f in ("dspark_workspace_size", "dspark_workspace_init", "dspark_read_error", "dspark_draft_sample",
               "dspark_schedule", "dspark_verify", "dspark_schedule_noalloc", "dspark_sts_fit_workspace_size",
               "dspark_sts_fit", "dspark_pack_rows", "dspark_draft_and_schedule", "dspark_quant_fp8",
               "dspark_matmul_fp8_workspace_size", "dspark_matmul_fp8", "dspark_token_logprobs_workspace_size",
-              "dspark_token_logprobs", "dspark_token_logprobs_grad"):
+              "dspark_token_logprobs", "dspark_token_logprobs_grad", "dspark_cache_write", "dspark_cache_read",
+              "dspark_cache_move", "dspark_tree_attention_workspace_size", "dspark_tree_attention"):
         getattr(lib, f).restype = c_int32
     lib.dspark_status_string.argtypes = [c_int32]
     lib.dspark_status_string.restype = c_char_p
@@ -257,7 +295,7 @@ def dspark_pack_rows(args: dspark_pack_args, workspace: int, stream: int) -> int
 
 
 def _at(args):
-    """What a vocabulary call is given: a struct's packed bytes, or the struct."""
+    """What a vocabulary or cache call is given: a struct's packed bytes, or the struct."""
     return args if type(args) is bytes else ctypes.byref(args)
 
 
@@ -287,3 +325,26 @@ def dspark_token_logprobs(args, workspace: int, nbytes: int, stream: int) -> int
 
 def dspark_token_logprobs_grad(args, workspace: int, stream: int) -> int:
     return (_lib or load()).dspark_token_logprobs_grad(_at(args), workspace, stream)
+
+
+def dspark_cache_write(args, workspace: int, stream: int) -> int:
+    return (_lib or load()).dspark_cache_write(_at(args), workspace, stream)
+
+
+def dspark_cache_read(args, workspace: int, stream: int) -> int:
+    return (_lib or load()).dspark_cache_read(_at(args), workspace, stream)
+
+
+def dspark_cache_move(args, workspace: int, stream: int) -> int:
+    return (_lib or load()).dspark_cache_move(_at(args), workspace, stream)
+
+
+def dspark_tree_attention_workspace_size(n_req: int, max_tree: int, n_q_heads: int, n_kv_heads: int,
+                                         head_dim: int) -> tuple[int, int]:
+    n = c_size_t(0)
+    st = load().dspark_tree_attention_workspace_size(n_req, max_tree, n_q_heads, n_kv_heads, head_dim, ctypes.byref(n))
+    return st, n.value
+
+
+def dspark_tree_attention(args, workspace: int, nbytes: int, stream: int) -> int:
+    return (_lib or load()).dspark_tree_attention(_at(args), workspace, nbytes, stream)

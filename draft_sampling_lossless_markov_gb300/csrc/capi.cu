@@ -2,6 +2,7 @@
 // Every check happens before anything is enqueued; nothing here allocates.
 #include <algorithm>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -398,6 +399,103 @@ dspark_status dspark_token_logprobs_grad(const dspark_token_logprobs_grad_args* 
   if (a->grad == a->rows.logits && a->rows.N > 1 && a->ldg != a->rows.ld) return DSPARK_INVALID_ARG;
   if (workspace && ((uintptr_t)workspace & 255u)) return DSPARK_INVALID_ARG;
   return launched([&] { return launch_token_logprobs_grad(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream); });
+}
+
+// The cache's own checks.  kMaxVocabDim keeps rows of the pool and positions in 32 bits.
+static dspark_status check_cache(const dspark_kv_cache& c) {
+  if (c.n_pages < 1 || c.n_kv_heads < 1 || c.n_req < 0 || c.max_pages < 1) return DSPARK_INVALID_ARG;
+  if (c.page_size < 1 || (c.page_size & (c.page_size - 1))) return DSPARK_INVALID_ARG;
+  if (c.dtype != DSPARK_E4M3 && c.dtype != DSPARK_BF16) return DSPARK_INVALID_ARG;
+  if (c.head_dim < 1) return DSPARK_INVALID_ARG;
+  if (c.page_size < 16 || c.page_size > 1024 || (c.head_dim != 64 && c.head_dim != 128)) return DSPARK_UNSUPPORTED;
+  if (c.n_pages > kMaxVocabDim / c.page_size || c.n_kv_heads > kMaxVocabDim / c.page_size / c.n_pages ||
+      c.max_pages > kMaxVocabDim / c.page_size || c.n_req > kMaxVocabDim)
+    return DSPARK_UNSUPPORTED;
+  if (!c.k || !c.v || !aligned16(c.k) || !aligned16(c.v)) return DSPARK_INVALID_ARG;
+  if (c.dtype == DSPARK_E4M3 && (!c.k_scale || !c.v_scale || !aligned16(c.k_scale) || !aligned16(c.v_scale)))
+    return DSPARK_INVALID_ARG;
+  if (c.n_req > 0 && (!c.table || !aligned_to(c.table, 4) || !rows_ok(c.n_req, c.max_pages, c.table_ld)))
+    return DSPARK_INVALID_ARG;
+  return DSPARK_OK;
+}
+
+// rows of `cols` elements of `size` bytes for 16-byte accesses
+static bool vector_rows_ok(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size) {
+  return p && aligned16(p) && rows_ok(rows, cols, ld) && (rows <= 1 || (ld * size) % 16 == 0);
+}
+
+static dspark_status check_cache_rows(const dspark_kv_cache& c, int32_t N, int32_t dtype, const void* k, int64_t ldk,
+                                      const void* v, int64_t ldv, const int32_t* mark_req, const int32_t* mark_pos,
+                                      const void* ws) {
+  if (N < 0 || !dtype_ok(dtype)) return DSPARK_INVALID_ARG;
+  const dspark_status st = check_cache(c);
+  if (st != DSPARK_OK || N == 0) return st;
+  const int64_t cols = (int64_t)c.n_kv_heads * c.head_dim, size = (int64_t)elem_size(dtype);
+  if (!vector_rows_ok(k, N, cols, ldk, size) || !vector_rows_ok(v, N, cols, ldv, size)) return DSPARK_INVALID_ARG;
+  if (!mark_req || !mark_pos || (ws && ((uintptr_t)ws & 255u))) return DSPARK_INVALID_ARG;
+  if (N > kMaxVocabDim) return DSPARK_UNSUPPORTED;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_cache_write(const dspark_cache_write_args* a, void* workspace, void* stream) {
+  if (!a) return DSPARK_INVALID_ARG;
+  const dspark_status st =
+      check_cache_rows(a->cache, a->N, a->dtype, a->k, a->ldk, a->v, a->ldv, a->mark_req, a->mark_pos, workspace);
+  if (st != DSPARK_OK || a->N == 0) return st;
+  return launched([&] { return launch_cache_write(*a, static_cast<WsHeader*>(workspace), (cudaStream_t)stream); });
+}
+
+dspark_status dspark_cache_read(const dspark_cache_read_args* a, void* workspace, void* stream) {
+  if (!a) return DSPARK_INVALID_ARG;
+  const dspark_status st =
+      check_cache_rows(a->cache, a->N, a->dtype, a->k, a->ldk, a->v, a->ldv, a->mark_req, a->mark_pos, workspace);
+  if (st != DSPARK_OK || a->N == 0) return st;
+  return launched([&] { return launch_cache_read(*a, static_cast<WsHeader*>(workspace), (cudaStream_t)stream); });
+}
+
+dspark_status dspark_cache_move(const dspark_cache_move_args* a, void* workspace, void* stream) {
+  if (!a || a->path_cols < 1) return DSPARK_INVALID_ARG;
+  if (a->path_cols > DSPARK_MAX_TREE) return DSPARK_UNSUPPORTED;
+  const dspark_status st = check_cache(a->cache);
+  if (st != DSPARK_OK || a->cache.n_req == 0) return st;
+  if (!a->base || !a->path || !a->n_path || !rows_ok(a->cache.n_req, a->path_cols, a->path_ld)) return DSPARK_INVALID_ARG;
+  if (workspace && ((uintptr_t)workspace & 255u)) return DSPARK_INVALID_ARG;
+  return launched([&] { return launch_cache_move(*a, static_cast<WsHeader*>(workspace), (cudaStream_t)stream); });
+}
+
+static dspark_status check_tree_sizes(int32_t n_req, int32_t max_tree, int32_t n_q_heads, int32_t n_kv_heads,
+                                      int32_t head_dim) {
+  if (n_req < 0 || max_tree < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads || head_dim < 1)
+    return DSPARK_INVALID_ARG;
+  if (max_tree > DSPARK_MAX_TREE || n_q_heads > (1 << 16) || n_req > kMaxVocabDim || (head_dim != 64 && head_dim != 128))
+    return DSPARK_UNSUPPORTED;
+  return DSPARK_OK;
+}
+
+dspark_status dspark_tree_attention_workspace_size(int32_t n_req, int32_t max_tree, int32_t n_q_heads, int32_t n_kv_heads,
+                                                   int32_t head_dim, size_t* bytes) {
+  if (!bytes) return DSPARK_INVALID_ARG;
+  const dspark_status st = check_tree_sizes(n_req, max_tree, n_q_heads, n_kv_heads, head_dim);
+  if (st == DSPARK_OK) *bytes = align_up(tree_attention_ws(n_req, max_tree, n_q_heads, n_kv_heads, head_dim), 256);
+  return st;
+}
+
+dspark_status dspark_tree_attention(const dspark_tree_attention_args* a, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (!a || a->N < 0 || !isfinite(a->scale)) return DSPARK_INVALID_ARG;
+  const dspark_kv_cache& c = a->cache;
+  dspark_status st = check_cache(c);
+  if (st != DSPARK_OK) return st;
+  st = check_tree_sizes(c.n_req, a->max_tree, a->n_q_heads, c.n_kv_heads, c.head_dim);
+  if (st != DSPARK_OK || a->N == 0 || c.n_req == 0) return st;
+  const int64_t cols = (int64_t)a->n_q_heads * c.head_dim;
+  if (!vector_rows_ok(a->q, a->N, cols, a->ldq, 2) || !vector_rows_ok(a->out, a->N, cols, a->ldo, 2))
+    return DSPARK_INVALID_ARG;
+  if (!a->offsets || !a->base || (a->tree && !aligned_to(a->tree, 8))) return DSPARK_INVALID_ARG;
+  if (!ws_ok(workspace, workspace_bytes, tree_attention_ws(c.n_req, a->max_tree, a->n_q_heads, c.n_kv_heads, c.head_dim)))
+    return DSPARK_INVALID_ARG;
+  if (a->N > kMaxVocabDim) return DSPARK_UNSUPPORTED;
+  return launched([&] { return launch_tree_attention(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream); });
 }
 
 }  // extern "C"

@@ -134,6 +134,13 @@ size_t token_logprobs_ws(int N, int V, int top);
 cudaError_t launch_token_logprobs(const dspark_token_logprobs_args& a, uint8_t* ws, cudaStream_t s);
 cudaError_t launch_token_logprobs_grad(const dspark_token_logprobs_grad_args& a, uint8_t* ws, cudaStream_t s);
 
+// The key/value cache (kv_cache.cu) and the attention over it (tree_attention.cu).
+cudaError_t launch_cache_write(const dspark_cache_write_args& a, WsHeader* hdr, cudaStream_t s);
+cudaError_t launch_cache_read(const dspark_cache_read_args& a, WsHeader* hdr, cudaStream_t s);
+cudaError_t launch_cache_move(const dspark_cache_move_args& a, WsHeader* hdr, cudaStream_t s);
+size_t tree_attention_ws(int n_req, int max_tree, int n_q_heads, int n_kv_heads, int head_dim);
+cudaError_t launch_tree_attention(const dspark_tree_attention_args& a, uint8_t* ws, cudaStream_t s);
+
 // STS fitting (sts_fit.cu): its own workspace, after a WsHeader.
 struct StsLayout {
   size_t hp = 0;         // [gamma * n_bins * n_grid] u64 fixed-point prediction sums

@@ -1,0 +1,360 @@
+// The paged key/value cache: rows written to it as e4m3 codes with one fp32 scale
+// for each row and head (or bf16), read back, and moved within it.
+//
+// All three are bounded by memory: a bf16 row and head of 128 is 256 bytes read and
+// 132 written.  A vector of 8 elements is one lane's (16 bytes of bf16), so a row and
+// head is D / 8 lanes, its maximum three or four shuffles, and a warp's accesses run
+// over neighbouring heads of one row.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv_pool.cuh"
+#include "launch.h"
+#include "quant_codes.cuh"
+#include "tc_ptx.cuh"
+#include "vec8.cuh"
+
+namespace dspark {
+
+namespace {
+
+constexpr int KT = 256;  // threads
+constexpr int KU = 4;    // rows and heads a group of lanes has on their way at a time
+
+struct CacheRows {
+  KvPool pool;
+  const int32_t* mark_req;
+  const int32_t* mark_pos;
+  const int32_t* base;
+  const int32_t* n_rows;
+  int32_t N, per;  // rows, rows a CTA
+  int64_t ldk, ldv;
+  WsHeader* hdr;
+};
+
+__device__ __forceinline__ int32_t count_rows(const CacheRows& c) {
+  return c.n_rows ? max(0, min(c.N, *c.n_rows)) : c.N;
+}
+
+// the pool's row of row i, -1 to skip it
+__device__ __forceinline__ int32_t place_of(const CacheRows& c, int32_t i) {
+  const int32_t req = c.mark_req[i];
+  if (req == -1) return -1;
+  int32_t row = -1;
+  if (req >= 0 && req < c.pool.n_req) row = pool_row(c.pool, req, (int64_t)(c.base ? c.base[req] : 0) + c.mark_pos[i]);
+  if (row < 0 && c.hdr) report_error(c.hdr, DSPARK_BAD_INPUT, i);
+  return row;
+}
+
+// Units of a CTA's rows: row, then k or v, then head.
+struct Unit {
+  int32_t row, head;  // row within the CTA
+  bool v;
+};
+__device__ __forceinline__ Unit unit_at(int u, int heads) {
+  Unit x;
+  x.row = u / (2 * heads);
+  const int rest = u - x.row * 2 * heads;
+  x.v = rest >= heads;
+  x.head = x.v ? rest - heads : rest;
+  return x;
+}
+
+template <int D, typename T, bool kCodes>
+__global__ void __launch_bounds__(KT) k_cache_write(const CacheRows c, const T* k, const T* v) {
+  ptx::launch_dependents();
+  ptx::grid_wait();
+  constexpr int LV = D / 8, G = KT / LV;  // lanes of a unit, groups of them
+  __shared__ int32_t place[KT];
+  const int32_t n = count_rows(c), row0 = blockIdx.x * c.per;
+  if (row0 >= n) return;
+  const int rows = min(c.per, n - row0), units = rows * 2 * c.pool.heads;
+  if (threadIdx.x < rows) place[threadIdx.x] = place_of(c, row0 + threadIdx.x);
+  const int g = threadIdx.x / LV, l = threadIdx.x % LV;
+  for (int u0 = 0; u0 < units; u0 += G * KU) {
+    Vec8<T> x[KU];
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      const int u = u0 + i * G + g;
+      if (u < units) {
+        const Unit at = unit_at(u, c.pool.heads);
+        x[i].load((at.v ? v + (int64_t)(row0 + at.row) * c.ldv : k + (int64_t)(row0 + at.row) * c.ldk) + at.head * D + l * 8);
+      } else {
+        const uint32_t zero[8] = {};
+        x[i].set(zero);
+      }
+    }
+    if (u0 == 0) __syncthreads();  // the places
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      const int u = u0 + i * G + g;
+      const Unit at = unit_at(min(u, units - 1), c.pool.heads);
+      const int32_t p = place[at.row];
+      const bool live = u < units && p >= 0;
+      const int64_t row = (int64_t)p + ((int64_t)at.head << c.pool.shift);
+      if constexpr (kCodes) {
+        uint32_t m = amax_bits(x[i]);
+#pragma unroll
+        for (int o = LV / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const bool finite = m < kInfBits;
+        if (__any_sync(0xffffffffu, !finite)) {
+          uint32_t f = finite_amax_bits(x[i]);
+#pragma unroll
+          for (int o = LV / 2; o > 0; o >>= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, o));
+          if (!finite) m = f;
+        }
+        const float a = fmaxf(__uint_as_float(m), kAmaxMin), inv = inv_of<T>(a);
+        const uint2 q = codes8(x[i], a, inv, inv_rest(a, inv), finite);
+        if (live) {
+          *reinterpret_cast<uint2*>((at.v ? c.pool.v : c.pool.k) + row * D + l * 8) = q;
+          if (l == 0) (at.v ? c.pool.v_scale : c.pool.k_scale)[row] = __fdiv_rn(a, 448.f);
+        }
+      } else if (live) {
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(at.v ? c.pool.v : c.pool.k) + row * D + l * 8;
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<uint4*>(dst) = x[i].a;
+        } else {
+          float f[8];
+          x[i].get(f);
+          Vec8<__nv_bfloat16>::store(dst, f, true);
+        }
+      }
+    }
+  }
+}
+
+template <int D, typename T, bool kCodes>
+__global__ void __launch_bounds__(KT) k_cache_read(const CacheRows c, T* k, T* v) {
+  ptx::launch_dependents();
+  ptx::grid_wait();
+  constexpr int LV = D / 8, G = KT / LV;
+  __shared__ int32_t place[KT];
+  const int32_t n = count_rows(c), row0 = blockIdx.x * c.per;
+  if (row0 >= n) return;
+  const int rows = min(c.per, n - row0), units = rows * 2 * c.pool.heads;
+  if (threadIdx.x < rows) place[threadIdx.x] = place_of(c, row0 + threadIdx.x);
+  __syncthreads();
+  const int g = threadIdx.x / LV, l = threadIdx.x % LV;
+  for (int u0 = 0; u0 < units; u0 += G * KU) {
+    uint4 x[KU];
+    float scale[KU];
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      const int u = u0 + i * G + g;
+      if (u >= units) continue;
+      const Unit at = unit_at(u, c.pool.heads);
+      const int32_t p = place[at.row];
+      if (p < 0) continue;
+      const int64_t row = (int64_t)p + ((int64_t)at.head << c.pool.shift);
+      const uint8_t* pool = at.v ? c.pool.v : c.pool.k;
+      if constexpr (kCodes) {
+        const uint2 q = *reinterpret_cast<const uint2*>(pool + row * D + l * 8);
+        x[i].x = q.x, x[i].y = q.y;
+        scale[i] = (at.v ? c.pool.v_scale : c.pool.k_scale)[row];
+      } else {
+        x[i] = *reinterpret_cast<const uint4*>(pool + (row * D + l * 8) * 2);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      const int u = u0 + i * G + g;
+      if (u >= units) continue;
+      const Unit at = unit_at(u, c.pool.heads);
+      if (place[at.row] < 0) continue;
+      T* dst = (at.v ? v + (int64_t)(row0 + at.row) * c.ldv : k + (int64_t)(row0 + at.row) * c.ldk) + at.head * D + l * 8;
+      float f[8];
+      if constexpr (kCodes) {
+        const uint32_t w[2] = {x[i].x, x[i].y};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3)));
+          f[2 * j] = y.x * scale[i];
+          f[2 * j + 1] = y.y * scale[i];
+        }
+      } else {
+        Vec8<__nv_bfloat16> y;
+        y.a = x[i];
+        y.get(f);
+      }
+      if constexpr (sizeof(T) == 2) {
+        Vec8<__nv_bfloat16>::store(dst, f, true);
+      } else {  // rows begin on 16 bytes, not on 32
+        __stcs(reinterpret_cast<float4*>(dst), make_float4(f[0], f[1], f[2], f[3]));
+        __stcs(reinterpret_cast<float4*>(dst) + 1, make_float4(f[4], f[5], f[6], f[7]));
+      }
+    }
+  }
+}
+
+// A CTA holds whole units (request, k or v of a head): all of a unit's rows are in
+// registers before the first is written, so a path may read what it writes.
+constexpr int MV = 4;  // 16-byte vectors a thread
+struct MoveArgs {
+  KvPool pool;
+  const int32_t* base;
+  const int32_t* path;
+  int64_t path_ld;
+  const int32_t* n_path;
+  int32_t cols, units;  // path columns, units a CTA
+  WsHeader* hdr;
+};
+
+template <int kRowBytes>
+__global__ void __launch_bounds__(KT) k_cache_move(const MoveArgs m) {
+  ptx::launch_dependents();
+  ptx::grid_wait();
+  constexpr int VR = kRowBytes / 16;  // vectors a row
+  const KvPool& pool = m.pool;
+  __shared__ int32_t from[KT], to[KT];  // of (request of the CTA, node of its path)
+  const int per_req = 2 * pool.heads;
+  const int64_t all = (int64_t)pool.n_req * per_req, u0 = (int64_t)blockIdx.x * m.units;
+  const int units = (int)min((int64_t)m.units, all - u0);
+  const int32_t req0 = (int32_t)(u0 / per_req);
+  const int first = (int)(u0 - (int64_t)req0 * per_req);  // of the CTA's units in request req0
+  const int entries = ((first + units - 1) / per_req + 1) * m.cols;
+  if (threadIdx.x < entries) {
+    const int32_t r = req0 + threadIdx.x / m.cols, i = threadIdx.x % m.cols;
+    int32_t a = -1, b = -1;
+    const int32_t n = m.n_path[r], base = m.base[r];
+    bool bad = n < 0 || n > m.cols || base < 0;
+    if (!bad && i < n) {
+      const int32_t node = m.path[r * m.path_ld + i];
+      bad = node < 0 || node >= DSPARK_MAX_TREE;
+      if (!bad) {
+        a = pool_row(pool, r, (int64_t)base + node);
+        b = pool_row(pool, r, (int64_t)base + i);
+        bad = a < 0 || b < 0;
+        if (bad) a = -1;
+      }
+    }
+    if (bad && m.hdr) report_error(m.hdr, DSPARK_BAD_INPUT, r);
+    from[threadIdx.x] = a == b ? -1 : a;  // a node that stays
+    to[threadIdx.x] = b;
+  }
+  __syncthreads();
+  const int vecs = units * m.cols * VR;
+  const auto entry = [&](int x, int* unit) {  // of vector or scale x of the CTA's rows
+    *unit = x / m.cols;
+    return (first + *unit) / per_req * m.cols + x % m.cols;
+  };
+  uint4 x[MV];
+#pragma unroll
+  for (int i = 0; i < MV; ++i) {
+    const int at = threadIdx.x + i * KT;
+    if (at >= vecs) continue;
+    int unit;
+    const int e = entry(at / VR, &unit);
+    if (from[e] < 0) continue;
+    const int rest = (first + unit) % per_req, head = rest % pool.heads;
+    x[i] = *reinterpret_cast<const uint4*>((rest < pool.heads ? pool.k : pool.v) +
+                                           ((int64_t)from[e] + ((int64_t)head << pool.shift)) * kRowBytes + at % VR * 16);
+  }
+  float scale = 0.f;
+  int64_t scale_to = -1;
+  float* scales = nullptr;
+  if (pool.k_scale && threadIdx.x < units * m.cols) {
+    int unit;
+    const int e = entry(threadIdx.x, &unit);
+    if (from[e] >= 0) {
+      const int rest = (first + unit) % per_req, head = rest % pool.heads;
+      scales = rest < pool.heads ? pool.k_scale : pool.v_scale;
+      scale = scales[(int64_t)from[e] + ((int64_t)head << pool.shift)];
+      scale_to = (int64_t)to[e] + ((int64_t)head << pool.shift);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MV; ++i) {
+    const int at = threadIdx.x + i * KT;
+    if (at >= vecs) continue;
+    int unit;
+    const int e = entry(at / VR, &unit);
+    if (from[e] < 0) continue;
+    const int rest = (first + unit) % per_req, head = rest % pool.heads;
+    *reinterpret_cast<uint4*>((rest < pool.heads ? pool.k : pool.v) +
+                              ((int64_t)to[e] + ((int64_t)head << pool.shift)) * kRowBytes + at % VR * 16) = x[i];
+  }
+  if (scale_to >= 0) scales[scale_to] = scale;
+}
+
+// rows a CTA: as many as give every group of lanes KU units, one at least
+int rows_per_cta(int heads, int D) { return std::max(1, std::min(KT, KT / (D / 8) * KU / (2 * heads))); }
+
+template <typename A>
+CacheRows cache_rows(const A& a, WsHeader* hdr) {
+  CacheRows c;
+  c.pool = kv_pool(a.cache);
+  c.mark_req = a.mark_req;
+  c.mark_pos = a.mark_pos;
+  c.base = a.base;
+  c.n_rows = a.n_rows;
+  c.N = a.N;
+  c.per = rows_per_cta(c.pool.heads, a.cache.head_dim);
+  c.ldk = a.ldk;
+  c.ldv = a.ldv;
+  c.hdr = hdr;
+  return c;
+}
+
+template <int D, typename T>
+cudaError_t write_t(const dspark_cache_write_args& a, WsHeader* hdr, cudaStream_t s) {
+  const CacheRows c = cache_rows(a, hdr);
+  const unsigned grid = (unsigned)((a.N + c.per - 1) / c.per);
+  const T *k = static_cast<const T*>(a.k), *v = static_cast<const T*>(a.v);
+  return launch_overlapped(a.cache.dtype == DSPARK_E4M3 ? k_cache_write<D, T, true> : k_cache_write<D, T, false>, grid, KT, 0,
+                           1, s, c, k, v);
+}
+template <int D, typename T>
+cudaError_t read_t(const dspark_cache_read_args& a, WsHeader* hdr, cudaStream_t s) {
+  const CacheRows c = cache_rows(a, hdr);
+  const unsigned grid = (unsigned)((a.N + c.per - 1) / c.per);
+  T *k = static_cast<T*>(a.k), *v = static_cast<T*>(a.v);
+  return launch_overlapped(a.cache.dtype == DSPARK_E4M3 ? k_cache_read<D, T, true> : k_cache_read<D, T, false>, grid, KT, 0, 1,
+                           s, c, k, v);
+}
+
+cudaError_t counted(cudaError_t e) {
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const dspark_cache_write_args& a, WsHeader* hdr, cudaStream_t s) {
+  const bool bf = a.dtype == DSPARK_BF16;
+  if (a.cache.head_dim == 64)
+    return counted(bf ? write_t<64, __nv_bfloat16>(a, hdr, s) : write_t<64, float>(a, hdr, s));
+  return counted(bf ? write_t<128, __nv_bfloat16>(a, hdr, s) : write_t<128, float>(a, hdr, s));
+}
+
+cudaError_t launch_cache_read(const dspark_cache_read_args& a, WsHeader* hdr, cudaStream_t s) {
+  const bool bf = a.dtype == DSPARK_BF16;
+  if (a.cache.head_dim == 64)
+    return counted(bf ? read_t<64, __nv_bfloat16>(a, hdr, s) : read_t<64, float>(a, hdr, s));
+  return counted(bf ? read_t<128, __nv_bfloat16>(a, hdr, s) : read_t<128, float>(a, hdr, s));
+}
+
+cudaError_t launch_cache_move(const dspark_cache_move_args& a, WsHeader* hdr, cudaStream_t s) {
+  MoveArgs m;
+  m.pool = kv_pool(a.cache);
+  m.base = a.base;
+  m.path = a.path;
+  m.path_ld = a.path_ld;
+  m.n_path = a.n_path;
+  m.cols = a.path_cols;
+  m.hdr = hdr;
+  const int row = a.cache.head_dim * (a.cache.dtype == DSPARK_E4M3 ? 1 : 2);
+  // units whose vectors fill the CTA's registers, and whose requests' paths its threads
+  m.units = std::max(1, KT * MV / (a.path_cols * (row / 16)));
+  while (m.units > 1 && ((m.units + 2 * m.pool.heads - 2) / (2 * m.pool.heads) + 1) * m.cols > KT) --m.units;
+  const int64_t grid = ((int64_t)m.pool.n_req * 2 * m.pool.heads + m.units - 1) / m.units;
+  if (grid > INT32_MAX) return cudaErrorNotSupported;
+  return counted(launch_overlapped(row == 64 ? k_cache_move<64> : row == 128 ? k_cache_move<128> : k_cache_move<256>,
+                                   (unsigned)grid, KT, 0, 1, s, m));
+}
+
+}  // namespace dspark

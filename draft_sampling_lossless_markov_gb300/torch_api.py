@@ -447,3 +447,138 @@ def token_logprobs_grad(ws: Optional[Workspace], logits, tokens, row_stat, entro
     _check("dspark_token_logprobs_grad",
            capi.dspark_token_logprobs_grad(a, ws.ptr if ws is not None else 0, _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# The key/value cache and the attention of a step's drafted rows
+# ---------------------------------------------------------------------------
+class KvCache:
+    """dspark_kv_cache: k and v [n_pages, n_kv_heads, page_size, head_dim] (e4m3 with k_scale and v_scale [n_pages,
+    n_kv_heads, page_size] f32, or bf16 without), table [n_req, max_pages] i32 (dense rows).  The tensors are checked
+    here, once; the calls write into them."""
+
+    def __init__(self, k, v, table, k_scale=None, v_scale=None):
+        if k.dim() != 4:
+            raise ValueError("k must be [n_pages, n_kv_heads, page_size, head_dim]")
+        shape = tuple(k.shape)
+        if k.dtype is _FP8:
+            dt = capi.DSPARK_E4M3
+            if k_scale is None or v_scale is None:
+                raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        elif k.dtype is torch.bfloat16:
+            dt = capi.DSPARK_BF16
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("a bf16 cache has no scales")
+        else:
+            raise TypeError(f"k: expected float8_e4m3fn or bfloat16, got {k.dtype}")
+        pt, ldt, n_req, max_pages = _rows(table, "table", torch.int32)
+        n_pages, heads, page, dim = shape
+        f32 = torch.float32
+        self.k, self.v, self.k_scale, self.v_scale, self.table = k, v, k_scale, v_scale, table
+        self.n_kv_heads, self.head_dim, self.n_req = heads, dim, n_req
+        self.fields = (n_pages, page, heads, dim, dt, n_req, max_pages, _dense(k, shape, "k", k.dtype),
+                       _dense(v, shape, "v", k.dtype), _dense(k_scale, shape[:3], "k_scale", f32),
+                       _dense(v_scale, shape[:3], "v_scale", f32), pt, ldt)
+
+    @classmethod
+    def create(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, table, dtype=_FP8) -> "KvCache":
+        """A cache of zeros."""
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        new = [torch.zeros(shape, dtype=torch.uint8 if dtype is _FP8 else dtype, device=table.device) for _ in range(2)]
+        if dtype is not _FP8:
+            return cls(*new, table)
+        scales = [torch.zeros(shape[:3], dtype=torch.float32, device=table.device) for _ in range(2)]
+        return cls(*(t.view(_FP8) for t in new), table, *scales)
+
+
+def _heads(t: torch.Tensor, what: str, dtype) -> tuple:
+    """(address, row stride in elements, rows, heads, head size) of a 3-D CUDA tensor whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError("dspark tensors must live on a CUDA device")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what} must be a 3-D tensor with dense rows")
+    (rows, heads, dim), (ld, per_head, step) = shape, t.stride()
+    if (step != 1 and dim > 1) or (per_head != dim and heads > 1):
+        raise ValueError(f"{what} must be a 3-D tensor with dense rows")
+    return t.data_ptr(), ld if rows > 1 else max(ld, heads * dim), rows, heads, dim
+
+
+def _cache_rows(cache: KvCache, k, v, mark_req, mark_pos, base, n_rows) -> tuple:
+    """The values of a cache write or read."""
+    dt = _io_dtype(k, "k")
+    pk, ldk, N, *got = _heads(k, "k", k.dtype)
+    if got != [cache.n_kv_heads, cache.head_dim]:
+        raise ValueError(f"k: expected [N, {cache.n_kv_heads}, {cache.head_dim}], got {tuple(k.shape)}")
+    pv, ldv, *got = _heads(v, "v", k.dtype)
+    if v.shape != k.shape:
+        raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    i32 = torch.int32
+    return (*cache.fields, N, dt, pk, ldk, pv, ldv, _dense(mark_req, (N,), "mark_req", i32),
+            _dense(mark_pos, (N,), "mark_pos", i32), _dense(base, (cache.n_req,), "base", i32),
+            _dense(n_rows, (1,), "n_rows", i32))
+
+
+def cache_write(cache: KvCache, k, v, mark_req, mark_pos, base=None, n_rows=None, ws: Optional[Workspace] = None,
+                stream=None) -> None:
+    """dspark_cache_write: rows k, v [N, n_kv_heads, head_dim] (bf16 or f32, dense rows) go to request mark_req[i],
+    position base[mark_req[i]] + mark_pos[i]; mark_req -1 skips a row; ws takes the errors, if given."""
+    a = capi.pack_cache_write(*_cache_rows(cache, k, v, mark_req, mark_pos, base, n_rows))
+    _check("dspark_cache_write", capi.dspark_cache_write(a, ws.ptr if ws is not None else 0, _stream(stream)))
+
+
+def cache_read(cache: KvCache, mark_req, mark_pos, base=None, n_rows=None, out: Optional[tuple] = None,
+               dtype=torch.bfloat16, ws: Optional[Workspace] = None, stream=None) -> tuple:
+    """dspark_cache_read: (k, v) [N, n_kv_heads, head_dim] of such places, in `dtype` or the type of `out`."""
+    if out is None:
+        shape = (mark_req.numel(), cache.n_kv_heads, cache.head_dim)
+        out = tuple(torch.empty(shape, dtype=dtype, device=cache.k.device) for _ in range(2))
+    a = capi.pack_cache_read(*_cache_rows(cache, out[0], out[1], mark_req, mark_pos, base, n_rows))
+    _check("dspark_cache_read", capi.dspark_cache_read(a, ws.ptr if ws is not None else 0, _stream(stream)))
+    return out
+
+
+def cache_move(cache: KvCache, base, path, n_path, ws: Optional[Workspace] = None, stream=None) -> None:
+    """dspark_cache_move: position base[r] + i takes what base[r] + path[r, i] held, for i < n_path[r]; path [n_req,
+    path_cols] i32 (dense rows), base and n_path [n_req] i32."""
+    i32 = torch.int32
+    pp, ldp, rows, cols = _rows(path, "path", i32)
+    if rows != cache.n_req:
+        raise ValueError(f"path: expected {cache.n_req} rows, got {rows}")
+    a = capi.pack_cache_move(*cache.fields, cols, _dense(base, (rows,), "base", i32), pp, ldp,
+                             _dense(n_path, (rows,), "n_path", i32))
+    _check("dspark_cache_move", capi.dspark_cache_move(a, ws.ptr if ws is not None else 0, _stream(stream)))
+
+
+def tree_attention_workspace(n_req: int, max_tree: int, n_q_heads: int, n_kv_heads: int, head_dim: int, device="cuda",
+                             stream=None) -> Workspace:
+    """Workspace of dspark_tree_attention for up to these sizes."""
+    st, n = capi.dspark_tree_attention_workspace_size(int(n_req), int(max_tree), int(n_q_heads), int(n_kv_heads),
+                                                      int(head_dim))
+    _check("dspark_tree_attention_workspace_size", st)
+    ws = Workspace(torch.empty(max(n, 256), dtype=torch.uint8, device=device))
+    _check("dspark_workspace_init", capi.dspark_workspace_init(ws.ptr, ws.nbytes, _stream(stream)))
+    return ws
+
+
+def tree_attention(ws: Workspace, cache: KvCache, q, offsets, base, max_tree: int, tree=None, scale: Optional[float] = None,
+                   out=None, stream=None):
+    """dspark_tree_attention: rows offsets[r] .. offsets[r + 1] - 1 of q [N, n_q_heads, head_dim] (bf16, dense rows), at
+    most max_tree of them, attend to request r's first base[r] cached positions and to the drafted rows behind them that
+    tree [N] i64 (bit t: the request's row t) shows, all up to themselves without a tree.  scale: head_dim ** -0.5."""
+    bf16, i32 = torch.bfloat16, torch.int32
+    pq, ldq, N, heads, dim = _heads(q, "q", bf16)
+    if dim != cache.head_dim:
+        raise ValueError(f"q: expected head size {cache.head_dim}, got {dim}")
+    if out is None:
+        out = torch.empty((N, heads, dim), dtype=bf16, device=q.device)
+    po, ldo, *got = _heads(out, "out", bf16)
+    if got != [N, heads, dim]:
+        raise ValueError(f"out: expected shape {(N, heads, dim)}, got {tuple(out.shape)}")
+    a = capi.pack_tree_attention(*cache.fields, N, heads, max_tree, dim ** -0.5 if scale is None else scale, pq, ldq, po, ldo,
+                                 _dense(offsets, (cache.n_req + 1,), "offsets", i32),
+                                 _dense(base, (cache.n_req,), "base", i32), _dense(tree, (N,), "tree", torch.int64))
+    _check("dspark_tree_attention", capi.dspark_tree_attention(a, ws.ptr, ws.nbytes, _stream(stream)))
+    return out

@@ -63,7 +63,7 @@ typedef enum {
   DSPARK_BAD_INPUT = 5      /* a kernel met an out-of-range token id (error word) */
 } dspark_status;
 
-typedef enum { DSPARK_BF16 = 0, DSPARK_F32 = 1 } dspark_dtype;
+typedef enum { DSPARK_BF16 = 0, DSPARK_F32 = 1, DSPARK_E4M3 = 2 /* a cache's codes only */ } dspark_dtype;
 
 typedef enum {
   DSPARK_SCHED_OFF = 0,        /* verify every draft token: l_r = gamma            */
@@ -626,6 +626,168 @@ typedef struct {
 
 DSPARK_API dspark_status dspark_token_logprobs_grad(const dspark_token_logprobs_grad_args* args, void* workspace,
                                                     void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The key/value cache and the attention of a step's drafted rows
+ * ---------------------------------------------------------------------------
+ * Between the rows to verify (dspark_schedule) and their hidden rows stands the
+ * target's attention over what was decoded before.  The drafted rows' keys and
+ * values are written to the cache first (dspark_cache_write) and attended there
+ * (dspark_tree_attention), so every row sees the very codes that decoding one
+ * token at a time would show it; of the drafted rows the accepted ones stay,
+ * those of a chain where they are, those of a tree moved behind the context
+ * (dspark_cache_move); the others are written over by the next step.  The pages
+ * have no counterpart to these calls; their conventions are those of the
+ * vocabulary calls above (strided rows, programmatic stream serialization, first
+ * calls under capture).
+ *
+ * A cache is a pool of n_pages pages of page_size tokens:
+ *     k, v              [n_pages, n_kv_heads, page_size, head_dim] dtype, dense
+ *     k_scale, v_scale  [n_pages, n_kv_heads, page_size] f32 (DSPARK_E4M3)
+ * DSPARK_E4M3: a row of head_dim codes stands for code * scale; DSPARK_BF16:
+ * the values themselves, the scales NULL.  Position p of request r is slot
+ * p % page_size of page table[r * table_ld + p / page_size].  Entries of pages
+ * past a request's tokens are not looked at.  Requests may share pages that are
+ * only read.  page_size is a power of two, 16 to 1024; head_dim 64 or 128; k, v
+ * and the scales are 16-byte aligned.  n_pages * n_kv_heads * page_size and
+ * max_pages * page_size up to 2^30, else DSPARK_UNSUPPORTED. */
+#define DSPARK_MAX_TREE 64 /* drafted rows of a request */
+
+typedef struct {
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;     /* DSPARK_E4M3 or DSPARK_BF16 */
+  int32_t n_req;     /* rows of the table */
+  int32_t max_pages; /* columns of the table, >= 1 */
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  int64_t table_ld; /* >= max_pages */
+} dspark_kv_cache;
+
+/* dspark_cache_write: row i of k and v [N, n_kv_heads, head_dim] (dtype
+ * DSPARK_BF16 or DSPARK_F32, row strides ldk, ldv elements, heads dense) goes to
+ * request mark_req[i], position base[mark_req[i]] + mark_pos[i] (base [n_req];
+ * NULL: 0).  DSPARK_E4M3 as dspark_quant_fp8 with one block of head_dim columns:
+ *     amax = max(|x|, 2^-100), scale = amax / 448, code = e4m3(x * 448 / amax),
+ * the exact quotient to the nearest code, ties to the even one; a NaN or an
+ * infinity takes no part in amax and becomes the NaN code.  DSPARK_BF16: x
+ * rounded to bf16.  Rows with mark_req -1, and rows from min(N, *n_rows) on
+ * (n_rows on the device; NULL: N) are skipped.  A mark_req outside [-1, n_req), a
+ * position outside [0, max_pages * page_size) or a page outside [0, n_pages) skips
+ * the row and is reported in the workspace error word (DSPARK_BAD_INPUT, detail =
+ * row).  Two rows of one call must not go to one place (its contents would be
+ * either's codes and either's scale).  k, v 16-byte aligned, ldk and ldv multiples
+ * of 16 bytes and >= n_kv_heads * head_dim; they must not overlap the cache.  The
+ * workspace is any initialised dspark workspace, for the error word only, or NULL
+ * (nothing reported). */
+typedef struct {
+  dspark_kv_cache cache;
+  int32_t N;
+  int32_t dtype;
+  const void* k;
+  int64_t ldk;
+  const void* v;
+  int64_t ldv;
+  const int32_t* mark_req;
+  const int32_t* mark_pos;
+  const int32_t* base;
+  const int32_t* n_rows;
+} dspark_cache_write_args;
+
+DSPARK_API dspark_status dspark_cache_write(const dspark_cache_write_args* args, void* workspace, void* stream);
+
+/* dspark_cache_read: the values of such places back: k and v [N, n_kv_heads,
+ * head_dim] (dtype, row strides ldk, ldv) take code * scale, rounded to fp32 and
+ * from there to dtype (or the bf16 value).  Rows, markers, alignments, errors and
+ * workspace as for dspark_cache_write; skipped rows are left as they were.  The
+ * same place may be read by several rows.  k and v must overlap neither each
+ * other nor the cache. */
+typedef struct {
+  dspark_kv_cache cache;
+  int32_t N;
+  int32_t dtype;
+  void* k;
+  int64_t ldk;
+  void* v;
+  int64_t ldv;
+  const int32_t* mark_req;
+  const int32_t* mark_pos;
+  const int32_t* base;
+  const int32_t* n_rows;
+} dspark_cache_read_args;
+
+DSPARK_API dspark_status dspark_cache_read(const dspark_cache_read_args* args, void* workspace, void* stream);
+
+/* dspark_cache_move: keeps a path of each request's drafted rows: for every
+ * i < n_path[r], position base[r] + i of request r takes what position base[r] +
+ * path[r, i] held when the call began (path [n_req, path_cols], row stride path_ld,
+ * path_cols 1..DSPARK_MAX_TREE; nodes 0..DSPARK_MAX_TREE - 1 in any order, one may
+ * come twice).  Codes and scales are copied as they are.  n_path[r] outside [0,
+ * path_cols], a node, a position or a page out of range leaves out the whole
+ * request (n_path, a position base < 0) or that node, and is reported
+ * (DSPARK_BAD_INPUT, detail = request).  A page that a call writes must not be
+ * shared by two requests.  base and n_path [n_req].  Workspace as for
+ * dspark_cache_write. */
+typedef struct {
+  dspark_kv_cache cache;
+  int32_t path_cols;
+  const int32_t* base;
+  const int32_t* path;
+  int64_t path_ld;
+  const int32_t* n_path;
+} dspark_cache_move_args;
+
+DSPARK_API dspark_status dspark_cache_move(const dspark_cache_move_args* args, void* workspace, void* stream);
+
+/* dspark_tree_attention: rows offsets[r] .. offsets[r + 1] - 1 of q and out [N,
+ * n_q_heads, head_dim] (bf16, row strides ldq, ldo elements, heads dense) are the
+ * drafted rows of request r, which the cache holds at positions base[r],
+ * base[r] + 1, ... (offsets [n_req + 1] ascending, as dspark_schedule writes them;
+ * base [n_req]: the tokens before).  With j = i - offsets[r], row i sees
+ *     position t < base[r], and
+ *     position base[r] + t for every set bit t of tree[i] (tree [N] u64; bits from
+ *     the request's row count on are ignored); tree = NULL: t <= j, a chain.
+ * A row of a tree usually has its own bit and its ancestors'.  Per query head h,
+ * over what row i sees of kv head h / (n_q_heads / n_kv_heads):
+ *     out[i, h] = sum_t p_t v_t,  p = softmax_t(scale * q[i, h] . k_t),
+ * rounded once to bf16.  A row that sees nothing gets 0.  What a row does not see
+ * never reaches it, NaN and infinities included; a NaN or infinite score makes its
+ * row of that head NaN.  Scores and sums are fp32 (q enters them exactly, or to
+ * 2^-18 of its row's largest element where smaller); a weight p enters the sum over
+ * v to 2^-8 of it.  Rows from offsets[n_req] on are left as they were.  A request with
+ * offsets or base out of range (0 <= offsets[r] <= offsets[r + 1] <= N, at most
+ * max_tree rows, 0 <= base, base + rows <= max_pages * page_size) is skipped; the
+ * tokens of a page outside [0, n_pages) are not seen by any row; both are reported
+ * (DSPARK_BAD_INPUT, detail = request).  n_q_heads is a multiple of n_kv_heads;
+ * max_tree is 1..DSPARK_MAX_TREE; scale finite.  q, out 16-byte aligned, ldq and ldo
+ * multiples of 8; out must not overlap q or the cache.  Equal calls give equal bits.
+ * A workspace of dspark_tree_attention_workspace_size bytes, initialised by
+ * dspark_workspace_init and kept to one stream at a time, is needed.  Needs sm_103,
+ * else DSPARK_UNSUPPORTED. */
+typedef struct {
+  dspark_kv_cache cache;
+  int32_t N;
+  int32_t n_q_heads;
+  int32_t max_tree;
+  float scale;
+  const void* q;
+  int64_t ldq;
+  void* out;
+  int64_t ldo;
+  const int32_t* offsets;
+  const int32_t* base;
+  const uint64_t* tree;
+} dspark_tree_attention_args;
+
+DSPARK_API dspark_status dspark_tree_attention_workspace_size(int32_t n_req, int32_t max_tree, int32_t n_q_heads,
+                                                              int32_t n_kv_heads, int32_t head_dim, size_t* bytes);
+DSPARK_API dspark_status dspark_tree_attention(const dspark_tree_attention_args* args, void* workspace,
+                                               size_t workspace_bytes, void* stream);
 
 /* Number of CUDA kernels this library has enqueued since it was loaded (a
  * host-side counter, incremented at launch time; a captured CUDA graph counts

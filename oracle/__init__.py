@@ -24,6 +24,7 @@ Modules:
   schedule  Sequential Temperature Scaling, Algorithm 1, flatten + markers
   verify    lossless rejection-sampling verification
   vocab     block-scaled e4m3 quantisation and product; token log probabilities and their gradient
+  kv_cache  paged key/value cache, and the attention of drafted rows over it
 
 Every function computes in fp64 unless its docstring says otherwise (the
 scheduler's survival products are fp32 by contract, because they are sort keys
