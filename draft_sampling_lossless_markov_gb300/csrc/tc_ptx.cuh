@@ -257,6 +257,11 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
+// the same with rows (or columns, MN-major) of 64 bytes and the 64-byte swizzle (mode 4)
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  return smem_desc_sw128(saddr, lbo_bytes, sbo_bytes) + ((uint64_t)2 << 61);
+}
+
 // instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, A K-major,
 // B MN-major (N contiguous), N and M as given
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
@@ -393,6 +398,45 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
 // instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B, both K-major
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// the same with e4m3 A and e5m2 B, both MN-major
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_mn_f32(int M, int N) {
+  return idesc_e4m3_f32(M, N) | (1u << 10) | (1u << 15) | (1u << 16);
+}
+// the accumulating switch as a value
+__device__ __forceinline__ void tc_mma_fp8_if(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// ---- barriers of some of a CTA's warps ----
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// true in every thread if `p` is in one
+__device__ __forceinline__ bool named_any(int id, int threads, bool p) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred q, w;\n\t"
+      "setp.ne.s32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.pred w, %1, %2, q;\n\t"
+      "selp.s32 %0, 1, 0, w;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((int)p)
+      : "memory");
+  return r != 0;
+}
+// the largest of the warp's values; NaN is passed over
+__device__ __forceinline__ float warp_max_redux(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // wait for this thread's TMEM loads, which define v

@@ -1,18 +1,58 @@
 // Attention of every request's drafted rows over its cached context and the drafted
-// rows they descend from, read from the paged cache.
+// rows they descend from, read from the paged cache, on the tensor cores.
+//
+// An item is a request, a kv head and up to NQ of its columns: column c is row c / group
+// of the request and query head c % group of the kv head.  An item runs over tiles of 128
+// tokens.  Both products have the tokens' side large and the columns' side small, so the
+// cache is the A operand and no tensor-core row is idle however few rows there are:
+//     S [128 tokens, NQ]   = K tile . Q^T
+//     O [D, NQ]           += (V tile)^T . P     (V read as it lies, MN-major)
+// Tokens are the TMEM lanes of S: a lane's scales are one register each, and the weights
+// are written as rows of the (MN-major) operand P by 16-byte stores.
+//
+// e4m3 codes are used as they are.  A column of q is scaled by a power of two and split
+// into two e4m3 pieces whose sum is q exactly (8 significant bits; elements below 2^-10 of
+// the column's largest to 2^-18 of it): S = K . Q1 + K . Q2.  A weight p times its
+// token's v scale is split into three e5m2 pieces, 9 significant bits: the upper bytes of
+// its fp16 form, of what they leave, and the rounded rest.
+//
+// Softmax: with y = score * log2 e + log2(v scale), weights are 2^(y - ref) about a
+// column's reference, which is raised (O and the sums scaled down) only when a tile
+// passes it by 2^15, and is set 12 below the largest y then; fp16 holds 2^-24 to
+// 2^16 of it.  The sum of the weights themselves, 2^(y - ref) / (v scale), is kept by each
+// lane in fp32.  Two warpgroups take the tiles in turn, each with its own references, sums
+// and O, which are joined at the end of an item.
+//
+// The tiles of all items are one list, dealt out evenly to the CTAs (one an SM): an item
+// that several CTAs share leaves its parts in the workspace, and a second kernel joins
+// them in order.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
 #include "kv_pool.cuh"
 #include "launch.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace dspark {
 
 namespace {
+
+constexpr int kTile = 128;           // tokens
+constexpr int kMaxCtas = 160;        // parts the workspace holds: two a CTA
+constexpr int kThreads = 320;        // two warpgroups of the softmax, loads, MMAs
+constexpr int kSoft = 256;
+constexpr long long kWaitLimit = 4000000000ll;  // cycles, about two seconds
+constexpr float kHead = 12.f;        // a column's largest exponent when its reference is set
+constexpr float kRaise = 15.f;       // the exponent that raises it: 2^15 is in fp16's range
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct TreeArgs {
   KvPool pool;
@@ -22,74 +62,852 @@ struct TreeArgs {
   const int32_t* base;
   const uint64_t* tree;
   int64_t ldq, ldo;
-  int32_t N, q_heads, max_tree;
+  int32_t N, q_heads, group, max_tree;
   float scale;
   WsHeader* hdr;
+  int4* meta;     // [CTAs] the item that begins in a CTA and goes on: request, its head and chunk, parts
+  float2* stat;   // [2 CTAs, NQ] a part's references and sums
+  float* part;    // [2 CTAs, NQ, D] a part's O
 };
 
-template <bool kCodes>
-__device__ __forceinline__ float element(const uint8_t* pool, int64_t at) {
-  if (kCodes) return __half2float(__half(__nv_cvt_fp8_to_halfraw(pool[at], __NV_E4M3)));
-  return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pool)[at]);
+template <bool kCodes, int D, int NQ>
+struct Form {
+  static constexpr int kElem = kCodes ? 1 : 2;
+  static constexpr int kRow = D * kElem < 128 ? D * kElem : 128;  // bytes of an operand row
+  static constexpr int kParts = D * kElem / kRow;                 // of a token's row
+  static constexpr uint32_t kPart = kTile * kRow;
+  static constexpr uint32_t kOperand = kPart * kParts;            // a tile of k or v
+  static constexpr int kQPieces = kCodes ? 2 : 1, kPPieces = kCodes ? 3 : 1;
+  static constexpr uint32_t kQPart = NQ * kRow;
+  static constexpr uint32_t kQ = kQPart * kParts * kQPieces;
+  static constexpr uint32_t kPCol = kTile * 128;                  // 128 bytes of P's row
+  static constexpr uint32_t kP = kPCol * ((NQ * kPPieces * kElem + 127) / 128);
+  static constexpr uint32_t kScales = kCodes ? 2 * kTile * 4 : 0;
+  static constexpr uint32_t kStage = 2 * kOperand + kScales;
+  static constexpr uint32_t kFixed = 2 * kP + (kQ + 1023) / 1024 * 1024;
+  static constexpr int kStages = (int)std::min<uint32_t>(6, (220 * 1024 - kFixed) / kStage);
+  static constexpr uint32_t kSmem = kFixed + kStages * kStage + 1024;
+  static constexpr uint32_t kTmemCols = 4 * NQ;                   // S and O of both warpgroups
+  static_assert(kStages >= 2 && kSmem <= 226 * 1024, "shared memory");
+};
+
+template <int kRow>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo) {
+  return kRow == 128 ? ptx::smem_desc_sw128(addr, lbo, 1024) : ptx::smem_desc_sw64(addr, lbo, 512);
+}
+// the place of byte `a` of an operand with rows of kRow bytes
+template <int kRow>
+__device__ __forceinline__ uint32_t swizzled(uint32_t a) {
+  return a ^ ((a >> 3) & (kRow == 128 ? 0x70u : 0x30u));
 }
 
-// One warp a row and query head, D / 32 elements of the head a lane, one token at
-// a time under a running maximum.
-template <int D, bool kCodes>
-__global__ void __launch_bounds__(128) k_tree_attention(const TreeArgs a) {
+// A request's rows and tiles; units are the tiles of all its items.
+struct Request {
+  int32_t lo, rows, base, tiles, chunks;
+  int64_t units;
+};
+__device__ __forceinline__ Request request_at(const TreeArgs& a, int r, int nq, bool* bad) {
+  Request q;
+  const int32_t lo = a.offsets[r], hi = a.offsets[r + 1];
+  q.base = a.base[r];
+  const int64_t held = (int64_t)q.base + hi - lo;
+  *bad = lo < 0 || hi < lo || hi > a.N || hi - lo > a.max_tree || q.base < 0 ||
+         held > (int64_t)a.pool.max_pages << a.pool.shift;
+  q.lo = lo;
+  q.rows = *bad ? 0 : hi - lo;
+  q.tiles = q.rows ? (int32_t)((held + kTile - 1) / kTile) : 0;
+  q.chunks = (q.rows * a.group + nq - 1) / nq;
+  q.units = (int64_t)q.tiles * q.chunks * a.pool.heads;
+  return q;
+}
+
+// The parts of items in a CTA's share of the units, one after the other; every warp walks by itself.
+struct Walk {
+  int r;
+  int64_t at, left;  // the next unit within request r, units left
+  Request q;
+  // the part
+  int head, chunk, tile, tiles;  // first tile, their number
+  bool begins, ends;             // the item's first and last tile are in it
+  __device__ __forceinline__ void start(const TreeArgs& a, int r0, int64_t at0, int64_t n, int nq) {
+    r = r0, at = at0, left = n;
+    bool bad;
+    if (n > 0) q = request_at(a, r, nq, &bad);
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& a, int nq) {
+    if (left <= 0) return false;
+    bool bad;
+    while (at >= q.units) {
+      at = 0;
+      if (++r >= a.pool.n_req) return false;
+      q = request_at(a, r, nq, &bad);
+    }
+    const int64_t item = at / q.tiles;
+    tile = (int)(at - item * q.tiles);
+    head = (int)(item / q.chunks);
+    chunk = (int)(item - (int64_t)head * q.chunks);
+    tiles = (int)min((int64_t)(q.tiles - tile), left);
+    begins = tile == 0;
+    ends = tile + tiles == q.tiles;
+    at += tiles;
+    left -= tiles;
+    return true;
+  }
+};
+
+// the sums of v[i] over the warp's lanes: lane l ends with column l's (of 32) or l % 16's (of 16)
+template <int n>
+__device__ __forceinline__ float lane_sums(float (&v)[n]) {
+  const int lane = threadIdx.x & 31;
+  if (n == 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+  }
+#pragma unroll
+  for (int o = n / 2; o > 0; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float mine = (lane & o) ? v[i + o] : v[i], send = (lane & o) ? v[i] : v[i + o];
+      v[i] = mine + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 bits_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ uint32_t e5m2x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3)));
+}
+// a word's non-finite elements: all ones in their place
+template <bool kCodes>
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) {
+  if (kCodes) return ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 255u;
+  return ((((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15) * 65535u;
+}
+
+template <bool kCodes, int D, int NQ>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_tree_attention(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
+  using F = Form<kCodes, D, NQ>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sP = sm;                  // [2] P
+  uint8_t* sQ = sm + 2 * F::kP;      // [pieces][parts]
+  uint8_t* sStage = sm + F::kFixed;  // [stages] k, v; then their scales
+  float* sScale = reinterpret_cast<float*>(sStage + F::kStages * 2 * F::kOperand);
+  __shared__ uint64_t kfull[F::kStages], vfull[F::kStages], empty[F::kStages], sfull[2], pready[2], pdone[2], qready;
+  __shared__ uint32_t tmem_slot, okmask[F::kStages];
+  __shared__ int abort_s, never_s, start_r;
+  __shared__ int64_t start_at, sums[kThreads / 32 + 1];
+  __shared__ unsigned long long hidden;  // drafted rows with non-finite v, of the item's part
+  __shared__ uint64_t words[DSPARK_MAX_TREE];
+  __shared__ uint8_t row_of[NQ];
+  __shared__ __align__(16) float qs[NQ], nref[2][NQ], delta[2][NQ], factor[2][NQ];
+  __shared__ float warp_top[8][NQ], coef[2][NQ], norm[NQ];
+  __shared__ bool set[2][NQ];
+  volatile int* abort_flag = &abort_s;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < F::kStages; ++i) {
+      ptx::mbar_init(&kfull[i], 1);
+      ptx::mbar_init(&vfull[i], 1);
+      ptx::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sfull[i], 1);
+      ptx::mbar_init(&pready[i], 4);
+      ptx::mbar_init(&pdone[i], 1);
+    }
+    ptx::mbar_init(&qready, 8);
+    ptx::fence_mbar_init();
+    abort_s = never_s = 0;
+    hidden = 0;
+    ptx::prefetch_map(&tmK);
+    ptx::prefetch_map(&tmV);
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(&tmem_slot, F::kTmemCols);
+    ptx::tmem_relinquish();
+  }
   ptx::launch_dependents();
   ptx::grid_wait();
-  constexpr int E = D / 32;
-  const int r = blockIdx.x / a.q_heads, h = blockIdx.x % a.q_heads, kv = h / (a.q_heads / a.pool.heads);
-  const int lane = threadIdx.x & 31;
-  const int32_t lo = a.offsets[r], hi = a.offsets[r + 1], base = a.base[r];
-  const int64_t held = (int64_t)base + hi - lo;
-  if (lo < 0 || hi < lo || hi > a.N || hi - lo > a.max_tree || base < 0 ||
-      held > (int64_t)a.pool.max_pages << a.pool.shift) {
-    if (threadIdx.x == 0 && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, r);
-    return;
+  auto fail = [&](int what) {
+    if (a.hdr) report_error(a.hdr, DSPARK_TIMEOUT, what);
+    *abort_flag = 1;
+  };
+
+  // this CTA's share of the units: a scan over the requests, a run of them a thread
+  const int per = (a.pool.n_req + kThreads - 1) / kThreads, from = threadIdx.x * per, to = min(a.pool.n_req, from + per);
+  int64_t mine = 0;
+  for (int r = from; r < to; ++r) {
+    bool bad;
+    mine += request_at(a, r, NQ, &bad).units;
+    if (bad && blockIdx.x == 0 && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, r);
   }
-  for (int j = threadIdx.x / 32; j < hi - lo; j += 4) {
-    const int64_t row = lo + j;
-    const uint64_t mask = a.tree ? a.tree[row] : ~0ull >> (63 - j);
-    float q[E], o[E], m = -INFINITY, l = 0.f;
+  int64_t before = mine;
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = ldf(a.q + row * a.ldq + h * D + lane + 32 * e), o[e] = 0.f;
-    for (int64_t t = 0; t < held; ++t) {
-      if (t >= base && !((mask >> (t - base)) & 1)) continue;
-      const int32_t p = pool_row(a.pool, r, t);
-      if (p < 0) {
-        if (lane == 0 && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, r);
-        continue;
-      }
-      const int64_t at = (int64_t)p + ((int64_t)kv << a.pool.shift);
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(q[e], element<kCodes>(a.pool.k, at * D + lane + 32 * e), s);
-      s = warp_sum(s) * a.scale * (kCodes ? a.pool.k_scale[at] : 1.f);
-      const float w = kCodes ? a.pool.v_scale[at] : 1.f;
-      if (s > m) {
-        const float f = __expf(m - s);
-        l *= f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= f;
-        m = s;
-      }
-      const float x = __expf(s - m);
-      l += x;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(x * w, element<kCodes>(a.pool.v, at * D + lane + 32 * e), o[e]);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) sums[warp] = before;
+  before -= mine;
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  int64_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  const int ctas = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
+  const int64_t u0 = cta < ctas ? total * cta / ctas : 0, u1 = cta < ctas ? total * (cta + 1) / ctas : 0;
+  if (u1 > u0 && before <= u0 && u0 < before + mine) {
+    int r = from;
+    int64_t at = u0 - before;
+    for (;; ++r) {
+      bool bad;
+      const int64_t n = request_at(a, r, NQ, &bad).units;
+      if (at < n) break;
+      at -= n;
     }
+    start_r = r;
+    start_at = at;
+  }
+  if (threadIdx.x == 0) a.meta[cta] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  Walk walk;
+  walk.start(a, start_r, start_at, u1 - u0, NQ);
+
+  if (warp == 8) {
+    // ---- loads: a lane a page of the tile, for k, v and their scales ----
+    const uint64_t policy = a.group * a.max_tree > NQ ? ptx::policy_evict_normal() : ptx::policy_evict_first();
+    const int box_shift = min(a.pool.shift, 7), box = 1 << box_shift, boxes = kTile >> box_shift;
+    const int i = lane & 7, what = lane >> 3;
+    uint32_t s = 0, ph = 1, n = 0;
+    bool ok = true;
+    while (ok && walk.next(a, NQ)) {
+      const int64_t len = (int64_t)walk.q.base + walk.q.rows;
+      for (int t = 0; t < walk.tiles; ++t) {
+        const int64_t pos = (int64_t)(walk.tile + t) * kTile + ((int64_t)i << box_shift);
+        int32_t row = -1;
+        const bool wanted = i < boxes && pos < len;
+        if (wanted) row = pool_row(a.pool, walk.r, pos);
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(&empty[s], ph, abort_flag, kWaitLimit));
+        if (!ok) {
+          if (lane == 0) fail(1);
+          break;
+        }
+        if (wanted && row < 0 && what == 0 && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, walk.r);
+        const uint32_t live = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu, count = __popc(live);
+        if (lane == 0) {
+          okmask[s] = live;
+          ptx::mbar_expect_tx(&kfull[s], count * (box * D * F::kElem + (kCodes ? 2 * box * 4 : 0)));
+          ptx::mbar_expect_tx(&vfull[s], count * (box * D * F::kElem));
+        }
+        __syncwarp();
+        if (row >= 0) {
+          row += walk.head << a.pool.shift;
+          uint8_t* stage = sStage + s * 2 * F::kOperand;
+          if (what < 2) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.out[row * a.ldo + h * D + lane + 32 * e] = __float2bfloat16_rn(l == 0.f ? 0.f : o[e] / l);
+            for (int p = 0; p < F::kParts; ++p)
+              ptx::tma_load_2d(stage + what * F::kOperand + p * F::kPart + i * box * F::kRow, what ? &tmV : &tmK,
+                               what ? &vfull[s] : &kfull[s], p * (F::kRow / F::kElem), row, policy);
+          } else if (kCodes) {
+            ptx::bulk_load(sScale + s * 2 * kTile + (what - 2) * kTile + i * box,
+                           (what == 2 ? a.pool.k_scale : a.pool.v_scale) + row, box * 4, &kfull[s], policy);
+          }
+        }
+        __syncwarp();
+        ++n;
+        if (++s == (uint32_t)F::kStages) s = 0, ph ^= 1;
+      }
+    }
+    // nothing may be in flight when the CTA leaves
+    for (uint32_t j = n > (uint32_t)F::kStages ? n - F::kStages : 0; j < n; ++j) {
+      ptx::mbar_wait_cycles(&kfull[j % F::kStages], (j / F::kStages) & 1, &never_s, kWaitLimit);
+      ptx::mbar_wait_cycles(&vfull[j % F::kStages], (j / F::kStages) & 1, &never_s, kWaitLimit);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ---- MMAs: S of a tile, then O of the tile before it ----
+    constexpr uint32_t idesc_s = kCodes ? ptx::idesc_e4m3_f32(128, NQ) : ptx::idesc_bf16_f32(128, NQ, false, false);
+    constexpr uint32_t idesc_o = kCodes ? ptx::idesc_e4m3_e5m2_mn_f32(128, NQ) : ptx::idesc_bf16_f32(128, NQ, true, true);
+    constexpr int kStepsS = D * F::kElem / 32, kStepTokens = 32 / F::kElem, kStepsO = kTile / kStepTokens;
+    // of D = 64 the tile's 64 columns serve as both halves of the 128 rows
+    constexpr uint32_t kLboV = F::kParts > 1 ? F::kPart : 0;
+    const uint32_t aQ = ptx::smem_u32(sQ), aP = ptx::smem_u32(sP), aStage = ptx::smem_u32(sStage);
+    uint32_t n = 0, parts = 0;  // tiles and parts so far
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
+      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit));
+      if (!got && lane == 0) fail(what);
+      return got;
+    };
+    uint32_t turns[2] = {0, 0};  // tiles of each warpgroup so far
+    auto o_of = [&](uint32_t tile, int w, bool first) {  // O of the CTA's tile number `tile`
+      const uint32_t s = tile % F::kStages;
+      if (!wait(&pready[w], turns[w] & 1, 2) || !wait(&vfull[s], (tile / F::kStages) & 1, 3)) return false;
+      ++turns[w];
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        const uint32_t av = aStage + s * 2 * F::kOperand + F::kOperand, ap = aP + w * F::kP;
+        const uint32_t d = tmem + 2 * NQ + w * NQ;
+#pragma unroll
+        for (int p = 0; p < F::kPPieces; ++p) {
+          const uint32_t off = p * NQ * F::kElem;
+#pragma unroll
+          for (int k = 0; k < kStepsO; ++k) {
+            const uint64_t da = operand_desc<F::kRow>(av + k * kStepTokens * F::kRow, kLboV);
+            const uint64_t db = ptx::smem_desc_sw128(ap + off / 128 * F::kPCol + off % 128 + k * kStepTokens * 128, F::kPCol, 1024);
+            const uint32_t acc = !(first && p == 0 && k == 0);
+            if constexpr (kCodes)
+              ptx::tc_mma_fp8_if(d, da, db, idesc_o, acc);
+            else
+              ptx::tc_mma(d, da, db, idesc_o, acc);
+          }
+        }
+        ptx::tc_commit(&empty[s]);
+        ptx::tc_commit(&pdone[w]);
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && walk.next(a, NQ)) {
+      ok = wait(&qready, parts++ & 1, 4);
+      for (int t = 0; ok && t < walk.tiles; ++t, ++n) {
+        const uint32_t s = n % F::kStages;
+        ok = wait(&kfull[s], (n / F::kStages) & 1, 5);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t ak = aStage + s * 2 * F::kOperand, d = tmem + (t & 1) * NQ;
+#pragma unroll
+          for (int p = 0; p < F::kQPieces; ++p)
+#pragma unroll
+            for (int k = 0; k < kStepsS; ++k) {
+              const int part = k * 32 / F::kRow, off = k * 32 % F::kRow;
+              const uint64_t da = operand_desc<F::kRow>(ak + part * F::kPart + off, 16);
+              const uint64_t db = operand_desc<F::kRow>(aQ + (p * F::kParts + part) * F::kQPart + off, 16);
+              const uint32_t acc = p + k > 0;
+              if constexpr (kCodes)
+                ptx::tc_mma_fp8_if(d, da, db, idesc_s, acc);
+              else
+                ptx::tc_mma(d, da, db, idesc_s, acc);
+            }
+          ptx::tc_commit(&sfull[t & 1]);
+        }
+        __syncwarp();
+        if (t > 0) ok = o_of(n - 1, (t - 1) & 1, t - 1 < 2);
+      }
+      if (ok) ok = o_of(n - 1, (walk.tiles - 1) & 1, walk.tiles - 1 < 2);
+    }
+  } else {
+    // ---- softmax ----
+    const int w = warp >> 2, quarter = warp & 3, token = quarter * 32 + lane;
+    const int group_threads = kSoft / 2, bar_own = 1 + w, bar_both = 3;
+    const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + w * NQ, tO = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * NQ;
+    const int box_shift = min(a.pool.shift, 7);
+    const uint32_t all_ok = (1u << (kTile >> box_shift)) - 1;
+    uint32_t n0 = 0, turn = 0;  // the CTA's tiles before this part, this warpgroup's so far
+    auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
+      if (!ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit)) fail(what);  // the loops run on: every later wait ends at once
+    };
+    while (walk.next(a, NQ)) {
+      const int columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
+      const int64_t base = walk.q.base, len = base + walk.q.rows;
+      // q as operand pieces, a warp a column
+      for (int c = warp; c < NQ; c += 8) {
+        constexpr int E = D / 32;
+        float x[E];
+        int j = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = 0.f;
+        if (c < columns) {
+          const int col = walk.chunk * NQ + c;
+          j = col / a.group;
+          const __nv_bfloat16* src = a.q + (int64_t)(walk.q.lo + j) * a.ldq + (walk.head * a.group + col % a.group) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(src + e);
+            x[e] = __uint_as_float(v << 16);
+            x[e + 1] = __uint_as_float(v & 0xFFFF0000u);
+          }
+        }
+        float top = 0.f;
+        bool fin = true;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          fin = fin && fabsf(x[e]) < INFINITY;
+          top = fmaxf(top, fabsf(x[e]));
+        }
+        fin = __all_sync(0xffffffffu, fin);
+        if (!fin) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = 0.f;
+          top = 0.f;
+        }
+        float unit = a.scale * kLog2e;
+        if constexpr (kCodes) {
+          top = ptx::warp_max_redux(top);
+          // top 2^k in 128 .. 256, k below 120 so that both powers are normal
+          const int k = top > 0.f ? min(7 - ((int)(__float_as_uint(top) >> 23) - 127), 120) : 0;
+          const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+          unit *= __uint_as_float((uint32_t)(127 - k) << 23);
+          uint32_t p1 = 0, p2 = 0;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 v = make_float2(x[e] * up, x[e + 1] * up);
+            const uint32_t c1 = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+            const float2 b = e4m3x2_values(c1);
+            const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(v.x - b.x, v.y - b.y), __NV_SATFINITE, __NV_E4M3);
+            p1 |= c1 << (8 * e);
+            p2 |= c2 << (8 * e);
+          }
+          const uint32_t at = swizzled<F::kRow>(c * F::kRow + lane * E);
+          if (E == 4) {
+            *reinterpret_cast<uint32_t*>(sQ + at) = p1;
+            *reinterpret_cast<uint32_t*>(sQ + F::kQPart + at) = p2;
+          } else {
+            *reinterpret_cast<uint16_t*>(sQ + at) = (uint16_t)p1;
+            *reinterpret_cast<uint16_t*>(sQ + F::kQPart + at) = (uint16_t)p2;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const int byte = (lane * E + e) * 2;
+            *reinterpret_cast<uint32_t*>(sQ + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) =
+                (__float_as_uint(x[e]) >> 16) | (__float_as_uint(x[e + 1]) & 0xFFFF0000u);
+          }
+        }
+        if (lane == 0) {
+          qs[c] = c < columns ? (fin ? unit : NAN) : 0.f;
+          row_of[c] = (uint8_t)j;
+        }
+      }
+      for (int j = threadIdx.x; j < walk.q.rows; j += kSoft) words[j] = a.tree ? a.tree[walk.q.lo + j] : ~0ull >> (63 - j);
+      if (token < NQ) nref[w][token] = 0.f, set[w][token] = false;
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&qready);
+      ptx::named_sync(bar_both, kSoft);
+
+      uint64_t l2[NQ / 2];
+#pragma unroll
+      for (int i = 0; i < NQ / 2; ++i) l2[i] = 0;
+      bool unset = true;  // a column has no reference yet
+      for (int t = w; t < walk.tiles; t += 2) {
+        const uint32_t n = n0 + t, s = n % F::kStages, ph = (n / F::kStages) & 1;
+        wait(&kfull[s], ph, 6);
+        const int64_t pos0 = (int64_t)(walk.tile + t) * kTile, pos = pos0 + token;
+        const bool masked = pos0 + kTile > base || okmask[s] != all_ok;
+        const bool held = pos < len && ((okmask[s] >> (token >> box_shift)) & 1);
+        float k_scale = 1.f, v_log = 0.f, v_inv = 1.f;
+        if (kCodes && (!masked || held)) {
+          k_scale = sScale[s * 2 * kTile + token];
+          float v = sScale[s * 2 * kTile + kTile + token];
+          if (v < 1.17549435e-38f) v = 1.17549435e-38f;  // 0 of a cache that was cleared
+          v_log = __log2f(v);
+          v_inv = __frcp_rn(v);
+        }
+        if (masked) {
+          // what no row or only some see must not reach the others through 0 * NaN
+          wait(&vfull[s], ph, 7);
+          uint8_t* row = sStage + s * 2 * F::kOperand + F::kOperand + token * F::kRow;
+          if (!held || pos >= base) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int p = 0; p < F::kParts; ++p)
+#pragma unroll
+              for (int i = 0; i < F::kRow / 16; ++i) {
+                uint4* at = reinterpret_cast<uint4*>(row + p * F::kPart) + i;
+                if (held) {
+                  const uint4 x = *at;
+                  const uint4 m = make_uint4(non_finite<kCodes>(x.x), non_finite<kCodes>(x.y), non_finite<kCodes>(x.z),
+                                             non_finite<kCodes>(x.w));
+                  if (m.x | m.y | m.z | m.w) {
+                    *at = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
+                    any = 1;
+                  }
+                } else {
+                  *at = make_uint4(0, 0, 0, 0);
+                }
+              }
+            if (any) atomicOr(&hidden, 1ull << (pos - base));
+          }
+        }
+        wait(&sfull[w], turn & 1, 8);
+        ++turn;
+        ptx::tc_fence_after();
+        // y, less the reference so far
+        uint64_t x2[NQ / 2];
+        {
+          const uint64_t ks2 = ptx::pack2(k_scale, k_scale), vl2 = ptx::pack2(v_log, v_log);
+          float v[2][16];
+          ptx::tmem_ld16(tS, v[0]);
+#pragma unroll
+          for (int c = 0; c < NQ / 16; ++c) {
+            ptx::tmem_ld_wait16(v[c & 1]);
+            if (c + 1 < NQ / 16) ptx::tmem_ld16(tS + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&qs[c * 16 + 2 * i]);
+              const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&nref[w][c * 16 + 2 * i]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint64_t y = ptx::mul2(ptx::pack2(v[c & 1][2 * (i + h)], v[c & 1][2 * (i + h) + 1]), h ? u.y : u.x);
+                if (kCodes) y = ptx::fma2(y, ks2, vl2);
+                x2[c * 8 + i + h] = ptx::add2(y, h ? r.y : r.x);
+              }
+            }
+          }
+        }
+        if (masked) {
+          const int node = (int)(pos - base);
+#pragma unroll
+          for (int i = 0; i < NQ / 2; ++i) {
+            float2 x = ptx::unpack2(x2[i]);
+            const bool see0 = held && (pos < base || ((words[row_of[2 * i]] >> node) & 1));
+            const bool see1 = held && (pos < base || ((words[row_of[2 * i + 1]] >> node) & 1));
+            x2[i] = ptx::pack2(see0 ? x.x : -INFINITY, see1 ? x.y : -INFINITY);
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NQ / 2; ++i) {
+          const float2 x = ptx::unpack2(x2[i]);
+          top = fmaxf(top, fmaxf(x.x, x.y));
+        }
+        if (ptx::named_any(bar_own, group_threads, top > kRaise) || unset) {
+          // the columns' largest, new references, what was summed so far brought to them
+#pragma unroll
+          for (int c = 0; c < NQ; ++c) {
+            const float2 x = ptx::unpack2(x2[c / 2]);
+            const float m = ptx::warp_max_redux((c & 1) ? x.y : x.x);
+            if (lane == (c & 31)) warp_top[warp][c] = m;
+          }
+          ptx::named_sync(bar_own, group_threads);
+          bool open = false;
+          if (token < NQ) {
+            const float* p = &warp_top[w * 4][token];
+            const float m = fmaxf(fmaxf(p[0], p[NQ]), fmaxf(p[2 * NQ], p[3 * NQ]));
+            float d = 0.f;
+            if (set[w][token])
+              d = fmaxf(0.f, m - kHead);
+            else if (m > -INFINITY)
+              d = m - kHead, set[w][token] = true;
+            else
+              open = true;
+            delta[w][token] = -d;
+            factor[w][token] = exp2f(-d);
+            nref[w][token] -= d;
+          }
+          unset = ptx::named_any(bar_own, group_threads, open);
+#pragma unroll
+          for (int i = 0; i < NQ / 2; ++i) {
+            x2[i] = ptx::add2(x2[i], *reinterpret_cast<const uint64_t*>(&delta[w][2 * i]));
+            if (t >= 2) l2[i] = ptx::mul2(l2[i], *reinterpret_cast<const uint64_t*>(&factor[w][2 * i]));
+          }
+          if (t >= 2) {  // S of this tile was issued after the last O, so that is complete
+#pragma unroll
+            for (int c = 0; c < NQ / 16; ++c) {
+              float v[16];
+              uint32_t u[16];
+              ptx::tmem_ld16(tO + w * NQ + c * 16, v);
+              ptx::tmem_ld_wait16(v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * factor[w][c * 16 + i]);
+              ptx::tmem_st16(tO + w * NQ + c * 16, u);
+            }
+            ptx::tmem_st_wait();
+          }
+        }
+        // weights, their sums and their pieces
+        uint8_t* prow = sP + w * F::kP + token * 128;
+        const uint64_t vi2 = ptx::pack2(v_inv, v_inv);
+#pragma unroll
+        for (int c = 0; c < NQ / 16; ++c) {
+          uint32_t h[8], r1[8], c3[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 x = ptx::unpack2(x2[c * 8 + i]);
+            const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
+            const uint64_t p2 = ptx::pack2(p0, p1);
+            uint64_t& l = l2[c * 8 + i];
+            if (!kCodes) {
+              l = ptx::add2(l, p2);
+            } else if (!masked) {
+              l = ptx::fma2(p2, vi2, l);
+            } else {  // a hidden row's scale may be NaN
+              const float2 b = ptx::unpack2(l);
+              l = ptx::pack2(x.x == -INFINITY ? b.x : fmaf(p0, v_inv, b.x), x.y == -INFINITY ? b.y : fmaf(p1, v_inv, b.y));
+            }
+            if constexpr (kCodes) {
+              h[i] = half2_bits(__floats2half2_rn(p0, p1));
+              r1[i] = half2_bits(__hsub2(bits_half2(h[i]), bits_half2(h[i] & 0xFF00FF00u)));
+              c3[i] = e5m2x2(half2_bits(__hsub2(bits_half2(r1[i]), bits_half2(r1[i] & 0xFF00FF00u))));
+            } else {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+              h[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+          }
+          auto store = [&](uint32_t byte, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
+            *reinterpret_cast<uint4*>(prow + byte / 128 * F::kPCol + (((byte % 128 >> 4) ^ (token & 7)) << 4)) = make_uint4(x, y, z, u);
+          };
+          if constexpr (kCodes) {
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = __byte_perm(h[2 * i], h[2 * i + 1], 0x7531);
+            store(c * 16, b[0], b[1], b[2], b[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = __byte_perm(r1[2 * i], r1[2 * i + 1], 0x7531);
+            store(NQ + c * 16, b[0], b[1], b[2], b[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = c3[2 * i] | (c3[2 * i + 1] << 16);
+            store(2 * NQ + c * 16, b[0], b[1], b[2], b[3]);
+          } else {
+            store(c * 32, h[0], h[1], h[2], h[3]);
+            store(c * 32 + 16, h[4], h[5], h[6], h[7]);
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&pready[w]);
+      }
+
+      // ---- the part's end: sums of both warpgroups, O joined and written ----
+      n0 += walk.tiles;
+      const bool has[2] = {true, walk.tiles > 1};
+      if (has[w]) wait(&pdone[w], (turn - 1) & 1, 9);
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < NQ; c += 32) {
+        constexpr int W = NQ < 32 ? NQ : 32;
+        float v[W];
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+          const float2 x = ptx::unpack2(l2[c / 2 + i]);
+          v[2 * i] = x.x;
+          v[2 * i + 1] = x.y;
+        }
+        const float sum = lane_sums<W>(v);
+        if (lane < W) warp_top[warp][c + lane] = sum;
+      }
+      ptx::named_sync(bar_both, kSoft);
+      const bool whole = walk.begins && walk.ends;
+      const int slot = 2 * cta + (walk.begins ? 1 : 0);
+      if (threadIdx.x < NQ) {
+        const int c = threadIdx.x;
+        float ref[2], l[2], m = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float* p = &warp_top[g * 4][c];
+          ref[g] = set[g][c] ? -nref[g][c] : -INFINITY;
+          l[g] = has[g] ? p[0] + p[NQ] + p[2 * NQ] + p[3 * NQ] : 0.f;
+          if (has[g]) m = fmaxf(m, ref[g]);
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float f = !has[g] ? 0.f : ref[g] == m ? 1.f : exp2f(ref[g] - m);
+          coef[g][c] = f;
+          if (has[g]) sum += f * l[g];
+        }
+        norm[c] = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        if (!whole) a.stat[(int64_t)slot * NQ + c] = make_float2(m, sum);
+      }
+      ptx::named_sync(bar_both, kSoft);
+      const int d = quarter * 32 + lane;
+      if (quarter * 32 < D) {
+        constexpr int W = NQ / 2 < 16 ? 8 : 16;  // columns at a time
+        const unsigned long long bad_rows = hidden;
+#pragma unroll 1
+        for (int c0 = w * (NQ / 2); c0 < (w + 1) * (NQ / 2); c0 += W) {
+          if (c0 >= columns) break;
+          // sixteen columns are loaded; of NQ = 16 the warpgroup takes its eight
+          float v0[16], v1[16];
+          const int first = W == 8 ? 0 : c0;
+          ptx::tmem_ld16(tO + first, v0);
+          ptx::tmem_ld_wait16(v0);
+          if (has[1]) {
+            ptx::tmem_ld16(tO + NQ + first, v1);
+            ptx::tmem_ld_wait16(v1);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = first + i;
+            if (W == 8 && (i >> 3) != w) continue;
+            if (c >= columns) continue;
+            float o = coef[0][c] * v0[i];
+            if (has[1]) o = fmaf(coef[1][c], v1[i], o);
+            for (unsigned long long left = bad_rows & words[row_of[c]]; left; left &= left - 1) {
+              const int32_t row = pool_row(a.pool, walk.r, base + __ffsll((long long)left) - 1);
+              if (row < 0) continue;
+              const int64_t at = ((int64_t)row + ((int64_t)walk.head << a.pool.shift)) * D + d;
+              const float x = kCodes ? ((a.pool.v[at] & 0x7F) == 0x7F ? NAN : 0.f)
+                                     : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.pool.v)[at]);
+              if (!(fabsf(x) < INFINITY)) o += x;
+            }
+            if (whole) {
+              const int col = walk.chunk * NQ + c;
+              a.out[(int64_t)(walk.q.lo + col / a.group) * a.ldo + (walk.head * a.group + col % a.group) * D + d] =
+                  __float2bfloat16_rn(o * norm[c]);
+            } else {
+              a.part[((int64_t)slot * NQ + c) * D + d] = o;
+            }
+          }
+        }
+      }
+      if (!whole && walk.begins && threadIdx.x == 0) {
+        // unit u is CTA ((u + 1) ctas - 1) / total's
+        const int64_t last = u1 + walk.q.tiles - walk.tiles - 1;
+        const int end = (int)(((last + 1) * ctas - 1) / total);
+        a.meta[cta] = make_int4(walk.r, walk.head * walk.q.chunks + walk.chunk, end - cta + 1, 0);
+      }
+      ptx::tc_fence_before();
+      ptx::named_sync(bar_both, kSoft);
+      if (threadIdx.x == 0) hidden = 0;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, F::kTmemCols);
+  }
+}
+
+// The items that several CTAs share: part 0 is the second slot of the CTA they begin in,
+// the others the first slots of those behind it.  A thread an element of the head, a block
+// every kJoin-th column.
+constexpr int kJoin = 8;
+template <int D, int NQ>
+__global__ void __launch_bounds__(D) k_tree_join(const TreeArgs a) {
+  ptx::launch_dependents();
+  ptx::grid_wait();
+  const int cta = blockIdx.x / kJoin;
+  const int4 m = a.meta[cta];
+  if (m.z < 2) return;
+  bool bad;
+  const Request q = request_at(a, m.x, NQ, &bad);
+  const int head = m.y / q.chunks, chunk = m.y % q.chunks, columns = min(NQ, q.rows * a.group - chunk * NQ);
+  const auto slot = [&](int p) { return (int64_t)(p ? 2 * (cta + p) : 2 * cta + 1); };
+  for (int c = blockIdx.x % kJoin; c < columns; c += kJoin) {
+    float ref = -INFINITY;
+    for (int p = 0; p < m.z; ++p) ref = fmaxf(ref, a.stat[slot(p) * NQ + c].x);
+    float sum = 0.f, o = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < m.z; ++p) {
+      const float2 s = a.stat[slot(p) * NQ + c];
+      const float f = s.x == ref ? 1.f : exp2f(s.x - ref);
+      sum = fmaf(f, s.y, sum);
+      o = fmaf(f, a.part[(slot(p) * NQ + c) * D + threadIdx.x], o);
+    }
+    const int col = chunk * NQ + c;
+    a.out[(int64_t)(q.lo + col / a.group) * a.ldo + (head * a.group + col % a.group) * D + threadIdx.x] =
+        __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+struct Layout {
+  size_t meta, stat, part, total;
+};
+int columns_of(int max_tree, int group) {
+  const int n = max_tree * group;
+  return n <= 16 ? 16 : n <= 32 ? 32 : 64;
+}
+Layout layout(int max_tree, int group, int head_dim) {
+  const size_t nq = columns_of(max_tree, group);
+  Layout l;
+  l.meta = align_up(sizeof(WsHeader), 256);
+  l.stat = align_up(l.meta + kMaxCtas * sizeof(int4), 256);
+  l.part = align_up(l.stat + 2 * kMaxCtas * nq * sizeof(float2), 256);
+  l.total = l.part + 2 * kMaxCtas * nq * head_dim * sizeof(float);
+  return l;
+}
+
+struct Dev {
+  int sms = 0;
+  bool sm103 = false;
+};
+// properties of the current device, looked up once each
+cudaError_t device(Dev* out) {
+  constexpr int kMaxDev = 64;
+  static Dev cache[kMaxDev];
+  static bool have[kMaxDev] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorNotSupported;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!have[dev]) {
+    int major = 0, minor = 0;
+    Dev d;
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    d.sm103 = major == 10 && minor == 3;
+    cache[dev] = d;
+    have[dev] = true;
+  }
+  *out = cache[dev];
+  return cudaSuccess;
+}
+
+template <bool kCodes, int D, int NQ>
+cudaError_t run(const dspark_kv_cache& c, const TreeArgs& t, const Dev& dev, cudaStream_t s) {
+  using F = Form<kCodes, D, NQ>;
+  CUtensorMap tmK, tmV;
+  const int64_t rows = (int64_t)c.n_pages * c.n_kv_heads * c.page_size;
+  const CUtensorMapDataType dt = kCodes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int box = std::min(c.page_size, kTile);
+  if (!tensor_map_2d(&tmK, dt, c.k, D, rows, D * F::kElem, F::kRow / F::kElem, box, F::kElem) ||
+      !tensor_map_2d(&tmV, dt, c.v, D, rows, D * F::kElem, F::kRow / F::kElem, box, F::kElem))
+    return cudaErrorInvalidValue;
+  const auto f = k_tree_attention<kCodes, D, NQ>;
+  if (const cudaError_t e = ensure_smem_limit((const void*)f, (int)F::kSmem); e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min(dev.sms, kMaxCtas);
+  if (const cudaError_t e = launch_overlapped(f, grid, kThreads, F::kSmem, 1, s, tmK, tmV, t); e != cudaSuccess) return e;
+  count_launches(1);
+  const cudaError_t e = launch_overlapped(k_tree_join<D, NQ>, grid * kJoin, D, 0, 1, s, t);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <bool kCodes, int D>
+cudaError_t run_columns(const dspark_kv_cache& c, const TreeArgs& t, const Dev& dev, cudaStream_t s) {
+  switch (columns_of(t.max_tree, t.group)) {
+    case 16: return run<kCodes, D, 16>(c, t, dev, s);
+    case 32: return run<kCodes, D, 32>(c, t, dev, s);
+    default: return run<kCodes, D, 64>(c, t, dev, s);
   }
 }
 
 }  // namespace
 
-size_t tree_attention_ws(int, int, int, int, int) { return sizeof(WsHeader); }
+size_t tree_attention_ws(int, int max_tree, int n_q_heads, int n_kv_heads, int head_dim) {
+  return layout(max_tree, n_q_heads / n_kv_heads, head_dim).total;
+}
 
 cudaError_t launch_tree_attention(const dspark_tree_attention_args& a, uint8_t* ws, cudaStream_t s) {
+  Dev dev;
+  if (const cudaError_t e = device(&dev); e != cudaSuccess) return e;
+  if (!dev.sm103) return cudaErrorNotSupported;
   TreeArgs t;
   t.pool = kv_pool(a.cache);
   t.q = static_cast<const __nv_bfloat16*>(a.q);
@@ -101,18 +919,18 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args& a, uint8_t* 
   t.ldo = a.ldo;
   t.N = a.N;
   t.q_heads = a.n_q_heads;
+  t.group = a.n_q_heads / a.cache.n_kv_heads;
   t.max_tree = a.max_tree;
   t.scale = a.scale;
   t.hdr = reinterpret_cast<WsHeader*>(ws);
-  const int64_t grid = (int64_t)a.cache.n_req * a.n_q_heads;
-  if (grid > INT32_MAX) return cudaErrorNotSupported;
-  const bool codes = a.cache.dtype == DSPARK_E4M3;
-  const cudaError_t e =
-      launch_overlapped(a.cache.head_dim == 64 ? (codes ? k_tree_attention<64, true> : k_tree_attention<64, false>)
-                                               : (codes ? k_tree_attention<128, true> : k_tree_attention<128, false>),
-                        (unsigned)grid, 128, 0, 1, s, t);
-  if (e == cudaSuccess) count_launches(1);
-  return e;
+  const Layout l = layout(a.max_tree, t.group, a.cache.head_dim);
+  t.meta = reinterpret_cast<int4*>(ws + l.meta);
+  t.stat = reinterpret_cast<float2*>(ws + l.stat);
+  t.part = reinterpret_cast<float*>(ws + l.part);
+  const bool small = a.cache.head_dim == 64;
+  if (a.cache.dtype == DSPARK_E4M3)
+    return small ? run_columns<true, 64>(a.cache, t, dev, s) : run_columns<true, 128>(a.cache, t, dev, s);
+  return small ? run_columns<false, 64>(a.cache, t, dev, s) : run_columns<false, 128>(a.cache, t, dev, s);
 }
 
 }  // namespace dspark
