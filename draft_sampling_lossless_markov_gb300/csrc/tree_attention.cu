@@ -47,11 +47,19 @@ namespace {
 
 constexpr int kTile = 128;           // tokens
 constexpr int kMaxCtas = 160;        // parts the workspace holds: two a CTA
-constexpr int kThreads = 320;        // two warpgroups of the softmax, loads, MMAs
+constexpr int kThreads = 384;        // two warpgroups of the softmax; loads, MMAs, two warps for q
 constexpr int kSoft = 256;
+// Registers of the softmax's threads, which hold a tile's exponents and the sums of all
+// columns, and of the others: launched at 168 each (384 threads), 652 bytes a thread went to
+// local memory with 64 columns.
+constexpr int kRegsHigh = 216, kRegsLow = 72;
 constexpr long long kWaitLimit = 4000000000ll;  // cycles, about two seconds
-constexpr float kHead = 12.f;        // a column's largest exponent when its reference is set
-constexpr float kRaise = 15.f;       // the exponent that raises it: 2^15 is in fp16's range
+// A column's largest exponent when its reference is set, and the exponent that raises it: 2^15 is in
+// fp16's range, bf16 weights have room up to 2^60.
+template <bool kCodes>
+constexpr float kHead = kCodes ? 6.f : 0.f;
+template <bool kCodes>
+constexpr float kRaise = kCodes ? 15.f : 60.f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct TreeArgs {
@@ -63,6 +71,7 @@ struct TreeArgs {
   const uint64_t* tree;
   int64_t ldq, ldo;
   int32_t N, q_heads, group, max_tree;
+  uint64_t group_inv;  // ceil(2^32 / group): c / group is c group_inv >> 32 for c below 2^16
   float scale;
   WsHeader* hdr;
   int4* meta;     // [CTAs] the item that begins in a CTA and goes on: request, its head and chunk, parts
@@ -84,7 +93,7 @@ struct Form {
   static constexpr uint32_t kP = kPCol * ((NQ * kPPieces * kElem + 127) / 128);
   static constexpr uint32_t kScales = kCodes ? 2 * kTile * 4 : 0;
   static constexpr uint32_t kStage = 2 * kOperand + kScales;
-  static constexpr uint32_t kFixed = 2 * kP + (kQ + 1023) / 1024 * 1024;
+  static constexpr uint32_t kFixed = 2 * kP + 2 * kQ;             // q of this part of an item and of the next
   static constexpr int kStages = (int)std::min<uint32_t>(6, (220 * 1024 - kFixed) / kStage);
   static constexpr uint32_t kSmem = kFixed + kStages * kStage + 1024;
   static constexpr uint32_t kTmemCols = 4 * NQ;                   // S and O of both warpgroups
@@ -155,20 +164,26 @@ struct Walk {
   }
 };
 
-// the sums of v[i] over the warp's lanes: lane l ends with column l's (of 32) or l % 16's (of 16)
-template <int n>
-__device__ __forceinline__ float lane_sums(float (&v)[n]) {
+// A part as the warps for q hand it on to the MMAs and the softmax; no tiles: the last was the one before.
+struct Part {
+  int32_t r, base, rows, head, tile, tiles, columns;
+  int32_t slot;  // of the workspace; -1: the item is whole
+};
+
+// v[i] combined over the warp's lanes: lane l ends with column l's (of 32) or l % 16's (of 16)
+template <int n, typename Op>
+__device__ __forceinline__ float over_lanes(float (&v)[n], Op op) {
   const int lane = threadIdx.x & 31;
   if (n == 16) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    for (int i = 0; i < 16; ++i) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
   }
 #pragma unroll
   for (int o = n / 2; o > 0; o >>= 1) {
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const float mine = (lane & o) ? v[i + o] : v[i], send = (lane & o) ? v[i] : v[i + o];
-      v[i] = mine + __shfl_xor_sync(0xffffffffu, send, o);
+      v[i] = op(mine, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
   return v[0];
@@ -191,24 +206,46 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
   return ((((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15) * 65535u;
 }
 
+// the sum of element d of v over the drafted rows `nodes`, those that are not finite
+template <bool kCodes, int D>
+__device__ __noinline__ float non_finite_v(const TreeArgs& a, int r, int32_t base, int head, unsigned long long nodes, int d) {
+  float sum = 0.f;
+  for (; nodes; nodes &= nodes - 1) {
+    const int32_t row = pool_row(a.pool, r, (int64_t)base + __ffsll((long long)nodes) - 1);
+    if (row < 0) continue;
+    const int64_t at = ((int64_t)row + ((int64_t)head << a.pool.shift)) * D + d;
+    const float x = kCodes ? ((a.pool.v[at] & 0x7F) == 0x7F ? NAN : 0.f)
+                           : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.pool.v)[at]);
+    if (!(fabsf(x) < INFINITY)) sum += x;
+  }
+  return sum;
+}
+
 template <bool kCodes, int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_tree_attention(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
+    k_tree_attention(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ TreeArgs a) {
   using F = Form<kCodes, D, NQ>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sP = sm;                  // [2] P
-  uint8_t* sQ = sm + 2 * F::kP;      // [pieces][parts]
+  uint8_t* sQ = sm + 2 * F::kP;      // [2][pieces][parts]
   uint8_t* sStage = sm + F::kFixed;  // [stages] k, v; then their scales
   float* sScale = reinterpret_cast<float*>(sStage + F::kStages * 2 * F::kOperand);
-  __shared__ uint64_t kfull[F::kStages], vfull[F::kStages], empty[F::kStages], sfull[2], pready[2], pdone[2], qready;
+  __shared__ uint64_t kfull[F::kStages], vfull[F::kStages], empty[F::kStages], sfull[2], sfree[2], pready[2], pdone[2], qfull[2],
+      qempty[2];
   __shared__ uint32_t tmem_slot, okmask[F::kStages];
   __shared__ int abort_s, never_s, start_r;
   __shared__ int64_t start_at, sums[kThreads / 32 + 1];
-  __shared__ unsigned long long hidden;  // drafted rows with non-finite v, of the item's part
-  __shared__ uint64_t words[DSPARK_MAX_TREE];
-  __shared__ uint8_t row_of[NQ];
-  __shared__ __align__(16) float qs[NQ], nref[2][NQ], delta[2][NQ], factor[2][NQ];
+  // of the part and the next: the drafted rows with non-finite v, the rows' words, each column's row,
+  // its place in out and its factor
+  __shared__ Part parts[2];
+  __shared__ unsigned long long hidden[2];
+  __shared__ uint64_t words[2][DSPARK_MAX_TREE];
+  __shared__ uint8_t row_of[2][NQ];
+  __shared__ int64_t out_at[2][NQ];
+  __shared__ __align__(16) float qs[2][NQ];
+  __shared__ __align__(16) float nref[2][NQ], delta[2][NQ], factor[2][NQ];
   __shared__ float warp_top[8][NQ], coef[2][NQ], norm[NQ];
   __shared__ bool set[2][NQ];
   volatile int* abort_flag = &abort_s;
@@ -222,13 +259,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sfull[i], 1);
+      ptx::mbar_init(&sfree[i], 4);
       ptx::mbar_init(&pready[i], 4);
       ptx::mbar_init(&pdone[i], 1);
+      ptx::mbar_init(&qfull[i], 2);
+      ptx::mbar_init(&qempty[i], 8);
+      hidden[i] = 0;
     }
-    ptx::mbar_init(&qready, 8);
     ptx::fence_mbar_init();
     abort_s = never_s = 0;
-    hidden = 0;
     ptx::prefetch_map(&tmK);
     ptx::prefetch_map(&tmV);
   }
@@ -286,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   Walk walk;
   walk.start(a, start_r, start_at, u1 - u0, NQ);
-
+  if (warp >= 8) {
+  ptx::reg_dec<kRegsLow>();
   if (warp == 8) {
     // ---- loads: a lane a page of the tile, for k, v and their scales ----
     const uint64_t policy = a.group * a.max_tree > NQ ? ptx::policy_evict_normal() : ptx::policy_evict_first();
@@ -339,79 +379,206 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    // ---- MMAs: S of a tile, then O of the tile before it ----
+    // ---- MMAs: S up to two tiles ahead of O, whichever has its operands ----
     constexpr uint32_t idesc_s = kCodes ? ptx::idesc_e4m3_f32(128, NQ) : ptx::idesc_bf16_f32(128, NQ, false, false);
     constexpr uint32_t idesc_o = kCodes ? ptx::idesc_e4m3_e5m2_mn_f32(128, NQ) : ptx::idesc_bf16_f32(128, NQ, true, true);
     constexpr int kStepsS = D * F::kElem / 32, kStepTokens = 32 / F::kElem, kStepsO = kTile / kStepTokens;
     // of D = 64 the tile's 64 columns serve as both halves of the 128 rows
     constexpr uint32_t kLboV = F::kParts > 1 ? F::kPart : 0;
     const uint32_t aQ = ptx::smem_u32(sQ), aP = ptx::smem_u32(sP), aStage = ptx::smem_u32(sStage);
-    uint32_t n = 0, parts = 0;  // tiles and parts so far
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
-      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit));
-      if (!got && lane == 0) fail(what);
-      return got;
-    };
-    uint32_t turns[2] = {0, 0};  // tiles of each warpgroup so far
-    auto o_of = [&](uint32_t tile, int w, bool first) {  // O of the CTA's tile number `tile`
-      const uint32_t s = tile % F::kStages;
-      if (!wait(&pready[w], turns[w] & 1, 2) || !wait(&vfull[s], (tile / F::kStages) & 1, 3)) return false;
-      ++turns[w];
-      ptx::tc_fence_after();
-      if (ptx::elect_one()) {
-        const uint32_t av = aStage + s * 2 * F::kOperand + F::kOperand, ap = aP + w * F::kP;
-        const uint32_t d = tmem + 2 * NQ + w * NQ;
-#pragma unroll
-        for (int p = 0; p < F::kPPieces; ++p) {
-          const uint32_t off = p * NQ * F::kElem;
-#pragma unroll
-          for (int k = 0; k < kStepsO; ++k) {
-            const uint64_t da = operand_desc<F::kRow>(av + k * kStepTokens * F::kRow, kLboV);
-            const uint64_t db = ptx::smem_desc_sw128(ap + off / 128 * F::kPCol + off % 128 + k * kStepTokens * 128, F::kPCol, 1024);
-            const uint32_t acc = !(first && p == 0 && k == 0);
-            if constexpr (kCodes)
-              ptx::tc_mma_fp8_if(d, da, db, idesc_o, acc);
-            else
-              ptx::tc_mma(d, da, db, idesc_o, acc);
-          }
+    struct Side {  // where S and O are: the part's tile and its number, the tile's stage and phase, the warpgroups' phases
+      int t = 0, tiles = 0;
+      uint32_t n = 0, s = 0, ph = 0, part = 0, turns = 0;
+      __device__ __forceinline__ void step() {
+        ++n;
+        turns ^= 1u << (t & 1);
+        if (++s == (uint32_t)F::kStages) s = 0, ph ^= 1;
+        if (++t == tiles) {
+          t = tiles = 0;
+          ++part;
         }
-        ptx::tc_commit(&empty[s]);
-        ptx::tc_commit(&pdone[w]);
       }
-      __syncwarp();
-      return true;
-    };
-    while (ok && walk.next(a, NQ)) {
-      ok = wait(&qready, parts++ & 1, 4);
-      for (int t = 0; ok && t < walk.tiles; ++t, ++n) {
-        const uint32_t s = n % F::kStages;
-        ok = wait(&kfull[s], (n / F::kStages) & 1, 5);
-        if (!ok) break;
+    } sS, sO;
+    bool more = true;  // parts
+    long long since = clock64();
+    for (uint32_t polls = 1; more || sO.n != sS.n; ++polls) {
+      const int ws = sS.t & 1, wo = sO.t & 1, qb = sS.part & 1;
+      if (more && sS.tiles == 0 && __all_sync(0xffffffffu, ptx::mbar_test(&qfull[qb], (sS.part >> 1) & 1))) {
+        sS.tiles = parts[qb].tiles;
+        if (sS.tiles == 0) more = false;
+      }
+      if (sS.tiles > 0 && __all_sync(0xffffffffu, ptx::mbar_test(&kfull[sS.s], sS.ph) && ptx::mbar_test(&sfree[ws], (~sS.turns >> ws) & 1))) {
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          const uint32_t ak = aStage + s * 2 * F::kOperand, d = tmem + (t & 1) * NQ;
+          const uint32_t ak = aStage + sS.s * 2 * F::kOperand, aq = aQ + qb * F::kQ, d = tmem + ws * NQ;
 #pragma unroll
           for (int p = 0; p < F::kQPieces; ++p)
 #pragma unroll
             for (int k = 0; k < kStepsS; ++k) {
               const int part = k * 32 / F::kRow, off = k * 32 % F::kRow;
               const uint64_t da = operand_desc<F::kRow>(ak + part * F::kPart + off, 16);
-              const uint64_t db = operand_desc<F::kRow>(aQ + (p * F::kParts + part) * F::kQPart + off, 16);
+              const uint64_t db = operand_desc<F::kRow>(aq + (p * F::kParts + part) * F::kQPart + off, 16);
               const uint32_t acc = p + k > 0;
               if constexpr (kCodes)
                 ptx::tc_mma_fp8_if(d, da, db, idesc_s, acc);
               else
                 ptx::tc_mma(d, da, db, idesc_s, acc);
             }
-          ptx::tc_commit(&sfull[t & 1]);
+          ptx::tc_commit(&sfull[ws]);
         }
         __syncwarp();
-        if (t > 0) ok = o_of(n - 1, (t - 1) & 1, t - 1 < 2);
+        sS.step();
+      } else if (sO.n != sS.n && __all_sync(0xffffffffu, ptx::mbar_test(&pready[wo], (sO.turns >> wo) & 1) && ptx::mbar_test(&vfull[sO.s], sO.ph))) {
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t av = aStage + sO.s * 2 * F::kOperand + F::kOperand, ap = aP + wo * F::kP;
+          const uint32_t d = tmem + 2 * NQ + wo * NQ;
+#pragma unroll
+          for (int p = 0; p < F::kPPieces; ++p) {
+            const uint32_t off = p * NQ * F::kElem;
+#pragma unroll
+            for (int k = 0; k < kStepsO; ++k) {
+              const uint64_t da = operand_desc<F::kRow>(av + k * kStepTokens * F::kRow, kLboV);
+              const uint64_t db = ptx::smem_desc_sw128(ap + off / 128 * F::kPCol + off % 128 + k * kStepTokens * 128, F::kPCol, 1024);
+              const uint32_t acc = !(sO.t < 2 && p == 0 && k == 0);
+              if constexpr (kCodes)
+                ptx::tc_mma_fp8_if(d, da, db, idesc_o, acc);
+              else
+                ptx::tc_mma(d, da, db, idesc_o, acc);
+            }
+          }
+          ptx::tc_commit(&empty[sO.s]);
+          ptx::tc_commit(&pdone[wo]);
+        }
+        __syncwarp();
+        if (sO.t == 0) sO.tiles = parts[sO.part & 1].tiles;
+        sO.step();
+      } else {
+        if ((polls & 255u) == 0 && (*abort_flag || clock64() - since > kWaitLimit)) {
+          if (lane == 0) fail(2);
+          break;
+        }
+        continue;
       }
-      if (ok) ok = o_of(n - 1, (walk.tiles - 1) & 1, walk.tiles - 1 < 2);
+      since = clock64();
     }
+    __syncwarp();
   } else {
+    // ---- q of a part as operand pieces, a warp eight columns at a time, one part ahead of the softmax ----
+    for (uint32_t part = 0;; ++part) {
+      const int b = part & 1;
+      const bool more = walk.next(a, NQ);
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait_cycles(&qempty[b], ~(part >> 1) & 1, abort_flag, kWaitLimit))) {
+        if (lane == 0) fail(4);
+        break;
+      }
+      if (!more) {
+        if (lane == 0) {
+          if (warp == 10) parts[b].tiles = 0;
+          ptx::mbar_arrive(&qfull[b]);
+        }
+        break;
+      }
+      const int columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
+      if (warp == 10 && lane == 0) {
+        Part p;
+        p.r = walk.r, p.base = walk.q.base, p.rows = walk.q.rows, p.head = walk.head;
+        p.tile = walk.tile, p.tiles = walk.tiles, p.columns = columns;
+        p.slot = walk.begins && walk.ends ? -1 : 2 * cta + walk.begins;
+        parts[b] = p;
+        if (walk.begins && !walk.ends) {  // so it is the last part here; unit u is CTA ((u + 1) ctas - 1) / total's
+          const int64_t end = u1 + walk.q.tiles - walk.tiles;
+          a.meta[cta] = make_int4(walk.r, walk.head * walk.q.chunks + walk.chunk, (int)((end * ctas - 1) / total) - cta + 1, 0);
+        }
+      }
+      for (int j = (warp - 10) * 32 + lane; j < walk.q.rows; j += 64)
+        words[b][j] = a.tree ? a.tree[walk.q.lo + j] : ~0ull >> (63 - j);
+      constexpr int E = D / 32;
+      uint8_t* dst = sQ + b * F::kQ;
+      for (int c0 = (warp - 10) * 8; c0 < NQ; c0 += 16) {
+        uint32_t v[8][E / 2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = c0 + i, col = walk.chunk * NQ + c;
+          const int j = c < columns ? (int)(col * a.group_inv >> 32) : 0, head = walk.head * a.group + col - j * a.group;
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) v[i][e] = 0;
+          if (c < columns) {
+            const __nv_bfloat16* src = a.q + (int64_t)(walk.q.lo + j) * a.ldq + head * D + lane * E;
+            if constexpr (E == 4) {
+              const uint2 x = *reinterpret_cast<const uint2*>(src);
+              v[i][0] = x.x, v[i][1] = x.y;
+            } else {
+              v[i][0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+          }
+          if (lane == 0) {
+            row_of[b][c] = (uint8_t)j;
+            out_at[b][c] = (int64_t)(walk.q.lo + j) * a.ldo + head * D;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = c0 + i;
+          float x[E];
+          float top = 0.f;
+          bool fin = true;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            x[e] = __uint_as_float((e & 1) ? v[i][e / 2] & 0xFFFF0000u : v[i][e / 2] << 16);
+            fin = fin && fabsf(x[e]) < INFINITY;
+            top = fmaxf(top, fabsf(x[e]));
+          }
+          fin = __all_sync(0xffffffffu, fin);
+          if (!fin) {  // the column's scores are NaN through its factor
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = 0.f;
+            top = 0.f;
+          }
+          float unit = a.scale * kLog2e;
+          if constexpr (kCodes) {
+            top = ptx::warp_max_redux(top);
+            // top 2^k in 128 .. 256, k up to 120 so that both powers are normal
+            const int k = top > 0.f ? min(7 - ((int)(__float_as_uint(top) >> 23) - 127), 120) : 0;
+            const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+            unit *= __uint_as_float((uint32_t)(127 - k) << 23);
+            uint32_t p1 = 0, p2 = 0;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const float2 y = make_float2(x[e] * up, x[e + 1] * up);
+              const uint32_t c1 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+              const float2 z = e4m3x2_values(c1);
+              const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
+              p1 |= c1 << (8 * e);
+              p2 |= c2 << (8 * e);
+            }
+            const uint32_t at = swizzled<F::kRow>(c * F::kRow + lane * E);
+            if constexpr (E == 4) {
+              *reinterpret_cast<uint32_t*>(dst + at) = p1;
+              *reinterpret_cast<uint32_t*>(dst + F::kQPart + at) = p2;
+            } else {
+              *reinterpret_cast<uint16_t*>(dst + at) = (uint16_t)p1;
+              *reinterpret_cast<uint16_t*>(dst + F::kQPart + at) = (uint16_t)p2;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const int byte = (lane * E + e) * 2;
+              *reinterpret_cast<uint32_t*>(dst + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) =
+                  (__float_as_uint(x[e]) >> 16) | (__float_as_uint(x[e + 1]) & 0xFFFF0000u);
+            }
+          }
+          if (lane == 0) qs[b][c] = c < columns ? (fin ? unit : NAN) : 0.f;
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&qfull[b]);
+    }
+    __syncwarp();
+  }
+  } else {
+    ptx::reg_inc<kRegsHigh>();
     // ---- softmax ----
     const int w = warp >> 2, quarter = warp & 3, token = quarter * 32 + lane;
     const int group_threads = kSoft / 2, bar_own = 1 + w, bar_both = 3;
@@ -422,93 +589,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
       if (!ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit)) fail(what);  // the loops run on: every later wait ends at once
     };
-    while (walk.next(a, NQ)) {
-      const int columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
-      const int64_t base = walk.q.base, len = base + walk.q.rows;
-      // q as operand pieces, a warp a column
-      for (int c = warp; c < NQ; c += 8) {
-        constexpr int E = D / 32;
-        float x[E];
-        int j = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = 0.f;
-        if (c < columns) {
-          const int col = walk.chunk * NQ + c;
-          j = col / a.group;
-          const __nv_bfloat16* src = a.q + (int64_t)(walk.q.lo + j) * a.ldq + (walk.head * a.group + col % a.group) * D + lane * E;
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(src + e);
-            x[e] = __uint_as_float(v << 16);
-            x[e + 1] = __uint_as_float(v & 0xFFFF0000u);
-          }
-        }
-        float top = 0.f;
-        bool fin = true;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          fin = fin && fabsf(x[e]) < INFINITY;
-          top = fmaxf(top, fabsf(x[e]));
-        }
-        fin = __all_sync(0xffffffffu, fin);
-        if (!fin) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[e] = 0.f;
-          top = 0.f;
-        }
-        float unit = a.scale * kLog2e;
-        if constexpr (kCodes) {
-          top = ptx::warp_max_redux(top);
-          // top 2^k in 128 .. 256, k below 120 so that both powers are normal
-          const int k = top > 0.f ? min(7 - ((int)(__float_as_uint(top) >> 23) - 127), 120) : 0;
-          const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-          unit *= __uint_as_float((uint32_t)(127 - k) << 23);
-          uint32_t p1 = 0, p2 = 0;
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const float2 v = make_float2(x[e] * up, x[e + 1] * up);
-            const uint32_t c1 = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-            const float2 b = e4m3x2_values(c1);
-            const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(v.x - b.x, v.y - b.y), __NV_SATFINITE, __NV_E4M3);
-            p1 |= c1 << (8 * e);
-            p2 |= c2 << (8 * e);
-          }
-          const uint32_t at = swizzled<F::kRow>(c * F::kRow + lane * E);
-          if (E == 4) {
-            *reinterpret_cast<uint32_t*>(sQ + at) = p1;
-            *reinterpret_cast<uint32_t*>(sQ + F::kQPart + at) = p2;
-          } else {
-            *reinterpret_cast<uint16_t*>(sQ + at) = (uint16_t)p1;
-            *reinterpret_cast<uint16_t*>(sQ + F::kQPart + at) = (uint16_t)p2;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const int byte = (lane * E + e) * 2;
-            *reinterpret_cast<uint32_t*>(sQ + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) =
-                (__float_as_uint(x[e]) >> 16) | (__float_as_uint(x[e + 1]) & 0xFFFF0000u);
-          }
-        }
-        if (lane == 0) {
-          qs[c] = c < columns ? (fin ? unit : NAN) : 0.f;
-          row_of[c] = (uint8_t)j;
-        }
-      }
-      for (int j = threadIdx.x; j < walk.q.rows; j += kSoft) words[j] = a.tree ? a.tree[walk.q.lo + j] : ~0ull >> (63 - j);
+    for (uint32_t part = 0;; ++part) {
+      const int b = part & 1;
       if (token < NQ) nref[w][token] = 0.f, set[w][token] = false;
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&qready);
-      ptx::named_sync(bar_both, kSoft);
+      const bool got = ptx::mbar_wait_cycles(&qfull[b], (part >> 1) & 1, abort_flag, kWaitLimit);
+      if (!got) fail(10);
+      if (ptx::named_any(bar_both, kSoft, !got)) break;
+      const int tiles = parts[b].tiles, tile0 = parts[b].tile;
+      if (tiles == 0) break;
+      const int64_t base = parts[b].base, len = base + parts[b].rows;
 
       uint64_t l2[NQ / 2];
 #pragma unroll
       for (int i = 0; i < NQ / 2; ++i) l2[i] = 0;
       bool unset = true;  // a column has no reference yet
-      for (int t = w; t < walk.tiles; t += 2) {
+      for (int t = w; t < tiles; t += 2) {
         const uint32_t n = n0 + t, s = n % F::kStages, ph = (n / F::kStages) & 1;
         wait(&kfull[s], ph, 6);
-        const int64_t pos0 = (int64_t)(walk.tile + t) * kTile, pos = pos0 + token;
+        const int64_t pos0 = (int64_t)(tile0 + t) * kTile, pos = pos0 + token;
         const bool masked = pos0 + kTile > base || okmask[s] != all_ok;
         const bool held = pos < len && ((okmask[s] >> (token >> box_shift)) & 1);
         float k_scale = 1.f, v_log = 0.f, v_inv = 1.f;
@@ -542,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   *at = make_uint4(0, 0, 0, 0);
                 }
               }
-            if (any) atomicOr(&hidden, 1ull << (pos - base));
+            if (any) atomicOr(&hidden[b], 1ull << (pos - base));
           }
         }
         wait(&sfull[w], turn & 1, 8);
@@ -560,8 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + 1 < NQ / 16) ptx::tmem_ld16(tS + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-              const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&qs[c * 16 + 2 * i]);
-              const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&nref[w][c * 16 + 2 * i]);
+              const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&qs[b][c * 16 + 2 * i]);
+              ulonglong2 r = make_ulonglong2(0, 0);
+              if (t >= 2) r = *reinterpret_cast<const ulonglong2*>(&nref[w][c * 16 + 2 * i]);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 uint64_t y = ptx::mul2(ptx::pack2(v[c & 1][2 * (i + h)], v[c & 1][2 * (i + h) + 1]), h ? u.y : u.x);
@@ -571,13 +670,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sfree[w]);
         if (masked) {
           const int node = (int)(pos - base);
 #pragma unroll
           for (int i = 0; i < NQ / 2; ++i) {
             float2 x = ptx::unpack2(x2[i]);
-            const bool see0 = held && (pos < base || ((words[row_of[2 * i]] >> node) & 1));
-            const bool see1 = held && (pos < base || ((words[row_of[2 * i + 1]] >> node) & 1));
+            const bool see0 = held && (pos < base || ((words[b][row_of[b][2 * i]] >> node) & 1));
+            const bool see1 = held && (pos < base || ((words[b][row_of[b][2 * i + 1]] >> node) & 1));
             x2[i] = ptx::pack2(see0 ? x.x : -INFINITY, see1 ? x.y : -INFINITY);
           }
         }
@@ -587,13 +689,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 x = ptx::unpack2(x2[i]);
           top = fmaxf(top, fmaxf(x.x, x.y));
         }
-        if (ptx::named_any(bar_own, group_threads, top > kRaise) || unset) {
+        const bool raise = ptx::named_any(bar_own, group_threads, top > kRaise<kCodes>) || unset;
+        if (turn > 1) {  // the tile before is in O, and its weights have been read
+          wait(&pdone[w], turn & 1, 9);
+          ptx::tc_fence_after();
+        }
+        if (raise) {
           // the columns' largest, new references, what was summed so far brought to them
 #pragma unroll
-          for (int c = 0; c < NQ; ++c) {
-            const float2 x = ptx::unpack2(x2[c / 2]);
-            const float m = ptx::warp_max_redux((c & 1) ? x.y : x.x);
-            if (lane == (c & 31)) warp_top[warp][c] = m;
+          for (int c = 0; c < NQ; c += 32) {
+            constexpr int W = NQ < 32 ? NQ : 32;
+            float v[W];
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+              const float2 x = ptx::unpack2(x2[c / 2 + i]);
+              v[2 * i] = x.x;
+              v[2 * i + 1] = x.y;
+            }
+            const float m = over_lanes<W>(v, [](float x, float y) { return fmaxf(x, y); });
+            if (lane < W) warp_top[warp][c + lane] = m;
           }
           ptx::named_sync(bar_own, group_threads);
           bool open = false;
@@ -602,9 +716,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float m = fmaxf(fmaxf(p[0], p[NQ]), fmaxf(p[2 * NQ], p[3 * NQ]));
             float d = 0.f;
             if (set[w][token])
-              d = fmaxf(0.f, m - kHead);
+              d = fmaxf(0.f, m - kHead<kCodes>);
             else if (m > -INFINITY)
-              d = m - kHead, set[w][token] = true;
+              d = m - kHead<kCodes>, set[w][token] = true;
             else
               open = true;
             delta[w][token] = -d;
@@ -617,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x2[i] = ptx::add2(x2[i], *reinterpret_cast<const uint64_t*>(&delta[w][2 * i]));
             if (t >= 2) l2[i] = ptx::mul2(l2[i], *reinterpret_cast<const uint64_t*>(&factor[w][2 * i]));
           }
-          if (t >= 2) {  // S of this tile was issued after the last O, so that is complete
+          if (t >= 2) {
 #pragma unroll
             for (int c = 0; c < NQ / 16; ++c) {
               float v[16];
@@ -686,10 +800,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- the part's end: sums of both warpgroups, O joined and written ----
-      n0 += walk.tiles;
-      const bool has[2] = {true, walk.tiles > 1};
-      if (has[w]) wait(&pdone[w], (turn - 1) & 1, 9);
-      ptx::tc_fence_after();
+      n0 += tiles;
+      const bool has[2] = {true, tiles > 1};
+      if (has[w]) wait(&pdone[w], (turn - 1) & 1, 11);
 #pragma unroll
       for (int c = 0; c < NQ; c += 32) {
         constexpr int W = NQ < 32 ? NQ : 32;
@@ -700,12 +813,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[2 * i] = x.x;
           v[2 * i + 1] = x.y;
         }
-        const float sum = lane_sums<W>(v);
+        const float sum = over_lanes<W>(v, [](float x, float y) { return x + y; });
         if (lane < W) warp_top[warp][c + lane] = sum;
       }
       ptx::named_sync(bar_both, kSoft);
-      const bool whole = walk.begins && walk.ends;
-      const int slot = 2 * cta + (walk.begins ? 1 : 0);
+      ptx::tc_fence_after();
+      const unsigned long long bad_rows = hidden[b];
+      if (threadIdx.x == 0) hidden[b ^ 1] = 0;
+      const int slot = parts[b].slot, columns = parts[b].columns;
+      const bool whole = slot < 0;
       if (threadIdx.x < NQ) {
         const int c = threadIdx.x;
         float ref[2], l[2], m = -INFINITY;
@@ -730,7 +846,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int d = quarter * 32 + lane;
       if (quarter * 32 < D) {
         constexpr int W = NQ / 2 < 16 ? 8 : 16;  // columns at a time
-        const unsigned long long bad_rows = hidden;
 #pragma unroll 1
         for (int c0 = w * (NQ / 2); c0 < (w + 1) * (NQ / 2); c0 += W) {
           if (c0 >= columns) break;
@@ -750,33 +865,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c >= columns) continue;
             float o = coef[0][c] * v0[i];
             if (has[1]) o = fmaf(coef[1][c], v1[i], o);
-            for (unsigned long long left = bad_rows & words[row_of[c]]; left; left &= left - 1) {
-              const int32_t row = pool_row(a.pool, walk.r, base + __ffsll((long long)left) - 1);
-              if (row < 0) continue;
-              const int64_t at = ((int64_t)row + ((int64_t)walk.head << a.pool.shift)) * D + d;
-              const float x = kCodes ? ((a.pool.v[at] & 0x7F) == 0x7F ? NAN : 0.f)
-                                     : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.pool.v)[at]);
-              if (!(fabsf(x) < INFINITY)) o += x;
-            }
-            if (whole) {
-              const int col = walk.chunk * NQ + c;
-              a.out[(int64_t)(walk.q.lo + col / a.group) * a.ldo + (walk.head * a.group + col % a.group) * D + d] =
-                  __float2bfloat16_rn(o * norm[c]);
-            } else {
+            if (bad_rows) o += non_finite_v<kCodes, D>(a, parts[b].r, parts[b].base, parts[b].head, bad_rows & words[b][row_of[b][c]], d);
+            if (whole)
+              a.out[out_at[b][c] + d] = __float2bfloat16_rn(o * norm[c]);
+            else
               a.part[((int64_t)slot * NQ + c) * D + d] = o;
-            }
           }
         }
       }
-      if (!whole && walk.begins && threadIdx.x == 0) {
-        // unit u is CTA ((u + 1) ctas - 1) / total's
-        const int64_t last = u1 + walk.q.tiles - walk.tiles - 1;
-        const int end = (int)(((last + 1) * ctas - 1) / total);
-        a.meta[cta] = make_int4(walk.r, walk.head * walk.q.chunks + walk.chunk, end - cta + 1, 0);
-      }
       ptx::tc_fence_before();
-      ptx::named_sync(bar_both, kSoft);
-      if (threadIdx.x == 0) hidden = 0;
+      ptx::named_sync(bar_both, kSoft);  // O may be written again
+      if (lane == 0) ptx::mbar_arrive(&qempty[b]);
     }
   }
   ptx::tc_fence_before();
@@ -788,34 +887,59 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The items that several CTAs share: part 0 is the second slot of the CTA they begin in,
-// the others the first slots of those behind it.  A thread an element of the head, a block
-// every kJoin-th column.
-constexpr int kJoin = 8;
+// the others the first slots of those behind it.  A block takes a column of one of them at
+// a time, a thread an element of the head.
+constexpr int kJoinThreads = 192;
 template <int D, int NQ>
-__global__ void __launch_bounds__(D) k_tree_join(const TreeArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, int ctas) {
+  static_assert(kMaxCtas <= kJoinThreads, "a thread a CTA");
+  __shared__ int items[kMaxCtas], counts[kJoinThreads / 32];
+  __shared__ float tops[kJoinThreads / 32], share[kMaxCtas];
+  __shared__ float sums[kJoinThreads / 32];
   ptx::launch_dependents();
   ptx::grid_wait();
-  const int cta = blockIdx.x / kJoin;
-  const int4 m = a.meta[cta];
-  if (m.z < 2) return;
-  bool bad;
-  const Request q = request_at(a, m.x, NQ, &bad);
-  const int head = m.y / q.chunks, chunk = m.y % q.chunks, columns = min(NQ, q.rows * a.group - chunk * NQ);
-  const auto slot = [&](int p) { return (int64_t)(p ? 2 * (cta + p) : 2 * cta + 1); };
-  for (int c = blockIdx.x % kJoin; c < columns; c += kJoin) {
-    float ref = -INFINITY;
-    for (int p = 0; p < m.z; ++p) ref = fmaxf(ref, a.stat[slot(p) * NQ + c].x);
-    float sum = 0.f, o = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < m.z; ++p) {
-      const float2 s = a.stat[slot(p) * NQ + c];
-      const float f = s.x == ref ? 1.f : exp2f(s.x - ref);
-      sum = fmaf(f, s.y, sum);
-      o = fmaf(f, a.part[(slot(p) * NQ + c) * D + threadIdx.x], o);
+  const int t = threadIdx.x, warp = t / 32, lane = t % 32;
+  const bool mine = t < ctas && a.meta[t].z > 1;
+  const uint32_t votes = __ballot_sync(0xffffffffu, mine);
+  if (lane == 0) counts[warp] = __popc(votes);
+  __syncthreads();
+  int n = 0, first = 0;
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    if (w < warp) first += counts[w];
+    n += counts[w];
+  }
+  if (mine) items[first + __popc(votes & ((1u << lane) - 1))] = t;
+  __syncthreads();
+  for (int at = blockIdx.x; at < n * NQ; at += gridDim.x) {
+    const int cta = items[at / NQ], c = at % NQ;
+    const int4 m = a.meta[cta];
+    bool bad;
+    const Request q = request_at(a, m.x, NQ, &bad);
+    const int head = m.y / q.chunks, chunk = m.y % q.chunks;
+    if (c >= q.rows * a.group - chunk * NQ) continue;
+    const int64_t slot = t ? 2 * (cta + t) : 2 * cta + 1;
+    float2 s = make_float2(-INFINITY, 0.f);
+    if (t < m.z) s = a.stat[slot * NQ + c];
+    float top = warp_max(s.x);
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, tops[w]);
+    const float f = s.x == top ? 1.f : exp2f(s.x - top);
+    if (t < m.z) share[t] = f;
+    const float sum = warp_sum(t < m.z ? f * s.y : 0.f);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    if (t < D) {
+      float total = 0.f, o = 0.f;
+      for (int w = 0; w < kJoinThreads / 32; ++w) total += sums[w];
+#pragma unroll 8
+      for (int p = 0; p < m.z; ++p)
+        o = fmaf(share[p], a.part[((int64_t)(p ? 2 * (cta + p) : 2 * cta + 1) * NQ + c) * D + t], o);
+      const int col = chunk * NQ + c;
+      a.out[(int64_t)(q.lo + col / a.group) * a.ldo + (head * a.group + col % a.group) * D + t] =
+          __float2bfloat16_rn(total == 0.f ? 0.f : o / total);
     }
-    const int col = chunk * NQ + c;
-    a.out[(int64_t)(q.lo + col / a.group) * a.ldo + (head * a.group + col % a.group) * D + threadIdx.x] =
-        __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+    __syncthreads();
   }
 }
 
@@ -843,6 +967,13 @@ struct Dev {
   int sms = 0;
   bool sm103 = false;
 };
+// The kernel's warps trade registers among themselves: what the softmax's warps ask for
+// has to be there, or they would wait for ever.
+cudaError_t check_registers(const void* f) {
+  cudaFuncAttributes at;
+  if (const cudaError_t e = cudaFuncGetAttributes(&at, f); e != cudaSuccess) return e;
+  return at.numRegs * kThreads < kSoft * kRegsHigh + (kThreads - kSoft) * kRegsLow ? cudaErrorNotSupported : cudaSuccess;
+}
 // properties of the current device, looked up once each
 cudaError_t device(Dev* out) {
   constexpr int kMaxDev = 64;
@@ -879,11 +1010,13 @@ cudaError_t run(const dspark_kv_cache& c, const TreeArgs& t, const Dev& dev, cud
       !tensor_map_2d(&tmV, dt, c.v, D, rows, D * F::kElem, F::kRow / F::kElem, box, F::kElem))
     return cudaErrorInvalidValue;
   const auto f = k_tree_attention<kCodes, D, NQ>;
+  static const cudaError_t registers = check_registers((const void*)f);
+  if (registers != cudaSuccess) return registers;
   if (const cudaError_t e = ensure_smem_limit((const void*)f, (int)F::kSmem); e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min(dev.sms, kMaxCtas);
   if (const cudaError_t e = launch_overlapped(f, grid, kThreads, F::kSmem, 1, s, tmK, tmV, t); e != cudaSuccess) return e;
   count_launches(1);
-  const cudaError_t e = launch_overlapped(k_tree_join<D, NQ>, grid * kJoin, D, 0, 1, s, t);
+  const cudaError_t e = launch_overlapped(k_tree_join<D, NQ>, grid * 4, kJoinThreads, 0, 1, s, t, (int)grid);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
@@ -920,6 +1053,7 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args& a, uint8_t* 
   t.N = a.N;
   t.q_heads = a.n_q_heads;
   t.group = a.n_q_heads / a.cache.n_kv_heads;
+  t.group_inv = ((1ull << 32) + t.group - 1) / t.group;
   t.max_tree = a.max_tree;
   t.scale = a.scale;
   t.hdr = reinterpret_cast<WsHeader*>(ws);
