@@ -96,7 +96,8 @@ struct Form {
   static constexpr uint32_t kFixed = 2 * kP + 2 * kQ;             // q of this part of an item and of the next
   static constexpr int kStages = (int)std::min<uint32_t>(6, (220 * 1024 - kFixed) / kStage);
   static constexpr uint32_t kSmem = kFixed + kStages * kStage + 1024;
-  static constexpr uint32_t kTmemCols = 4 * NQ;                   // S and O of both warpgroups
+  static constexpr int kO = NQ * kPPieces;                         // columns of O: the pieces side by side
+  static constexpr uint32_t kTmemCols = 2 * (NQ + kO) <= 64 ? 64 : 2 * (NQ + kO) <= 128 ? 128 : 2 * (NQ + kO) <= 256 ? 256 : 512;
   static_assert(kStages >= 2 && kSmem <= 226 * 1024, "shared memory");
 };
 
@@ -204,6 +205,90 @@ template <bool kCodes>
 __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
   if (kCodes) return ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 255u;
   return ((((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15) * 65535u;
+}
+
+// The columns of q of a part as operand pieces, with their factors, rows and places in out: eight
+// lanes a column (16 or 8 elements each), four columns a warp at a time, warp `w` of `warps`.
+template <bool kCodes, int D, int NQ>
+__device__ __forceinline__ void prepare_q(const TreeArgs& a, const Walk& walk, uint8_t* dst, int w, int warps, float* qs,
+                                          uint8_t* row_of, int64_t* out_at) {
+  using F = Form<kCodes, D, NQ>;
+  constexpr int E = D / 8, V = E / 8;  // elements, 16-byte vectors of a lane
+  const int lane = threadIdx.x & 31, l = lane & 7, columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
+#pragma unroll 2
+  for (int c = w * 4 + (lane >> 3); c < NQ; c += warps * 4) {
+    const int col = walk.chunk * NQ + c;
+    const int j = c < columns ? (int)(col * a.group_inv >> 32) : 0, head = walk.head * a.group + col - j * a.group;
+    uint4 v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      v[i] = c < columns ? *reinterpret_cast<const uint4*>(a.q + (int64_t)(walk.q.lo + j) * a.ldq + head * D + l * E + i * 8)
+                         : make_uint4(0, 0, 0, 0);
+    uint32_t* x = reinterpret_cast<uint32_t*>(v);
+    uint32_t top = 0;  // the largest magnitude's bits; infinities and NaN are above all others
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[i] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool fin = top < 0x7F80u;
+    if (!fin) {  // the column's scores are NaN through its factor
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) x[i] = 0;
+      top = 0;
+    }
+    float unit = a.scale * kLog2e;
+    if constexpr (kCodes) {
+      // top 2^k in 128 .. 256, k up to 120 so that both powers are normal
+      const int k = top ? min(7 - ((int)(top >> 7) - 127), 120) : 0;
+      const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+      unit *= __uint_as_float((uint32_t)(127 - k) << 23);
+      uint32_t p1[E / 4], p2[E / 4];
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const float2 y = make_float2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xFFFF0000u) * up);
+        const uint32_t c1 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+        const float2 z = e4m3x2_values(c1);
+        const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
+        p1[i / 2] = (i & 1) ? p1[i / 2] | c1 << 16 : c1;
+        p2[i / 2] = (i & 1) ? p2[i / 2] | c2 << 16 : c2;
+      }
+      const uint32_t at = swizzled<F::kRow>(c * F::kRow + l * E);
+      if constexpr (E == 16) {
+        *reinterpret_cast<uint4*>(dst + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+        *reinterpret_cast<uint4*>(dst + F::kQPart + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+      } else {
+        *reinterpret_cast<uint2*>(dst + at) = make_uint2(p1[0], p1[1]);
+        *reinterpret_cast<uint2*>(dst + F::kQPart + at) = make_uint2(p2[0], p2[1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int byte = l * E * 2 + i * 16;
+        *reinterpret_cast<uint4*>(dst + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) = v[i];
+      }
+    }
+    if (l == 0) {
+      qs[c] = c < columns ? (fin ? unit : NAN) : 0.f;
+      row_of[c] = (uint8_t)j;
+      out_at[c] = (int64_t)(walk.q.lo + j) * a.ldo + head * D;
+    }
+  }
+}
+
+// sixteen columns of O, its pieces summed (the smallest first)
+template <int kPieces>
+__device__ __forceinline__ void load_sum(uint32_t taddr, int apart, float (&v)[16]) {
+  ptx::tmem_ld16(taddr + (kPieces - 1) * apart, v);
+  ptx::tmem_ld_wait16(v);
+#pragma unroll
+  for (int p = kPieces - 2; p >= 0; --p) {
+    float u[16];
+    ptx::tmem_ld16(taddr + p * apart, u);
+    ptx::tmem_ld_wait16(u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += u[i];
+  }
 }
 
 // the sum of element d of v over the drafted rows `nodes`, those that are not finite
@@ -381,11 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9) {
     // ---- MMAs: S up to two tiles ahead of O, whichever has its operands ----
     constexpr uint32_t idesc_s = kCodes ? ptx::idesc_e4m3_f32(128, NQ) : ptx::idesc_bf16_f32(128, NQ, false, false);
-    constexpr uint32_t idesc_o = kCodes ? ptx::idesc_e4m3_e5m2_mn_f32(128, NQ) : ptx::idesc_bf16_f32(128, NQ, true, true);
+    constexpr uint32_t idesc_o = kCodes ? ptx::idesc_e4m3_e5m2_mn_f32(128, F::kO) : ptx::idesc_bf16_f32(128, F::kO, true, true);
     constexpr int kStepsS = D * F::kElem / 32, kStepTokens = 32 / F::kElem, kStepsO = kTile / kStepTokens;
     // of D = 64 the tile's 64 columns serve as both halves of the 128 rows
     constexpr uint32_t kLboV = F::kParts > 1 ? F::kPart : 0;
-    const uint32_t aQ = ptx::smem_u32(sQ), aP = ptx::smem_u32(sP), aStage = ptx::smem_u32(sStage);
+    // descriptors of the first stage and buffer; all others are so many 16-byte units further
+    const uint64_t dk0 = operand_desc<F::kRow>(ptx::smem_u32(sStage), 16);
+    const uint64_t dv0 = operand_desc<F::kRow>(ptx::smem_u32(sStage) + F::kOperand, kLboV);
+    const uint64_t dq0 = operand_desc<F::kRow>(ptx::smem_u32(sQ), 16);
+    const uint64_t dp0 = ptx::smem_desc_sw128(ptx::smem_u32(sP), F::kPCol, 1024);
     struct Side {  // where S and O are: the part's tile and its number, the tile's stage and phase, the warpgroups' phases
       int t = 0, tiles = 0;
       uint32_t n = 0, s = 0, ph = 0, part = 0, turns = 0;
@@ -399,30 +488,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } sS, sO;
-    bool more = true;  // parts
+    bool open = true;  // there may be another part
     long long since = clock64();
-    for (uint32_t polls = 1; more || sO.n != sS.n; ++polls) {
+    for (uint32_t polls = 1; open || sO.n != sS.n; ++polls) {
       const int ws = sS.t & 1, wo = sO.t & 1, qb = sS.part & 1;
-      if (more && sS.tiles == 0 && __all_sync(0xffffffffu, ptx::mbar_test(&qfull[qb], (sS.part >> 1) & 1))) {
+      if (open && sS.tiles == 0 && __all_sync(0xffffffffu, ptx::mbar_test(&qfull[qb], (sS.part >> 1) & 1))) {
         sS.tiles = parts[qb].tiles;
-        if (sS.tiles == 0) more = false;
+        if (sS.tiles == 0) open = false;
       }
       if (sS.tiles > 0 && __all_sync(0xffffffffu, ptx::mbar_test(&kfull[sS.s], sS.ph) && ptx::mbar_test(&sfree[ws], (~sS.turns >> ws) & 1))) {
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          const uint32_t ak = aStage + sS.s * 2 * F::kOperand, aq = aQ + qb * F::kQ, d = tmem + ws * NQ;
+          const uint64_t dk = dk0 + sS.s * (2 * F::kOperand >> 4), dq = dq0 + qb * (F::kQ >> 4);
+          const uint32_t d = tmem + ws * NQ;
 #pragma unroll
           for (int p = 0; p < F::kQPieces; ++p)
 #pragma unroll
             for (int k = 0; k < kStepsS; ++k) {
               const int part = k * 32 / F::kRow, off = k * 32 % F::kRow;
-              const uint64_t da = operand_desc<F::kRow>(ak + part * F::kPart + off, 16);
-              const uint64_t db = operand_desc<F::kRow>(aq + (p * F::kParts + part) * F::kQPart + off, 16);
-              const uint32_t acc = p + k > 0;
-              if constexpr (kCodes)
-                ptx::tc_mma_fp8_if(d, da, db, idesc_s, acc);
+              const uint64_t da = dk + ((part * F::kPart + off) >> 4), db = dq + (((p * F::kParts + part) * F::kQPart + off) >> 4);
+              if constexpr (!kCodes)
+                ptx::tc_mma(d, da, db, idesc_s, k > 0);
+              else if (p + k == 0)
+                ptx::tc_mma_fp8<0>(d, da, db, idesc_s);
               else
-                ptx::tc_mma(d, da, db, idesc_s, acc);
+                ptx::tc_mma_fp8<1>(d, da, db, idesc_s);
             }
           ptx::tc_commit(&sfull[ws]);
         }
@@ -431,21 +521,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (sO.n != sS.n && __all_sync(0xffffffffu, ptx::mbar_test(&pready[wo], (sO.turns >> wo) & 1) && ptx::mbar_test(&vfull[sO.s], sO.ph))) {
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          const uint32_t av = aStage + sO.s * 2 * F::kOperand + F::kOperand, ap = aP + wo * F::kP;
-          const uint32_t d = tmem + 2 * NQ + wo * NQ;
+          const uint64_t dv = dv0 + sO.s * (2 * F::kOperand >> 4), dp = dp0 + wo * (F::kP >> 4);
+          const uint32_t d = tmem + 2 * NQ + wo * F::kO, more = sO.t >= 2;
 #pragma unroll
-          for (int p = 0; p < F::kPPieces; ++p) {
-            const uint32_t off = p * NQ * F::kElem;
-#pragma unroll
-            for (int k = 0; k < kStepsO; ++k) {
-              const uint64_t da = operand_desc<F::kRow>(av + k * kStepTokens * F::kRow, kLboV);
-              const uint64_t db = ptx::smem_desc_sw128(ap + off / 128 * F::kPCol + off % 128 + k * kStepTokens * 128, F::kPCol, 1024);
-              const uint32_t acc = !(sO.t < 2 && p == 0 && k == 0);
-              if constexpr (kCodes)
-                ptx::tc_mma_fp8_if(d, da, db, idesc_o, acc);
-              else
-                ptx::tc_mma(d, da, db, idesc_o, acc);
-            }
+          for (int k = 0; k < kStepsO; ++k) {
+            const uint64_t da = dv + (k * kStepTokens * F::kRow >> 4), db = dp + (k * kStepTokens * 128 >> 4);
+            if constexpr (!kCodes)
+              ptx::tc_mma(d, da, db, idesc_o, k > 0 ? 1 : more);
+            else if (k == 0)
+              ptx::tc_mma_fp8_if(d, da, db, idesc_o, more);
+            else
+              ptx::tc_mma_fp8<1>(d, da, db, idesc_o);
           }
           ptx::tc_commit(&empty[sO.s]);
           ptx::tc_commit(&pdone[wo]);
@@ -464,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ---- q of a part as operand pieces, a warp eight columns at a time, one part ahead of the softmax ----
+    // ---- q of a part, one part ahead of the softmax ----
     for (uint32_t part = 0;; ++part) {
       const int b = part & 1;
       const bool more = walk.next(a, NQ);
@@ -493,84 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int j = (warp - 10) * 32 + lane; j < walk.q.rows; j += 64)
         words[b][j] = a.tree ? a.tree[walk.q.lo + j] : ~0ull >> (63 - j);
-      constexpr int E = D / 32;
-      uint8_t* dst = sQ + b * F::kQ;
-      for (int c0 = (warp - 10) * 8; c0 < NQ; c0 += 16) {
-        uint32_t v[8][E / 2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = c0 + i, col = walk.chunk * NQ + c;
-          const int j = c < columns ? (int)(col * a.group_inv >> 32) : 0, head = walk.head * a.group + col - j * a.group;
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) v[i][e] = 0;
-          if (c < columns) {
-            const __nv_bfloat16* src = a.q + (int64_t)(walk.q.lo + j) * a.ldq + head * D + lane * E;
-            if constexpr (E == 4) {
-              const uint2 x = *reinterpret_cast<const uint2*>(src);
-              v[i][0] = x.x, v[i][1] = x.y;
-            } else {
-              v[i][0] = *reinterpret_cast<const uint32_t*>(src);
-            }
-          }
-          if (lane == 0) {
-            row_of[b][c] = (uint8_t)j;
-            out_at[b][c] = (int64_t)(walk.q.lo + j) * a.ldo + head * D;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = c0 + i;
-          float x[E];
-          float top = 0.f;
-          bool fin = true;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            x[e] = __uint_as_float((e & 1) ? v[i][e / 2] & 0xFFFF0000u : v[i][e / 2] << 16);
-            fin = fin && fabsf(x[e]) < INFINITY;
-            top = fmaxf(top, fabsf(x[e]));
-          }
-          fin = __all_sync(0xffffffffu, fin);
-          if (!fin) {  // the column's scores are NaN through its factor
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = 0.f;
-            top = 0.f;
-          }
-          float unit = a.scale * kLog2e;
-          if constexpr (kCodes) {
-            top = ptx::warp_max_redux(top);
-            // top 2^k in 128 .. 256, k up to 120 so that both powers are normal
-            const int k = top > 0.f ? min(7 - ((int)(__float_as_uint(top) >> 23) - 127), 120) : 0;
-            const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-            unit *= __uint_as_float((uint32_t)(127 - k) << 23);
-            uint32_t p1 = 0, p2 = 0;
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              const float2 y = make_float2(x[e] * up, x[e + 1] * up);
-              const uint32_t c1 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-              const float2 z = e4m3x2_values(c1);
-              const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
-              p1 |= c1 << (8 * e);
-              p2 |= c2 << (8 * e);
-            }
-            const uint32_t at = swizzled<F::kRow>(c * F::kRow + lane * E);
-            if constexpr (E == 4) {
-              *reinterpret_cast<uint32_t*>(dst + at) = p1;
-              *reinterpret_cast<uint32_t*>(dst + F::kQPart + at) = p2;
-            } else {
-              *reinterpret_cast<uint16_t*>(dst + at) = (uint16_t)p1;
-              *reinterpret_cast<uint16_t*>(dst + F::kQPart + at) = (uint16_t)p2;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              const int byte = (lane * E + e) * 2;
-              *reinterpret_cast<uint32_t*>(dst + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) =
-                  (__float_as_uint(x[e]) >> 16) | (__float_as_uint(x[e + 1]) & 0xFFFF0000u);
-            }
-          }
-          if (lane == 0) qs[b][c] = c < columns ? (fin ? unit : NAN) : 0.f;
-        }
-      }
+      if (part > 0)
+        prepare_q<kCodes, D, NQ>(a, walk, sQ + b * F::kQ, warp - 10, 2, qs[b], row_of[b], out_at[b]);
+      else
+        ptx::named_sync(4, kSoft + 64);  // the softmax's warps, which have nothing else to do yet
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&qfull[b]);
@@ -582,13 +594,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- softmax ----
     const int w = warp >> 2, quarter = warp & 3, token = quarter * 32 + lane;
     const int group_threads = kSoft / 2, bar_own = 1 + w, bar_both = 3;
-    const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + w * NQ, tO = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * NQ;
+    const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + w * NQ,
+                   tO = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * NQ;
     const int box_shift = min(a.pool.shift, 7);
     const uint32_t all_ok = (1u << (kTile >> box_shift)) - 1;
     uint32_t n0 = 0, turn = 0;  // the CTA's tiles before this part, this warpgroup's so far
     auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
       if (!ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit)) fail(what);  // the loops run on: every later wait ends at once
     };
+    if (walk.next(a, NQ)) {
+      prepare_q<kCodes, D, NQ>(a, walk, sQ, warp, 8, qs[0], row_of[0], out_at[0]);
+      ptx::fence_proxy_async_smem();
+      ptx::named_arrive(4, kSoft + 64);
+    }
     for (uint32_t part = 0;; ++part) {
       const int b = part & 1;
       if (token < NQ) nref[w][token] = 0.f, set[w][token] = false;
@@ -733,14 +751,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (t >= 2) {
 #pragma unroll
-            for (int c = 0; c < NQ / 16; ++c) {
+            for (int c = 0; c < F::kO / 16; ++c) {
               float v[16];
               uint32_t u[16];
-              ptx::tmem_ld16(tO + w * NQ + c * 16, v);
+              ptx::tmem_ld16(tO + w * F::kO + c * 16, v);
               ptx::tmem_ld_wait16(v);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * factor[w][c * 16 + i]);
-              ptx::tmem_st16(tO + w * NQ + c * 16, u);
+              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * factor[w][c * 16 % NQ + i]);
+              ptx::tmem_st16(tO + w * F::kO + c * 16, u);
             }
             ptx::tmem_st_wait();
           }
@@ -850,14 +868,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c0 = w * (NQ / 2); c0 < (w + 1) * (NQ / 2); c0 += W) {
           if (c0 >= columns) break;
           // sixteen columns are loaded; of NQ = 16 the warpgroup takes its eight
-          float v0[16], v1[16];
           const int first = W == 8 ? 0 : c0;
-          ptx::tmem_ld16(tO + first, v0);
-          ptx::tmem_ld_wait16(v0);
-          if (has[1]) {
-            ptx::tmem_ld16(tO + NQ + first, v1);
-            ptx::tmem_ld_wait16(v1);
-          }
+          float v0[16], v1[16];
+          load_sum<F::kPPieces>(tO + first, NQ, v0);
+          if (has[1]) load_sum<F::kPPieces>(tO + F::kO + first, NQ, v1);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int c = first + i;
