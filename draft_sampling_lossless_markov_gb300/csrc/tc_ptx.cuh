@@ -455,6 +455,37 @@ __device__ __forceinline__ float warp_max_redux(float x) {
   return r;
 }
 
+// 8 consecutive fp32 columns of this thread's TMEM lane (warp-collective)
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(taddr));
+}
+// wait for this thread's TMEM loads, which define n values from v on
+template <int n>
+__device__ __forceinline__ void tmem_ld_wait(float* v) {
+  static_assert(n % 8 == 0, "eight at a time");
+#pragma unroll
+  for (int i = 0; i < n; i += 8)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]),
+                   "+f"(v[i + 7])
+                 :
+                 : "memory");
+}
+// 8 consecutive 32-bit columns of this thread's TMEM lane (warp-collective)
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+// 1 / x to 1 ulp
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // wait for this thread's TMEM loads, which define v
 __device__ __forceinline__ void tmem_ld_wait16(float (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"

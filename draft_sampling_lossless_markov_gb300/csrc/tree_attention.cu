@@ -47,12 +47,12 @@ namespace {
 
 constexpr int kTile = 128;           // tokens
 constexpr int kMaxCtas = 160;        // parts the workspace holds: two a CTA
-constexpr int kThreads = 384;        // two warpgroups of the softmax; loads, MMAs, two warps for q
-constexpr int kSoft = 256;
-// Registers of the softmax's threads, which hold a tile's exponents and the sums of all
-// columns, and of the others: launched at 168 each (384 threads), 652 bytes a thread went to
-// local memory with 64 columns.
-constexpr int kRegsHigh = 216, kRegsLow = 72;
+constexpr int kSoftWarps = 16;       // four warpgroups of the softmax: two a tile, each with half of the columns
+constexpr int kSoft = 32 * kSoftWarps;
+constexpr int kThreads = kSoft + 128;  // and the warps for loads, S, O and q
+constexpr int kItemCost = 2;         // what an item costs beside its tiles, in tiles
+// Registers of the softmax's threads and of the others, of the 96 a thread (640 threads) at launch.
+constexpr int kRegsHigh = 104, kRegsLow = 64;
 constexpr long long kWaitLimit = 4000000000ll;  // cycles, about two seconds
 // A column's largest exponent when its reference is set, and the exponent that raises it: 2^15 is in
 // fp16's range, bf16 weights have room up to 2^60.
@@ -111,7 +111,7 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t a) {
   return a ^ ((a >> 3) & (kRow == 128 ? 0x70u : 0x30u));
 }
 
-// A request's rows and tiles; units are the tiles of all its items.
+// A request's rows and tiles; its units are the costs of all its items: their tiles, behind the units of an item itself.
 struct Request {
   int32_t lo, rows, base, tiles, chunks;
   int64_t units;
@@ -127,7 +127,7 @@ __device__ __forceinline__ Request request_at(const TreeArgs& a, int r, int nq, 
   q.rows = *bad ? 0 : hi - lo;
   q.tiles = q.rows ? (int32_t)((held + kTile - 1) / kTile) : 0;
   q.chunks = (q.rows * a.group + nq - 1) / nq;
-  q.units = (int64_t)q.tiles * q.chunks * a.pool.heads;
+  q.units = q.tiles ? (int64_t)(q.tiles + kItemCost) * q.chunks * a.pool.heads : 0;
   return q;
 }
 
@@ -145,23 +145,28 @@ struct Walk {
     if (n > 0) q = request_at(a, r, nq, &bad);
   }
   __device__ __forceinline__ bool next(const TreeArgs& a, int nq) {
-    if (left <= 0) return false;
-    bool bad;
-    while (at >= q.units) {
-      at = 0;
-      if (++r >= a.pool.n_req) return false;
-      q = request_at(a, r, nq, &bad);
+    for (;;) {
+      if (left <= 0) return false;
+      bool bad;
+      while (at >= q.units) {
+        at = 0;
+        if (++r >= a.pool.n_req) return false;
+        q = request_at(a, r, nq, &bad);
+      }
+      const int cost = q.tiles + kItemCost;
+      const int64_t item = at / cost;
+      const int x = (int)(at - item * cost), y = (int)min((int64_t)cost, x + left);
+      at += y - x;
+      left -= y - x;
+      tile = max(0, x - kItemCost);
+      tiles = max(0, y - kItemCost) - tile;
+      if (tiles == 0) continue;  // nothing but the item's own cost: it begins in the next CTA
+      head = (int)(item / q.chunks);
+      chunk = (int)(item - (int64_t)head * q.chunks);
+      begins = tile == 0;
+      ends = tile + tiles == q.tiles;
+      return true;
     }
-    const int64_t item = at / q.tiles;
-    tile = (int)(at - item * q.tiles);
-    head = (int)(item / q.chunks);
-    chunk = (int)(item - (int64_t)head * q.chunks);
-    tiles = (int)min((int64_t)(q.tiles - tile), left);
-    begins = tile == 0;
-    ends = tile + tiles == q.tiles;
-    at += tiles;
-    left -= tiles;
-    return true;
   }
 };
 
@@ -171,14 +176,14 @@ struct Part {
   int32_t slot;  // of the workspace; -1: the item is whole
 };
 
-// v[i] combined over the warp's lanes: lane l ends with column l's (of 32) or l % 16's (of 16)
+// v[i] combined over the warp's lanes: lane l ends with column l % n's
 template <int n, typename Op>
 __device__ __forceinline__ float over_lanes(float (&v)[n], Op op) {
   const int lane = threadIdx.x & 31;
-  if (n == 16) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
-  }
+  for (int o = 16; o >= n; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = op(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
 #pragma unroll
   for (int o = n / 2; o > 0; o >>= 1) {
 #pragma unroll
@@ -276,18 +281,24 @@ __device__ __forceinline__ void prepare_q(const TreeArgs& a, const Walk& walk, u
   }
 }
 
-// sixteen columns of O, its pieces summed (the smallest first)
-template <int kPieces>
-__device__ __forceinline__ void load_sum(uint32_t taddr, int apart, float (&v)[16]) {
-  ptx::tmem_ld16(taddr + (kPieces - 1) * apart, v);
-  ptx::tmem_ld_wait16(v);
+template <int n>
+__device__ __forceinline__ void load_columns(uint32_t taddr, float* v) {
 #pragma unroll
-  for (int p = kPieces - 2; p >= 0; --p) {
-    float u[16];
-    ptx::tmem_ld16(taddr + p * apart, u);
-    ptx::tmem_ld_wait16(u);
+  for (int i = 0; i < n; i += 8) ptx::tmem_ld8(taddr + i, v + i);
+}
+// columns of O, its pieces summed (the smallest first)
+template <int kPieces, int n>
+__device__ __forceinline__ void load_sum(uint32_t taddr, int apart, float (&v)[n]) {
+  float u[kPieces][n];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += u[i];
+  for (int p = 0; p < kPieces; ++p) load_columns<n>(taddr + p * apart, u[p]);
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) ptx::tmem_ld_wait<n>(u[p]);
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    v[i] = u[kPieces - 1][i];
+#pragma unroll
+    for (int p = kPieces - 2; p >= 0; --p) v[i] += u[p][i];
   }
 }
 
@@ -331,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int64_t out_at[2][NQ];
   __shared__ __align__(16) float qs[2][NQ];
   __shared__ __align__(16) float nref[2][NQ], delta[2][NQ], factor[2][NQ];
-  __shared__ float warp_top[8][NQ], coef[2][NQ], norm[NQ];
+  __shared__ float warp_top[kSoftWarps][NQ / 2], coef[2][NQ], norm[NQ];
   __shared__ bool set[2][NQ];
   volatile int* abort_flag = &abort_s;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -344,11 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sfull[i], 1);
-      ptx::mbar_init(&sfree[i], 4);
-      ptx::mbar_init(&pready[i], 4);
+      ptx::mbar_init(&sfree[i], kSoftWarps / 2);
+      ptx::mbar_init(&pready[i], kSoftWarps / 2);
       ptx::mbar_init(&pdone[i], 1);
-      ptx::mbar_init(&qfull[i], 2);
-      ptx::mbar_init(&qempty[i], 8);
+      ptx::mbar_init(&qfull[i], 1);
+      ptx::mbar_init(&qempty[i], kSoftWarps);
       hidden[i] = 0;
     }
     ptx::fence_mbar_init();
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_map(&tmK);
     ptx::prefetch_map(&tmV);
   }
-  if (warp == 9) {
+  if (warp == kSoftWarps + 1) {
     ptx::tmem_alloc(&tmem_slot, F::kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -410,9 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   Walk walk;
   walk.start(a, start_r, start_at, u1 - u0, NQ);
-  if (warp >= 8) {
+  if (warp >= kSoftWarps) {
   ptx::reg_dec<kRegsLow>();
-  if (warp == 8) {
+  if (warp == kSoftWarps) {
     // ---- loads: a lane a page of the tile, for k, v and their scales ----
     const uint64_t policy = a.group * a.max_tree > NQ ? ptx::policy_evict_normal() : ptx::policy_evict_first();
     const int box_shift = min(a.pool.shift, 7), box = 1 << box_shift, boxes = kTile >> box_shift;
@@ -463,8 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_wait_cycles(&vfull[j % F::kStages], (j / F::kStages) & 1, &never_s, kWaitLimit);
     }
     __syncwarp();
-  } else if (warp == 9) {
-    // ---- MMAs: S up to two tiles ahead of O, whichever has its operands ----
+  } else if (warp < kSoftWarps + 3) {
+    // ---- MMAs: one warp for S, up to two tiles ahead, and one for O (one warp's waits and issues for
+    // both took 1850 cycles a tile) ----
     constexpr uint32_t idesc_s = kCodes ? ptx::idesc_e4m3_f32(128, NQ) : ptx::idesc_bf16_f32(128, NQ, false, false);
     constexpr uint32_t idesc_o = kCodes ? ptx::idesc_e4m3_e5m2_mn_f32(128, F::kO) : ptx::idesc_bf16_f32(128, F::kO, true, true);
     constexpr int kStepsS = D * F::kElem / 32, kStepTokens = 32 / F::kElem, kStepsO = kTile / kStepTokens;
@@ -475,78 +487,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dv0 = operand_desc<F::kRow>(ptx::smem_u32(sStage) + F::kOperand, kLboV);
     const uint64_t dq0 = operand_desc<F::kRow>(ptx::smem_u32(sQ), 16);
     const uint64_t dp0 = ptx::smem_desc_sw128(ptx::smem_u32(sP), F::kPCol, 1024);
-    struct Side {  // where S and O are: the part's tile and its number, the tile's stage and phase, the warpgroups' phases
-      int t = 0, tiles = 0;
-      uint32_t n = 0, s = 0, ph = 0, part = 0, turns = 0;
-      __device__ __forceinline__ void step() {
-        ++n;
-        turns ^= 1u << (t & 1);
-        if (++s == (uint32_t)F::kStages) s = 0, ph ^= 1;
-        if (++t == tiles) {
-          t = tiles = 0;
-          ++part;
-        }
-      }
-    } sS, sO;
-    bool open = true;  // there may be another part
-    long long since = clock64();
-    for (uint32_t polls = 1; open || sO.n != sS.n; ++polls) {
-      const int ws = sS.t & 1, wo = sO.t & 1, qb = sS.part & 1;
-      if (open && sS.tiles == 0 && __all_sync(0xffffffffu, ptx::mbar_test(&qfull[qb], (sS.part >> 1) & 1))) {
-        sS.tiles = parts[qb].tiles;
-        if (sS.tiles == 0) open = false;
-      }
-      if (sS.tiles > 0 && __all_sync(0xffffffffu, ptx::mbar_test(&kfull[sS.s], sS.ph) && ptx::mbar_test(&sfree[ws], (~sS.turns >> ws) & 1))) {
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          const uint64_t dk = dk0 + sS.s * (2 * F::kOperand >> 4), dq = dq0 + qb * (F::kQ >> 4);
-          const uint32_t d = tmem + ws * NQ;
+    const bool is_s = warp == kSoftWarps + 1;
+    auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
+      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit));
+      if (!got && lane == 0) fail(what);
+      return got;
+    };
+    uint32_t s = 0, ph = 0, turns = 0;  // the tile's stage and phase, the phases of the pairs of warpgroups
+    bool ok = true;
+    for (uint32_t part = 0; ok; ++part) {
+      const int qb = part & 1;
+      ok = wait(&qfull[qb], (part >> 1) & 1, 2);
+      if (!ok) break;
+      const int tiles = parts[qb].tiles;
+      if (tiles == 0) break;
+      for (int t = 0; t < tiles; ++t) {
+        const int w = t & 1;
+        if (is_s) {
+          ok = wait(&sfree[w], (~turns >> w) & 1, 3) && wait(&kfull[s], ph, 4);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint64_t dk = dk0 + s * (2 * F::kOperand >> 4), dq = dq0 + qb * (F::kQ >> 4);
+            const uint32_t d = tmem + w * NQ;
 #pragma unroll
-          for (int p = 0; p < F::kQPieces; ++p)
+            for (int p = 0; p < F::kQPieces; ++p)
 #pragma unroll
-            for (int k = 0; k < kStepsS; ++k) {
-              const int part = k * 32 / F::kRow, off = k * 32 % F::kRow;
-              const uint64_t da = dk + ((part * F::kPart + off) >> 4), db = dq + (((p * F::kParts + part) * F::kQPart + off) >> 4);
-              if constexpr (!kCodes)
-                ptx::tc_mma(d, da, db, idesc_s, k > 0);
-              else if (p + k == 0)
-                ptx::tc_mma_fp8<0>(d, da, db, idesc_s);
-              else
-                ptx::tc_mma_fp8<1>(d, da, db, idesc_s);
-            }
-          ptx::tc_commit(&sfull[ws]);
-        }
-        __syncwarp();
-        sS.step();
-      } else if (sO.n != sS.n && __all_sync(0xffffffffu, ptx::mbar_test(&pready[wo], (sO.turns >> wo) & 1) && ptx::mbar_test(&vfull[sO.s], sO.ph))) {
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          const uint64_t dv = dv0 + sO.s * (2 * F::kOperand >> 4), dp = dp0 + wo * (F::kP >> 4);
-          const uint32_t d = tmem + 2 * NQ + wo * F::kO, more = sO.t >= 2;
-#pragma unroll
-          for (int k = 0; k < kStepsO; ++k) {
-            const uint64_t da = dv + (k * kStepTokens * F::kRow >> 4), db = dp + (k * kStepTokens * 128 >> 4);
-            if constexpr (!kCodes)
-              ptx::tc_mma(d, da, db, idesc_o, k > 0 ? 1 : more);
-            else if (k == 0)
-              ptx::tc_mma_fp8_if(d, da, db, idesc_o, more);
-            else
-              ptx::tc_mma_fp8<1>(d, da, db, idesc_o);
+              for (int k = 0; k < kStepsS; ++k) {
+                const int row = k * 32 / F::kRow, off = k * 32 % F::kRow;
+                const uint64_t da = dk + ((row * F::kPart + off) >> 4), db = dq + (((p * F::kParts + row) * F::kQPart + off) >> 4);
+                if constexpr (!kCodes)
+                  ptx::tc_mma(d, da, db, idesc_s, k > 0);
+                else if (p + k == 0)
+                  ptx::tc_mma_fp8<0>(d, da, db, idesc_s);
+                else
+                  ptx::tc_mma_fp8<1>(d, da, db, idesc_s);
+              }
+            ptx::tc_commit(&sfull[w]);
           }
-          ptx::tc_commit(&empty[sO.s]);
-          ptx::tc_commit(&pdone[wo]);
+        } else {
+          ok = wait(&pready[w], (turns >> w) & 1, 5) && wait(&vfull[s], ph, 6);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint64_t dv = dv0 + s * (2 * F::kOperand >> 4), dp = dp0 + w * (F::kP >> 4);
+            const uint32_t d = tmem + 2 * NQ + w * F::kO, more = t >= 2;
+#pragma unroll
+            for (int k = 0; k < kStepsO; ++k) {
+              const uint64_t da = dv + (k * kStepTokens * F::kRow >> 4), db = dp + (k * kStepTokens * 128 >> 4);
+              if constexpr (!kCodes)
+                ptx::tc_mma(d, da, db, idesc_o, k > 0 ? 1 : more);
+              else if (k == 0)
+                ptx::tc_mma_fp8_if(d, da, db, idesc_o, more);
+              else
+                ptx::tc_mma_fp8<1>(d, da, db, idesc_o);
+            }
+            ptx::tc_commit(&empty[s]);
+            ptx::tc_commit(&pdone[w]);
+          }
         }
         __syncwarp();
-        if (sO.t == 0) sO.tiles = parts[sO.part & 1].tiles;
-        sO.step();
-      } else {
-        if ((polls & 255u) == 0 && (*abort_flag || clock64() - since > kWaitLimit)) {
-          if (lane == 0) fail(2);
-          break;
-        }
-        continue;
+        turns ^= 1u << w;
+        if (++s == (uint32_t)F::kStages) s = 0, ph ^= 1;
       }
-      since = clock64();
     }
     __syncwarp();
   } else {
@@ -555,21 +558,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b = part & 1;
       const bool more = walk.next(a, NQ);
       if (!__all_sync(0xffffffffu, ptx::mbar_wait_cycles(&qempty[b], ~(part >> 1) & 1, abort_flag, kWaitLimit))) {
-        if (lane == 0) fail(4);
+        if (lane == 0) fail(7);
         break;
       }
       if (!more) {
         if (lane == 0) {
-          if (warp == 10) parts[b].tiles = 0;
+          parts[b].tiles = 0;
           ptx::mbar_arrive(&qfull[b]);
         }
         break;
       }
-      const int columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
-      if (warp == 10 && lane == 0) {
+      if (lane == 0) {
         Part p;
         p.r = walk.r, p.base = walk.q.base, p.rows = walk.q.rows, p.head = walk.head;
-        p.tile = walk.tile, p.tiles = walk.tiles, p.columns = columns;
+        p.tile = walk.tile, p.tiles = walk.tiles, p.columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
         p.slot = walk.begins && walk.ends ? -1 : 2 * cta + walk.begins;
         parts[b] = p;
         if (walk.begins && !walk.ends) {  // so it is the last part here; unit u is CTA ((u + 1) ctas - 1) / total's
@@ -577,12 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.meta[cta] = make_int4(walk.r, walk.head * walk.q.chunks + walk.chunk, (int)((end * ctas - 1) / total) - cta + 1, 0);
         }
       }
-      for (int j = (warp - 10) * 32 + lane; j < walk.q.rows; j += 64)
-        words[b][j] = a.tree ? a.tree[walk.q.lo + j] : ~0ull >> (63 - j);
+      for (int j = lane; j < walk.q.rows; j += 32) words[b][j] = a.tree ? a.tree[walk.q.lo + j] : ~0ull >> (63 - j);
       if (part > 0)
-        prepare_q<kCodes, D, NQ>(a, walk, sQ + b * F::kQ, warp - 10, 2, qs[b], row_of[b], out_at[b]);
+        prepare_q<kCodes, D, NQ>(a, walk, sQ + b * F::kQ, 0, 1, qs[b], row_of[b], out_at[b]);
       else
-        ptx::named_sync(4, kSoft + 64);  // the softmax's warps, which have nothing else to do yet
+        ptx::named_sync(6, kSoft + 32);  // the softmax's warps, which have nothing else to do yet
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&qfull[b]);
@@ -591,11 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
     ptx::reg_inc<kRegsHigh>();
-    // ---- softmax ----
-    const int w = warp >> 2, quarter = warp & 3, token = quarter * 32 + lane;
-    const int group_threads = kSoft / 2, bar_own = 1 + w, bar_both = 3;
-    const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + w * NQ,
-                   tO = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * NQ;
+    // ---- softmax: tiles w, w + 2, .. of a part and half of the columns a warpgroup ----
+    constexpr int HQ = NQ / 2, kAll = 5;
+    const int wg = warp >> 2, w = wg >> 1, h = wg & 1, quarter = warp & 3, token = quarter * 32 + lane;
+    const int own = 1 + wg;  // its barrier
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), tS = lanes + w * NQ + h * HQ, tO = lanes + 2 * NQ;
     const int box_shift = min(a.pool.shift, 7);
     const uint32_t all_ok = (1u << (kTile >> box_shift)) - 1;
     uint32_t n0 = 0, turn = 0;  // the CTA's tiles before this part, this warpgroup's so far
@@ -603,163 +604,162 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit)) fail(what);  // the loops run on: every later wait ends at once
     };
     if (walk.next(a, NQ)) {
-      prepare_q<kCodes, D, NQ>(a, walk, sQ, warp, 8, qs[0], row_of[0], out_at[0]);
+      prepare_q<kCodes, D, NQ>(a, walk, sQ, warp, kSoftWarps, qs[0], row_of[0], out_at[0]);
       ptx::fence_proxy_async_smem();
-      ptx::named_arrive(4, kSoft + 64);
+      ptx::named_arrive(6, kSoft + 32);
     }
     for (uint32_t part = 0;; ++part) {
       const int b = part & 1;
-      if (token < NQ) nref[w][token] = 0.f, set[w][token] = false;
+      // this warpgroup's references and their like
+      float* my_nref = &nref[w][h * HQ];
+      float* my_delta = &delta[w][h * HQ];
+      float* my_factor = &factor[w][h * HQ];
+      if (token < HQ) my_nref[token] = 0.f, set[w][h * HQ + token] = false;
       const bool got = ptx::mbar_wait_cycles(&qfull[b], (part >> 1) & 1, abort_flag, kWaitLimit);
       if (!got) fail(10);
-      if (ptx::named_any(bar_both, kSoft, !got)) break;
+      if (ptx::named_any(kAll, kSoft, !got)) break;
       const int tiles = parts[b].tiles, tile0 = parts[b].tile;
       if (tiles == 0) break;
-      const int64_t base = parts[b].base, len = base + parts[b].rows;
+      const int base = parts[b].base, len = base + parts[b].rows;
 
-      uint64_t l2[NQ / 2];
+      uint64_t l2[HQ / 2];
 #pragma unroll
-      for (int i = 0; i < NQ / 2; ++i) l2[i] = 0;
+      for (int i = 0; i < HQ / 2; ++i) l2[i] = 0;
       bool unset = true;  // a column has no reference yet
+#pragma unroll 1
       for (int t = w; t < tiles; t += 2) {
         const uint32_t n = n0 + t, s = n % F::kStages, ph = (n / F::kStages) & 1;
-        wait(&kfull[s], ph, 6);
-        const int64_t pos0 = (int64_t)(tile0 + t) * kTile, pos = pos0 + token;
-        const bool masked = pos0 + kTile > base || okmask[s] != all_ok;
-        const bool held = pos < len && ((okmask[s] >> (token >> box_shift)) & 1);
+        wait(&kfull[s], ph, 11);
+        const int pos0 = (tile0 + t) * kTile, pos = pos0 + token;
+        const uint32_t have = okmask[s];
+        const bool masked = pos0 + kTile > base || have != all_ok;
+        const bool held = pos < len && ((have >> (token >> box_shift)) & 1);
         float k_scale = 1.f, v_log = 0.f, v_inv = 1.f;
         if (kCodes && (!masked || held)) {
           k_scale = sScale[s * 2 * kTile + token];
           float v = sScale[s * 2 * kTile + kTile + token];
           if (v < 1.17549435e-38f) v = 1.17549435e-38f;  // 0 of a cache that was cleared
           v_log = __log2f(v);
-          v_inv = __frcp_rn(v);
+          v_inv = ptx::rcp(v);
         }
-        if (masked) {
+        if (masked && h == 0) {
           // what no row or only some see must not reach the others through 0 * NaN
-          wait(&vfull[s], ph, 7);
+          wait(&vfull[s], ph, 12);
           uint8_t* row = sStage + s * 2 * F::kOperand + F::kOperand + token * F::kRow;
           if (!held || pos >= base) {
             uint32_t any = 0;
-#pragma unroll
-            for (int p = 0; p < F::kParts; ++p)
-#pragma unroll
-              for (int i = 0; i < F::kRow / 16; ++i) {
-                uint4* at = reinterpret_cast<uint4*>(row + p * F::kPart) + i;
-                if (held) {
-                  const uint4 x = *at;
-                  const uint4 m = make_uint4(non_finite<kCodes>(x.x), non_finite<kCodes>(x.y), non_finite<kCodes>(x.z),
-                                             non_finite<kCodes>(x.w));
-                  if (m.x | m.y | m.z | m.w) {
-                    *at = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
-                    any = 1;
-                  }
-                } else {
-                  *at = make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+            for (int i = 0; i < F::kParts * F::kRow / 16; ++i) {
+              uint4* at = reinterpret_cast<uint4*>(row + i * 16 / F::kRow * F::kPart + i * 16 % F::kRow);
+              if (held) {
+                const uint4 x = *at;
+                const uint4 m = make_uint4(non_finite<kCodes>(x.x), non_finite<kCodes>(x.y), non_finite<kCodes>(x.z),
+                                           non_finite<kCodes>(x.w));
+                if (m.x | m.y | m.z | m.w) {
+                  *at = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
+                  any = 1;
                 }
+              } else {
+                *at = make_uint4(0, 0, 0, 0);
               }
+            }
             if (any) atomicOr(&hidden[b], 1ull << (pos - base));
           }
         }
-        wait(&sfull[w], turn & 1, 8);
+        wait(&sfull[w], turn & 1, 13);
         ++turn;
         ptx::tc_fence_after();
         // y, less the reference so far
-        uint64_t x2[NQ / 2];
+        uint64_t x2[HQ / 2];
         {
           const uint64_t ks2 = ptx::pack2(k_scale, k_scale), vl2 = ptx::pack2(v_log, v_log);
-          float v[2][16];
-          ptx::tmem_ld16(tS, v[0]);
+          float v[HQ];
+          load_columns<HQ>(tS, v);
+          ptx::tmem_ld_wait<HQ>(v);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sfree[w]);
 #pragma unroll
-          for (int c = 0; c < NQ / 16; ++c) {
-            ptx::tmem_ld_wait16(v[c & 1]);
-            if (c + 1 < NQ / 16) ptx::tmem_ld16(tS + (c + 1) * 16, v[(c + 1) & 1]);
+          for (int i = 0; i < HQ / 2; i += 2) {
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&qs[b][h * HQ + 2 * i]);
+            const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&my_nref[2 * i]);  // 0 before they are set
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&qs[b][c * 16 + 2 * i]);
-              ulonglong2 r = make_ulonglong2(0, 0);
-              if (t >= 2) r = *reinterpret_cast<const ulonglong2*>(&nref[w][c * 16 + 2 * i]);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint64_t y = ptx::mul2(ptx::pack2(v[c & 1][2 * (i + h)], v[c & 1][2 * (i + h) + 1]), h ? u.y : u.x);
-                if (kCodes) y = ptx::fma2(y, ks2, vl2);
-                x2[c * 8 + i + h] = ptx::add2(y, h ? r.y : r.x);
-              }
+            for (int e = 0; e < 2; ++e) {
+              uint64_t y = ptx::mul2(ptx::pack2(v[2 * (i + e)], v[2 * (i + e) + 1]), e ? u.y : u.x);
+              if (kCodes) y = ptx::fma2(y, ks2, vl2);
+              x2[i + e] = ptx::add2(y, e ? r.y : r.x);
             }
           }
         }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sfree[w]);
         if (masked) {
-          const int node = (int)(pos - base);
+          const int node = pos - base;
 #pragma unroll
-          for (int i = 0; i < NQ / 2; ++i) {
-            float2 x = ptx::unpack2(x2[i]);
-            const bool see0 = held && (pos < base || ((words[b][row_of[b][2 * i]] >> node) & 1));
-            const bool see1 = held && (pos < base || ((words[b][row_of[b][2 * i + 1]] >> node) & 1));
+          for (int i = 0; i < HQ / 2; ++i) {
+            const float2 x = ptx::unpack2(x2[i]);
+            const bool see0 = held && (pos < base || ((words[b][row_of[b][h * HQ + 2 * i]] >> node) & 1));
+            const bool see1 = held && (pos < base || ((words[b][row_of[b][h * HQ + 2 * i + 1]] >> node) & 1));
             x2[i] = ptx::pack2(see0 ? x.x : -INFINITY, see1 ? x.y : -INFINITY);
           }
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NQ / 2; ++i) {
+        for (int i = 0; i < HQ / 2; ++i) {
           const float2 x = ptx::unpack2(x2[i]);
           top = fmaxf(top, fmaxf(x.x, x.y));
         }
-        const bool raise = ptx::named_any(bar_own, group_threads, top > kRaise<kCodes>) || unset;
+        const bool raise = ptx::named_any(own, 128, top > kRaise<kCodes>) || unset;
         if (turn > 1) {  // the tile before is in O, and its weights have been read
-          wait(&pdone[w], turn & 1, 9);
+          wait(&pdone[w], turn & 1, 14);
           ptx::tc_fence_after();
         }
         if (raise) {
           // the columns' largest, new references, what was summed so far brought to them
+          {
+            float v[HQ];
 #pragma unroll
-          for (int c = 0; c < NQ; c += 32) {
-            constexpr int W = NQ < 32 ? NQ : 32;
-            float v[W];
-#pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-              const float2 x = ptx::unpack2(x2[c / 2 + i]);
+            for (int i = 0; i < HQ / 2; ++i) {
+              const float2 x = ptx::unpack2(x2[i]);
               v[2 * i] = x.x;
               v[2 * i + 1] = x.y;
             }
-            const float m = over_lanes<W>(v, [](float x, float y) { return fmaxf(x, y); });
-            if (lane < W) warp_top[warp][c + lane] = m;
+            const float m = over_lanes<HQ>(v, [](float x, float y) { return fmaxf(x, y); });
+            if (lane < HQ) warp_top[warp][lane] = m;
           }
-          ptx::named_sync(bar_own, group_threads);
-          bool open = false;
-          if (token < NQ) {
-            const float* p = &warp_top[w * 4][token];
-            const float m = fmaxf(fmaxf(p[0], p[NQ]), fmaxf(p[2 * NQ], p[3 * NQ]));
+          ptx::named_sync(own, 128);
+          bool none = false;
+          if (token < HQ) {
+            const float m = fmaxf(fmaxf(warp_top[wg * 4][token], warp_top[wg * 4 + 1][token]),
+                                  fmaxf(warp_top[wg * 4 + 2][token], warp_top[wg * 4 + 3][token]));
             float d = 0.f;
-            if (set[w][token])
+            if (set[w][h * HQ + token])
               d = fmaxf(0.f, m - kHead<kCodes>);
             else if (m > -INFINITY)
-              d = m - kHead<kCodes>, set[w][token] = true;
+              d = m - kHead<kCodes>, set[w][h * HQ + token] = true;
             else
-              open = true;
-            delta[w][token] = -d;
-            factor[w][token] = exp2f(-d);
-            nref[w][token] -= d;
+              none = true;
+            my_delta[token] = -d;
+            my_factor[token] = exp2f(-d);
+            my_nref[token] -= d;
           }
-          unset = ptx::named_any(bar_own, group_threads, open);
+          unset = ptx::named_any(own, 128, none);
 #pragma unroll
-          for (int i = 0; i < NQ / 2; ++i) {
-            x2[i] = ptx::add2(x2[i], *reinterpret_cast<const uint64_t*>(&delta[w][2 * i]));
-            if (t >= 2) l2[i] = ptx::mul2(l2[i], *reinterpret_cast<const uint64_t*>(&factor[w][2 * i]));
+          for (int i = 0; i < HQ / 2; ++i) {
+            x2[i] = ptx::add2(x2[i], *reinterpret_cast<const uint64_t*>(&my_delta[2 * i]));
+            if (t >= 2) l2[i] = ptx::mul2(l2[i], *reinterpret_cast<const uint64_t*>(&my_factor[2 * i]));
           }
           if (t >= 2) {
 #pragma unroll
-            for (int c = 0; c < F::kO / 16; ++c) {
-              float v[16];
-              uint32_t u[16];
-              ptx::tmem_ld16(tO + w * F::kO + c * 16, v);
-              ptx::tmem_ld_wait16(v);
+            for (int p = 0; p < F::kPPieces; ++p)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * factor[w][c * 16 % NQ + i]);
-              ptx::tmem_st16(tO + w * F::kO + c * 16, u);
-            }
+              for (int c = 0; c < HQ; c += 8) {
+                const uint32_t at = tO + w * F::kO + p * NQ + h * HQ + c;
+                float v[8];
+                ptx::tmem_ld8(at, v);
+                ptx::tmem_ld_wait<8>(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= my_factor[c + i];
+                ptx::tmem_st8(at, v);
+              }
             ptx::tmem_st_wait();
           }
         }
@@ -767,48 +767,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* prow = sP + w * F::kP + token * 128;
         const uint64_t vi2 = ptx::pack2(v_inv, v_inv);
 #pragma unroll
-        for (int c = 0; c < NQ / 16; ++c) {
-          uint32_t h[8], r1[8], c3[8];
+        for (int c = 0; c < HQ; c += 8) {
+          uint32_t hh[4], r1[4], c3[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 x = ptx::unpack2(x2[c * 8 + i]);
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = ptx::unpack2(x2[c / 2 + i]);
             const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
             const uint64_t p2 = ptx::pack2(p0, p1);
-            uint64_t& l = l2[c * 8 + i];
+            uint64_t& l = l2[c / 2 + i];
             if (!kCodes) {
               l = ptx::add2(l, p2);
             } else if (!masked) {
               l = ptx::fma2(p2, vi2, l);
             } else {  // a hidden row's scale may be NaN
-              const float2 b = ptx::unpack2(l);
-              l = ptx::pack2(x.x == -INFINITY ? b.x : fmaf(p0, v_inv, b.x), x.y == -INFINITY ? b.y : fmaf(p1, v_inv, b.y));
+              const float2 o = ptx::unpack2(l);
+              l = ptx::pack2(x.x == -INFINITY ? o.x : fmaf(p0, v_inv, o.x), x.y == -INFINITY ? o.y : fmaf(p1, v_inv, o.y));
             }
             if constexpr (kCodes) {
-              h[i] = half2_bits(__floats2half2_rn(p0, p1));
-              r1[i] = half2_bits(__hsub2(bits_half2(h[i]), bits_half2(h[i] & 0xFF00FF00u)));
+              hh[i] = half2_bits(__floats2half2_rn(p0, p1));
+              r1[i] = half2_bits(__hsub2(bits_half2(hh[i]), bits_half2(hh[i] & 0xFF00FF00u)));
               c3[i] = e5m2x2(half2_bits(__hsub2(bits_half2(r1[i]), bits_half2(r1[i] & 0xFF00FF00u))));
             } else {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-              h[i] = *reinterpret_cast<const uint32_t*>(&b);
+              const __nv_bfloat162 o = __floats2bfloat162_rn(p0, p1);
+              hh[i] = *reinterpret_cast<const uint32_t*>(&o);
             }
           }
-          auto store = [&](uint32_t byte, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
-            *reinterpret_cast<uint4*>(prow + byte / 128 * F::kPCol + (((byte % 128 >> 4) ^ (token & 7)) << 4)) = make_uint4(x, y, z, u);
+          // 16-byte unit u of row r lies at u ^ (r % 8)
+          auto place = [&](uint32_t byte) {
+            return prow + byte / 128 * F::kPCol + ((((byte % 128) >> 4) ^ (token & 7)) << 4) + (byte & 15);
           };
           if constexpr (kCodes) {
-            uint32_t b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = __byte_perm(h[2 * i], h[2 * i + 1], 0x7531);
-            store(c * 16, b[0], b[1], b[2], b[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = __byte_perm(r1[2 * i], r1[2 * i + 1], 0x7531);
-            store(NQ + c * 16, b[0], b[1], b[2], b[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = c3[2 * i] | (c3[2 * i + 1] << 16);
-            store(2 * NQ + c * 16, b[0], b[1], b[2], b[3]);
+            const uint32_t byte = h * HQ + c;
+            *reinterpret_cast<uint2*>(place(byte)) = make_uint2(__byte_perm(hh[0], hh[1], 0x7531), __byte_perm(hh[2], hh[3], 0x7531));
+            *reinterpret_cast<uint2*>(place(NQ + byte)) =
+                make_uint2(__byte_perm(r1[0], r1[1], 0x7531), __byte_perm(r1[2], r1[3], 0x7531));
+            *reinterpret_cast<uint2*>(place(2 * NQ + byte)) =
+                make_uint2(__byte_perm(c3[0], c3[1], 0x5410), __byte_perm(c3[2], c3[3], 0x5410));
           } else {
-            store(c * 32, h[0], h[1], h[2], h[3]);
-            store(c * 32 + 16, h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4*>(place((h * HQ + c) * 2)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
           }
         }
         ptx::fence_proxy_async_smem();
@@ -817,84 +813,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&pready[w]);
       }
 
-      // ---- the part's end: sums of both warpgroups, O joined and written ----
+      // ---- the part's end: sums of both tile sequences, O joined and written ----
       n0 += tiles;
-      const bool has[2] = {true, tiles > 1};
-      if (has[w]) wait(&pdone[w], (turn - 1) & 1, 11);
+      const bool two = tiles > 1;  // both have a tile
+      if (w == 0 || two) wait(&pdone[w], (turn - 1) & 1, 15);
+      {
+        float v[HQ];
 #pragma unroll
-      for (int c = 0; c < NQ; c += 32) {
-        constexpr int W = NQ < 32 ? NQ : 32;
-        float v[W];
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-          const float2 x = ptx::unpack2(l2[c / 2 + i]);
+        for (int i = 0; i < HQ / 2; ++i) {
+          const float2 x = ptx::unpack2(l2[i]);
           v[2 * i] = x.x;
           v[2 * i + 1] = x.y;
         }
-        const float sum = over_lanes<W>(v, [](float x, float y) { return x + y; });
-        if (lane < W) warp_top[warp][c + lane] = sum;
+        const float sum = over_lanes<HQ>(v, [](float x, float y) { return x + y; });
+        if (lane < HQ) warp_top[warp][lane] = sum;
       }
-      ptx::named_sync(bar_both, kSoft);
+      ptx::named_sync(kAll, kSoft);
       ptx::tc_fence_after();
       const unsigned long long bad_rows = hidden[b];
       if (threadIdx.x == 0) hidden[b ^ 1] = 0;
       const int slot = parts[b].slot, columns = parts[b].columns;
       const bool whole = slot < 0;
       if (threadIdx.x < NQ) {
-        const int c = threadIdx.x;
-        float ref[2], l[2], m = -INFINITY;
+        const int c = threadIdx.x, half = c / HQ, i = c % HQ;
+        float ref[2], l[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const float* p = &warp_top[g * 4][c];
+          const int first = (g * 2 + half) * 4;
           ref[g] = set[g][c] ? -nref[g][c] : -INFINITY;
-          l[g] = has[g] ? p[0] + p[NQ] + p[2 * NQ] + p[3 * NQ] : 0.f;
-          if (has[g]) m = fmaxf(m, ref[g]);
+          l[g] = (warp_top[first][i] + warp_top[first + 1][i]) + (warp_top[first + 2][i] + warp_top[first + 3][i]);
         }
-        float sum = 0.f;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float f = !has[g] ? 0.f : ref[g] == m ? 1.f : exp2f(ref[g] - m);
-          coef[g][c] = f;
-          if (has[g]) sum += f * l[g];
-        }
-        norm[c] = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        const float m = two ? fmaxf(ref[0], ref[1]) : ref[0];
+        const float f0 = ref[0] == m ? 1.f : exp2f(ref[0] - m), f1 = !two ? 0.f : ref[1] == m ? 1.f : exp2f(ref[1] - m);
+        const float sum = two ? f0 * l[0] + f1 * l[1] : l[0];
+        const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        coef[0][c] = f0 * inv;
+        coef[1][c] = f1 * inv;
         if (!whole) a.stat[(int64_t)slot * NQ + c] = make_float2(m, sum);
       }
-      ptx::named_sync(bar_both, kSoft);
-      const int d = quarter * 32 + lane;
-      if (quarter * 32 < D) {
-        constexpr int W = NQ / 2 < 16 ? 8 : 16;  // columns at a time
-#pragma unroll 1
-        for (int c0 = w * (NQ / 2); c0 < (w + 1) * (NQ / 2); c0 += W) {
-          if (c0 >= columns) break;
-          // sixteen columns are loaded; of NQ = 16 the warpgroup takes its eight
-          const int first = W == 8 ? 0 : c0;
-          float v0[16], v1[16];
-          load_sum<F::kPPieces>(tO + first, NQ, v0);
-          if (has[1]) load_sum<F::kPPieces>(tO + F::kO + first, NQ, v1);
+      ptx::named_sync(kAll, kSoft);
+      // a quarter of the columns a warpgroup, eight at least
+      constexpr int W = NQ >= 32 ? NQ / 4 : 8;
+      const int d = quarter * 32 + lane, c0 = wg * W;
+      if (quarter * 32 < D && c0 < columns) {
+        float v0[W], v1[W];
+        load_sum<F::kPPieces, W>(tO + c0, NQ, v0);
+        if (two) load_sum<F::kPPieces, W>(tO + F::kO + c0, NQ, v1);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = first + i;
-            if (W == 8 && (i >> 3) != w) continue;
-            if (c >= columns) continue;
-            float o = coef[0][c] * v0[i];
-            if (has[1]) o = fmaf(coef[1][c], v1[i], o);
-            if (bad_rows) o += non_finite_v<kCodes, D>(a, parts[b].r, parts[b].base, parts[b].head, bad_rows & words[b][row_of[b][c]], d);
-            if (whole)
-              a.out[out_at[b][c] + d] = __float2bfloat16_rn(o * norm[c]);
-            else
-              a.part[((int64_t)slot * NQ + c) * D + d] = o;
-          }
+        for (int i = 0; i < W; ++i) {
+          const int c = c0 + i;
+          if (c >= columns) break;
+          float o = coef[0][c] * v0[i];
+          if (two) o = fmaf(coef[1][c], v1[i], o);
+          if (bad_rows) o += non_finite_v<kCodes, D>(a, parts[b].r, parts[b].base, parts[b].head, bad_rows & words[b][row_of[b][c]], d);
+          if (whole)
+            a.out[out_at[b][c] + d] = __float2bfloat16_rn(o);
+          else
+            a.part[((int64_t)slot * NQ + c) * D + d] = o;
         }
       }
       ptx::tc_fence_before();
-      ptx::named_sync(bar_both, kSoft);  // O may be written again
+      ptx::named_sync(kAll, kSoft);  // O may be written again
       if (lane == 0) ptx::mbar_arrive(&qempty[b]);
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kSoftWarps + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, F::kTmemCols);
   }
