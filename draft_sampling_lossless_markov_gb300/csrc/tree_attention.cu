@@ -220,63 +220,75 @@ __device__ __forceinline__ void prepare_q(const TreeArgs& a, const Walk& walk, u
   using F = Form<kCodes, D, NQ>;
   constexpr int E = D / 8, V = E / 8;  // elements, 16-byte vectors of a lane
   const int lane = threadIdx.x & 31, l = lane & 7, columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
-#pragma unroll 2
-  for (int c = w * 4 + (lane >> 3); c < NQ; c += warps * 4) {
-    const int col = walk.chunk * NQ + c;
-    const int j = c < columns ? (int)(col * a.group_inv >> 32) : 0, head = walk.head * a.group + col - j * a.group;
-    uint4 v[V];
+  constexpr int kBatch = NQ >= 64 && V == 2 ? 4 : NQ / 16;  // column groups whose loads are on their way at a time
+  for (int g0 = w; g0 < NQ / 4; g0 += warps * kBatch) {
+    uint4 all[kBatch][V];
+    int rows[kBatch], heads[kBatch];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      v[i] = c < columns ? *reinterpret_cast<const uint4*>(a.q + (int64_t)(walk.q.lo + j) * a.ldq + head * D + l * E + i * 8)
-                         : make_uint4(0, 0, 0, 0);
-    uint32_t* x = reinterpret_cast<uint32_t*>(v);
-    uint32_t top = 0;  // the largest magnitude's bits; infinities and NaN are above all others
+    for (int u = 0; u < kBatch; ++u) {
+      const int c = (g0 + u * warps) * 4 + (lane >> 3), col = walk.chunk * NQ + c;
+      rows[u] = c < columns ? (int)(col * a.group_inv >> 32) : 0;
+      heads[u] = walk.head * a.group + col - rows[u] * a.group;
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[i] & 0x7FFF7FFFu);
-    top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool fin = top < 0x7F80u;
-    if (!fin) {  // the column's scores are NaN through its factor
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) x[i] = 0;
-      top = 0;
+      for (int i = 0; i < V; ++i)
+        all[u][i] = c < columns ? *reinterpret_cast<const uint4*>(a.q + (int64_t)(walk.q.lo + rows[u]) * a.ldq + heads[u] * D + l * E + i * 8)
+                                : make_uint4(0, 0, 0, 0);
     }
-    float unit = a.scale * kLog2e;
-    if constexpr (kCodes) {
-      // top 2^k in 128 .. 256, k up to 120 so that both powers are normal
-      const int k = top ? min(7 - ((int)(top >> 7) - 127), 120) : 0;
-      const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-      unit *= __uint_as_float((uint32_t)(127 - k) << 23);
-      uint32_t p1[E / 4], p2[E / 4];
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        const float2 y = make_float2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xFFFF0000u) * up);
-        const uint32_t c1 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-        const float2 z = e4m3x2_values(c1);
-        const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
-        p1[i / 2] = (i & 1) ? p1[i / 2] | c1 << 16 : c1;
-        p2[i / 2] = (i & 1) ? p2[i / 2] | c2 << 16 : c2;
+    for (int u = 0; u < kBatch; ++u) {
+      const int c = (g0 + u * warps) * 4 + (lane >> 3);
+      if (c >= NQ) break;
+      const int j = rows[u], head = heads[u];
+      uint4 (&v)[V] = all[u];
+      uint32_t* x = reinterpret_cast<uint32_t*>(v);
+      uint32_t top = 0;  // the largest magnitude's bits; infinities and NaN are above all others
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[i] & 0x7FFF7FFFu);
+      top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool fin = top < 0x7F80u;
+      if (!fin) {  // the column's scores are NaN through its factor
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) x[i] = 0;
+        top = 0;
       }
-      const uint32_t at = swizzled<F::kRow>(c * F::kRow + l * E);
-      if constexpr (E == 16) {
-        *reinterpret_cast<uint4*>(dst + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-        *reinterpret_cast<uint4*>(dst + F::kQPart + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+      float unit = a.scale * kLog2e;
+      if constexpr (kCodes) {
+        // top 2^k in 128 .. 256, k up to 120 so that both powers are normal
+        const int k = top ? min(7 - ((int)(top >> 7) - 127), 120) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+        unit *= __uint_as_float((uint32_t)(127 - k) << 23);
+        uint32_t p1[E / 4], p2[E / 4];
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          const float2 y = make_float2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xFFFF0000u) * up);
+          const uint32_t c1 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+          const float2 z = e4m3x2_values(c1);
+          const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
+          p1[i / 2] = (i & 1) ? p1[i / 2] | c1 << 16 : c1;
+          p2[i / 2] = (i & 1) ? p2[i / 2] | c2 << 16 : c2;
+        }
+        const uint32_t at = swizzled<F::kRow>(c * F::kRow + l * E);
+        if constexpr (E == 16) {
+          *reinterpret_cast<uint4*>(dst + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+          *reinterpret_cast<uint4*>(dst + F::kQPart + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+        } else {
+          *reinterpret_cast<uint2*>(dst + at) = make_uint2(p1[0], p1[1]);
+          *reinterpret_cast<uint2*>(dst + F::kQPart + at) = make_uint2(p2[0], p2[1]);
+        }
       } else {
-        *reinterpret_cast<uint2*>(dst + at) = make_uint2(p1[0], p1[1]);
-        *reinterpret_cast<uint2*>(dst + F::kQPart + at) = make_uint2(p2[0], p2[1]);
-      }
-    } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int byte = l * E * 2 + i * 16;
-        *reinterpret_cast<uint4*>(dst + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) = v[i];
+        for (int i = 0; i < V; ++i) {
+          const int byte = l * E * 2 + i * 16;
+          *reinterpret_cast<uint4*>(dst + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) = v[i];
+        }
       }
-    }
-    if (l == 0) {
-      qs[c] = c < columns ? (fin ? unit : NAN) : 0.f;
-      row_of[c] = (uint8_t)j;
-      out_at[c] = (int64_t)(walk.q.lo + j) * a.ldo + head * D;
+      if (l == 0) {
+        qs[c] = c < columns ? (fin ? unit : NAN) : 0.f;
+        row_of[c] = (uint8_t)j;
+        out_at[c] = (int64_t)(walk.q.lo + j) * a.ldo + head * D;
+      }
     }
   }
 }
@@ -349,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < F::kStages; ++i) {
-      ptx::mbar_init(&kfull[i], 1);
+      ptx::mbar_init(&kfull[i], kCodes ? 33 : 1);  // and every lane's copies of scales
       ptx::mbar_init(&vfull[i], 1);
       ptx::mbar_init(&empty[i], 1);
     }
@@ -424,44 +436,54 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoftWarps) {
   ptx::reg_dec<kRegsLow>();
   if (warp == kSoftWarps) {
-    // ---- loads: a lane a page of the tile, for k, v and their scales ----
+    // ---- loads: a lane a page of k or v, four tokens' scales a lane; the page numbers a tile ahead ----
     const uint64_t policy = a.group * a.max_tree > NQ ? ptx::policy_evict_normal() : ptx::policy_evict_first();
     const int box_shift = min(a.pool.shift, 7), box = 1 << box_shift, boxes = kTile >> box_shift;
-    const int i = lane & 7, what = lane >> 3;
+    const int i = lane & 7, what = (lane >> 3) & 1;
     uint32_t s = 0, ph = 1, n = 0;
     bool ok = true;
     while (ok && walk.next(a, NQ)) {
-      const int64_t len = (int64_t)walk.q.base + walk.q.rows;
+      const int len = walk.q.base + walk.q.rows;
+      const int32_t* table = a.pool.table + walk.r * a.pool.table_ld;
+      int pos = walk.tile * kTile + (i << box_shift);
+      // (positions below len have an entry: request_at)
+      int32_t page = i < boxes && pos < len ? table[pos >> a.pool.shift] : -1;
       for (int t = 0; t < walk.tiles; ++t) {
-        const int64_t pos = (int64_t)(walk.tile + t) * kTile + ((int64_t)i << box_shift);
-        int32_t row = -1;
-        const bool wanted = i < boxes && pos < len;
-        if (wanted) row = pool_row(a.pool, walk.r, pos);
+        const int32_t here = page, at = pos;
+        pos += kTile;
+        page = i < boxes && pos < len && t + 1 < walk.tiles ? table[pos >> a.pool.shift] : -1;
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(&empty[s], ph, abort_flag, kWaitLimit));
         if (!ok) {
           if (lane == 0) fail(1);
           break;
         }
-        if (wanted && row < 0 && what == 0 && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, walk.r);
-        const uint32_t live = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu, count = __popc(live);
+        const bool wanted = i < boxes && at < len;
+        const bool live = wanted && here >= 0 && here < a.pool.n_pages;
+        if (wanted && !live && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, walk.r);
+        const int32_t row = live ? ((here * a.pool.heads + walk.head) << a.pool.shift) + (at & ((1 << a.pool.shift) - 1)) : -1;
+        const uint32_t mask = __ballot_sync(0xffffffffu, live) & 0xFFu, bytes = __popc(mask) * (box * D * F::kElem);
         if (lane == 0) {
-          okmask[s] = live;
-          ptx::mbar_expect_tx(&kfull[s], count * (box * D * F::kElem + (kCodes ? 2 * box * 4 : 0)));
-          ptx::mbar_expect_tx(&vfull[s], count * (box * D * F::kElem));
+          okmask[s] = mask;
+          ptx::mbar_expect_tx(&kfull[s], bytes);
+          ptx::mbar_expect_tx(&vfull[s], bytes);
         }
         __syncwarp();
-        if (row >= 0) {
-          row += walk.head << a.pool.shift;
-          uint8_t* stage = sStage + s * 2 * F::kOperand;
-          if (what < 2) {
+        uint8_t* stage = sStage + s * 2 * F::kOperand;
+        if (live && lane < 16) {
 #pragma unroll
-            for (int p = 0; p < F::kParts; ++p)
-              ptx::tma_load_2d(stage + what * F::kOperand + p * F::kPart + i * box * F::kRow, what ? &tmV : &tmK,
-                               what ? &vfull[s] : &kfull[s], p * (F::kRow / F::kElem), row, policy);
-          } else if (kCodes) {
-            ptx::bulk_load(sScale + s * 2 * kTile + (what - 2) * kTile + i * box,
-                           (what == 2 ? a.pool.k_scale : a.pool.v_scale) + row, box * 4, &kfull[s], policy);
+          for (int p = 0; p < F::kParts; ++p)
+            ptx::tma_load_2d(stage + what * F::kOperand + p * F::kPart + i * box * F::kRow, what ? &tmV : &tmK,
+                             what ? &vfull[s] : &kfull[s], p * (F::kRow / F::kElem), row, policy);
+        }
+        if constexpr (kCodes) {
+          const int32_t from = __shfl_sync(0xffffffffu, row, (4 * lane) >> box_shift);
+          if (from >= 0) {
+            const int32_t first = from + ((4 * lane) & (box - 1));
+            float* dst = sScale + s * 2 * kTile + 4 * lane;
+            ptx::cp_async16_cg(dst, a.pool.k_scale + first);
+            ptx::cp_async16_cg(dst + kTile, a.pool.v_scale + first);
           }
+          ptx::cp_async_arrive(&kfull[s]);
         }
         __syncwarp();
         ++n;
@@ -792,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               hh[i] = *reinterpret_cast<const uint32_t*>(&o);
             }
           }
-          // 16-byte unit u of row r lies at u ^ (r % 8)
+          // (16-byte unit u of row r lies at u ^ (r % 8))
           auto place = [&](uint32_t byte) {
             return prow + byte / 128 * F::kPCol + ((((byte % 128) >> 4) ^ (token & 7)) << 4) + (byte & 15);
           };
@@ -886,15 +908,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The items that several CTAs share: part 0 is the second slot of the CTA they begin in,
-// the others the first slots of those behind it.  A block takes a column of one of them at
-// a time, a thread an element of the head.
-constexpr int kJoinThreads = 192;
+// the others the first slots of those behind it.  A warp takes a column of one of them,
+// D / 32 elements a lane.
+constexpr int kJoinThreads = 256, kJoinCtas = 4;  // an SM
 template <int D, int NQ>
 __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, int ctas) {
   static_assert(kMaxCtas <= kJoinThreads, "a thread a CTA");
+  constexpr int E = D / 32;
   __shared__ int items[kMaxCtas], counts[kJoinThreads / 32];
-  __shared__ float tops[kJoinThreads / 32], share[kMaxCtas];
-  __shared__ float sums[kJoinThreads / 32];
   ptx::launch_dependents();
   ptx::grid_wait();
   const int t = threadIdx.x, warp = t / 32, lane = t % 32;
@@ -909,36 +930,49 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, in
   }
   if (mine) items[first + __popc(votes & ((1u << lane) - 1))] = t;
   __syncthreads();
-  for (int at = blockIdx.x; at < n * NQ; at += gridDim.x) {
+  for (int at = blockIdx.x * (kJoinThreads / 32) + warp; at < n * NQ; at += gridDim.x * (kJoinThreads / 32)) {
     const int cta = items[at / NQ], c = at % NQ;
     const int4 m = a.meta[cta];
+    const auto slot = [&](int p) { return (int64_t)(p ? 2 * (cta + p) : 2 * cta + 1) * NQ + c; };
     bool bad;
     const Request q = request_at(a, m.x, NQ, &bad);
-    const int head = m.y / q.chunks, chunk = m.y % q.chunks;
-    if (c >= q.rows * a.group - chunk * NQ) continue;
-    const int64_t slot = t ? 2 * (cta + t) : 2 * cta + 1;
-    float2 s = make_float2(-INFINITY, 0.f);
-    if (t < m.z) s = a.stat[slot * NQ + c];
-    float top = warp_max(s.x);
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-    for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, tops[w]);
-    const float f = s.x == top ? 1.f : exp2f(s.x - top);
-    if (t < m.z) share[t] = f;
-    const float sum = warp_sum(t < m.z ? f * s.y : 0.f);
-    if (lane == 0) sums[warp] = sum;
-    __syncthreads();
-    if (t < D) {
-      float total = 0.f, o = 0.f;
-      for (int w = 0; w < kJoinThreads / 32; ++w) total += sums[w];
-#pragma unroll 8
-      for (int p = 0; p < m.z; ++p)
-        o = fmaf(share[p], a.part[((int64_t)(p ? 2 * (cta + p) : 2 * cta + 1) * NQ + c) * D + t], o);
-      const int col = chunk * NQ + c;
-      a.out[(int64_t)(q.lo + col / a.group) * a.ldo + (head * a.group + col % a.group) * D + t] =
-          __float2bfloat16_rn(total == 0.f ? 0.f : o / total);
+    const int head = m.y / q.chunks, col = m.y % q.chunks * NQ + c, row = (int)(col * a.group_inv >> 32);
+    if (row >= q.rows) continue;
+    float ref = -INFINITY;
+    for (int p = lane; p < m.z; p += 32) ref = fmaxf(ref, a.stat[slot(p)].x);
+    ref = warp_max(ref);
+    float sum = 0.f, o[E] = {};
+    for (int p0 = 0; p0 < m.z; p0 += 32) {
+      float2 s = make_float2(-INFINITY, 0.f);
+      if (p0 + lane < m.z) s = a.stat[slot(p0 + lane)];
+      const float f = p0 + lane >= m.z ? 0.f : s.x == ref ? 1.f : exp2f(s.x - ref);
+      sum += f * s.y;
+#pragma unroll 4
+      for (int p = 0; p < min(32, m.z - p0); ++p) {
+        const float g = __shfl_sync(0xffffffffu, f, p);
+        const float* src = a.part + slot(p0 + p) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          o[0] = fmaf(g, x.x, o[0]), o[1] = fmaf(g, x.y, o[1]), o[2] = fmaf(g, x.z, o[2]), o[3] = fmaf(g, x.w, o[3]);
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          o[0] = fmaf(g, x.x, o[0]), o[1] = fmaf(g, x.y, o[1]);
+        }
+      }
     }
-    __syncthreads();
+    sum = warp_sum(sum);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t out[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+      out[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    __nv_bfloat16* dst = a.out + (int64_t)(q.lo + row) * a.ldo + (head * a.group + col - row * a.group) * D + lane * E;
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst) = out[0];
   }
 }
 
@@ -1015,7 +1049,7 @@ cudaError_t run(const dspark_kv_cache& c, const TreeArgs& t, const Dev& dev, cud
   const unsigned grid = (unsigned)std::min(dev.sms, kMaxCtas);
   if (const cudaError_t e = launch_overlapped(f, grid, kThreads, F::kSmem, 1, s, tmK, tmV, t); e != cudaSuccess) return e;
   count_launches(1);
-  const cudaError_t e = launch_overlapped(k_tree_join<D, NQ>, grid * 4, kJoinThreads, 0, 1, s, t, (int)grid);
+  const cudaError_t e = launch_overlapped(k_tree_join<D, NQ>, grid * kJoinCtas, kJoinThreads, 0, 1, s, t, (int)grid);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
