@@ -46,13 +46,8 @@ namespace dspark {
 namespace {
 
 constexpr int kTile = 128;           // tokens
-constexpr int kMaxCtas = 160;        // parts the workspace holds: two a CTA
-constexpr int kSoftWarps = 16;       // four warpgroups of the softmax: two a tile, each with half of the columns
-constexpr int kSoft = 32 * kSoftWarps;
-constexpr int kThreads = kSoft + 128;  // and the warps for loads, S, O and q
+constexpr int kMaxCtas = 320;        // parts the workspace holds: two a CTA
 constexpr int kItemCost = 2;         // what an item costs beside its tiles, in tiles
-// Registers of the softmax's threads and of the others, of the 96 a thread (640 threads) at launch.
-constexpr int kRegsHigh = 104, kRegsLow = 64;
 constexpr long long kWaitLimit = 4000000000ll;  // cycles, about two seconds
 // A column's largest exponent when its reference is set, and the exponent that raises it: 2^15 is in
 // fp16's range, bf16 weights have room up to 2^60.
@@ -89,16 +84,30 @@ struct Form {
   static constexpr int kQPieces = kCodes ? 2 : 1, kPPieces = kCodes ? 3 : 1;
   static constexpr uint32_t kQPart = NQ * kRow;
   static constexpr uint32_t kQ = kQPart * kParts * kQPieces;
-  static constexpr uint32_t kPCol = kTile * 128;                  // 128 bytes of P's row
-  static constexpr uint32_t kP = kPCol * ((NQ * kPPieces * kElem + 127) / 128);
+  // P's rows: the pieces side by side in 128 bytes; of 64 columns the third in rows of 64 bytes behind them
+  static constexpr int kPWide = NQ * kPPieces * kElem <= 128 ? NQ * kPPieces : 128 / kElem;
+  static constexpr int kPRest = NQ * kPPieces - kPWide;
+  static constexpr uint32_t kPCol = kTile * 128;
+  static constexpr uint32_t kP = kPCol + (kPRest > 0 ? kTile * 64 : 0);
   static constexpr uint32_t kScales = kCodes ? 2 * kTile * 4 : 0;
   static constexpr uint32_t kStage = 2 * kOperand + kScales;
-  static constexpr uint32_t kFixed = 2 * kP + 2 * kQ;             // q of this part of an item and of the next
-  static constexpr int kStages = (int)std::min<uint32_t>(6, (220 * 1024 - kFixed) / kStage);
-  static constexpr uint32_t kSmem = kFixed + kStages * kStage + 1024;
   static constexpr int kO = NQ * kPPieces;                         // columns of O: the pieces side by side
-  static constexpr uint32_t kTmemCols = 2 * (NQ + kO) <= 64 ? 64 : 2 * (NQ + kO) <= 128 ? 128 : 2 * (NQ + kO) <= 256 ? 256 : 512;
-  static_assert(kStages >= 2 && kSmem <= 226 * 1024, "shared memory");
+  // One pair of warpgroups a CTA and two CTAs an SM where they fit (what one waits for at an item's end
+  // the other fills), else two pairs a CTA.  q of this part of an item and of the next.
+  static constexpr bool kSmall = NQ <= 32 && kP + 2 * kQ + 2 * kStage <= 104 * 1024 && NQ + kO <= 256;
+  static constexpr int kPairs = kSmall ? 1 : 2;
+  static constexpr uint32_t kFixed = kPairs * kP + 2 * kQ;
+  static constexpr int kStages = (int)std::min<uint32_t>(6, ((kSmall ? 106 : 212) * 1024 - kFixed) / kStage);
+  static constexpr uint32_t kSmem = kFixed + kStages * kStage + 1024;
+  static constexpr int kCols = kPairs * (NQ + kO);                 // S and O of the pairs
+  static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static constexpr int kSoftWarps = 8 * kPairs, kSoft = 32 * kSoftWarps;
+  static constexpr int kThreads = kSoft + 128;                     // and the warps for loads, S, O and q
+  static constexpr int kCtas = kSmall ? 2 : 1;                     // an SM
+  // registers of the softmax's threads and of the others, of the 80 or 96 a thread at launch
+  static constexpr int kRegs = kSmall ? 80 : 96, kRegsHigh = kSmall ? 96 : 104, kRegsLow = kSmall ? 48 : 64;
+  static_assert(kSoft * kRegsHigh + 128 * kRegsLow <= kThreads * kRegs, "registers");
+  static_assert(kStages >= 2 && kCols <= 512 && kCtas * kTmemCols <= 512, "shared memory and TMEM");
 };
 
 template <int kRow>
@@ -330,17 +339,18 @@ __device__ __noinline__ float non_finite_v(const TreeArgs& a, int r, int32_t bas
 }
 
 template <bool kCodes, int D, int NQ>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D, NQ>::kCtas)
     k_tree_attention(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ TreeArgs a) {
   using F = Form<kCodes, D, NQ>;
+  constexpr int kSoftWarps = F::kSoftWarps, kSoft = F::kSoft, kThreads = F::kThreads, kPairs = F::kPairs;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sP = sm;                  // [2] P
-  uint8_t* sQ = sm + 2 * F::kP;      // [2][pieces][parts]
+  uint8_t* sP = sm;                  // [pairs] P
+  uint8_t* sQ = sm + kPairs * F::kP;  // [2][pieces][parts]
   uint8_t* sStage = sm + F::kFixed;  // [stages] k, v; then their scales
   float* sScale = reinterpret_cast<float*>(sStage + F::kStages * 2 * F::kOperand);
-  __shared__ uint64_t kfull[F::kStages], vfull[F::kStages], empty[F::kStages], sfull[2], sfree[2], pready[2], pdone[2], qfull[2],
+  __shared__ uint64_t kfull[F::kStages], vfull[F::kStages], empty[F::kStages], sfull[kPairs], sfree[kPairs], pready[kPairs], pdone[kPairs], qfull[2],
       qempty[2];
   __shared__ uint32_t tmem_slot, okmask[F::kStages];
   __shared__ int abort_s, never_s, start_r;
@@ -353,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint8_t row_of[2][NQ];
   __shared__ int64_t out_at[2][NQ];
   __shared__ __align__(16) float qs[2][NQ];
-  __shared__ __align__(16) float nref[2][NQ], delta[2][NQ], factor[2][NQ];
-  __shared__ float warp_top[kSoftWarps][NQ / 2], coef[2][NQ], norm[NQ];
-  __shared__ bool set[2][NQ];
+  __shared__ __align__(16) float nref[kPairs][NQ], delta[kPairs][NQ], factor[kPairs][NQ];
+  __shared__ float warp_top[kSoftWarps][NQ / 2], coef[kPairs][NQ];
+  __shared__ bool set[kPairs][NQ];
   volatile int* abort_flag = &abort_s;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -365,11 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&vfull[i], 1);
       ptx::mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       ptx::mbar_init(&sfull[i], 1);
-      ptx::mbar_init(&sfree[i], kSoftWarps / 2);
-      ptx::mbar_init(&pready[i], kSoftWarps / 2);
+      ptx::mbar_init(&sfree[i], 8);
+      ptx::mbar_init(&pready[i], 8);
       ptx::mbar_init(&pdone[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&qfull[i], 1);
       ptx::mbar_init(&qempty[i], kSoftWarps);
       hidden[i] = 0;
@@ -434,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk walk;
   walk.start(a, start_r, start_at, u1 - u0, NQ);
   if (warp >= kSoftWarps) {
-  ptx::reg_dec<kRegsLow>();
+  ptx::reg_dec<F::kRegsLow>();
   if (warp == kSoftWarps) {
     // ---- loads: a lane a page of k or v, four tokens' scales a lane; the page numbers a tile ahead ----
     const uint64_t policy = a.group * a.max_tree > NQ ? ptx::policy_evict_normal() : ptx::policy_evict_first();
@@ -500,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- MMAs: one warp for S, up to two tiles ahead, and one for O (one warp's waits and issues for
     // both took 1850 cycles a tile) ----
     constexpr uint32_t idesc_s = kCodes ? ptx::idesc_e4m3_f32(128, NQ) : ptx::idesc_bf16_f32(128, NQ, false, false);
-    constexpr uint32_t idesc_o = kCodes ? ptx::idesc_e4m3_e5m2_mn_f32(128, F::kO) : ptx::idesc_bf16_f32(128, F::kO, true, true);
+    constexpr uint32_t idesc_o = kCodes ? ptx::idesc_e4m3_e5m2_mn_f32(128, F::kPWide) : ptx::idesc_bf16_f32(128, NQ, true, true);
     constexpr int kStepsS = D * F::kElem / 32, kStepTokens = 32 / F::kElem, kStepsO = kTile / kStepTokens;
     // of D = 64 the tile's 64 columns serve as both halves of the 128 rows
     constexpr uint32_t kLboV = F::kParts > 1 ? F::kPart : 0;
@@ -508,7 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dk0 = operand_desc<F::kRow>(ptx::smem_u32(sStage), 16);
     const uint64_t dv0 = operand_desc<F::kRow>(ptx::smem_u32(sStage) + F::kOperand, kLboV);
     const uint64_t dq0 = operand_desc<F::kRow>(ptx::smem_u32(sQ), 16);
-    const uint64_t dp0 = ptx::smem_desc_sw128(ptx::smem_u32(sP), F::kPCol, 1024);
+    const uint64_t dp0 = ptx::smem_desc_sw128(ptx::smem_u32(sP), 16, 1024);
+    const uint64_t dr0 = ptx::smem_desc_sw64(ptx::smem_u32(sP) + F::kPCol, 16, 512);
     const bool is_s = warp == kSoftWarps + 1;
     auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
       const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit));
@@ -524,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tiles = parts[qb].tiles;
       if (tiles == 0) break;
       for (int t = 0; t < tiles; ++t) {
-        const int w = t & 1;
+        const int w = t % kPairs;
         if (is_s) {
           ok = wait(&sfree[w], (~turns >> w) & 1, 3) && wait(&kfull[s], ph, 4);
           if (!ok) break;
@@ -553,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
             const uint64_t dv = dv0 + s * (2 * F::kOperand >> 4), dp = dp0 + w * (F::kP >> 4);
-            const uint32_t d = tmem + 2 * NQ + w * F::kO, more = t >= 2;
+            const uint32_t d = tmem + kPairs * NQ + w * F::kO, more = t >= kPairs;
 #pragma unroll
             for (int k = 0; k < kStepsO; ++k) {
               const uint64_t da = dv + (k * kStepTokens * F::kRow >> 4), db = dp + (k * kStepTokens * 128 >> 4);
@@ -563,6 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_mma_fp8_if(d, da, db, idesc_o, more);
               else
                 ptx::tc_mma_fp8<1>(d, da, db, idesc_o);
+            }
+            if constexpr (F::kPRest > 0) {
+              const uint64_t dr = dr0 + w * (F::kP >> 4);
+#pragma unroll
+              for (int k = 0; k < kStepsO; ++k)
+                ptx::tc_mma_fp8_if(d + F::kPWide, dv + (k * kStepTokens * F::kRow >> 4), dr + (k * kStepTokens * 64 >> 4),
+                                   ptx::idesc_e4m3_e5m2_mn_f32(128, F::kPRest), k > 0 ? 1 : more);
             }
             ptx::tc_commit(&empty[s]);
             ptx::tc_commit(&pdone[w]);
@@ -613,12 +633,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   }
   } else {
-    ptx::reg_inc<kRegsHigh>();
+    ptx::reg_inc<F::kRegsHigh>();
     // ---- softmax: tiles w, w + 2, .. of a part and half of the columns a warpgroup ----
     constexpr int HQ = NQ / 2, kAll = 5;
     const int wg = warp >> 2, w = wg >> 1, h = wg & 1, quarter = warp & 3, token = quarter * 32 + lane;
     const int own = 1 + wg;  // its barrier
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), tS = lanes + w * NQ + h * HQ, tO = lanes + 2 * NQ;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), tS = lanes + w * NQ + h * HQ, tO = lanes + kPairs * NQ;
     const int box_shift = min(a.pool.shift, 7);
     const uint32_t all_ok = (1u << (kTile >> box_shift)) - 1;
     uint32_t n0 = 0, turn = 0;  // the CTA's tiles before this part, this warpgroup's so far
@@ -649,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < HQ / 2; ++i) l2[i] = 0;
       bool unset = true;  // a column has no reference yet
 #pragma unroll 1
-      for (int t = w; t < tiles; t += 2) {
+      for (int t = w; t < tiles; t += kPairs) {
         const uint32_t n = n0 + t, s = n % F::kStages, ph = (n / F::kStages) & 1;
         wait(&kfull[s], ph, 11);
         const int pos0 = (tile0 + t) * kTile, pos = pos0 + token;
@@ -767,9 +787,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < HQ / 2; ++i) {
             x2[i] = ptx::add2(x2[i], *reinterpret_cast<const uint64_t*>(&my_delta[2 * i]));
-            if (t >= 2) l2[i] = ptx::mul2(l2[i], *reinterpret_cast<const uint64_t*>(&my_factor[2 * i]));
+            if (t >= kPairs) l2[i] = ptx::mul2(l2[i], *reinterpret_cast<const uint64_t*>(&my_factor[2 * i]));
           }
-          if (t >= 2) {
+          if (t >= kPairs) {
 #pragma unroll
             for (int p = 0; p < F::kPPieces; ++p)
 #pragma unroll
@@ -816,15 +836,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // (16-byte unit u of row r lies at u ^ (r % 8))
           auto place = [&](uint32_t byte) {
-            return prow + byte / 128 * F::kPCol + ((((byte % 128) >> 4) ^ (token & 7)) << 4) + (byte & 15);
+            return prow + (((byte >> 4) ^ (token & 7)) << 4) + (byte & 15);
           };
           if constexpr (kCodes) {
             const uint32_t byte = h * HQ + c;
             *reinterpret_cast<uint2*>(place(byte)) = make_uint2(__byte_perm(hh[0], hh[1], 0x7531), __byte_perm(hh[2], hh[3], 0x7531));
             *reinterpret_cast<uint2*>(place(NQ + byte)) =
                 make_uint2(__byte_perm(r1[0], r1[1], 0x7531), __byte_perm(r1[2], r1[3], 0x7531));
-            *reinterpret_cast<uint2*>(place(2 * NQ + byte)) =
-                make_uint2(__byte_perm(c3[0], c3[1], 0x5410), __byte_perm(c3[2], c3[3], 0x5410));
+            uint8_t* third = place(2 * NQ + byte);
+            if constexpr (F::kPRest > 0)
+              third = sP + w * F::kP + F::kPCol + swizzled<64>(token * 64 + byte);
+            *reinterpret_cast<uint2*>(third) = make_uint2(__byte_perm(c3[0], c3[1], 0x5410), __byte_perm(c3[2], c3[3], 0x5410));
           } else {
             *reinterpret_cast<uint4*>(place((h * HQ + c) * 2)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
           }
@@ -837,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the part's end: sums of both tile sequences, O joined and written ----
       n0 += tiles;
-      const bool two = tiles > 1;  // both have a tile
+      const bool two = kPairs > 1 && tiles > 1;  // both pairs have a tile
       if (w == 0 || two) wait(&pdone[w], (turn - 1) & 1, 15);
       {
         float v[HQ];
@@ -858,35 +880,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = slot < 0;
       if (threadIdx.x < NQ) {
         const int c = threadIdx.x, half = c / HQ, i = c % HQ;
-        float ref[2], l[2];
+        float ref[kPairs], l[kPairs];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < kPairs; ++g) {
           const int first = (g * 2 + half) * 4;
           ref[g] = set[g][c] ? -nref[g][c] : -INFINITY;
           l[g] = (warp_top[first][i] + warp_top[first + 1][i]) + (warp_top[first + 2][i] + warp_top[first + 3][i]);
         }
-        const float m = two ? fmaxf(ref[0], ref[1]) : ref[0];
-        const float f0 = ref[0] == m ? 1.f : exp2f(ref[0] - m), f1 = !two ? 0.f : ref[1] == m ? 1.f : exp2f(ref[1] - m);
-        const float sum = two ? f0 * l[0] + f1 * l[1] : l[0];
+        float m = ref[0], sum = l[0], f[kPairs] = {1.f};
+        if constexpr (kPairs > 1) {
+          f[1] = 0.f;
+          if (two) {
+            m = fmaxf(ref[0], ref[1]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) f[g] = ref[g] == m ? 1.f : exp2f(ref[g] - m);
+            sum = f[0] * l[0] + f[1] * l[1];
+          }
+        }
         const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-        coef[0][c] = f0 * inv;
-        coef[1][c] = f1 * inv;
+#pragma unroll
+        for (int g = 0; g < kPairs; ++g) coef[g][c] = f[g] * inv;
         if (!whole) a.stat[(int64_t)slot * NQ + c] = make_float2(m, sum);
       }
       ptx::named_sync(kAll, kSoft);
-      // a quarter of the columns a warpgroup, eight at least
-      constexpr int W = NQ >= 32 ? NQ / 4 : 8;
+      // its share of the columns a warpgroup, eight at least
+      constexpr int W = NQ / (2 * kPairs) >= 8 ? NQ / (2 * kPairs) : 8;
       const int d = quarter * 32 + lane, c0 = wg * W;
       if (quarter * 32 < D && c0 < columns) {
-        float v0[W], v1[W];
-        load_sum<F::kPPieces, W>(tO + c0, NQ, v0);
-        if (two) load_sum<F::kPPieces, W>(tO + F::kO + c0, NQ, v1);
+        float v[kPairs][W];
+#pragma unroll
+        for (int g = 0; g < kPairs; ++g)
+          if (g == 0 || two) load_sum<F::kPPieces, W>(tO + g * F::kO + c0, NQ, v[g]);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
           const int c = c0 + i;
           if (c >= columns) break;
-          float o = coef[0][c] * v0[i];
-          if (two) o = fmaf(coef[1][c], v1[i], o);
+          float o = coef[0][c] * v[0][i];
+          if (two) o = fmaf(coef[kPairs - 1][c], v[kPairs - 1][i], o);
           if (bad_rows) o += non_finite_v<kCodes, D>(a, parts[b].r, parts[b].base, parts[b].head, bad_rows & words[b][row_of[b][c]], d);
           if (whole)
             a.out[out_at[b][c] + d] = __float2bfloat16_rn(o);
@@ -913,22 +943,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinThreads = 256, kJoinCtas = 4;  // an SM
 template <int D, int NQ>
 __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, int ctas) {
-  static_assert(kMaxCtas <= kJoinThreads, "a thread a CTA");
+  static_assert(kMaxCtas <= 2 * kJoinThreads, "two CTAs a thread");
   constexpr int E = D / 32;
-  __shared__ int items[kMaxCtas], counts[kJoinThreads / 32];
+  __shared__ int items[kMaxCtas], counts[2][kJoinThreads / 32];
   ptx::launch_dependents();
   ptx::grid_wait();
   const int t = threadIdx.x, warp = t / 32, lane = t % 32;
-  const bool mine = t < ctas && a.meta[t].z > 1;
-  const uint32_t votes = __ballot_sync(0xffffffffu, mine);
-  if (lane == 0) counts[warp] = __popc(votes);
-  __syncthreads();
-  int n = 0, first = 0;
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    if (w < warp) first += counts[w];
-    n += counts[w];
+  uint32_t votes[2];
+  bool mine[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    mine[i] = t + i * kJoinThreads < ctas && a.meta[t + i * kJoinThreads].z > 1;
+    votes[i] = __ballot_sync(0xffffffffu, mine[i]);
+    if (lane == 0) counts[i][warp] = __popc(votes[i]);
   }
-  if (mine) items[first + __popc(votes & ((1u << lane) - 1))] = t;
+  __syncthreads();
+  int n = 0;
+  for (int i = 0; i < 2; ++i) {
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      if (w == warp && mine[i]) items[n + __popc(votes[i] & ((1u << lane) - 1))] = t + i * kJoinThreads;
+      n += counts[i][w];
+    }
+  }
   __syncthreads();
   for (int at = blockIdx.x * (kJoinThreads / 32) + warp; at < n * NQ; at += gridDim.x * (kJoinThreads / 32)) {
     const int cta = items[at / NQ], c = at % NQ;
@@ -1002,10 +1038,11 @@ struct Dev {
 };
 // The kernel's warps trade registers among themselves: what the softmax's warps ask for
 // has to be there, or they would wait for ever.
+template <typename F>
 cudaError_t check_registers(const void* f) {
   cudaFuncAttributes at;
   if (const cudaError_t e = cudaFuncGetAttributes(&at, f); e != cudaSuccess) return e;
-  return at.numRegs * kThreads < kSoft * kRegsHigh + (kThreads - kSoft) * kRegsLow ? cudaErrorNotSupported : cudaSuccess;
+  return at.numRegs * F::kThreads < F::kSoft * F::kRegsHigh + 128 * F::kRegsLow ? cudaErrorNotSupported : cudaSuccess;
 }
 // properties of the current device, looked up once each
 cudaError_t device(Dev* out) {
@@ -1043,13 +1080,13 @@ cudaError_t run(const dspark_kv_cache& c, const TreeArgs& t, const Dev& dev, cud
       !tensor_map_2d(&tmV, dt, c.v, D, rows, D * F::kElem, F::kRow / F::kElem, box, F::kElem))
     return cudaErrorInvalidValue;
   const auto f = k_tree_attention<kCodes, D, NQ>;
-  static const cudaError_t registers = check_registers((const void*)f);
+  static const cudaError_t registers = check_registers<F>((const void*)f);
   if (registers != cudaSuccess) return registers;
   if (const cudaError_t e = ensure_smem_limit((const void*)f, (int)F::kSmem); e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)std::min(dev.sms, kMaxCtas);
-  if (const cudaError_t e = launch_overlapped(f, grid, kThreads, F::kSmem, 1, s, tmK, tmV, t); e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min(dev.sms * F::kCtas, kMaxCtas);
+  if (const cudaError_t e = launch_overlapped(f, grid, F::kThreads, F::kSmem, 1, s, tmK, tmV, t); e != cudaSuccess) return e;
   count_launches(1);
-  const cudaError_t e = launch_overlapped(k_tree_join<D, NQ>, grid * kJoinCtas, kJoinThreads, 0, 1, s, t, (int)grid);
+  const cudaError_t e = launch_overlapped(k_tree_join<D, NQ>, (unsigned)dev.sms * kJoinCtas, kJoinThreads, 0, 1, s, t, (int)grid);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
