@@ -211,8 +211,13 @@ __device__ __forceinline__ uint32_t e5m2x2(uint32_t h) {
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
   return r;
 }
-__device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3)));
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ __half2 e4m3x2_halves(uint32_t c) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3));
 }
 // a word's non-finite elements: all ones in their place
 template <bool kCodes>
@@ -221,83 +226,80 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
   return ((((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15) * 65535u;
 }
 
-// The columns of q of a part as operand pieces, with their factors, rows and places in out: eight
+// The columns of q of a part as operand pieces, with their factors and places in out: eight
 // lanes a column (16 or 8 elements each), four columns a warp at a time, warp `w` of `warps`.
 template <bool kCodes, int D, int NQ>
 __device__ __forceinline__ void prepare_q(const TreeArgs& a, const Walk& walk, uint8_t* dst, int w, int warps, float* qs,
-                                          uint8_t* row_of, int64_t* out_at) {
+                                          int64_t* out_at) {
   using F = Form<kCodes, D, NQ>;
   constexpr int E = D / 8, V = E / 8;  // elements, 16-byte vectors of a lane
   const int lane = threadIdx.x & 31, l = lane & 7, columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
-  constexpr int kBatch = NQ >= 64 && V == 2 ? 4 : NQ / 16;  // column groups whose loads are on their way at a time
-  for (int g0 = w; g0 < NQ / 4; g0 += warps * kBatch) {
-    uint4 all[kBatch][V];
-    int rows[kBatch], heads[kBatch];
+  struct Group {  // of four columns: this lane's part of its column
+    uint4 v[V];
+    int j, head;
+  };
+  const auto load = [&](int c) {
+    Group g;
+    const int col = walk.chunk * NQ + c;
+    g.j = c < columns ? (int)(col * a.group_inv >> 32) : 0;
+    g.head = walk.head * a.group + col - g.j * a.group;
+    const __nv_bfloat16* src = a.q + (int64_t)(walk.q.lo + g.j) * a.ldq + g.head * D + l * E;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int c = (g0 + u * warps) * 4 + (lane >> 3), col = walk.chunk * NQ + c;
-      rows[u] = c < columns ? (int)(col * a.group_inv >> 32) : 0;
-      heads[u] = walk.head * a.group + col - rows[u] * a.group;
+    for (int i = 0; i < V; ++i) g.v[i] = c < columns ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
+    return g;
+  };
+  int c = w * 4 + (lane >> 3);
+  Group next = load(c);
+#pragma unroll 1
+  for (; c < NQ; c += warps * 4) {
+    Group g = next;
+    if (c + warps * 4 < NQ) next = load(c + warps * 4);
+    uint32_t* x = reinterpret_cast<uint32_t*>(g.v);
+    uint32_t top = 0;  // the largest magnitude's bits; infinities and NaN are above all others
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        all[u][i] = c < columns ? *reinterpret_cast<const uint4*>(a.q + (int64_t)(walk.q.lo + rows[u]) * a.ldq + heads[u] * D + l * E + i * 8)
-                                : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[i] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool fin = top < 0x7F80u;
+    if (!fin) {  // the column's scores are NaN through its factor
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) x[i] = 0;
+      top = 0;
     }
+    float unit = a.scale * kLog2e;
+    if constexpr (kCodes) {
+      // top 2^k in 128 .. 256, k up to 120 so that both powers are normal
+      const int k = top ? min(7 - ((int)(top >> 7) - 127), 120) : 0;
+      const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+      unit *= __uint_as_float((uint32_t)(127 - k) << 23);
+      uint32_t p1[E / 4], p2[E / 4];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int c = (g0 + u * warps) * 4 + (lane >> 3);
-      if (c >= NQ) break;
-      const int j = rows[u], head = heads[u];
-      uint4 (&v)[V] = all[u];
-      uint32_t* x = reinterpret_cast<uint32_t*>(v);
-      uint32_t top = 0;  // the largest magnitude's bits; infinities and NaN are above all others
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[i] & 0x7FFF7FFFu);
-      top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool fin = top < 0x7F80u;
-      if (!fin) {  // the column's scores are NaN through its factor
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) x[i] = 0;
-        top = 0;
+      for (int i = 0; i < E / 2; ++i) {  // below 2^8 the eight bits are exact in fp16, whose step is 2^-24 at the bottom
+        const __half2 y = __floats2half2_rn(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xFFFF0000u) * up);
+        const uint32_t c1 = e4m3x2(half2_bits(y));
+        const uint32_t c2 = e4m3x2(half2_bits(__hsub2(y, e4m3x2_halves(c1))));
+        p1[i / 2] = (i & 1) ? __byte_perm(p1[i / 2], c1, 0x5410) : c1;
+        p2[i / 2] = (i & 1) ? __byte_perm(p2[i / 2], c2, 0x5410) : c2;
       }
-      float unit = a.scale * kLog2e;
-      if constexpr (kCodes) {
-        // top 2^k in 128 .. 256, k up to 120 so that both powers are normal
-        const int k = top ? min(7 - ((int)(top >> 7) - 127), 120) : 0;
-        const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-        unit *= __uint_as_float((uint32_t)(127 - k) << 23);
-        uint32_t p1[E / 4], p2[E / 4];
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          const float2 y = make_float2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xFFFF0000u) * up);
-          const uint32_t c1 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-          const float2 z = e4m3x2_values(c1);
-          const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
-          p1[i / 2] = (i & 1) ? p1[i / 2] | c1 << 16 : c1;
-          p2[i / 2] = (i & 1) ? p2[i / 2] | c2 << 16 : c2;
-        }
-        const uint32_t at = swizzled<F::kRow>(c * F::kRow + l * E);
-        if constexpr (E == 16) {
-          *reinterpret_cast<uint4*>(dst + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-          *reinterpret_cast<uint4*>(dst + F::kQPart + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-        } else {
-          *reinterpret_cast<uint2*>(dst + at) = make_uint2(p1[0], p1[1]);
-          *reinterpret_cast<uint2*>(dst + F::kQPart + at) = make_uint2(p2[0], p2[1]);
-        }
+      const uint32_t at = swizzled<F::kRow>(c * F::kRow + l * E);
+      if constexpr (E == 16) {
+        *reinterpret_cast<uint4*>(dst + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+        *reinterpret_cast<uint4*>(dst + F::kQPart + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
       } else {
+        *reinterpret_cast<uint2*>(dst + at) = make_uint2(p1[0], p1[1]);
+        *reinterpret_cast<uint2*>(dst + F::kQPart + at) = make_uint2(p2[0], p2[1]);
+      }
+    } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int byte = l * E * 2 + i * 16;
-          *reinterpret_cast<uint4*>(dst + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) = v[i];
-        }
+      for (int i = 0; i < V; ++i) {
+        const int byte = l * E * 2 + i * 16;
+        *reinterpret_cast<uint4*>(dst + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) = g.v[i];
       }
-      if (l == 0) {
-        qs[c] = c < columns ? (fin ? unit : NAN) : 0.f;
-        row_of[c] = (uint8_t)j;
-        out_at[c] = (int64_t)(walk.q.lo + j) * a.ldo + head * D;
-      }
+    }
+    if (l == 0) {
+      qs[c] = c < columns ? (fin ? unit : NAN) : 0.f;
+      out_at[c] = (int64_t)(walk.q.lo + g.j) * a.ldo + g.head * D;
     }
   }
 }
@@ -307,16 +309,16 @@ __device__ __forceinline__ void load_columns(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < n; i += 8) ptx::tmem_ld8(taddr + i, v + i);
 }
-// columns of O, its pieces summed (the smallest first)
-template <int kPieces, int n>
-__device__ __forceinline__ void load_sum(uint32_t taddr, int apart, float (&v)[n]) {
-  float u[kPieces][n];
+// eight columns of O, its pieces summed (the smallest first)
+template <int kPieces>
+__device__ __forceinline__ void load_sum(uint32_t taddr, int apart, float (&v)[8]) {
+  float u[kPieces][8];
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p) load_columns<n>(taddr + p * apart, u[p]);
+  for (int p = 0; p < kPieces; ++p) ptx::tmem_ld8(taddr + p * apart, u[p]);
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p) ptx::tmem_ld_wait<n>(u[p]);
+  for (int p = 0; p < kPieces; ++p) ptx::tmem_ld_wait<8>(u[p]);
 #pragma unroll
-  for (int i = 0; i < n; ++i) {
+  for (int i = 0; i < 8; ++i) {
     v[i] = u[kPieces - 1][i];
 #pragma unroll
     for (int p = kPieces - 2; p >= 0; --p) v[i] += u[p][i];
@@ -355,12 +357,11 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   __shared__ uint32_t tmem_slot, okmask[F::kStages];
   __shared__ int abort_s, never_s, start_r;
   __shared__ int64_t start_at, sums[kThreads / 32 + 1];
-  // of the part and the next: the drafted rows with non-finite v, the rows' words, each column's row,
-  // its place in out and its factor
+  // of the part and the next: the drafted rows with non-finite v, the columns that see a drafted row, each
+  // column's place in out and its factor
   __shared__ Part parts[2];
   __shared__ unsigned long long hidden[2];
-  __shared__ uint64_t words[2][DSPARK_MAX_TREE];
-  __shared__ uint8_t row_of[2][NQ];
+  __shared__ uint64_t seers[2][DSPARK_MAX_TREE];
   __shared__ int64_t out_at[2][NQ];
   __shared__ __align__(16) float qs[2][NQ];
   __shared__ __align__(16) float nref[kPairs][NQ], delta[kPairs][NQ], factor[kPairs][NQ];
@@ -621,9 +622,32 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           a.meta[cta] = make_int4(walk.r, walk.head * walk.q.chunks + walk.chunk, (int)((end * ctas - 1) / total) - cta + 1, 0);
         }
       }
-      for (int j = lane; j < walk.q.rows; j += 32) words[b][j] = a.tree ? a.tree[walk.q.lo + j] : ~0ull >> (63 - j);
+      {
+        // bits of the chunk's columns, row after row: those of row j begin at j group - chunk NQ
+        const int j0 = (int)((uint32_t)(walk.chunk * NQ) * a.group_inv >> 32);
+        const int j1 = min(walk.q.rows, (int)((uint32_t)(walk.chunk * NQ + NQ - 1) * a.group_inv >> 32) + 1);
+        uint64_t see0 = 0, see1 = 0;    // of nodes `lane` and lane + 32
+        uint64_t mine0 = 0, mine1 = 0;  // the words of rows `lane` and lane + 32
+        if (a.tree) {
+          if (lane < walk.q.rows) mine0 = a.tree[walk.q.lo + lane];
+          if (lane + 32 < walk.q.rows) mine1 = a.tree[walk.q.lo + lane + 32];
+        } else {
+          mine0 = ~0ull >> (63 - lane);
+          mine1 = ~0ull >> (31 - lane);
+        }
+#pragma unroll 1
+        for (int j = j0; j < j1; ++j) {
+          const uint64_t word = __shfl_sync(0xffffffffu, j < 32 ? mine0 : mine1, j & 31);
+          const int first = max(0, j * a.group - walk.chunk * NQ), last = min(NQ, (j + 1) * a.group - walk.chunk * NQ);
+          const uint64_t bits = (~0ull >> (64 - (last - first))) << first;
+          if ((word >> lane) & 1) see0 |= bits;
+          if ((word >> (lane + 32)) & 1) see1 |= bits;
+        }
+        seers[b][lane] = see0;
+        seers[b][lane + 32] = see1;
+      }
       if (part > 0)
-        prepare_q<kCodes, D, NQ>(a, walk, sQ + b * F::kQ, 0, 1, qs[b], row_of[b], out_at[b]);
+        prepare_q<kCodes, D, NQ>(a, walk, sQ + b * F::kQ, 0, 1, qs[b], out_at[b]);
       else
         ptx::named_sync(6, kSoft + 32);  // the softmax's warps, which have nothing else to do yet
       ptx::fence_proxy_async_smem();
@@ -646,7 +670,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       if (!ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit)) fail(what);  // the loops run on: every later wait ends at once
     };
     if (walk.next(a, NQ)) {
-      prepare_q<kCodes, D, NQ>(a, walk, sQ, warp, kSoftWarps, qs[0], row_of[0], out_at[0]);
+      prepare_q<kCodes, D, NQ>(a, walk, sQ, warp, kSoftWarps, qs[0], out_at[0]);
       ptx::fence_proxy_async_smem();
       ptx::named_arrive(6, kSoft + 32);
     }
@@ -683,6 +707,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           if (v < 1.17549435e-38f) v = 1.17549435e-38f;  // 0 of a cache that was cleared
           v_log = __log2f(v);
           v_inv = ptx::rcp(v);
+          if (v != v) v_inv = 1.f;  // the weights of those that see it are NaN, of the others 0
         }
         if (masked && h == 0) {
           // what no row or only some see must not reach the others through 0 * NaN
@@ -690,7 +715,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           uint8_t* row = sStage + s * 2 * F::kOperand + F::kOperand + token * F::kRow;
           if (!held || pos >= base) {
             uint32_t any = 0;
-#pragma unroll 2
+#pragma unroll 1
             for (int i = 0; i < F::kParts * F::kRow / 16; ++i) {
               uint4* at = reinterpret_cast<uint4*>(row + i * 16 / F::kRow * F::kPart + i * 16 % F::kRow);
               if (held) {
@@ -734,13 +759,11 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           }
         }
         if (masked) {
-          const int node = pos - base;
+          const uint32_t see = !held ? 0u : pos < base ? ~0u : (uint32_t)(seers[b][pos - base] >> (h * HQ));
 #pragma unroll
           for (int i = 0; i < HQ / 2; ++i) {
             const float2 x = ptx::unpack2(x2[i]);
-            const bool see0 = held && (pos < base || ((words[b][row_of[b][h * HQ + 2 * i]] >> node) & 1));
-            const bool see1 = held && (pos < base || ((words[b][row_of[b][h * HQ + 2 * i + 1]] >> node) & 1));
-            x2[i] = ptx::pack2(see0 ? x.x : -INFINITY, see1 ? x.y : -INFINITY);
+            x2[i] = ptx::pack2((see >> (2 * i)) & 1 ? x.x : -INFINITY, (see >> (2 * i + 1)) & 1 ? x.y : -INFINITY);
           }
         }
         float top = -INFINITY;
@@ -790,9 +813,9 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
             if (t >= kPairs) l2[i] = ptx::mul2(l2[i], *reinterpret_cast<const uint64_t*>(&my_factor[2 * i]));
           }
           if (t >= kPairs) {
-#pragma unroll
+#pragma unroll 1
             for (int p = 0; p < F::kPPieces; ++p)
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < HQ; c += 8) {
                 const uint32_t at = tO + w * F::kO + p * NQ + h * HQ + c;
                 float v[8];
@@ -817,14 +840,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
             const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
             const uint64_t p2 = ptx::pack2(p0, p1);
             uint64_t& l = l2[c / 2 + i];
-            if (!kCodes) {
-              l = ptx::add2(l, p2);
-            } else if (!masked) {
-              l = ptx::fma2(p2, vi2, l);
-            } else {  // a hidden row's scale may be NaN
-              const float2 o = ptx::unpack2(l);
-              l = ptx::pack2(x.x == -INFINITY ? o.x : fmaf(p0, v_inv, o.x), x.y == -INFINITY ? o.y : fmaf(p1, v_inv, o.y));
-            }
+            l = kCodes ? ptx::fma2(p2, vi2, l) : ptx::add2(l, p2);
             if constexpr (kCodes) {
               hh[i] = half2_bits(__floats2half2_rn(p0, p1));
               r1[i] = half2_bits(__hsub2(bits_half2(hh[i]), bits_half2(hh[i] & 0xFF00FF00u)));
@@ -903,25 +919,43 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
         if (!whole) a.stat[(int64_t)slot * NQ + c] = make_float2(m, sum);
       }
       ptx::named_sync(kAll, kSoft);
-      // its share of the columns a warpgroup, eight at least
+      // its share of the columns a warpgroup, eight at a time (a loop: straight-line code this rarely
+      // run waits for its instructions, 8700 cycles for 16 columns)
       constexpr int W = NQ / (2 * kPairs) >= 8 ? NQ / (2 * kPairs) : 8;
-      const int d = quarter * 32 + lane, c0 = wg * W;
-      if (quarter * 32 < D && c0 < columns) {
-        float v[kPairs][W];
+      const int d = quarter * 32 + lane;
+      if (quarter * 32 < D) {
+#pragma unroll 1
+        for (int c0 = wg * W; c0 < min(columns, (wg + 1) * W); c0 += 8) {
+          float v[8], u[8];
+          load_sum<F::kPPieces>(tO + c0, NQ, v);
+          if (two) load_sum<F::kPPieces>(tO + (kPairs - 1) * F::kO + c0, NQ, u);
+          const int n = min(8, columns - c0);
+          const float* f0 = &coef[0][c0];
+          const float* f1 = &coef[kPairs - 1][c0];
 #pragma unroll
-        for (int g = 0; g < kPairs; ++g)
-          if (g == 0 || two) load_sum<F::kPPieces, W>(tO + g * F::kO + c0, NQ, v[g]);
+          for (int i = 0; i < 8; ++i) v[i] = two ? fmaf(f1[i], u[i], f0[i] * v[i]) : f0[i] * v[i];
+          if (bad_rows) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const int c = c0 + i;
-          if (c >= columns) break;
-          float o = coef[0][c] * v[0][i];
-          if (two) o = fmaf(coef[kPairs - 1][c], v[kPairs - 1][i], o);
-          if (bad_rows) o += non_finite_v<kCodes, D>(a, parts[b].r, parts[b].base, parts[b].head, bad_rows & words[b][row_of[b][c]], d);
-          if (whole)
-            a.out[out_at[b][c] + d] = __float2bfloat16_rn(o);
-          else
-            a.part[((int64_t)slot * NQ + c) * D + d] = o;
+            for (int i = 0; i < 8; ++i) {
+              unsigned long long nodes = 0;  // that column c0 + i sees
+              for (unsigned long long left = bad_rows; left; left &= left - 1) {
+                const int node = __ffsll((long long)left) - 1;
+                if ((seers[b][node] >> (c0 + i)) & 1) nodes |= 1ull << node;
+              }
+              if (nodes) v[i] += non_finite_v<kCodes, D>(a, parts[b].r, parts[b].base, parts[b].head, nodes, d);
+            }
+          }
+          if (whole) {
+            const int64_t* at = &out_at[b][c0];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < n) a.out[at[i] + d] = __float2bfloat16_rn(v[i]);
+          } else {
+            float* at = a.part + ((int64_t)slot * NQ + c0) * D + d;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < n) at[i * D] = v[i];
+          }
         }
       }
       ptx::tc_fence_before();
