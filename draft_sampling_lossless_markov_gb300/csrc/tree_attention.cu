@@ -47,8 +47,8 @@ namespace {
 
 constexpr int kTile = 128;           // tokens
 constexpr int kMaxCtas = 320;        // parts the workspace holds: two a CTA
-constexpr int kItemCost = 2;         // what an item costs beside its tiles, in tiles
-constexpr long long kWaitLimit = 4000000000ll;  // cycles, about two seconds
+template <int NQ>
+constexpr int kItemCost = NQ == 64 ? 4 : 3;  // what an item costs beside its tiles, in tiles
 // A column's largest exponent when its reference is set, and the exponent that raises it: 2^15 is in
 // fp16's range, bf16 weights have room up to 2^60.
 template <bool kCodes>
@@ -125,7 +125,8 @@ struct Request {
   int32_t lo, rows, base, tiles, chunks;
   int64_t units;
 };
-__device__ __forceinline__ Request request_at(const TreeArgs& a, int r, int nq, bool* bad) {
+template <int NQ>
+__device__ __forceinline__ Request request_at(const TreeArgs& a, int r, bool* bad) {
   Request q;
   const int32_t lo = a.offsets[r], hi = a.offsets[r + 1];
   q.base = a.base[r];
@@ -135,55 +136,76 @@ __device__ __forceinline__ Request request_at(const TreeArgs& a, int r, int nq, 
   q.lo = lo;
   q.rows = *bad ? 0 : hi - lo;
   q.tiles = q.rows ? (int32_t)((held + kTile - 1) / kTile) : 0;
-  q.chunks = (q.rows * a.group + nq - 1) / nq;
-  q.units = q.tiles ? (int64_t)(q.tiles + kItemCost) * q.chunks * a.pool.heads : 0;
+  q.chunks = (q.rows * a.group + NQ - 1) / NQ;
+  q.units = q.tiles ? (int64_t)(q.tiles + kItemCost<NQ>) * q.chunks * a.pool.heads : 0;
   return q;
 }
 
-// The parts of items in a CTA's share of the units, one after the other; every warp walks by itself.
+// Where a CTA's share begins: the request, the item and the unit within it.
+struct Start {
+  int r, head, chunk, x;
+};
+// The parts of items in a CTA's share of the units, one after the other; the warps that need them walk by themselves.
+template <int NQ>
 struct Walk {
-  int r;
-  int64_t at, left;  // the next unit within request r, units left
+  int r, head, chunk, x;  // the next unit: x of that item
+  int64_t left;           // units
   Request q;
   // the part
-  int head, chunk, tile, tiles;  // first tile, their number
-  bool begins, ends;             // the item's first and last tile are in it
-  __device__ __forceinline__ void start(const TreeArgs& a, int r0, int64_t at0, int64_t n, int nq) {
-    r = r0, at = at0, left = n;
+  int tile, tiles;    // first tile, their number
+  bool begins, ends;  // the item's first and last tile are in it
+  __device__ __forceinline__ void start(const TreeArgs& a, const Start& at, int64_t n) {
+    left = n;
     bool bad;
-    if (n > 0) q = request_at(a, r, nq, &bad);
+    if (n > 0) {
+      r = at.r, head = at.head, chunk = at.chunk, x = at.x;
+      q = request_at<NQ>(a, r, &bad);
+    }
   }
-  __device__ __forceinline__ bool next(const TreeArgs& a, int nq) {
-    for (;;) {
-      if (left <= 0) return false;
-      bool bad;
-      while (at >= q.units) {
-        at = 0;
-        if (++r >= a.pool.n_req) return false;
-        q = request_at(a, r, nq, &bad);
+  __device__ __forceinline__ bool next(const TreeArgs& a) {
+#pragma unroll 1
+    while (left > 0) {
+      if (x == q.tiles + kItemCost<NQ>) {
+        x = 0;
+        if (++chunk == q.chunks) {
+          chunk = 0;
+          if (++head == a.pool.heads) {
+            head = 0;
+            do {
+              if (++r >= a.pool.n_req) return false;
+              bool bad;
+              q = request_at<NQ>(a, r, &bad);
+            } while (q.units == 0);
+          }
+        }
       }
-      const int cost = q.tiles + kItemCost;
-      const int64_t item = at / cost;
-      const int x = (int)(at - item * cost), y = (int)min((int64_t)cost, x + left);
-      at += y - x;
+      const int y = (int)min((int64_t)(q.tiles + kItemCost<NQ>), x + left);
+      tile = max(0, x - kItemCost<NQ>);
+      tiles = max(0, y - kItemCost<NQ>) - tile;
       left -= y - x;
-      tile = max(0, x - kItemCost);
-      tiles = max(0, y - kItemCost) - tile;
+      x = y;
       if (tiles == 0) continue;  // nothing but the item's own cost: it begins in the next CTA
-      head = (int)(item / q.chunks);
-      chunk = (int)(item - (int64_t)head * q.chunks);
       begins = tile == 0;
       ends = tile + tiles == q.tiles;
       return true;
     }
+    return false;
   }
 };
 
-// A part as the warps for q hand it on to the MMAs and the softmax; no tiles: the last was the one before.
+// A part as the planning warp hands it on; no tiles: the last was the one before.
 struct Part {
-  int32_t r, base, rows, head, tile, tiles, columns;
-  int32_t slot;  // of the workspace; -1: the item is whole
+  int32_t r, lo, base, rows, head, tile, tiles, col0, columns;  // col0: the chunk's first column
+  int32_t slot;                                                 // of the workspace; -1: the item is whole
 };
+constexpr int kPlans = 4;  // parts planned ahead
+
+// x, which the compiler does not know: a loop whose first round is special is not cut in two (the copy
+// would be fetched anew for every part)
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
 
 // v[i] combined over the warp's lanes: lane l ends with column l % n's
 template <int n, typename Op>
@@ -226,35 +248,24 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
   return ((((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15) * 65535u;
 }
 
-// The columns of q of a part as operand pieces, with their factors and places in out: eight
-// lanes a column (16 or 8 elements each), four columns a warp at a time, warp `w` of `warps`.
-template <bool kCodes, int D, int NQ>
-__device__ __forceinline__ void prepare_q(const TreeArgs& a, const Walk& walk, uint8_t* dst, int w, int warps, float* qs,
-                                          int64_t* out_at) {
-  using F = Form<kCodes, D, NQ>;
-  constexpr int E = D / 8, V = E / 8;  // elements, 16-byte vectors of a lane
-  const int lane = threadIdx.x & 31, l = lane & 7, columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
-  struct Group {  // of four columns: this lane's part of its column
-    uint4 v[V];
-    int j, head;
-  };
-  const auto load = [&](int c) {
-    Group g;
-    const int col = walk.chunk * NQ + c;
-    g.j = c < columns ? (int)(col * a.group_inv >> 32) : 0;
-    g.head = walk.head * a.group + col - g.j * a.group;
-    const __nv_bfloat16* src = a.q + (int64_t)(walk.q.lo + g.j) * a.ldq + g.head * D + l * E;
+// q of a part as operand pieces, eight lanes a column: this lane's elements (16 or 8) of column c.
+template <int D>
+struct QColumn {
+  static constexpr int E = D / 8, V = E / 8;
+  uint4 v[V];
+  __device__ __forceinline__ void load(const TreeArgs& a, const Part& p, int c) {
+    const int col = p.col0 + c, j = (int)((uint32_t)col * a.group_inv >> 32);
+    const __nv_bfloat16* src =
+        a.q + (int64_t)(p.lo + j) * a.ldq + (p.head * a.group + col - j * a.group) * D + (threadIdx.x & 7) * E;
 #pragma unroll
-    for (int i = 0; i < V; ++i) g.v[i] = c < columns ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
-    return g;
-  };
-  int c = w * 4 + (lane >> 3);
-  Group next = load(c);
-#pragma unroll 1
-  for (; c < NQ; c += warps * 4) {
-    Group g = next;
-    if (c + warps * 4 < NQ) next = load(c + warps * 4);
-    uint32_t* x = reinterpret_cast<uint32_t*>(g.v);
+    for (int i = 0; i < V; ++i) v[i] = c < p.columns ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
+  }
+  // to the operand at dst, the column's factor and its place in out
+  template <bool kCodes, int NQ>
+  __device__ __forceinline__ void store(const TreeArgs& a, const Part& p, int c, uint8_t* dst, float* qs, int64_t* out_at) {
+    using F = Form<kCodes, D, NQ>;
+    const int l = threadIdx.x & 7;
+    uint32_t* x = reinterpret_cast<uint32_t*>(v);
     uint32_t top = 0;  // the largest magnitude's bits; infinities and NaN are above all others
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) top = __vmaxu2(top, x[i] & 0x7FFF7FFFu);
@@ -294,15 +305,16 @@ __device__ __forceinline__ void prepare_q(const TreeArgs& a, const Walk& walk, u
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int byte = l * E * 2 + i * 16;
-        *reinterpret_cast<uint4*>(dst + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) = g.v[i];
+        *reinterpret_cast<uint4*>(dst + byte / F::kRow * F::kQPart + swizzled<F::kRow>(c * F::kRow + byte % F::kRow)) = v[i];
       }
     }
     if (l == 0) {
-      qs[c] = c < columns ? (fin ? unit : NAN) : 0.f;
-      out_at[c] = (int64_t)(walk.q.lo + g.j) * a.ldo + g.head * D;
+      const int col = p.col0 + c, j = (int)((uint32_t)col * a.group_inv >> 32);
+      qs[c] = c < p.columns ? (fin ? unit : NAN) : 0.f;
+      out_at[c] = (int64_t)(p.lo + j) * a.ldo + (p.head * a.group + col - j * a.group) * D;
     }
   }
-}
+};
 
 template <int n>
 __device__ __forceinline__ void load_columns(uint32_t taddr, float* v) {
@@ -325,19 +337,30 @@ __device__ __forceinline__ void load_sum(uint32_t taddr, int apart, float (&v)[8
   }
 }
 
-// the sum of element d of v over the drafted rows `nodes`, those that are not finite
-template <bool kCodes, int D>
-__device__ __noinline__ float non_finite_v(const TreeArgs& a, int r, int32_t base, int head, unsigned long long nodes, int d) {
-  float sum = 0.f;
+// Adds the non-finite elements of v that columns c0 .. c1 see of the drafted rows `nodes` to what was
+// written for them (element d of the head).
+template <bool kCodes, int D, int NQ>
+__device__ __noinline__ void add_non_finite(const TreeArgs& a, const Part& p, const uint64_t* seers, const int64_t* out_at,
+                                            unsigned long long nodes, int c0, int c1, int d) {
   for (; nodes; nodes &= nodes - 1) {
-    const int32_t row = pool_row(a.pool, r, (int64_t)base + __ffsll((long long)nodes) - 1);
+    const int node = __ffsll((long long)nodes) - 1;
+    const int32_t row = pool_row(a.pool, p.r, (int64_t)p.base + node);
     if (row < 0) continue;
-    const int64_t at = ((int64_t)row + ((int64_t)head << a.pool.shift)) * D + d;
+    const int64_t at = ((int64_t)row + ((int64_t)p.head << a.pool.shift)) * D + d;
     const float x = kCodes ? ((a.pool.v[at] & 0x7F) == 0x7F ? NAN : 0.f)
                            : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.pool.v)[at]);
-    if (!(fabsf(x) < INFINITY)) sum += x;
+    if (fabsf(x) < INFINITY) continue;
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+      if (!((seers[node] >> c) & 1)) continue;
+      if (p.slot < 0) {
+        __nv_bfloat16* o = a.out + out_at[c] + d;
+        *o = __float2bfloat16_rn(__bfloat162float(*o) + x);
+      } else {
+        a.part[((int64_t)p.slot * NQ + c) * D + d] += x;
+      }
+    }
   }
-  return sum;
 }
 
 template <bool kCodes, int D, int NQ>
@@ -353,15 +376,16 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   uint8_t* sStage = sm + F::kFixed;  // [stages] k, v; then their scales
   float* sScale = reinterpret_cast<float*>(sStage + F::kStages * 2 * F::kOperand);
   __shared__ uint64_t kfull[F::kStages], vfull[F::kStages], empty[F::kStages], sfull[kPairs], sfree[kPairs], pready[kPairs], pdone[kPairs], qfull[2],
-      qempty[2];
+      planned[kPlans], ended[kPlans];
   __shared__ uint32_t tmem_slot, okmask[F::kStages];
-  __shared__ int abort_s, never_s, start_r;
-  __shared__ int64_t start_at, sums[kThreads / 32 + 1];
-  // of the part and the next: the drafted rows with non-finite v, the columns that see a drafted row, each
-  // column's place in out and its factor
-  __shared__ Part parts[2];
+  __shared__ int abort_s, never_s;
+  __shared__ Start start;
+  __shared__ int64_t sums[kThreads / 32 + 1];
+  // the parts planned and the columns that see each drafted row; of this part and the next the drafted rows
+  // with non-finite v, each column's place in out and its factor
+  __shared__ Part parts[kPlans];
+  __shared__ uint64_t seers[kPlans][DSPARK_MAX_TREE];
   __shared__ unsigned long long hidden[2];
-  __shared__ uint64_t seers[2][DSPARK_MAX_TREE];
   __shared__ int64_t out_at[2][NQ];
   __shared__ __align__(16) float qs[2][NQ];
   __shared__ __align__(16) float nref[kPairs][NQ], delta[kPairs][NQ], factor[kPairs][NQ];
@@ -383,9 +407,12 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       ptx::mbar_init(&pdone[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&qfull[i], 1);
-      ptx::mbar_init(&qempty[i], kSoftWarps);
+      ptx::mbar_init(&qfull[i], kSoftWarps);
       hidden[i] = 0;
+    }
+    for (int i = 0; i < kPlans; ++i) {
+      ptx::mbar_init(&planned[i], 1);
+      ptx::mbar_init(&ended[i], kSoftWarps);
     }
     ptx::fence_mbar_init();
     abort_s = never_s = 0;
@@ -398,17 +425,15 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   }
   ptx::launch_dependents();
   ptx::grid_wait();
-  auto fail = [&](int what) {
-    if (a.hdr) report_error(a.hdr, DSPARK_TIMEOUT, what);
-    *abort_flag = 1;
-  };
+  auto fail = [&](int what) { *abort_flag = what; };  // reported at the end
 
   // this CTA's share of the units: a scan over the requests, a run of them a thread
   const int per = (a.pool.n_req + kThreads - 1) / kThreads, from = threadIdx.x * per, to = min(a.pool.n_req, from + per);
   int64_t mine = 0;
+#pragma unroll 1
   for (int r = from; r < to; ++r) {
     bool bad;
-    mine += request_at(a, r, NQ, &bad).units;
+    mine += request_at<NQ>(a, r, &bad).units;
     if (bad && blockIdx.x == 0 && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, r);
   }
   int64_t before = mine;
@@ -429,23 +454,29 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     total += sums[w];
   }
   const int ctas = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
-  const int64_t u0 = cta < ctas ? total * cta / ctas : 0, u1 = cta < ctas ? total * (cta + 1) / ctas : 0;
+  // CTA c's units: an even share, the first total % ctas of the CTAs one more
+  const int64_t each = ctas ? total / ctas : 0, rest = total - each * ctas;
+  const int64_t u0 = cta < ctas ? each * cta + min((int64_t)cta, rest) : 0;
+  const int64_t u1 = cta < ctas ? u0 + each + (cta < rest) : 0;
   if (u1 > u0 && before <= u0 && u0 < before + mine) {
     int r = from;
     int64_t at = u0 - before;
+    Request q;
+#pragma unroll 1
     for (;; ++r) {
       bool bad;
-      const int64_t n = request_at(a, r, NQ, &bad).units;
-      if (at < n) break;
-      at -= n;
+      q = request_at<NQ>(a, r, &bad);
+      if (at < q.units) break;
+      at -= q.units;
     }
-    start_r = r;
-    start_at = at;
+    const int cost = q.tiles + kItemCost<NQ>;
+    const int64_t item = at / cost;
+    start = Start{r, (int)(item / q.chunks), (int)(item % q.chunks), (int)(at - item * cost)};
   }
   if (threadIdx.x == 0) a.meta[cta] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  Walk walk;
-  walk.start(a, start_r, start_at, u1 - u0, NQ);
+  Walk<NQ> walk;
+  walk.start(a, start, u1 - u0);
   if (warp >= kSoftWarps) {
   ptx::reg_dec<F::kRegsLow>();
   if (warp == kSoftWarps) {
@@ -455,7 +486,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     const int i = lane & 7, what = (lane >> 3) & 1;
     uint32_t s = 0, ph = 1, n = 0;
     bool ok = true;
-    while (ok && walk.next(a, NQ)) {
+    while (ok && walk.next(a)) {
       const int len = walk.q.base + walk.q.rows;
       const int32_t* table = a.pool.table + walk.r * a.pool.table_ld;
       int pos = walk.tile * kTile + (i << box_shift);
@@ -465,7 +496,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
         const int32_t here = page, at = pos;
         pos += kTile;
         page = i < boxes && pos < len && t + 1 < walk.tiles ? table[pos >> a.pool.shift] : -1;
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(&empty[s], ph, abort_flag, kWaitLimit));
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_polls(&empty[s], ph, abort_flag));
         if (!ok) {
           if (lane == 0) fail(1);
           break;
@@ -505,8 +536,8 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     }
     // nothing may be in flight when the CTA leaves
     for (uint32_t j = n > (uint32_t)F::kStages ? n - F::kStages : 0; j < n; ++j) {
-      ptx::mbar_wait_cycles(&kfull[j % F::kStages], (j / F::kStages) & 1, &never_s, kWaitLimit);
-      ptx::mbar_wait_cycles(&vfull[j % F::kStages], (j / F::kStages) & 1, &never_s, kWaitLimit);
+      ptx::mbar_wait_polls(&kfull[j % F::kStages], (j / F::kStages) & 1, &never_s);
+      ptx::mbar_wait_polls(&vfull[j % F::kStages], (j / F::kStages) & 1, &never_s);
     }
     __syncwarp();
   } else if (warp < kSoftWarps + 3) {
@@ -525,7 +556,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     const uint64_t dr0 = ptx::smem_desc_sw64(ptx::smem_u32(sP) + F::kPCol, 16, 512);
     const bool is_s = warp == kSoftWarps + 1;
     auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
-      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit));
+      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_polls(bar, parity, abort_flag));
       if (!got && lane == 0) fail(what);
       return got;
     };
@@ -535,7 +566,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       const int qb = part & 1;
       ok = wait(&qfull[qb], (part >> 1) & 1, 2);
       if (!ok) break;
-      const int tiles = parts[qb].tiles;
+      const int tiles = parts[part % kPlans].tiles;
       if (tiles == 0) break;
       for (int t = 0; t < tiles; ++t) {
         const int w = t % kPairs;
@@ -596,36 +627,19 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     }
     __syncwarp();
   } else {
-    // ---- q of a part, one part ahead of the softmax ----
+    // ---- the parts, ahead of the softmax ----
     for (uint32_t part = 0;; ++part) {
-      const int b = part & 1;
-      const bool more = walk.next(a, NQ);
-      if (!__all_sync(0xffffffffu, ptx::mbar_wait_cycles(&qempty[b], ~(part >> 1) & 1, abort_flag, kWaitLimit))) {
+      const int b = part % kPlans;
+      const bool more = walk.next(a);
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait_polls(&ended[b], ~(part / kPlans) & 1, abort_flag))) {
         if (lane == 0) fail(7);
         break;
       }
-      if (!more) {
-        if (lane == 0) {
-          parts[b].tiles = 0;
-          ptx::mbar_arrive(&qfull[b]);
-        }
-        break;
-      }
-      if (lane == 0) {
-        Part p;
-        p.r = walk.r, p.base = walk.q.base, p.rows = walk.q.rows, p.head = walk.head;
-        p.tile = walk.tile, p.tiles = walk.tiles, p.columns = min(NQ, walk.q.rows * a.group - walk.chunk * NQ);
-        p.slot = walk.begins && walk.ends ? -1 : 2 * cta + walk.begins;
-        parts[b] = p;
-        if (walk.begins && !walk.ends) {  // so it is the last part here; unit u is CTA ((u + 1) ctas - 1) / total's
-          const int64_t end = u1 + walk.q.tiles - walk.tiles;
-          a.meta[cta] = make_int4(walk.r, walk.head * walk.q.chunks + walk.chunk, (int)((end * ctas - 1) / total) - cta + 1, 0);
-        }
-      }
-      {
-        // bits of the chunk's columns, row after row: those of row j begin at j group - chunk NQ
-        const int j0 = (int)((uint32_t)(walk.chunk * NQ) * a.group_inv >> 32);
-        const int j1 = min(walk.q.rows, (int)((uint32_t)(walk.chunk * NQ + NQ - 1) * a.group_inv >> 32) + 1);
+      if (more) {
+        // bits of the chunk's columns, row after row: those of row j begin at j group - col0
+        const int col0 = walk.chunk * NQ;
+        const int j0 = (int)((uint32_t)col0 * a.group_inv >> 32);
+        const int j1 = min(walk.q.rows, (int)((uint32_t)(col0 + NQ - 1) * a.group_inv >> 32) + 1);
         uint64_t see0 = 0, see1 = 0;    // of nodes `lane` and lane + 32
         uint64_t mine0 = 0, mine1 = 0;  // the words of rows `lane` and lane + 32
         if (a.tree) {
@@ -638,7 +652,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
 #pragma unroll 1
         for (int j = j0; j < j1; ++j) {
           const uint64_t word = __shfl_sync(0xffffffffu, j < 32 ? mine0 : mine1, j & 31);
-          const int first = max(0, j * a.group - walk.chunk * NQ), last = min(NQ, (j + 1) * a.group - walk.chunk * NQ);
+          const int first = max(0, j * a.group - col0), last = min(NQ, (j + 1) * a.group - col0);
           const uint64_t bits = (~0ull >> (64 - (last - first))) << first;
           if ((word >> lane) & 1) see0 |= bits;
           if ((word >> (lane + 32)) & 1) see1 |= bits;
@@ -646,13 +660,25 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
         seers[b][lane] = see0;
         seers[b][lane + 32] = see1;
       }
-      if (part > 0)
-        prepare_q<kCodes, D, NQ>(a, walk, sQ + b * F::kQ, 0, 1, qs[b], out_at[b]);
-      else
-        ptx::named_sync(6, kSoft + 32);  // the softmax's warps, which have nothing else to do yet
-      ptx::fence_proxy_async_smem();
+      if (lane == 0) {
+        Part p;
+        p.tiles = 0;
+        if (more) {
+          p.r = walk.r, p.lo = walk.q.lo, p.base = walk.q.base, p.rows = walk.q.rows, p.head = walk.head;
+          p.tile = walk.tile, p.tiles = walk.tiles, p.col0 = walk.chunk * NQ;
+          p.columns = min(NQ, walk.q.rows * a.group - p.col0);
+          p.slot = walk.begins && walk.ends ? -1 : 2 * cta + walk.begins;
+          if (walk.begins && !walk.ends) {  // so it is the last part here; which CTA has the item's last unit:
+            const int64_t last = u1 + walk.q.tiles - walk.tiles - 1, wide = (each + 1) * rest;
+            const int end = (int)(last < wide ? last / (each + 1) : rest + (last - wide) / each);
+            a.meta[cta] = make_int4(walk.r, walk.head * walk.q.chunks + walk.chunk, end - cta + 1, 0);
+          }
+        }
+        parts[b] = p;
+      }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&qfull[b]);
+      if (lane == 0) ptx::mbar_arrive(&planned[b]);
+      if (!more) break;
     }
     __syncwarp();
   }
@@ -665,49 +691,69 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16), tS = lanes + w * NQ + h * HQ, tO = lanes + kPairs * NQ;
     const int box_shift = min(a.pool.shift, 7);
     const uint32_t all_ok = (1u << (kTile >> box_shift)) - 1;
-    uint32_t n0 = 0, turn = 0;  // the CTA's tiles before this part, this warpgroup's so far
+    uint32_t n0 = opaque(0), turn = opaque(0);  // the CTA's tiles before this part, this warpgroup's so far
     auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
-      if (!ptx::mbar_wait_cycles(bar, parity, abort_flag, kWaitLimit)) fail(what);  // the loops run on: every later wait ends at once
+      if (!ptx::mbar_wait_polls(bar, parity, abort_flag)) fail(what);  // the loops run on: every later wait ends at once
     };
-    if (walk.next(a, NQ)) {
-      prepare_q<kCodes, D, NQ>(a, walk, sQ, warp, kSoftWarps, qs[0], out_at[0]);
-      ptx::fence_proxy_async_smem();
-      ptx::named_arrive(6, kSoft + 32);
-    }
-    for (uint32_t part = 0;; ++part) {
+    // q of part `part`: four columns a warp, loaded before it is needed
+    QColumn<D> q;
+    const int qc = warp * 4 + (lane >> 3);
+    static_assert(NQ <= 4 * kSoftWarps, "four columns a warp");
+    const auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };  // of a value that the warp shares
+    const auto load_q = [&](int part) {
+      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_polls(&planned[part % kPlans], (part / kPlans) & 1, abort_flag));
+      if (!got) fail(8);
+      if (got && same(parts[part % kPlans].tiles) > 0 && warp * 4 < NQ) q.load(a, parts[part % kPlans], qc);
+    };
+    const auto store_q = [&](int part) {
+      if (same(*abort_flag) == 0 && same(parts[part % kPlans].tiles) > 0 && warp * 4 < NQ) {
+        q.template store<kCodes, NQ>(a, parts[part % kPlans], qc, sQ + (part & 1) * F::kQ, qs[part & 1], out_at[part & 1]);
+        ptx::fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&qfull[part & 1]);
+    };
+    int stored = opaque(0), last = opaque(0), loaded = opaque(0);  // parts whose q is in place, ..
+    for (int part = opaque(0);; ++part) {
       const int b = part & 1;
+      const Part& now = parts[part % kPlans];
+      // q of this part and the next (this part's is there already but for the first)
+#pragma unroll 1
+      while (stored < part + 2 && !last) {
+        if (!loaded) load_q(stored);
+        loaded = 0;
+        store_q(stored);
+        last = same(parts[stored % kPlans].tiles) <= 0;
+        ++stored;
+      }
       // this warpgroup's references and their like
       float* my_nref = &nref[w][h * HQ];
       float* my_delta = &delta[w][h * HQ];
       float* my_factor = &factor[w][h * HQ];
       if (token < HQ) my_nref[token] = 0.f, set[w][h * HQ + token] = false;
-      const bool got = ptx::mbar_wait_cycles(&qfull[b], (part >> 1) & 1, abort_flag, kWaitLimit);
+      const bool got = ptx::mbar_wait_polls(&qfull[b], (part >> 1) & 1, abort_flag);
       if (!got) fail(10);
-      if (ptx::named_any(kAll, kSoft, !got)) break;
-      const int tiles = parts[b].tiles, tile0 = parts[b].tile;
+      if (same(ptx::named_any(kAll, kSoft, !got))) break;
+      const int tiles = same(now.tiles), tile0 = same(now.tile);
       if (tiles == 0) break;
-      const int base = parts[b].base, len = base + parts[b].rows;
+      const int base = same(now.base), len = base + same(now.rows);
 
       uint64_t l2[HQ / 2];
 #pragma unroll
       for (int i = 0; i < HQ / 2; ++i) l2[i] = 0;
-      bool unset = true;  // a column has no reference yet
+      bool unset = opaque(1) != 0;  // a column has no reference yet
+      uint32_t s = (n0 + w) % F::kStages, ph = ((n0 + w) / F::kStages) & 1;
 #pragma unroll 1
-      for (int t = w; t < tiles; t += kPairs) {
-        const uint32_t n = n0 + t, s = n % F::kStages, ph = (n / F::kStages) & 1;
+      for (int t = opaque(w); t < tiles; t += kPairs) {
         wait(&kfull[s], ph, 11);
         const int pos0 = (tile0 + t) * kTile, pos = pos0 + token;
         const uint32_t have = okmask[s];
         const bool masked = pos0 + kTile > base || have != all_ok;
-        const bool held = pos < len && ((have >> (token >> box_shift)) & 1);
-        float k_scale = 1.f, v_log = 0.f, v_inv = 1.f;
-        if (kCodes && (!masked || held)) {
+        const bool held = pos < len && ((have >> (token >> box_shift)) & 1);  // looked at where masked
+        float k_scale = 1.f, v_scale = 1.f;
+        if (kCodes) {
           k_scale = sScale[s * 2 * kTile + token];
-          float v = sScale[s * 2 * kTile + kTile + token];
-          if (v < 1.17549435e-38f) v = 1.17549435e-38f;  // 0 of a cache that was cleared
-          v_log = __log2f(v);
-          v_inv = ptx::rcp(v);
-          if (v != v) v_inv = 1.f;  // the weights of those that see it are NaN, of the others 0
+          v_scale = sScale[s * 2 * kTile + kTile + token];
         }
         if (masked && h == 0) {
           // what no row or only some see must not reach the others through 0 * NaN
@@ -736,30 +782,43 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
         wait(&sfull[w], turn & 1, 13);
         ++turn;
         ptx::tc_fence_after();
-        // y, less the reference so far
+        // y, less the reference so far: S (qs ks) + (log2 vs - ref); both factors are formed while S arrives
         uint64_t x2[HQ / 2];
-        {
-          const uint64_t ks2 = ptx::pack2(k_scale, k_scale), vl2 = ptx::pack2(v_log, v_log);
-          float v[HQ];
-          load_columns<HQ>(tS, v);
-          ptx::tmem_ld_wait<HQ>(v);
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sfree[w]);
+        constexpr int L = HQ < 16 ? HQ : 16;  // columns at a time
+        float v[HQ / L][L], v_inv = 1.f;
+        load_columns<L>(tS, v[0]);
+        uint64_t ks2 = 0, vl2 = 0;
+        if (kCodes) {
+          if (v_scale < 1.17549435e-38f) v_scale = 1.17549435e-38f;  // 0 of a cache that was cleared
+          const float v_log = __log2f(v_scale);
+          v_inv = ptx::rcp(v_scale);
+          // what is no token's scale, and NaN: then the weights of those that see it are NaN, of the others 0
+          if (masked && !(held && v_scale == v_scale)) v_inv = 1.f;
+          ks2 = ptx::pack2(k_scale, k_scale);
+          vl2 = ptx::pack2(v_log, v_log);
+        }
 #pragma unroll
-          for (int i = 0; i < HQ / 2; i += 2) {
-            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&qs[b][h * HQ + 2 * i]);
-            const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&my_nref[2 * i]);  // 0 before they are set
+        for (int c = 0; c < HQ; c += L) {
+          uint64_t f[L / 2], g[L / 2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint64_t y = ptx::mul2(ptx::pack2(v[2 * (i + e)], v[2 * (i + e) + 1]), e ? u.y : u.x);
-              if (kCodes) y = ptx::fma2(y, ks2, vl2);
-              x2[i + e] = ptx::add2(y, e ? r.y : r.x);
-            }
+          for (int i = 0; i < L / 2; i += 2) {
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&qs[b][h * HQ + c + 2 * i]);
+            const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&my_nref[c + 2 * i]);  // 0 before they are set
+            f[i] = kCodes ? ptx::mul2(u.x, ks2) : u.x, f[i + 1] = kCodes ? ptx::mul2(u.y, ks2) : u.y;
+            g[i] = kCodes ? ptx::add2(r.x, vl2) : r.x, g[i + 1] = kCodes ? ptx::add2(r.y, vl2) : r.y;
           }
+          ptx::tmem_ld_wait<L>(v[c / L]);
+          if (c + L < HQ) load_columns<L>(tS + c + L, v[c / L + (c + L < HQ)]);
+          if (c + L == HQ) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sfree[w]);
+          }
+#pragma unroll
+          for (int i = 0; i < L / 2; ++i) x2[c / 2 + i] = ptx::fma2(ptx::pack2(v[c / L][2 * i], v[c / L][2 * i + 1]), f[i], g[i]);
         }
         if (masked) {
-          const uint32_t see = !held ? 0u : pos < base ? ~0u : (uint32_t)(seers[b][pos - base] >> (h * HQ));
+          const uint32_t see = !held ? 0u : pos < base ? ~0u : (uint32_t)(seers[part % kPlans][pos - base] >> (h * HQ));
 #pragma unroll
           for (int i = 0; i < HQ / 2; ++i) {
             const float2 x = ptx::unpack2(x2[i]);
@@ -779,17 +838,14 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
         }
         if (raise) {
           // the columns' largest, new references, what was summed so far brought to them
-          {
-            float v[HQ];
+          float m = -INFINITY;  // of column `lane`
 #pragma unroll
-            for (int i = 0; i < HQ / 2; ++i) {
-              const float2 x = ptx::unpack2(x2[i]);
-              v[2 * i] = x.x;
-              v[2 * i + 1] = x.y;
-            }
-            const float m = over_lanes<HQ>(v, [](float x, float y) { return fmaxf(x, y); });
-            if (lane < HQ) warp_top[warp][lane] = m;
+          for (int i = 0; i < HQ / 2; ++i) {
+            const float2 x = ptx::unpack2(x2[i]);
+            const float m0 = ptx::warp_max_redux(x.x), m1 = ptx::warp_max_redux(x.y);
+            m = lane == 2 * i ? m0 : lane == 2 * i + 1 ? m1 : m;
           }
+          if (lane < HQ) warp_top[warp][lane] = m;
           ptx::named_sync(own, 128);
           bool none = false;
           if (token < HQ) {
@@ -803,7 +859,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
             else
               none = true;
             my_delta[token] = -d;
-            my_factor[token] = exp2f(-d);
+            my_factor[token] = ptx::ex2(-d);
             my_nref[token] -= d;
           }
           unset = ptx::named_any(own, 128, none);
@@ -831,11 +887,12 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
         // weights, their sums and their pieces
         uint8_t* prow = sP + w * F::kP + token * 128;
         const uint64_t vi2 = ptx::pack2(v_inv, v_inv);
+        constexpr int G = HQ < 16 ? HQ : 16;  // columns at a time
 #pragma unroll
-        for (int c = 0; c < HQ; c += 8) {
-          uint32_t hh[4], r1[4], c3[4];
+        for (int c = 0; c < HQ; c += G) {
+          uint32_t hh[G / 2], r1[G / 2], c3[G / 2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < G / 2; ++i) {
             const float2 x = ptx::unpack2(x2[c / 2 + i]);
             const float p0 = ptx::ex2(x.x), p1 = ptx::ex2(x.y);
             const uint64_t p2 = ptx::pack2(p0, p1);
@@ -851,30 +908,47 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
             }
           }
           // (16-byte unit u of row r lies at u ^ (r % 8))
-          auto place = [&](uint32_t byte) {
-            return prow + (((byte >> 4) ^ (token & 7)) << 4) + (byte & 15);
-          };
+          auto place = [&](uint32_t byte) { return prow + (((byte >> 4) ^ (token & 7)) << 4) + (byte & 15); };
           if constexpr (kCodes) {
             const uint32_t byte = h * HQ + c;
-            *reinterpret_cast<uint2*>(place(byte)) = make_uint2(__byte_perm(hh[0], hh[1], 0x7531), __byte_perm(hh[2], hh[3], 0x7531));
-            *reinterpret_cast<uint2*>(place(NQ + byte)) =
-                make_uint2(__byte_perm(r1[0], r1[1], 0x7531), __byte_perm(r1[2], r1[3], 0x7531));
+            uint32_t b1[G / 4], b2[G / 4], b3[G / 4];
+#pragma unroll
+            for (int i = 0; i < G / 4; ++i) {
+              b1[i] = __byte_perm(hh[2 * i], hh[2 * i + 1], 0x7531);
+              b2[i] = __byte_perm(r1[2 * i], r1[2 * i + 1], 0x7531);
+              b3[i] = __byte_perm(c3[2 * i], c3[2 * i + 1], 0x5410);
+            }
             uint8_t* third = place(2 * NQ + byte);
-            if constexpr (F::kPRest > 0)
-              third = sP + w * F::kP + F::kPCol + swizzled<64>(token * 64 + byte);
-            *reinterpret_cast<uint2*>(third) = make_uint2(__byte_perm(c3[0], c3[1], 0x5410), __byte_perm(c3[2], c3[3], 0x5410));
+            if constexpr (F::kPRest > 0) third = sP + w * F::kP + F::kPCol + swizzled<64>(token * 64 + byte);
+            if constexpr (G == 16) {
+              *reinterpret_cast<uint4*>(place(byte)) = make_uint4(b1[0], b1[1], b1[2], b1[3]);
+              *reinterpret_cast<uint4*>(place(NQ + byte)) = make_uint4(b2[0], b2[1], b2[2], b2[3]);
+              *reinterpret_cast<uint4*>(third) = make_uint4(b3[0], b3[1], b3[2], b3[3]);
+            } else {
+              *reinterpret_cast<uint2*>(place(byte)) = make_uint2(b1[0], b1[1]);
+              *reinterpret_cast<uint2*>(place(NQ + byte)) = make_uint2(b2[0], b2[1]);
+              *reinterpret_cast<uint2*>(third) = make_uint2(b3[0], b3[1]);
+            }
           } else {
-            *reinterpret_cast<uint4*>(place((h * HQ + c) * 2)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+#pragma unroll
+            for (int i = 0; i < G / 8; ++i)
+              *reinterpret_cast<uint4*>(place((h * HQ + c + 8 * i) * 2)) = make_uint4(hh[4 * i], hh[4 * i + 1], hh[4 * i + 2], hh[4 * i + 3]);
           }
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&pready[w]);
+        s += kPairs;
+        if (s >= (uint32_t)F::kStages) s -= F::kStages, ph ^= 1;
       }
 
       // ---- the part's end: sums of both tile sequences, O joined and written ----
       n0 += tiles;
+      if (!last) {
+        load_q(stored);
+        loaded = 1;
+      }
       const bool two = kPairs > 1 && tiles > 1;  // both pairs have a tile
       if (w == 0 || two) wait(&pdone[w], (turn - 1) & 1, 15);
       {
@@ -892,7 +966,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       ptx::tc_fence_after();
       const unsigned long long bad_rows = hidden[b];
       if (threadIdx.x == 0) hidden[b ^ 1] = 0;
-      const int slot = parts[b].slot, columns = parts[b].columns;
+      const int slot = same(now.slot), columns = same(now.columns);
       const bool whole = slot < 0;
       if (threadIdx.x < NQ) {
         const int c = threadIdx.x, half = c / HQ, i = c % HQ;
@@ -909,11 +983,11 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           if (two) {
             m = fmaxf(ref[0], ref[1]);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) f[g] = ref[g] == m ? 1.f : exp2f(ref[g] - m);
+            for (int g = 0; g < 2; ++g) f[g] = ref[g] == m ? 1.f : ptx::ex2(ref[g] - m);
             sum = f[0] * l[0] + f[1] * l[1];
           }
         }
-        const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = !whole ? 1.f : sum == 0.f ? 0.f : __frcp_rn(sum);
 #pragma unroll
         for (int g = 0; g < kPairs; ++g) coef[g][c] = f[g] * inv;
         if (!whole) a.stat[(int64_t)slot * NQ + c] = make_float2(m, sum);
@@ -934,17 +1008,6 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           const float* f1 = &coef[kPairs - 1][c0];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = two ? fmaf(f1[i], u[i], f0[i] * v[i]) : f0[i] * v[i];
-          if (bad_rows) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              unsigned long long nodes = 0;  // that column c0 + i sees
-              for (unsigned long long left = bad_rows; left; left &= left - 1) {
-                const int node = __ffsll((long long)left) - 1;
-                if ((seers[b][node] >> (c0 + i)) & 1) nodes |= 1ull << node;
-              }
-              if (nodes) v[i] += non_finite_v<kCodes, D>(a, parts[b].r, parts[b].base, parts[b].head, nodes, d);
-            }
-          }
           if (whole) {
             const int64_t* at = &out_at[b][c0];
 #pragma unroll
@@ -957,14 +1020,17 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
               if (i < n) at[i * D] = v[i];
           }
         }
+        if (bad_rows && d < D)
+          add_non_finite<kCodes, D, NQ>(a, now, seers[part % kPlans], out_at[b], bad_rows, wg * W, min(columns, (wg + 1) * W), d);
       }
       ptx::tc_fence_before();
       ptx::named_sync(kAll, kSoft);  // O may be written again
-      if (lane == 0) ptx::mbar_arrive(&qempty[b]);
+      if (lane == 0) ptx::mbar_arrive(&ended[part % kPlans]);
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && abort_s && a.hdr) report_error(a.hdr, DSPARK_TIMEOUT, abort_s);
   if (warp == kSoftWarps + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, F::kTmemCols);
@@ -980,6 +1046,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, in
   static_assert(kMaxCtas <= 2 * kJoinThreads, "two CTAs a thread");
   constexpr int E = D / 32;
   __shared__ int items[kMaxCtas], counts[2][kJoinThreads / 32];
+  __shared__ float sums[kJoinThreads / 32], os[kJoinThreads / 32][D];
   ptx::launch_dependents();
   ptx::grid_wait();
   const int t = threadIdx.x, warp = t / 32, lane = t % 32;
@@ -1000,27 +1067,33 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, in
     }
   }
   __syncthreads();
-  for (int at = blockIdx.x * (kJoinThreads / 32) + warp; at < n * NQ; at += gridDim.x * (kJoinThreads / 32)) {
+  // a warp a column, or all warps of a block where there are blocks for every column (parts taken in turn
+  // and added in the warps' order)
+  constexpr int kWarps = kJoinThreads / 32;
+  const int team = n * NQ <= gridDim.x ? kWarps : 1, member = team > 1 ? warp : 0;
+  for (int at = team > 1 ? blockIdx.x : blockIdx.x * kWarps + warp; at < n * NQ; at += gridDim.x * (kWarps / team)) {
     const int cta = items[at / NQ], c = at % NQ;
     const int4 m = a.meta[cta];
     const auto slot = [&](int p) { return (int64_t)(p ? 2 * (cta + p) : 2 * cta + 1) * NQ + c; };
     bool bad;
-    const Request q = request_at(a, m.x, NQ, &bad);
+    const Request q = request_at<NQ>(a, m.x, &bad);
     const int head = m.y / q.chunks, col = m.y % q.chunks * NQ + c, row = (int)(col * a.group_inv >> 32);
     if (row >= q.rows) continue;
     float ref = -INFINITY;
     for (int p = lane; p < m.z; p += 32) ref = fmaxf(ref, a.stat[slot(p)].x);
     ref = warp_max(ref);
     float sum = 0.f, o[E] = {};
-    for (int p0 = 0; p0 < m.z; p0 += 32) {
+    for (int p0 = member; p0 < m.z; p0 += 32 * team) {  // this warp's parts p0, p0 + team, ..
       float2 s = make_float2(-INFINITY, 0.f);
-      if (p0 + lane < m.z) s = a.stat[slot(p0 + lane)];
-      const float f = p0 + lane >= m.z ? 0.f : s.x == ref ? 1.f : exp2f(s.x - ref);
+      const int mine = p0 + lane * team;
+      if (mine < m.z) s = a.stat[slot(mine)];
+      const float f = mine >= m.z ? 0.f : s.x == ref ? 1.f : exp2f(s.x - ref);
       sum += f * s.y;
+      const int count = min(32, (m.z - p0 + team - 1) / team);
 #pragma unroll 4
-      for (int p = 0; p < min(32, m.z - p0); ++p) {
-        const float g = __shfl_sync(0xffffffffu, f, p);
-        const float* src = a.part + slot(p0 + p) * D + lane * E;
+      for (int i = 0; i < count; ++i) {
+        const float g = __shfl_sync(0xffffffffu, f, i);
+        const float* src = a.part + slot(p0 + i * team) * D + lane * E;
         if constexpr (E == 4) {
           const float4 x = *reinterpret_cast<const float4*>(src);
           o[0] = fmaf(g, x.x, o[0]), o[1] = fmaf(g, x.y, o[1]), o[2] = fmaf(g, x.z, o[2]), o[3] = fmaf(g, x.w, o[3]);
@@ -1031,6 +1104,22 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, in
       }
     }
     sum = warp_sum(sum);
+    if (team > 1) {  // (the block's warps take the same turns)
+      __syncthreads();
+      if (lane == 0) sums[warp] = sum;
+#pragma unroll
+      for (int e = 0; e < E; ++e) os[warp][lane * E + e] = o[e];
+      __syncthreads();
+      if (warp > 0) continue;
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
+      for (int w = 0; w < kWarps; ++w) {
+        sum += sums[w];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += os[w][lane * E + e];
+      }
+    }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint32_t out[E / 2];
 #pragma unroll
