@@ -57,6 +57,11 @@ template <bool kCodes>
 constexpr float kRaise = kCodes ? 15.f : 60.f;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// An item that several CTAs share: where its rows and columns are, and its parts (0: there is none).
+struct Shared {
+  int32_t lo, head, col0, columns, parts;
+};
+
 struct TreeArgs {
   KvPool pool;
   const __nv_bfloat16* q;
@@ -69,7 +74,7 @@ struct TreeArgs {
   uint64_t group_inv;  // ceil(2^32 / group): c / group is c group_inv >> 32 for c below 2^16
   float scale;
   WsHeader* hdr;
-  int4* meta;     // [CTAs] the item that begins in a CTA and goes on: request, its head and chunk, parts
+  Shared* meta;   // [CTAs] the item that begins in a CTA and goes on
   float2* stat;   // [2 CTAs, NQ] a part's references and sums
   float* part;    // [2 CTAs, NQ, D] a part's O
 };
@@ -144,7 +149,12 @@ __device__ __forceinline__ Request request_at(const TreeArgs& a, int r, bool* ba
 // Where a CTA's share begins: the request, the item and the unit within it.
 struct Start {
   int r, head, chunk, x;
+  Request q;
 };
+// (32-bit division where the numbers allow: a 64-bit one takes some 300 cycles)
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return (a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // The parts of items in a CTA's share of the units, one after the other; the warps that need them walk by themselves.
 template <int NQ>
 struct Walk {
@@ -154,13 +164,9 @@ struct Walk {
   // the part
   int tile, tiles;    // first tile, their number
   bool begins, ends;  // the item's first and last tile are in it
-  __device__ __forceinline__ void start(const TreeArgs& a, const Start& at, int64_t n) {
+  __device__ __forceinline__ void start(const Start& at, int64_t n) {
     left = n;
-    bool bad;
-    if (n > 0) {
-      r = at.r, head = at.head, chunk = at.chunk, x = at.x;
-      q = request_at<NQ>(a, r, &bad);
-    }
+    if (n > 0) r = at.r, head = at.head, chunk = at.chunk, x = at.x, q = at.q;
   }
   __device__ __forceinline__ bool next(const TreeArgs& a) {
 #pragma unroll 1
@@ -430,10 +436,13 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   // this CTA's share of the units: a scan over the requests, a run of them a thread
   const int per = (a.pool.n_req + kThreads - 1) / kThreads, from = threadIdx.x * per, to = min(a.pool.n_req, from + per);
   int64_t mine = 0;
+  Request q;  // the run's last
+  q.units = 0;
 #pragma unroll 1
   for (int r = from; r < to; ++r) {
     bool bad;
-    mine += request_at<NQ>(a, r, &bad).units;
+    q = request_at<NQ>(a, r, &bad);
+    mine += q.units;
     if (bad && blockIdx.x == 0 && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, r);
   }
   int64_t before = mine;
@@ -455,28 +464,30 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   }
   const int ctas = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
   // CTA c's units: an even share, the first total % ctas of the CTAs one more
-  const int64_t each = ctas ? total / ctas : 0, rest = total - each * ctas;
+  const int64_t each = ctas ? quotient(total, ctas) : 0, rest = total - each * ctas;
   const int64_t u0 = cta < ctas ? each * cta + min((int64_t)cta, rest) : 0;
   const int64_t u1 = cta < ctas ? u0 + each + (cta < rest) : 0;
   if (u1 > u0 && before <= u0 && u0 < before + mine) {
     int r = from;
     int64_t at = u0 - before;
-    Request q;
 #pragma unroll 1
-    for (;; ++r) {
+    for (; r < to - 1; ++r) {
       bool bad;
-      q = request_at<NQ>(a, r, &bad);
-      if (at < q.units) break;
-      at -= q.units;
+      const Request p = request_at<NQ>(a, r, &bad);
+      if (at < p.units) {
+        q = p;
+        break;
+      }
+      at -= p.units;
     }
     const int cost = q.tiles + kItemCost<NQ>;
-    const int64_t item = at / cost;
-    start = Start{r, (int)(item / q.chunks), (int)(item % q.chunks), (int)(at - item * cost)};
+    const int64_t item = quotient(at, cost);
+    start = Start{r, (int)((uint32_t)item / (uint32_t)q.chunks), (int)((uint32_t)item % (uint32_t)q.chunks), (int)(at - item * cost), q};
   }
-  if (threadIdx.x == 0) a.meta[cta] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0) a.meta[cta].parts = 0;
   __syncthreads();
   Walk<NQ> walk;
-  walk.start(a, start, u1 - u0);
+  walk.start(start, u1 - u0);
   if (warp >= kSoftWarps) {
   ptx::reg_dec<F::kRegsLow>();
   if (warp == kSoftWarps) {
@@ -671,7 +682,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           if (walk.begins && !walk.ends) {  // so it is the last part here; which CTA has the item's last unit:
             const int64_t last = u1 + walk.q.tiles - walk.tiles - 1, wide = (each + 1) * rest;
             const int end = (int)(last < wide ? last / (each + 1) : rest + (last - wide) / each);
-            a.meta[cta] = make_int4(walk.r, walk.head * walk.q.chunks + walk.chunk, end - cta + 1, 0);
+            a.meta[cta] = Shared{p.lo, p.head, p.col0, p.columns, end - cta + 1};
           }
         }
         parts[b] = p;
@@ -1040,7 +1051,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
 // The items that several CTAs share: part 0 is the second slot of the CTA they begin in,
 // the others the first slots of those behind it.  A warp takes a column of one of them,
 // D / 32 elements a lane.
-constexpr int kJoinThreads = 256, kJoinCtas = 4;  // an SM
+constexpr int kJoinThreads = 256, kJoinCtas = 8;  // an SM
 template <int D, int NQ>
 __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, int ctas) {
   static_assert(kMaxCtas <= 2 * kJoinThreads, "two CTAs a thread");
@@ -1054,7 +1065,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, in
   bool mine[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    mine[i] = t + i * kJoinThreads < ctas && a.meta[t + i * kJoinThreads].z > 1;
+    mine[i] = t + i * kJoinThreads < ctas && a.meta[t + i * kJoinThreads].parts > 1;
     votes[i] = __ballot_sync(0xffffffffu, mine[i]);
     if (lane == 0) counts[i][warp] = __popc(votes[i]);
   }
@@ -1073,23 +1084,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, in
   const int team = n * NQ <= gridDim.x ? kWarps : 1, member = team > 1 ? warp : 0;
   for (int at = team > 1 ? blockIdx.x : blockIdx.x * kWarps + warp; at < n * NQ; at += gridDim.x * (kWarps / team)) {
     const int cta = items[at / NQ], c = at % NQ;
-    const int4 m = a.meta[cta];
+    const Shared m = a.meta[cta];
     const auto slot = [&](int p) { return (int64_t)(p ? 2 * (cta + p) : 2 * cta + 1) * NQ + c; };
-    bool bad;
-    const Request q = request_at<NQ>(a, m.x, &bad);
-    const int head = m.y / q.chunks, col = m.y % q.chunks * NQ + c, row = (int)(col * a.group_inv >> 32);
-    if (row >= q.rows) continue;
+    if (c >= m.columns) continue;
     float ref = -INFINITY;
-    for (int p = lane; p < m.z; p += 32) ref = fmaxf(ref, a.stat[slot(p)].x);
+    for (int p = lane; p < m.parts; p += 32) ref = fmaxf(ref, a.stat[slot(p)].x);
     ref = warp_max(ref);
     float sum = 0.f, o[E] = {};
-    for (int p0 = member; p0 < m.z; p0 += 32 * team) {  // this warp's parts p0, p0 + team, ..
+    for (int p0 = member; p0 < m.parts; p0 += 32 * team) {  // this warp's parts p0, p0 + team, ..
       float2 s = make_float2(-INFINITY, 0.f);
       const int mine = p0 + lane * team;
-      if (mine < m.z) s = a.stat[slot(mine)];
-      const float f = mine >= m.z ? 0.f : s.x == ref ? 1.f : exp2f(s.x - ref);
+      if (mine < m.parts) s = a.stat[slot(mine)];
+      const float f = mine >= m.parts ? 0.f : s.x == ref ? 1.f : exp2f(s.x - ref);
       sum += f * s.y;
-      const int count = min(32, (m.z - p0 + team - 1) / team);
+      const int count = min(32, (m.parts - p0 + team - 1) / team);
 #pragma unroll 4
       for (int i = 0; i < count; ++i) {
         const float g = __shfl_sync(0xffffffffu, f, i);
@@ -1127,7 +1135,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, in
       const __nv_bfloat162 x = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
       out[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
     }
-    __nv_bfloat16* dst = a.out + (int64_t)(q.lo + row) * a.ldo + (head * a.group + col - row * a.group) * D + lane * E;
+    const int col = m.col0 + c, row = (int)((uint32_t)col * a.group_inv >> 32);
+    __nv_bfloat16* dst = a.out + (int64_t)(m.lo + row) * a.ldo + (m.head * a.group + col - row * a.group) * D + lane * E;
     if constexpr (E == 4)
       *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
     else
@@ -1149,7 +1158,7 @@ Layout layout(int max_tree, int group, int head_dim) {
   const size_t nq = columns_of(max_tree, group);
   Layout l;
   l.meta = align_up(sizeof(WsHeader), 256);
-  l.stat = align_up(l.meta + kMaxCtas * sizeof(int4), 256);
+  l.stat = align_up(l.meta + kMaxCtas * sizeof(Shared), 256);
   l.part = align_up(l.stat + 2 * kMaxCtas * nq * sizeof(float2), 256);
   l.total = l.part + 2 * kMaxCtas * nq * head_dim * sizeof(float);
   return l;
@@ -1251,7 +1260,7 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args& a, uint8_t* 
   t.scale = a.scale;
   t.hdr = reinterpret_cast<WsHeader*>(ws);
   const Layout l = layout(a.max_tree, t.group, a.cache.head_dim);
-  t.meta = reinterpret_cast<int4*>(ws + l.meta);
+  t.meta = reinterpret_cast<Shared*>(ws + l.meta);
   t.stat = reinterpret_cast<float2*>(ws + l.stat);
   t.part = reinterpret_cast<float*>(ws + l.part);
   const bool small = a.cache.head_dim == 64;
