@@ -23,7 +23,9 @@ namespace dspark {
 namespace {
 
 constexpr int KT = 256;  // threads
-constexpr int KU = 4;    // rows and heads a group of lanes has on their way at a time
+constexpr int kSms = 152;
+constexpr int KU = 2;    // rows and heads a group of lanes has on their way at a time
+constexpr int kPasses = 4;  // such pairs a group sees at most
 
 struct CacheRows {
   KvPool pool;
@@ -31,7 +33,8 @@ struct CacheRows {
   const int32_t* mark_pos;
   const int32_t* base;
   const int32_t* n_rows;
-  int32_t N, per;  // rows, rows a CTA
+  int32_t N, per;     // rows, rows a CTA
+  uint64_t row_inv;   // u / (2 heads) is u row_inv >> 32 for a unit u of a CTA (below 2^16, or of its only row)
   int64_t ldk, ldv;
   WsHeader* hdr;
 };
@@ -55,12 +58,12 @@ struct Unit {
   int32_t row, head;  // row within the CTA
   bool v;
 };
-__device__ __forceinline__ Unit unit_at(int u, int heads) {
+__device__ __forceinline__ Unit unit_at(const CacheRows& c, int u) {
   Unit x;
-  x.row = u / (2 * heads);
-  const int rest = u - x.row * 2 * heads;
-  x.v = rest >= heads;
-  x.head = x.v ? rest - heads : rest;
+  x.row = (int)((uint32_t)u * c.row_inv >> 32);
+  const int rest = u - x.row * 2 * c.pool.heads;
+  x.v = rest >= c.pool.heads;
+  x.head = x.v ? rest - c.pool.heads : rest;
   return x;
 }
 
@@ -68,59 +71,62 @@ template <int D, typename T, bool kCodes>
 __global__ void __launch_bounds__(KT) k_cache_write(const CacheRows c, const T* k, const T* v) {
   ptx::launch_dependents();
   ptx::grid_wait();
-  constexpr int LV = D / 8, G = KT / LV;  // lanes of a unit, groups of them
+  constexpr int LV = D / 16, G = KT / LV;  // lanes of a unit, groups of them
   __shared__ int32_t place[KT];
   const int32_t n = count_rows(c), row0 = blockIdx.x * c.per;
   if (row0 >= n) return;
   const int rows = min(c.per, n - row0), units = rows * 2 * c.pool.heads;
   if (threadIdx.x < rows) place[threadIdx.x] = place_of(c, row0 + threadIdx.x);
   const int g = threadIdx.x / LV, l = threadIdx.x % LV;
+#pragma unroll 1
   for (int u0 = 0; u0 < units; u0 += G * KU) {
-    Vec8<T> x[KU];
+    Vec8<T> x[KU][2];
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
       const int u = u0 + i * G + g;
-      if (u < units) {
-        const Unit at = unit_at(u, c.pool.heads);
-        x[i].load((at.v ? v + (int64_t)(row0 + at.row) * c.ldv : k + (int64_t)(row0 + at.row) * c.ldk) + at.head * D + l * 8);
-      } else {
-        const uint32_t zero[8] = {};
-        x[i].set(zero);
-      }
+      const Unit at = unit_at(c, min(u, units - 1));
+      const T* src = (at.v ? v + (row0 + at.row) * c.ldv : k + (row0 + at.row) * c.ldk) + at.head * D + l * 8;
+      x[i][0].load(src);
+      x[i][1].load(src + D / 2);
     }
     if (u0 == 0) __syncthreads();  // the places
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
       const int u = u0 + i * G + g;
-      const Unit at = unit_at(min(u, units - 1), c.pool.heads);
+      const Unit at = unit_at(c, min(u, units - 1));
       const int32_t p = place[at.row];
       const bool live = u < units && p >= 0;
       const int64_t row = (int64_t)p + ((int64_t)at.head << c.pool.shift);
       if constexpr (kCodes) {
-        uint32_t m = amax_bits(x[i]);
+        uint32_t m = max(amax_bits(x[i][0]), amax_bits(x[i][1]));
 #pragma unroll
         for (int o = LV / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const bool finite = m < kInfBits;
         if (__any_sync(0xffffffffu, !finite)) {
-          uint32_t f = finite_amax_bits(x[i]);
+          uint32_t f = max(finite_amax_bits(x[i][0]), finite_amax_bits(x[i][1]));
 #pragma unroll
           for (int o = LV / 2; o > 0; o >>= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, o));
           if (!finite) m = f;
         }
-        const float a = fmaxf(__uint_as_float(m), kAmaxMin), inv = inv_of<T>(a);
-        const uint2 q = codes8(x[i], a, inv, inv_rest(a, inv), finite);
+        const float a = fmaxf(__uint_as_float(m), kAmaxMin), inv = inv_of<T>(a), rest = inv_rest(a, inv);
+        const uint2 q0 = codes8(x[i][0], a, inv, rest, finite), q1 = codes8(x[i][1], a, inv, rest, finite);
         if (live) {
-          *reinterpret_cast<uint2*>((at.v ? c.pool.v : c.pool.k) + row * D + l * 8) = q;
+          uint8_t* dst = (at.v ? c.pool.v : c.pool.k) + row * D + l * 8;
+          *reinterpret_cast<uint2*>(dst) = q0;
+          *reinterpret_cast<uint2*>(dst + D / 2) = q1;
           if (l == 0) (at.v ? c.pool.v_scale : c.pool.k_scale)[row] = __fdiv_rn(a, 448.f);
         }
       } else if (live) {
         __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(at.v ? c.pool.v : c.pool.k) + row * D + l * 8;
-        if constexpr (sizeof(T) == 2) {
-          *reinterpret_cast<uint4*>(dst) = x[i].a;
-        } else {
-          float f[8];
-          x[i].get(f);
-          Vec8<__nv_bfloat16>::store(dst, f, true);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(dst + h * (D / 2)) = x[i][h].a;
+          } else {
+            float f[8];
+            x[i][h].get(f);
+            Vec8<__nv_bfloat16>::store(dst + h * (D / 2), f, true);
+          }
         }
       }
     }
@@ -131,7 +137,7 @@ template <int D, typename T, bool kCodes>
 __global__ void __launch_bounds__(KT) k_cache_read(const CacheRows c, T* k, T* v) {
   ptx::launch_dependents();
   ptx::grid_wait();
-  constexpr int LV = D / 8, G = KT / LV;
+  constexpr int LV = D / 16, G = KT / LV;
   __shared__ int32_t place[KT];
   const int32_t n = count_rows(c), row0 = blockIdx.x * c.per;
   if (row0 >= n) return;
@@ -139,52 +145,58 @@ __global__ void __launch_bounds__(KT) k_cache_read(const CacheRows c, T* k, T* v
   if (threadIdx.x < rows) place[threadIdx.x] = place_of(c, row0 + threadIdx.x);
   __syncthreads();
   const int g = threadIdx.x / LV, l = threadIdx.x % LV;
+#pragma unroll 1
   for (int u0 = 0; u0 < units; u0 += G * KU) {
-    uint4 x[KU];
+    uint4 x[KU][2];
     float scale[KU];
+    T* dst[KU];
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
       const int u = u0 + i * G + g;
-      if (u >= units) continue;
-      const Unit at = unit_at(u, c.pool.heads);
+      const Unit at = unit_at(c, min(u, units - 1));
       const int32_t p = place[at.row];
-      if (p < 0) continue;
+      dst[i] = nullptr;
+      if (u >= units || p < 0) continue;
+      dst[i] = (at.v ? v + (row0 + at.row) * c.ldv : k + (row0 + at.row) * c.ldk) + at.head * D + l * 8;
       const int64_t row = (int64_t)p + ((int64_t)at.head << c.pool.shift);
       const uint8_t* pool = at.v ? c.pool.v : c.pool.k;
-      if constexpr (kCodes) {
-        const uint2 q = *reinterpret_cast<const uint2*>(pool + row * D + l * 8);
-        x[i].x = q.x, x[i].y = q.y;
-        scale[i] = (at.v ? c.pool.v_scale : c.pool.k_scale)[row];
-      } else {
-        x[i] = *reinterpret_cast<const uint4*>(pool + (row * D + l * 8) * 2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (kCodes) {
+          const uint2 q = *reinterpret_cast<const uint2*>(pool + row * D + h * (D / 2) + l * 8);
+          x[i][h].x = q.x, x[i][h].y = q.y;
+        } else {
+          x[i][h] = *reinterpret_cast<const uint4*>(pool + (row * D + h * (D / 2) + l * 8) * 2);
+        }
       }
+      if constexpr (kCodes) scale[i] = (at.v ? c.pool.v_scale : c.pool.k_scale)[row];
     }
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
-      const int u = u0 + i * G + g;
-      if (u >= units) continue;
-      const Unit at = unit_at(u, c.pool.heads);
-      if (place[at.row] < 0) continue;
-      T* dst = (at.v ? v + (int64_t)(row0 + at.row) * c.ldv : k + (int64_t)(row0 + at.row) * c.ldk) + at.head * D + l * 8;
-      float f[8];
-      if constexpr (kCodes) {
-        const uint32_t w[2] = {x[i].x, x[i].y};
+      if (!dst[i]) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3)));
-          f[2 * j] = y.x * scale[i];
-          f[2 * j + 1] = y.y * scale[i];
+      for (int h = 0; h < 2; ++h) {
+        float f[8];
+        if constexpr (kCodes) {
+          const uint32_t w[2] = {x[i][h].x, x[i][h].y};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3)));
+            f[2 * j] = y.x * scale[i];
+            f[2 * j + 1] = y.y * scale[i];
+          }
+        } else {
+          Vec8<__nv_bfloat16> y;
+          y.a = x[i][h];
+          y.get(f);
         }
-      } else {
-        Vec8<__nv_bfloat16> y;
-        y.a = x[i];
-        y.get(f);
-      }
-      if constexpr (sizeof(T) == 2) {
-        Vec8<__nv_bfloat16>::store(dst, f, true);
-      } else {  // rows begin on 16 bytes, not on 32
-        __stcs(reinterpret_cast<float4*>(dst), make_float4(f[0], f[1], f[2], f[3]));
-        __stcs(reinterpret_cast<float4*>(dst) + 1, make_float4(f[4], f[5], f[6], f[7]));
+        T* to = dst[i] + h * (D / 2);
+        if constexpr (sizeof(T) == 2) {
+          Vec8<__nv_bfloat16>::store(to, f, true);
+        } else {  // rows begin on 16 bytes, not on 32
+          __stcs(reinterpret_cast<float4*>(to), make_float4(f[0], f[1], f[2], f[3]));
+          __stcs(reinterpret_cast<float4*>(to) + 1, make_float4(f[4], f[5], f[6], f[7]));
+        }
       }
     }
   }
@@ -192,15 +204,21 @@ __global__ void __launch_bounds__(KT) k_cache_read(const CacheRows c, T* k, T* v
 
 // A CTA holds whole units (request, k or v of a head): all of a unit's rows are in
 // registers before the first is written, so a path may read what it writes.
-constexpr int MV = 4;  // 16-byte vectors a thread
+constexpr int MV = 8;  // 16-byte vectors a thread, at most
 struct MoveArgs {
   KvPool pool;
   const int32_t* base;
   const int32_t* path;
   int64_t path_ld;
   const int32_t* n_path;
-  int32_t cols, units;  // path columns, units a CTA
+  int32_t cols, units;  // path columns, units a CTA (at most KT)
+  uint64_t cols_inv;    // i / cols is i cols_inv >> 32 for i below 2^16
   WsHeader* hdr;
+};
+struct MoveUnit {
+  uint8_t* rows;  // of the unit's head
+  float* scales;
+  int32_t entry;  // of node 0 of its path
 };
 
 template <int kRowBytes>
@@ -210,19 +228,20 @@ __global__ void __launch_bounds__(KT) k_cache_move(const MoveArgs m) {
   constexpr int VR = kRowBytes / 16;  // vectors a row
   const KvPool& pool = m.pool;
   __shared__ int32_t from[KT], to[KT];  // of (request of the CTA, node of its path)
-  const int per_req = 2 * pool.heads;
+  __shared__ MoveUnit at_unit[KT];
+  const int t = threadIdx.x, per_req = 2 * pool.heads;
   const int64_t all = (int64_t)pool.n_req * per_req, u0 = (int64_t)blockIdx.x * m.units;
   const int units = (int)min((int64_t)m.units, all - u0);
   const int32_t req0 = (int32_t)(u0 / per_req);
   const int first = (int)(u0 - (int64_t)req0 * per_req);  // of the CTA's units in request req0
   const int entries = ((first + units - 1) / per_req + 1) * m.cols;
-  if (threadIdx.x < entries) {
-    const int32_t r = req0 + threadIdx.x / m.cols, i = threadIdx.x % m.cols;
+  if (t < entries) {
+    const int of = (int)((uint32_t)t * m.cols_inv >> 32), i = t - of * m.cols;
+    const int32_t r = req0 + of;
     int32_t a = -1, b = -1;
-    const int32_t n = m.n_path[r], base = m.base[r];
+    const int32_t n = m.n_path[r], base = m.base[r], node = m.path[r * m.path_ld + i];
     bool bad = n < 0 || n > m.cols || base < 0;
     if (!bad && i < n) {
-      const int32_t node = m.path[r * m.path_ld + i];
       bad = node < 0 || node >= DSPARK_MAX_TREE;
       if (!bad) {
         a = pool_row(pool, r, (int64_t)base + node);
@@ -232,57 +251,67 @@ __global__ void __launch_bounds__(KT) k_cache_move(const MoveArgs m) {
       }
     }
     if (bad && m.hdr) report_error(m.hdr, DSPARK_BAD_INPUT, r);
-    from[threadIdx.x] = a == b ? -1 : a;  // a node that stays
-    to[threadIdx.x] = b;
+    from[t] = a == b ? -1 : a;  // a node that stays
+    to[t] = b;
+  }
+  if (t < units) {
+    const int of = (first + t) / per_req, rest = first + t - of * per_req;
+    const int64_t head = (int64_t)(rest < pool.heads ? rest : rest - pool.heads) << pool.shift;
+    at_unit[t].rows = (rest < pool.heads ? pool.k : pool.v) + head * kRowBytes;
+    at_unit[t].scales = pool.k_scale ? (rest < pool.heads ? pool.k_scale : pool.v_scale) + head : nullptr;
+    at_unit[t].entry = of * m.cols;
   }
   __syncthreads();
-  const int vecs = units * m.cols * VR;
-  const auto entry = [&](int x, int* unit) {  // of vector or scale x of the CTA's rows
-    *unit = x / m.cols;
-    return (first + *unit) / per_req * m.cols + x % m.cols;
-  };
+  const int rows = units * m.cols;  // (unit, node)
   uint4 x[MV];
+  uint8_t* dst[MV];
 #pragma unroll
   for (int i = 0; i < MV; ++i) {
-    const int at = threadIdx.x + i * KT;
-    if (at >= vecs) continue;
-    int unit;
-    const int e = entry(at / VR, &unit);
-    if (from[e] < 0) continue;
-    const int rest = (first + unit) % per_req, head = rest % pool.heads;
-    x[i] = *reinterpret_cast<const uint4*>((rest < pool.heads ? pool.k : pool.v) +
-                                           ((int64_t)from[e] + ((int64_t)head << pool.shift)) * kRowBytes + at % VR * 16);
+    const int row = (t + i * KT) / VR;
+    dst[i] = nullptr;
+    if (row >= rows) continue;
+    const int of = (int)((uint32_t)row * m.cols_inv >> 32);
+    const MoveUnit& u = at_unit[of];
+    const int e = u.entry + row - of * m.cols;
+    const int32_t src = from[e];
+    if (src < 0) continue;
+    uint8_t* lane = u.rows + t % VR * 16;
+    x[i] = *reinterpret_cast<const uint4*>(lane + (int64_t)src * kRowBytes);
+    dst[i] = lane + (int64_t)to[e] * kRowBytes;
   }
-  float scale = 0.f;
-  int64_t scale_to = -1;
-  float* scales = nullptr;
-  if (pool.k_scale && threadIdx.x < units * m.cols) {
-    int unit;
-    const int e = entry(threadIdx.x, &unit);
-    if (from[e] >= 0) {
-      const int rest = (first + unit) % per_req, head = rest % pool.heads;
-      scales = rest < pool.heads ? pool.k_scale : pool.v_scale;
-      scale = scales[(int64_t)from[e] + ((int64_t)head << pool.shift)];
-      scale_to = (int64_t)to[e] + ((int64_t)head << pool.shift);
-    }
+  // the scales: one each a thread
+  constexpr int SV = MV / VR > 0 ? MV / VR : 1;
+  float scale[SV];
+  float* scale_to[SV];
+#pragma unroll
+  for (int i = 0; i < SV; ++i) {
+    const int row = t + i * KT;
+    scale_to[i] = nullptr;
+    if (!pool.k_scale || row >= rows) continue;
+    const int of = (int)((uint32_t)row * m.cols_inv >> 32);
+    const MoveUnit& u = at_unit[of];
+    const int e = u.entry + row - of * m.cols;
+    if (from[e] < 0) continue;
+    scale[i] = u.scales[from[e]];
+    scale_to[i] = u.scales + to[e];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < MV; ++i) {
-    const int at = threadIdx.x + i * KT;
-    if (at >= vecs) continue;
-    int unit;
-    const int e = entry(at / VR, &unit);
-    if (from[e] < 0) continue;
-    const int rest = (first + unit) % per_req, head = rest % pool.heads;
-    *reinterpret_cast<uint4*>((rest < pool.heads ? pool.k : pool.v) +
-                              ((int64_t)to[e] + ((int64_t)head << pool.shift)) * kRowBytes + at % VR * 16) = x[i];
-  }
-  if (scale_to >= 0) scales[scale_to] = scale;
+  for (int i = 0; i < MV; ++i)
+    if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = x[i];
+#pragma unroll
+  for (int i = 0; i < SV; ++i)
+    if (scale_to[i]) *scale_to[i] = scale[i];
 }
 
-// rows a CTA: as many as give every group of lanes KU units, one at least
-int rows_per_cta(int heads, int D) { return std::max(1, std::min(KT, KT / (D / 8) * KU / (2 * heads))); }
+// rows a CTA: as many as give every group of lanes KU units, up to kPasses times while
+// each SM has eight CTAs; one at least
+int rows_per_cta(int64_t N, int heads, int D) {
+  const int pass = KT / (D / 16) * KU;
+  const int64_t each = N * 2 * heads / ((int64_t)8 * kSms * pass);
+  const int units = pass * (int)std::max<int64_t>(1, std::min<int64_t>(kPasses, each));
+  return std::max(1, std::min(KT, units / (2 * heads)));
+}
 
 template <typename A>
 CacheRows cache_rows(const A& a, WsHeader* hdr) {
@@ -293,7 +322,8 @@ CacheRows cache_rows(const A& a, WsHeader* hdr) {
   c.base = a.base;
   c.n_rows = a.n_rows;
   c.N = a.N;
-  c.per = rows_per_cta(c.pool.heads, a.cache.head_dim);
+  c.per = rows_per_cta(a.N, c.pool.heads, a.cache.head_dim);
+  c.row_inv = c.per == 1 ? 0 : ((1ull << 32) + 2 * c.pool.heads - 1) / (2 * c.pool.heads);
   c.ldk = a.ldk;
   c.ldv = a.ldv;
   c.hdr = hdr;
@@ -348,10 +378,14 @@ cudaError_t launch_cache_move(const dspark_cache_move_args& a, WsHeader* hdr, cu
   m.cols = a.path_cols;
   m.hdr = hdr;
   const int row = a.cache.head_dim * (a.cache.dtype == DSPARK_E4M3 ? 1 : 2);
-  // units whose vectors fill the CTA's registers, and whose requests' paths its threads
-  m.units = std::max(1, KT * MV / (a.path_cols * (row / 16)));
+  m.cols_inv = ((1ull << 32) + a.path_cols - 1) / a.path_cols;
+  // units whose vectors fill the CTA's registers and whose requests' paths its threads, fewer
+  // where that would leave an SM less than four CTAs
+  const int64_t all = (int64_t)m.pool.n_req * 2 * m.pool.heads;
+  m.units = std::min(KT, std::max(1, KT * MV / (a.path_cols * (row / 16))));
+  m.units = (int)std::max<int64_t>(1, std::min<int64_t>(m.units, all / ((int64_t)4 * kSms)));
   while (m.units > 1 && ((m.units + 2 * m.pool.heads - 2) / (2 * m.pool.heads) + 1) * m.cols > KT) --m.units;
-  const int64_t grid = ((int64_t)m.pool.n_req * 2 * m.pool.heads + m.units - 1) / m.units;
+  const int64_t grid = (all + m.units - 1) / m.units;
   if (grid > INT32_MAX) return cudaErrorNotSupported;
   return counted(launch_overlapped(row == 64 ? k_cache_move<64> : row == 128 ? k_cache_move<128> : k_cache_move<256>,
                                    (unsigned)grid, KT, 0, 1, s, m));
