@@ -24,8 +24,9 @@ namespace {
 
 constexpr int KT = 256;  // threads
 constexpr int kSms = 152;
-constexpr int KU = 2;    // rows and heads a group of lanes has on their way at a time
-constexpr int kPasses = 4;  // such pairs a group sees at most
+// rows and heads a group of lanes has on their way at a time, and such passes a CTA makes at most
+constexpr int kWriteUnits = 1, kWritePasses = 4;
+constexpr int kReadUnits = 2, kReadPasses = 2;
 
 struct CacheRows {
   KvPool pool;
@@ -71,7 +72,7 @@ template <int D, typename T, bool kCodes>
 __global__ void __launch_bounds__(KT) k_cache_write(const CacheRows c, const T* k, const T* v) {
   ptx::launch_dependents();
   ptx::grid_wait();
-  constexpr int LV = D / 16, G = KT / LV;  // lanes of a unit, groups of them
+  constexpr int LV = D / 16, G = KT / LV, KU = kWriteUnits;  // lanes of a unit, groups of them
   __shared__ int32_t place[KT];
   const int32_t n = count_rows(c), row0 = blockIdx.x * c.per;
   if (row0 >= n) return;
@@ -137,7 +138,7 @@ template <int D, typename T, bool kCodes>
 __global__ void __launch_bounds__(KT) k_cache_read(const CacheRows c, T* k, T* v) {
   ptx::launch_dependents();
   ptx::grid_wait();
-  constexpr int LV = D / 16, G = KT / LV;
+  constexpr int LV = D / 16, G = KT / LV, KU = kReadUnits;
   __shared__ int32_t place[KT];
   const int32_t n = count_rows(c), row0 = blockIdx.x * c.per;
   if (row0 >= n) return;
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(KT) k_cache_read(const CacheRows c, T* k, T* v
 
 // A CTA holds whole units (request, k or v of a head): all of a unit's rows are in
 // registers before the first is written, so a path may read what it writes.
-constexpr int MV = 8;  // 16-byte vectors a thread, at most
+constexpr int MV = 4;  // 16-byte vectors a thread, at most
 struct MoveArgs {
   KvPool pool;
   const int32_t* base;
@@ -222,7 +223,7 @@ struct MoveUnit {
 };
 
 template <int kRowBytes>
-__global__ void __launch_bounds__(KT) k_cache_move(const MoveArgs m) {
+__global__ void __launch_bounds__(KT, 8) k_cache_move(const MoveArgs m) {
   ptx::launch_dependents();
   ptx::grid_wait();
   constexpr int VR = kRowBytes / 16;  // vectors a row
@@ -304,17 +305,17 @@ __global__ void __launch_bounds__(KT) k_cache_move(const MoveArgs m) {
     if (scale_to[i]) *scale_to[i] = scale[i];
 }
 
-// rows a CTA: as many as give every group of lanes KU units, up to kPasses times while
+// rows a CTA: as many as give every group of lanes KU units, up to `passes` times while
 // each SM has eight CTAs; one at least
-int rows_per_cta(int64_t N, int heads, int D) {
+int rows_per_cta(int64_t N, int heads, int D, int KU, int passes) {
   const int pass = KT / (D / 16) * KU;
   const int64_t each = N * 2 * heads / ((int64_t)8 * kSms * pass);
-  const int units = pass * (int)std::max<int64_t>(1, std::min<int64_t>(kPasses, each));
+  const int units = pass * (int)std::max<int64_t>(1, std::min<int64_t>(passes, each));
   return std::max(1, std::min(KT, units / (2 * heads)));
 }
 
 template <typename A>
-CacheRows cache_rows(const A& a, WsHeader* hdr) {
+CacheRows cache_rows(const A& a, int KU, int passes, WsHeader* hdr) {
   CacheRows c;
   c.pool = kv_pool(a.cache);
   c.mark_req = a.mark_req;
@@ -322,7 +323,7 @@ CacheRows cache_rows(const A& a, WsHeader* hdr) {
   c.base = a.base;
   c.n_rows = a.n_rows;
   c.N = a.N;
-  c.per = rows_per_cta(a.N, c.pool.heads, a.cache.head_dim);
+  c.per = rows_per_cta(a.N, c.pool.heads, a.cache.head_dim, KU, passes);
   c.row_inv = c.per == 1 ? 0 : ((1ull << 32) + 2 * c.pool.heads - 1) / (2 * c.pool.heads);
   c.ldk = a.ldk;
   c.ldv = a.ldv;
@@ -332,7 +333,7 @@ CacheRows cache_rows(const A& a, WsHeader* hdr) {
 
 template <int D, typename T>
 cudaError_t write_t(const dspark_cache_write_args& a, WsHeader* hdr, cudaStream_t s) {
-  const CacheRows c = cache_rows(a, hdr);
+  const CacheRows c = cache_rows(a, kWriteUnits, kWritePasses, hdr);
   const unsigned grid = (unsigned)((a.N + c.per - 1) / c.per);
   const T *k = static_cast<const T*>(a.k), *v = static_cast<const T*>(a.v);
   return launch_overlapped(a.cache.dtype == DSPARK_E4M3 ? k_cache_write<D, T, true> : k_cache_write<D, T, false>, grid, KT, 0,
@@ -340,7 +341,7 @@ cudaError_t write_t(const dspark_cache_write_args& a, WsHeader* hdr, cudaStream_
 }
 template <int D, typename T>
 cudaError_t read_t(const dspark_cache_read_args& a, WsHeader* hdr, cudaStream_t s) {
-  const CacheRows c = cache_rows(a, hdr);
+  const CacheRows c = cache_rows(a, kReadUnits, kReadPasses, hdr);
   const unsigned grid = (unsigned)((a.N + c.per - 1) / c.per);
   T *k = static_cast<T*>(a.k), *v = static_cast<T*>(a.v);
   return launch_overlapped(a.cache.dtype == DSPARK_E4M3 ? k_cache_read<D, T, true> : k_cache_read<D, T, false>, grid, KT, 0, 1,
