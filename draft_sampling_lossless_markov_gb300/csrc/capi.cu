@@ -426,13 +426,15 @@ static bool vector_rows_ok(const void* p, int64_t rows, int64_t cols, int64_t ld
 
 static dspark_status check_cache_rows(const dspark_kv_cache& c, int32_t N, int32_t dtype, const void* k, int64_t ldk,
                                       const void* v, int64_t ldv, const int32_t* mark_req, const int32_t* mark_pos,
-                                      const void* ws) {
+                                      const int32_t* base, const int32_t* n_rows, const void* ws) {
   if (N < 0 || !dtype_ok(dtype)) return DSPARK_INVALID_ARG;
   const dspark_status st = check_cache(c);
   if (st != DSPARK_OK || N == 0) return st;
   const int64_t cols = (int64_t)c.n_kv_heads * c.head_dim, size = (int64_t)elem_size(dtype);
   if (!vector_rows_ok(k, N, cols, ldk, size) || !vector_rows_ok(v, N, cols, ldv, size)) return DSPARK_INVALID_ARG;
   if (!mark_req || !mark_pos || (ws && ((uintptr_t)ws & 255u))) return DSPARK_INVALID_ARG;
+  for (const void* p : {(const void*)mark_req, (const void*)mark_pos, (const void*)base, (const void*)n_rows})
+    if (!aligned_to(p, 4)) return DSPARK_INVALID_ARG;
   if (N > kMaxVocabDim) return DSPARK_UNSUPPORTED;
   return DSPARK_OK;
 }
@@ -440,7 +442,8 @@ static dspark_status check_cache_rows(const dspark_kv_cache& c, int32_t N, int32
 dspark_status dspark_cache_write(const dspark_cache_write_args* a, void* workspace, void* stream) {
   if (!a) return DSPARK_INVALID_ARG;
   const dspark_status st =
-      check_cache_rows(a->cache, a->N, a->dtype, a->k, a->ldk, a->v, a->ldv, a->mark_req, a->mark_pos, workspace);
+      check_cache_rows(a->cache, a->N, a->dtype, a->k, a->ldk, a->v, a->ldv, a->mark_req, a->mark_pos, a->base, a->n_rows,
+                       workspace);
   if (st != DSPARK_OK || a->N == 0) return st;
   return launched([&] { return launch_cache_write(*a, static_cast<WsHeader*>(workspace), (cudaStream_t)stream); });
 }
@@ -448,7 +451,8 @@ dspark_status dspark_cache_write(const dspark_cache_write_args* a, void* workspa
 dspark_status dspark_cache_read(const dspark_cache_read_args* a, void* workspace, void* stream) {
   if (!a) return DSPARK_INVALID_ARG;
   const dspark_status st =
-      check_cache_rows(a->cache, a->N, a->dtype, a->k, a->ldk, a->v, a->ldv, a->mark_req, a->mark_pos, workspace);
+      check_cache_rows(a->cache, a->N, a->dtype, a->k, a->ldk, a->v, a->ldv, a->mark_req, a->mark_pos, a->base, a->n_rows,
+                       workspace);
   if (st != DSPARK_OK || a->N == 0) return st;
   return launched([&] { return launch_cache_read(*a, static_cast<WsHeader*>(workspace), (cudaStream_t)stream); });
 }
@@ -459,6 +463,7 @@ dspark_status dspark_cache_move(const dspark_cache_move_args* a, void* workspace
   const dspark_status st = check_cache(a->cache);
   if (st != DSPARK_OK || a->cache.n_req == 0) return st;
   if (!a->base || !a->path || !a->n_path || !rows_ok(a->cache.n_req, a->path_cols, a->path_ld)) return DSPARK_INVALID_ARG;
+  if (!aligned_to(a->base, 4) || !aligned_to(a->path, 4) || !aligned_to(a->n_path, 4)) return DSPARK_INVALID_ARG;
   if (workspace && ((uintptr_t)workspace & 255u)) return DSPARK_INVALID_ARG;
   return launched([&] { return launch_cache_move(*a, static_cast<WsHeader*>(workspace), (cudaStream_t)stream); });
 }
@@ -467,7 +472,8 @@ static dspark_status check_tree_sizes(int32_t n_req, int32_t max_tree, int32_t n
                                       int32_t head_dim) {
   if (n_req < 0 || max_tree < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads || head_dim < 1)
     return DSPARK_INVALID_ARG;
-  if (max_tree > DSPARK_MAX_TREE || n_q_heads > (1 << 16) || n_req > kMaxVocabDim || (head_dim != 64 && head_dim != 128))
+  if (max_tree > DSPARK_MAX_TREE || n_q_heads > (1 << 16) || n_q_heads / n_kv_heads > kMaxTreeGroup || n_req > kMaxVocabDim ||
+      (head_dim != 64 && head_dim != 128))
     return DSPARK_UNSUPPORTED;
   return DSPARK_OK;
 }
@@ -491,7 +497,8 @@ dspark_status dspark_tree_attention(const dspark_tree_attention_args* a, void* w
   const int64_t cols = (int64_t)a->n_q_heads * c.head_dim;
   if (!vector_rows_ok(a->q, a->N, cols, a->ldq, 2) || !vector_rows_ok(a->out, a->N, cols, a->ldo, 2))
     return DSPARK_INVALID_ARG;
-  if (!a->offsets || !a->base || (a->tree && !aligned_to(a->tree, 8))) return DSPARK_INVALID_ARG;
+  if (!a->offsets || !a->base || !aligned_to(a->offsets, 4) || !aligned_to(a->base, 4) || !aligned_to(a->tree, 8))
+    return DSPARK_INVALID_ARG;
   if (!ws_ok(workspace, workspace_bytes, tree_attention_ws(c.n_req, a->max_tree, a->n_q_heads, c.n_kv_heads, c.head_dim)))
     return DSPARK_INVALID_ARG;
   if (a->N > kMaxVocabDim) return DSPARK_UNSUPPORTED;

@@ -62,6 +62,7 @@ struct Shared {
   int32_t lo, head, col0, columns, parts;
 };
 
+static_assert((64ll * kMaxTreeGroup + 64) * kMaxTreeGroup < 1ll << 32, "columns divided by a multiplication");
 struct TreeArgs {
   KvPool pool;
   const __nv_bfloat16* q;
@@ -71,7 +72,9 @@ struct TreeArgs {
   const uint64_t* tree;
   int64_t ldq, ldo;
   int32_t N, q_heads, group, max_tree;
-  uint64_t group_inv;  // ceil(2^32 / group): c / group is c group_inv >> 32 for c below 2^16
+  // ceil(2^32 / group): c / group is c group_inv >> 32 for the columns c < 64 group + 64, as c group
+  // is below 2^32 (kMaxTreeGroup)
+  uint64_t group_inv;
   float scale;
   WsHeader* hdr;
   Shared* meta;   // [CTAs] the item that begins in a CTA and goes on

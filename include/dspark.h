@@ -763,9 +763,10 @@ DSPARK_API dspark_status dspark_cache_move(const dspark_cache_move_args* args, v
  * offsets or base out of range (0 <= offsets[r] <= offsets[r + 1] <= N, at most
  * max_tree rows, 0 <= base, base + rows <= max_pages * page_size) is skipped; the
  * tokens of a page outside [0, n_pages) are not seen by any row; both are reported
- * (DSPARK_BAD_INPUT, detail = request).  n_q_heads is a multiple of n_kv_heads;
- * max_tree is 1..DSPARK_MAX_TREE; scale finite.  q, out 16-byte aligned, ldq and ldo
- * multiples of 8; out must not overlap q or the cache.  Equal calls give equal bits.
+ * (DSPARK_BAD_INPUT, detail = request).  n_q_heads is a multiple of n_kv_heads, at
+ * most 65536 and 4096 times it; max_tree is 1..DSPARK_MAX_TREE; scale finite.  q, out
+ * 16-byte aligned, ldq and ldo multiples of 8; out must not overlap q or the cache.
+ * Equal calls give equal bits.
  * A workspace of dspark_tree_attention_workspace_size bytes, initialised by
  * dspark_workspace_init and kept to one stream at a time, is needed.  Needs sm_103,
  * else DSPARK_UNSUPPORTED. */

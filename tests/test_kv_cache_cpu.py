@@ -102,6 +102,28 @@ def test_attention_checks(lib):
     assert call(_but(a, cache=_but(a.cache, n_req=0, table=None)), 0, 0) == OK
 
 
+def test_addresses_and_sizes_beyond_the_kernels(lib):
+    """Integers that do not begin on 4 bytes, and more query heads a kv head than columns can be told apart for."""
+    for name in ("write", "read"):
+        a = _rows(getattr(capi, f"dspark_cache_{name}_args"))
+        for kw in (dict(mark_req=0x80002), dict(mark_pos=0x90001), dict(base=0xA0002), dict(n_rows=0xB0003)):
+            assert getattr(capi, f"dspark_cache_{name}")(_but(a, **kw), 0, 0) == BAD, kw
+    a = _set(capi.dspark_cache_move_args(), cache=_cache(), path_cols=4, base=0x60000, path=0x70000, path_ld=4, n_path=0x80000)
+    for kw in (dict(base=0x60002), dict(path=0x70001), dict(n_path=0x80002)):
+        assert capi.dspark_cache_move(_but(a, **kw), 0, 0) == BAD, kw
+    n = capi.dspark_tree_attention_workspace_size(3, 8, 8, 2, 64)[1]
+    a = _set(capi.dspark_tree_attention_args(), cache=_cache(), N=20, n_q_heads=8, max_tree=8, scale=0.1, q=0x60000, ldq=512,
+             out=0x70000, ldo=512, offsets=0x80000, base=0x90000)
+    for kw in (dict(offsets=0x80002), dict(base=0x90001)):
+        assert capi.dspark_tree_attention(_but(a, **kw), 0x100000, n, 0) == BAD, kw
+    size = capi.dspark_tree_attention_workspace_size
+    assert size(3, 64, 4096, 1, 64)[0] == OK and size(3, 64, 1 << 16, 16, 64)[0] == OK
+    assert size(3, 1, 4097, 1, 64)[0] == NO and size(3, 1, (1 << 16) + 16, 16, 64)[0] == NO
+    for group in (1, 3, 7, 100, 4095, 4096):  # a column over the group, as the kernel forms it
+        inv, c = ((1 << 32) + group - 1) // group, np.arange(64 * group + 64, dtype=np.uint64)
+        np.testing.assert_array_equal(c * np.uint64(inv) >> np.uint64(32), c // np.uint64(group))
+
+
 def test_packed_structs_are_the_c_structs():
     for name in ("cache_write", "cache_read", "cache_move", "tree_attention"):
         kind = getattr(capi, f"dspark_{name}_args")
