@@ -48,24 +48,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// The same with a count of polls as the limit, each of which the hardware may hold for about a microsecond:
-// two million are between a tenth of a second and two.  No clock and no call: few instructions and registers.
-__device__ __forceinline__ bool mbar_wait_polls(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint32_t at = smem_u32(bar);
-  for (uint32_t i = 1;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 255u) == 0 && (i >> 21 || *abort)) return false;
-  }
-}
-// whether the phase of `parity` is complete, without waiting
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -76,6 +58,29 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
+}
+// Waits for a CTA whose work is a long row of steps: state[0] is the flag by which one thread that gives up
+// ends the waits of all, state[1] the SM's cycle counter at the last step (mbar_progress, by the thread that
+// sets the pace).  A wait ends without its phase when the flag is up, or 2^30 cycles (half a second)
+// after the last step.  The hardware holds a poll for as long as it likes (half a millisecond and
+// more), so the time is looked at every eighth; one poll that does not wait comes first, so that waits
+// end at once when the flag is up.  No cycle count of its own to keep: few registers.
+__device__ __forceinline__ uint32_t cycles_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ void mbar_progress(volatile int* state) { state[1] = (int)cycles_lo(); }
+__device__ __forceinline__ bool mbar_wait_paced(uint64_t* bar, uint32_t parity, volatile int* state) {
+  if (mbar_test(bar, parity)) return true;
+  for (uint32_t i = 1;; ++i) {
+    if (state[0]) return false;
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 7u) == 0u) {
+      const uint32_t step = (uint32_t)state[1];  // read before the counter, or it might be the later one
+      if (cycles_lo() - step > 1u << 30) return false;
+    }
+  }
 }
 // Wait for the phase of `parity` to complete; gives up (returns false) after
 // `limit_ns` of wall time or when another thread of the CTA has raised `abort`.

@@ -47,8 +47,6 @@ namespace {
 
 constexpr int kTile = 128;           // tokens
 constexpr int kMaxCtas = 320;        // parts the workspace holds: two a CTA
-template <int NQ>
-constexpr int kItemCost = NQ == 64 ? 4 : 3;  // what an item costs beside its tiles, in tiles
 // A column's largest exponent when its reference is set, and the exponent that raises it: 2^15 is in
 // fp16's range, bf16 weights have room up to 2^60.
 template <bool kCodes>
@@ -84,6 +82,10 @@ struct TreeArgs {
 
 template <bool kCodes, int D, int NQ>
 struct Form {
+  static constexpr int kColumns = NQ;
+  // What an item costs beside its tiles, in tiles (3 to 12 tried: 16 requests x 64 nodes 252, 215, 202, 202, 204 us
+  // with 3 to 7, 64 x 16 rows bf16 144, 121, 110, 108 us with 3, 6, 8, 10, 256 x 8 rows 382, 374, 378 us with 3, 4, 7)
+  static constexpr int kItemCost = NQ < 64 ? 4 : kCodes ? 5 : 8;
   static constexpr int kElem = kCodes ? 1 : 2;
   static constexpr int kRow = D * kElem < 128 ? D * kElem : 128;  // bytes of an operand row
   static constexpr int kParts = D * kElem / kRow;                 // of a token's row
@@ -98,15 +100,20 @@ struct Form {
   static constexpr uint32_t kPCol = kTile * 128;
   static constexpr uint32_t kP = kPCol + (kPRest > 0 ? kTile * 64 : 0);
   static constexpr uint32_t kScales = kCodes ? 2 * kTile * 4 : 0;
-  static constexpr uint32_t kStage = 2 * kOperand + kScales;
   static constexpr int kO = NQ * kPPieces;                         // columns of O: the pieces side by side
   // One pair of warpgroups a CTA and two CTAs an SM where they fit (what one waits for at an item's end
   // the other fills), else two pairs a CTA.  q of this part of an item and of the next.
-  static constexpr bool kSmall = NQ <= 32 && kP + 2 * kQ + 2 * kStage <= 104 * 1024 && NQ + kO <= 256;
+  static constexpr bool kSmall = NQ <= 32 && kP + 2 * kQ + 4 * kOperand + 2 * kScales <= 104 * 1024 && NQ + kO <= 256;
   static constexpr int kPairs = kSmall ? 1 : 2;
-  static constexpr uint32_t kFixed = kPairs * kP + 2 * kQ;
-  static constexpr int kStages = (int)std::min<uint32_t>(6, ((kSmall ? 106 : 212) * 1024 - kFixed) / kStage);
-  static constexpr uint32_t kSmem = kFixed + kStages * kStage + 1024;
+  // Tiles of k and of v have rings of their own: one of k is free again as soon as S is formed (with one
+  // ring a tile's loads waited for O two tiles before).  What the softmax reads, scales and the pages that
+  // are there, has a ring of kNotes: when k of tile n is loaded, S of tile n - kStagesK has been formed, so
+  // S of every tile up to n - kStagesK - 3 has been read.
+  static constexpr int kNotes = 8;
+  static constexpr uint32_t kFixed = kPairs * kP + 2 * kQ + kNotes * kScales;
+  static constexpr int kSlots = (int)std::min<uint32_t>(10, ((kSmall ? 106 : 212) * 1024 - kFixed) / kOperand);
+  static constexpr int kStagesK = kSlots / 2, kStagesV = kSlots - kStagesK;
+  static constexpr uint32_t kSmem = kFixed + kSlots * kOperand + 1024;
   static constexpr int kCols = kPairs * (NQ + kO);                 // S and O of the pairs
   static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr int kSoftWarps = 8 * kPairs, kSoft = 32 * kSoftWarps;
@@ -115,7 +122,7 @@ struct Form {
   // registers of the softmax's threads and of the others, of the 80 or 96 a thread at launch
   static constexpr int kRegs = kSmall ? 80 : 96, kRegsHigh = kSmall ? 96 : 104, kRegsLow = kSmall ? 48 : 64;
   static_assert(kSoft * kRegsHigh + 128 * kRegsLow <= kThreads * kRegs, "registers");
-  static_assert(kStages >= 2 && kCols <= 512 && kCtas * kTmemCols <= 512, "shared memory and TMEM");
+  static_assert(kStagesK >= 2 && kStagesK + 3 <= kNotes && kCols <= 512 && kCtas * kTmemCols <= 512, "shared memory and TMEM");
 };
 
 template <int kRow>
@@ -133,7 +140,7 @@ struct Request {
   int32_t lo, rows, base, tiles, chunks;
   int64_t units;
 };
-template <int NQ>
+template <typename F>
 __device__ __forceinline__ Request request_at(const TreeArgs& a, int r, bool* bad) {
   Request q;
   const int32_t lo = a.offsets[r], hi = a.offsets[r + 1];
@@ -144,8 +151,8 @@ __device__ __forceinline__ Request request_at(const TreeArgs& a, int r, bool* ba
   q.lo = lo;
   q.rows = *bad ? 0 : hi - lo;
   q.tiles = q.rows ? (int32_t)((held + kTile - 1) / kTile) : 0;
-  q.chunks = (q.rows * a.group + NQ - 1) / NQ;
-  q.units = q.tiles ? (int64_t)(q.tiles + kItemCost<NQ>) * q.chunks * a.pool.heads : 0;
+  q.chunks = (q.rows * a.group + F::kColumns - 1) / F::kColumns;
+  q.units = q.tiles ? (int64_t)(q.tiles + F::kItemCost) * q.chunks * a.pool.heads : 0;
   return q;
 }
 
@@ -159,7 +166,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int b) {
   return (a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 // The parts of items in a CTA's share of the units, one after the other; the warps that need them walk by themselves.
-template <int NQ>
+template <typename F>
 struct Walk {
   int r, head, chunk, x;  // the next unit: x of that item
   int64_t left;           // units
@@ -171,10 +178,10 @@ struct Walk {
     left = n;
     if (n > 0) r = at.r, head = at.head, chunk = at.chunk, x = at.x, q = at.q;
   }
-  __device__ __forceinline__ bool next(const TreeArgs& a) {
+  __device__ __forceinline__ bool next(const TreeArgs& a, volatile int* state) {
 #pragma unroll 1
     while (left > 0) {
-      if (x == q.tiles + kItemCost<NQ>) {
+      if (x == q.tiles + F::kItemCost) {
         x = 0;
         if (++chunk == q.chunks) {
           chunk = 0;
@@ -182,15 +189,16 @@ struct Walk {
             head = 0;
             do {
               if (++r >= a.pool.n_req) return false;
+              ptx::mbar_progress(state);  // there may be any number of empty ones
               bool bad;
-              q = request_at<NQ>(a, r, &bad);
+              q = request_at<F>(a, r, &bad);
             } while (q.units == 0);
           }
         }
       }
-      const int y = (int)min((int64_t)(q.tiles + kItemCost<NQ>), x + left);
-      tile = max(0, x - kItemCost<NQ>);
-      tiles = max(0, y - kItemCost<NQ>) - tile;
+      const int y = (int)min((int64_t)(q.tiles + F::kItemCost), x + left);
+      tile = max(0, x - F::kItemCost);
+      tiles = max(0, y - F::kItemCost) - tile;
       left -= y - x;
       x = y;
       if (tiles == 0) continue;  // nothing but the item's own cost: it begins in the next CTA
@@ -382,12 +390,13 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   uint8_t* sm = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sP = sm;                  // [pairs] P
   uint8_t* sQ = sm + kPairs * F::kP;  // [2][pieces][parts]
-  uint8_t* sStage = sm + F::kFixed;  // [stages] k, v; then their scales
-  float* sScale = reinterpret_cast<float*>(sStage + F::kStages * 2 * F::kOperand);
-  __shared__ uint64_t kfull[F::kStages], vfull[F::kStages], empty[F::kStages], sfull[kPairs], sfree[kPairs], pready[kPairs], pdone[kPairs], qfull[2],
-      planned[kPlans], ended[kPlans];
-  __shared__ uint32_t tmem_slot, okmask[F::kStages];
-  __shared__ int abort_s, never_s;
+  uint8_t* sK = sm + F::kFixed;  // [stages] tiles
+  uint8_t* sV = sK + F::kStagesK * F::kOperand;
+  float* sScale = reinterpret_cast<float*>(sQ + 2 * F::kQ);  // [notes] of k, of v
+  __shared__ uint64_t kfull[F::kStagesK], kempty[F::kStagesK], noted[F::kNotes], vfull[F::kStagesV], vempty[F::kStagesV], sfull[kPairs], sfree[kPairs],
+      pready[kPairs], pdone[kPairs], qfull[2], planned[kPlans], ended[kPlans];
+  __shared__ uint32_t tmem_slot, okmask[F::kNotes];
+  __shared__ int abort_s[2], never_s[2];  // mbar_wait_paced
   __shared__ Start start;
   __shared__ int64_t sums[kThreads / 32 + 1];
   // the parts planned and the columns that see each drafted row; of this part and the next the drafted rows
@@ -400,14 +409,18 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   __shared__ __align__(16) float nref[kPairs][NQ], delta[kPairs][NQ], factor[kPairs][NQ];
   __shared__ float warp_top[kSoftWarps][NQ / 2], coef[kPairs][NQ];
   __shared__ bool set[kPairs][NQ];
-  volatile int* abort_flag = &abort_s;
+  volatile int* abort_flag = abort_s;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < F::kStages; ++i) {
-      ptx::mbar_init(&kfull[i], kCodes ? 33 : 1);  // and every lane's copies of scales
+    for (int i = 0; i < F::kStagesK; ++i) {
+      ptx::mbar_init(&kfull[i], 1);
+      ptx::mbar_init(&kempty[i], 1);
+    }
+    for (int i = 0; i < F::kNotes; ++i) ptx::mbar_init(&noted[i], kCodes ? 33 : 1);  // and every lane's copies of scales
+    for (int i = 0; i < F::kStagesV; ++i) {
       ptx::mbar_init(&vfull[i], 1);
-      ptx::mbar_init(&empty[i], 1);
+      ptx::mbar_init(&vempty[i], 1);
     }
     for (int i = 0; i < kPairs; ++i) {
       ptx::mbar_init(&sfull[i], 1);
@@ -424,7 +437,8 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       ptx::mbar_init(&ended[i], kSoftWarps);
     }
     ptx::fence_mbar_init();
-    abort_s = never_s = 0;
+    abort_s[0] = never_s[0] = 0;
+    ptx::mbar_progress(abort_s);
     ptx::prefetch_map(&tmK);
     ptx::prefetch_map(&tmV);
   }
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
 #pragma unroll 1
   for (int r = from; r < to; ++r) {
     bool bad;
-    q = request_at<NQ>(a, r, &bad);
+    q = request_at<F>(a, r, &bad);
     mine += q.units;
     if (bad && blockIdx.x == 0 && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, r);
   }
@@ -476,83 +490,116 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
 #pragma unroll 1
     for (; r < to - 1; ++r) {
       bool bad;
-      const Request p = request_at<NQ>(a, r, &bad);
+      const Request p = request_at<F>(a, r, &bad);
       if (at < p.units) {
         q = p;
         break;
       }
       at -= p.units;
     }
-    const int cost = q.tiles + kItemCost<NQ>;
+    const int cost = q.tiles + F::kItemCost;
     const int64_t item = quotient(at, cost);
     start = Start{r, (int)((uint32_t)item / (uint32_t)q.chunks), (int)((uint32_t)item % (uint32_t)q.chunks), (int)(at - item * cost), q};
   }
-  if (threadIdx.x == 0) a.meta[cta].parts = 0;
+  if (threadIdx.x == 0) {
+    a.meta[cta].parts = 0;
+    ptx::mbar_progress(abort_flag);
+  }
   __syncthreads();
-  Walk<NQ> walk;
+  Walk<F> walk;
   walk.start(start, u1 - u0);
   if (warp >= kSoftWarps) {
   ptx::reg_dec<F::kRegsLow>();
   if (warp == kSoftWarps) {
-    // ---- loads: a lane a page of k or v, four tokens' scales a lane; the page numbers a tile ahead ----
+    // ---- loads: a lane a page of k or v, four tokens' scales a lane; the page numbers a tile ahead, v a
+    // tile behind k but at a part's end ----
     const uint64_t policy = a.group * a.max_tree > NQ ? ptx::policy_evict_normal() : ptx::policy_evict_first();
     const int box_shift = min(a.pool.shift, 7), box = 1 << box_shift, boxes = kTile >> box_shift;
-    const int i = lane & 7, what = (lane >> 3) & 1;
-    uint32_t s = 0, ph = 1, n = 0;
+    const int i = lane & 7;
+    uint32_t n = 0, nv = 0;  // tiles of k, of v
+    uint32_t sk = 0, phk = 1, sv = 0, phv = 1;
+    int32_t row = -1;        // of the lane's page (lanes 0-7: k, 8-15: v), of the last tile of k
+    uint32_t bytes = 0;
     bool ok = true;
-    while (ok && walk.next(a)) {
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait_paced(bar, parity, abort_flag));
+      if (!ok && lane == 0) fail(1);
+      return ok;
+    };
+    const auto load = [&](uint8_t* tile, const CUtensorMap* map, uint64_t* full) {
+#pragma unroll
+      for (int p = 0; p < F::kParts; ++p)
+        ptx::tma_load_2d(tile + p * F::kPart + i * box * F::kRow, map, full, p * (F::kRow / F::kElem), row, policy);
+    };
+    const auto load_v = [&] {
+      if (!wait(&vempty[sv], phv)) return;
+      if (lane == 0) ptx::mbar_expect_tx(&vfull[sv], bytes);
+      __syncwarp();
+      if (row >= 0 && lane >= 8 && lane < 16) load(sV + sv * F::kOperand, &tmV, &vfull[sv]);
+      __syncwarp();
+      ++nv;
+      if (++sv == (uint32_t)F::kStagesV) sv = 0, phv ^= 1;
+    };
+    while (ok && walk.next(a, abort_flag)) {
       const int len = walk.q.base + walk.q.rows;
       const int32_t* table = a.pool.table + walk.r * a.pool.table_ld;
       int pos = walk.tile * kTile + (i << box_shift);
       // (positions below len have an entry: request_at)
       int32_t page = i < boxes && pos < len ? table[pos >> a.pool.shift] : -1;
+#pragma unroll 1
       for (int t = 0; t < walk.tiles; ++t) {
         const int32_t here = page, at = pos;
         pos += kTile;
         page = i < boxes && pos < len && t + 1 < walk.tiles ? table[pos >> a.pool.shift] : -1;
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait_polls(&empty[s], ph, abort_flag));
-        if (!ok) {
-          if (lane == 0) fail(1);
-          break;
-        }
+        if (!wait(&kempty[sk], phk)) break;
         const bool wanted = i < boxes && at < len;
         const bool live = wanted && here >= 0 && here < a.pool.n_pages;
         if (wanted && !live && a.hdr) report_error(a.hdr, DSPARK_BAD_INPUT, walk.r);
-        const int32_t row = live ? ((here * a.pool.heads + walk.head) << a.pool.shift) + (at & ((1 << a.pool.shift) - 1)) : -1;
-        const uint32_t mask = __ballot_sync(0xffffffffu, live) & 0xFFu, bytes = __popc(mask) * (box * D * F::kElem);
+        const int32_t row_v = row;
+        const uint32_t bytes_v = bytes;
+        row = live ? ((here * a.pool.heads + walk.head) << a.pool.shift) + (at & ((1 << a.pool.shift) - 1)) : -1;
+        const uint32_t mask = __ballot_sync(0xffffffffu, live) & 0xFFu;
+        bytes = __popc(mask) * (box * D * F::kElem);
         if (lane == 0) {
-          okmask[s] = mask;
-          ptx::mbar_expect_tx(&kfull[s], bytes);
-          ptx::mbar_expect_tx(&vfull[s], bytes);
+          ptx::mbar_progress(abort_flag);
+          ptx::mbar_expect_tx(&kfull[sk], bytes);
+          okmask[n % F::kNotes] = mask;
+          ptx::mbar_arrive(&noted[n % F::kNotes]);
         }
         __syncwarp();
-        uint8_t* stage = sStage + s * 2 * F::kOperand;
-        if (live && lane < 16) {
-#pragma unroll
-          for (int p = 0; p < F::kParts; ++p)
-            ptx::tma_load_2d(stage + what * F::kOperand + p * F::kPart + i * box * F::kRow, what ? &tmV : &tmK,
-                             what ? &vfull[s] : &kfull[s], p * (F::kRow / F::kElem), row, policy);
-        }
+        if (live && lane < 8) load(sK + sk * F::kOperand, &tmK, &kfull[sk]);
         if constexpr (kCodes) {
           const int32_t from = __shfl_sync(0xffffffffu, row, (4 * lane) >> box_shift);
           if (from >= 0) {
             const int32_t first = from + ((4 * lane) & (box - 1));
-            float* dst = sScale + s * 2 * kTile + 4 * lane;
+            float* dst = sScale + n % F::kNotes * 2 * kTile + 4 * lane;
             ptx::cp_async16_cg(dst, a.pool.k_scale + first);
             ptx::cp_async16_cg(dst + kTile, a.pool.v_scale + first);
           }
-          ptx::cp_async_arrive(&kfull[s]);
+          ptx::cp_async_arrive(&noted[n % F::kNotes]);
         }
         __syncwarp();
         ++n;
-        if (++s == (uint32_t)F::kStages) s = 0, ph ^= 1;
+        if (++sk == (uint32_t)F::kStagesK) sk = 0, phk ^= 1;
+        if (t > 0) {  // v of the tile before
+          const int32_t row_k = row;
+          const uint32_t bytes_k = bytes;
+          row = row_v, bytes = bytes_v;
+          load_v();
+          row = row_k, bytes = bytes_k;
+        }
+        if (t + 1 == walk.tiles) load_v();
+        if (!ok) break;
       }
     }
     // nothing may be in flight when the CTA leaves
-    for (uint32_t j = n > (uint32_t)F::kStages ? n - F::kStages : 0; j < n; ++j) {
-      ptx::mbar_wait_polls(&kfull[j % F::kStages], (j / F::kStages) & 1, &never_s);
-      ptx::mbar_wait_polls(&vfull[j % F::kStages], (j / F::kStages) & 1, &never_s);
-    }
+    ptx::mbar_progress(never_s);
+    for (uint32_t j = n > (uint32_t)F::kNotes ? n - F::kNotes : 0; kCodes && j < n; ++j)
+      ptx::mbar_wait_paced(&noted[j % F::kNotes], (j / F::kNotes) & 1, never_s);
+    for (uint32_t j = n > (uint32_t)F::kStagesK ? n - F::kStagesK : 0; j < n; ++j)
+      ptx::mbar_wait_paced(&kfull[j % F::kStagesK], (j / F::kStagesK) & 1, never_s);
+    for (uint32_t j = nv > (uint32_t)F::kStagesV ? nv - F::kStagesV : 0; j < nv; ++j)
+      ptx::mbar_wait_paced(&vfull[j % F::kStagesV], (j / F::kStagesV) & 1, never_s);
     __syncwarp();
   } else if (warp < kSoftWarps + 3) {
     // ---- MMAs: one warp for S, up to two tiles ahead, and one for O (one warp's waits and issues for
@@ -563,14 +610,15 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     // of D = 64 the tile's 64 columns serve as both halves of the 128 rows
     constexpr uint32_t kLboV = F::kParts > 1 ? F::kPart : 0;
     // descriptors of the first stage and buffer; all others are so many 16-byte units further
-    const uint64_t dk0 = operand_desc<F::kRow>(ptx::smem_u32(sStage), 16);
-    const uint64_t dv0 = operand_desc<F::kRow>(ptx::smem_u32(sStage) + F::kOperand, kLboV);
+    const uint64_t dk0 = operand_desc<F::kRow>(ptx::smem_u32(sK), 16);
+    const uint64_t dv0 = operand_desc<F::kRow>(ptx::smem_u32(sV), kLboV);
     const uint64_t dq0 = operand_desc<F::kRow>(ptx::smem_u32(sQ), 16);
     const uint64_t dp0 = ptx::smem_desc_sw128(ptx::smem_u32(sP), 16, 1024);
     const uint64_t dr0 = ptx::smem_desc_sw64(ptx::smem_u32(sP) + F::kPCol, 16, 512);
     const bool is_s = warp == kSoftWarps + 1;
+    const uint32_t stages = is_s ? F::kStagesK : F::kStagesV;
     auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
-      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_polls(bar, parity, abort_flag));
+      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_paced(bar, parity, abort_flag));
       if (!got && lane == 0) fail(what);
       return got;
     };
@@ -589,7 +637,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           if (!ok) break;
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
-            const uint64_t dk = dk0 + s * (2 * F::kOperand >> 4), dq = dq0 + qb * (F::kQ >> 4);
+            const uint64_t dk = dk0 + s * (F::kOperand >> 4), dq = dq0 + qb * (F::kQ >> 4);
             const uint32_t d = tmem + w * NQ;
 #pragma unroll
             for (int p = 0; p < F::kQPieces; ++p)
@@ -605,13 +653,14 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
                   ptx::tc_mma_fp8<1>(d, da, db, idesc_s);
               }
             ptx::tc_commit(&sfull[w]);
+            ptx::tc_commit(&kempty[s]);
           }
         } else {
           ok = wait(&pready[w], (turns >> w) & 1, 5) && wait(&vfull[s], ph, 6);
           if (!ok) break;
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
-            const uint64_t dv = dv0 + s * (2 * F::kOperand >> 4), dp = dp0 + w * (F::kP >> 4);
+            const uint64_t dv = dv0 + s * (F::kOperand >> 4), dp = dp0 + w * (F::kP >> 4);
             const uint32_t d = tmem + kPairs * NQ + w * F::kO, more = t >= kPairs;
 #pragma unroll
             for (int k = 0; k < kStepsO; ++k) {
@@ -630,13 +679,13 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
                 ptx::tc_mma_fp8_if(d + F::kPWide, dv + (k * kStepTokens * F::kRow >> 4), dr + (k * kStepTokens * 64 >> 4),
                                    ptx::idesc_e4m3_e5m2_mn_f32(128, F::kPRest), k > 0 ? 1 : more);
             }
-            ptx::tc_commit(&empty[s]);
+            ptx::tc_commit(&vempty[s]);
             ptx::tc_commit(&pdone[w]);
           }
         }
         __syncwarp();
         turns ^= 1u << w;
-        if (++s == (uint32_t)F::kStages) s = 0, ph ^= 1;
+        if (++s == stages) s = 0, ph ^= 1;
       }
     }
     __syncwarp();
@@ -644,8 +693,8 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     // ---- the parts, ahead of the softmax ----
     for (uint32_t part = 0;; ++part) {
       const int b = part % kPlans;
-      const bool more = walk.next(a);
-      if (!__all_sync(0xffffffffu, ptx::mbar_wait_polls(&ended[b], ~(part / kPlans) & 1, abort_flag))) {
+      const bool more = walk.next(a, abort_flag);
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait_paced(&ended[b], ~(part / kPlans) & 1, abort_flag))) {
         if (lane == 0) fail(7);
         break;
       }
@@ -707,7 +756,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     const uint32_t all_ok = (1u << (kTile >> box_shift)) - 1;
     uint32_t n0 = opaque(0), turn = opaque(0);  // the CTA's tiles before this part, this warpgroup's so far
     auto wait = [&](uint64_t* bar, uint32_t parity, int what) {
-      if (!ptx::mbar_wait_polls(bar, parity, abort_flag)) fail(what);  // the loops run on: every later wait ends at once
+      if (!ptx::mbar_wait_paced(bar, parity, abort_flag)) fail(what);  // the loops run on: every later wait ends at once
     };
     // q of part `part`: four columns a warp, loaded before it is needed
     QColumn<D> q;
@@ -715,7 +764,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     static_assert(NQ <= 4 * kSoftWarps, "four columns a warp");
     const auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };  // of a value that the warp shares
     const auto load_q = [&](int part) {
-      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_polls(&planned[part % kPlans], (part / kPlans) & 1, abort_flag));
+      const bool got = __all_sync(0xffffffffu, ptx::mbar_wait_paced(&planned[part % kPlans], (part / kPlans) & 1, abort_flag));
       if (!got) fail(8);
       if (got && same(parts[part % kPlans].tiles) > 0 && warp * 4 < NQ) q.load(a, parts[part % kPlans], qc);
     };
@@ -745,9 +794,10 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       float* my_delta = &delta[w][h * HQ];
       float* my_factor = &factor[w][h * HQ];
       if (token < HQ) my_nref[token] = 0.f, set[w][h * HQ + token] = false;
-      const bool got = ptx::mbar_wait_polls(&qfull[b], (part >> 1) & 1, abort_flag);
+      const bool got = ptx::mbar_wait_paced(&qfull[b], (part >> 1) & 1, abort_flag);
       if (!got) fail(10);
-      if (same(ptx::named_any(kAll, kSoft, !got))) break;
+      // after a fault all leave together (q is counted as ready, and the plans are no more than they were)
+      if (same(ptx::named_any(kAll, kSoft, !got || *abort_flag != 0))) break;
       const int tiles = same(now.tiles), tile0 = same(now.tile);
       if (tiles == 0) break;
       const int base = same(now.base), len = base + same(now.rows);
@@ -756,23 +806,23 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
 #pragma unroll
       for (int i = 0; i < HQ / 2; ++i) l2[i] = 0;
       bool unset = opaque(1) != 0;  // a column has no reference yet
-      uint32_t s = (n0 + w) % F::kStages, ph = ((n0 + w) / F::kStages) & 1;
 #pragma unroll 1
       for (int t = opaque(w); t < tiles; t += kPairs) {
-        wait(&kfull[s], ph, 11);
+        const uint32_t n = n0 + t, note = n % F::kNotes;
+        wait(&noted[note], (n / F::kNotes) & 1, 11);  // (not k itself: S may have let it go)
         const int pos0 = (tile0 + t) * kTile, pos = pos0 + token;
-        const uint32_t have = okmask[s];
+        const uint32_t have = okmask[note];
         const bool masked = pos0 + kTile > base || have != all_ok;
         const bool held = pos < len && ((have >> (token >> box_shift)) & 1);  // looked at where masked
         float k_scale = 1.f, v_scale = 1.f;
         if (kCodes) {
-          k_scale = sScale[s * 2 * kTile + token];
-          v_scale = sScale[s * 2 * kTile + kTile + token];
+          k_scale = sScale[note * 2 * kTile + token];
+          v_scale = sScale[note * 2 * kTile + kTile + token];
         }
         if (masked && h == 0) {
           // what no row or only some see must not reach the others through 0 * NaN
-          wait(&vfull[s], ph, 12);
-          uint8_t* row = sStage + s * 2 * F::kOperand + F::kOperand + token * F::kRow;
+          wait(&vfull[n % F::kStagesV], (n / F::kStagesV) & 1, 12);
+          uint8_t* row = sV + n % F::kStagesV * F::kOperand + token * F::kRow;
           if (!held || pos >= base) {
             uint32_t any = 0;
 #pragma unroll 1
@@ -953,8 +1003,6 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&pready[w]);
-        s += kPairs;
-        if (s >= (uint32_t)F::kStages) s -= F::kStages, ph ^= 1;
       }
 
       // ---- the part's end: sums of both tile sequences, O joined and written ----
@@ -1044,7 +1092,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && abort_s && a.hdr) report_error(a.hdr, DSPARK_TIMEOUT, abort_s);
+  if (threadIdx.x == 0 && abort_s[0] && a.hdr) report_error(a.hdr, DSPARK_TIMEOUT, abort_s[0]);
   if (warp == kSoftWarps + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, F::kTmemCols);
