@@ -55,9 +55,10 @@ template <bool kCodes>
 constexpr float kRaise = kCodes ? 15.f : 60.f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// An item that several CTAs share: where its rows and columns are, and its parts (0: there is none).
+// An item that begins in a CTA and goes on in others: where its rows and columns are, and its parts (0: there is
+// none).  first: the CTA that the item of this CTA's first part begins in, -1 if that is this one.
 struct Shared {
-  int32_t lo, head, col0, columns, parts;
+  int32_t lo, head, col0, columns, parts, first;
 };
 
 static_assert((64ll * kMaxTreeGroup + 64) * kMaxTreeGroup < 1ll << 32, "columns divided by a multiplication");
@@ -75,7 +76,7 @@ struct TreeArgs {
   uint64_t group_inv;
   float scale;
   WsHeader* hdr;
-  Shared* meta;   // [CTAs] the item that begins in a CTA and goes on
+  Shared* meta;   // [CTAs]
   float2* stat;   // [2 CTAs, NQ] a part's references and sums
   float* part;    // [2 CTAs, NQ, D] a part's O
 };
@@ -503,6 +504,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   }
   if (threadIdx.x == 0) {
     a.meta[cta].parts = 0;
+    a.meta[cta].first = -1;
     ptx::mbar_progress(abort_flag);
   }
   __syncthreads();
@@ -691,6 +693,10 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     __syncwarp();
   } else {
     // ---- the parts, ahead of the softmax ----
+    const auto owner = [&](int64_t unit) {  // the CTA that has it
+      const int64_t wide = (each + 1) * rest;
+      return (int)(unit < wide ? quotient(unit, (int)(each + 1)) : rest + quotient(unit - wide, (int)each));
+    };
     for (uint32_t part = 0;; ++part) {
       const int b = part % kPlans;
       const bool more = walk.next(a, abort_flag);
@@ -732,9 +738,9 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           p.columns = min(NQ, walk.q.rows * a.group - p.col0);
           p.slot = walk.begins && walk.ends ? -1 : 2 * cta + walk.begins;
           if (walk.begins && !walk.ends) {  // so it is the last part here; which CTA has the item's last unit:
-            const int64_t last = u1 + walk.q.tiles - walk.tiles - 1, wide = (each + 1) * rest;
-            const int end = (int)(last < wide ? last / (each + 1) : rest + (last - wide) / each);
-            a.meta[cta] = Shared{p.lo, p.head, p.col0, p.columns, end - cta + 1};
+            Shared* m = &a.meta[cta];
+            m->lo = p.lo, m->head = p.head, m->col0 = p.col0, m->columns = p.columns;
+            m->parts = owner(u1 + walk.q.tiles - walk.tiles - 1) - cta + 1;
           }
         }
         parts[b] = p;
@@ -743,6 +749,8 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       if (lane == 0) ptx::mbar_arrive(&planned[b]);
       if (!more) break;
     }
+    // the first part's item began elsewhere (said last: nobody here waits for it)
+    if (lane == 0 && u1 > u0 && start.x > F::kItemCost) a.meta[cta].first = owner(u0 - start.x + F::kItemCost);
     __syncwarp();
   }
   } else {
@@ -1100,99 +1108,96 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
 }
 
 // The items that several CTAs share: part 0 is the second slot of the CTA they begin in,
-// the others the first slots of those behind it.  A warp takes a column of one of them,
-// D / 32 elements a lane.
-constexpr int kJoinThreads = 256, kJoinCtas = 8;  // an SM
+// the others the first slots of those behind it.  The blocks of CTA blockIdx.x / (NQ / 8) take eight
+// columns each of the item that begins in it and goes on, a warp a column, D / 32 elements a lane; of
+// more than eight parts one column each, a warp every eighth part, and the blocks of the seven CTAs
+// behind it the other columns.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 template <int D, int NQ>
-__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a, int ctas) {
-  static_assert(kMaxCtas <= 2 * kJoinThreads, "two CTAs a thread");
+__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
+  static_assert(kJoinWarps == 8, "columns of a block");
   constexpr int E = D / 32;
-  __shared__ int items[kMaxCtas], counts[2][kJoinThreads / 32];
-  __shared__ float sums[kJoinThreads / 32], os[kJoinThreads / 32][D];
+  __shared__ float sums[8], os[8][D];
   ptx::launch_dependents();
   ptx::grid_wait();
-  const int t = threadIdx.x, warp = t / 32, lane = t % 32;
-  uint32_t votes[2];
-  bool mine[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    mine[i] = t + i * kJoinThreads < ctas && a.meta[t + i * kJoinThreads].parts > 1;
-    votes[i] = __ballot_sync(0xffffffffu, mine[i]);
-    if (lane == 0) counts[i][warp] = __popc(votes[i]);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int cta = blockIdx.x / (NQ / 8), c = blockIdx.x % (NQ / 8) * 8;
+  Shared m = a.meta[cta];
+  if (m.parts <= 1) {
+    const int behind = cta - m.first;
+    if (m.first < 0 || behind > 7) return;
+    cta = m.first, c += behind;
+    m = a.meta[cta];
+    if (m.parts <= 8) return;
   }
-  __syncthreads();
-  int n = 0;
-  for (int i = 0; i < 2; ++i) {
-    for (int w = 0; w < kJoinThreads / 32; ++w) {
-      if (w == warp && mine[i]) items[n + __popc(votes[i] & ((1u << lane) - 1))] = t + i * kJoinThreads;
-      n += counts[i][w];
+  const bool team = m.parts > 8;
+  if (!team) c += warp;
+  if (c >= m.columns) return;
+  const auto slot = [&](int p) { return (int64_t)(p ? 2 * (cta + p) : 2 * cta + 1) * NQ + c; };
+  float ref = -INFINITY;
+  for (int p = lane; p < m.parts; p += 32) ref = fmaxf(ref, a.stat[slot(p)].x);
+  ref = warp_max(ref);
+  float sum = 0.f, o[E] = {};
+  const auto add = [&](float g, int p) {
+    const float* src = a.part + slot(p) * D + lane * E;
+    if constexpr (E == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      o[0] = fmaf(g, x.x, o[0]), o[1] = fmaf(g, x.y, o[1]), o[2] = fmaf(g, x.z, o[2]), o[3] = fmaf(g, x.w, o[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      o[0] = fmaf(g, x.x, o[0]), o[1] = fmaf(g, x.y, o[1]);
     }
-  }
-  __syncthreads();
-  // a warp a column, or all warps of a block where there are blocks for every column (parts taken in turn
-  // and added in the warps' order)
-  constexpr int kWarps = kJoinThreads / 32;
-  const int team = n * NQ <= gridDim.x ? kWarps : 1, member = team > 1 ? warp : 0;
-  for (int at = team > 1 ? blockIdx.x : blockIdx.x * kWarps + warp; at < n * NQ; at += gridDim.x * (kWarps / team)) {
-    const int cta = items[at / NQ], c = at % NQ;
-    const Shared m = a.meta[cta];
-    const auto slot = [&](int p) { return (int64_t)(p ? 2 * (cta + p) : 2 * cta + 1) * NQ + c; };
-    if (c >= m.columns) continue;
-    float ref = -INFINITY;
-    for (int p = lane; p < m.parts; p += 32) ref = fmaxf(ref, a.stat[slot(p)].x);
-    ref = warp_max(ref);
-    float sum = 0.f, o[E] = {};
-    for (int p0 = member; p0 < m.parts; p0 += 32 * team) {  // this warp's parts p0, p0 + team, ..
-      float2 s = make_float2(-INFINITY, 0.f);
-      const int mine = p0 + lane * team;
-      if (mine < m.parts) s = a.stat[slot(mine)];
-      const float f = mine >= m.parts ? 0.f : s.x == ref ? 1.f : exp2f(s.x - ref);
-      sum += f * s.y;
-      const int count = min(32, (m.parts - p0 + team - 1) / team);
-#pragma unroll 4
-      for (int i = 0; i < count; ++i) {
-        const float g = __shfl_sync(0xffffffffu, f, i);
-        const float* src = a.part + slot(p0 + i * team) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          o[0] = fmaf(g, x.x, o[0]), o[1] = fmaf(g, x.y, o[1]), o[2] = fmaf(g, x.z, o[2]), o[3] = fmaf(g, x.w, o[3]);
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(src);
-          o[0] = fmaf(g, x.x, o[0]), o[1] = fmaf(g, x.y, o[1]);
-        }
-      }
+  };
+  const auto factor = [&](int p) {  // of part p, whose sum is added
+    if (p >= m.parts) return 0.f;
+    const float2 s = a.stat[slot(p)];
+    const float f = s.x == ref ? 1.f : exp2f(s.x - ref);
+    sum += f * s.y;
+    return f;
+  };
+  if (!team) {
+    const float f = factor(lane);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float g = __shfl_sync(0xffffffffu, f, p);
+      if (p < m.parts) add(g, p);
     }
     sum = warp_sum(sum);
-    if (team > 1) {  // (the block's warps take the same turns)
-      __syncthreads();
-      if (lane == 0) sums[warp] = sum;
-#pragma unroll
-      for (int e = 0; e < E; ++e) os[warp][lane * E + e] = o[e];
-      __syncthreads();
-      if (warp > 0) continue;
-      sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = 0.f;
-      for (int w = 0; w < kWarps; ++w) {
-        sum += sums[w];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += os[w][lane * E + e];
-      }
+  } else {
+    for (int p0 = warp; p0 < m.parts; p0 += 32 * 8) {  // this warp's parts p0, p0 + 8, ..
+      const float f = factor(p0 + lane * 8);
+      const int count = min(32, (m.parts - p0 + 7) / 8);
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) add(__shfl_sync(0xffffffffu, f, i), p0 + i * 8);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint32_t out[E / 2];
+    sum = warp_sum(sum);
+    if (lane == 0) sums[warp] = sum;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
-      out[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
+    for (int e = 0; e < E; ++e) os[warp][lane * E + e] = o[e];
+    __syncthreads();
+    if (warp > 0) return;
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int w = 0; w < 8; ++w) {
+      sum += sums[w];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += os[w][lane * E + e];
     }
-    const int col = m.col0 + c, row = (int)((uint32_t)col * a.group_inv >> 32);
-    __nv_bfloat16* dst = a.out + (int64_t)(m.lo + row) * a.ldo + (m.head * a.group + col - row * a.group) * D + lane * E;
-    if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-    else
-      *reinterpret_cast<uint32_t*>(dst) = out[0];
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t out[E / 2];
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+    out[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  const int col = m.col0 + c, row = (int)((uint32_t)col * a.group_inv >> 32);
+  __nv_bfloat16* dst = a.out + (int64_t)(m.lo + row) * a.ldo + (m.head * a.group + col - row * a.group) * D + lane * E;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = out[0];
 }
 
 // ---------------------------------------------------------------------------
@@ -1269,7 +1274,7 @@ cudaError_t run(const dspark_kv_cache& c, const TreeArgs& t, const Dev& dev, cud
   const unsigned grid = (unsigned)std::min(dev.sms * F::kCtas, kMaxCtas);
   if (const cudaError_t e = launch_overlapped(f, grid, F::kThreads, F::kSmem, 1, s, tmK, tmV, t); e != cudaSuccess) return e;
   count_launches(1);
-  const cudaError_t e = launch_overlapped(k_tree_join<D, NQ>, (unsigned)dev.sms * kJoinCtas, kJoinThreads, 0, 1, s, t, (int)grid);
+  const cudaError_t e = launch_overlapped(k_tree_join<D, NQ>, grid * (NQ / 8), kJoinThreads, 0, 1, s, t);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
