@@ -18,14 +18,29 @@
 //
 // Softmax: with y = score * log2 e + log2(v scale), weights are 2^(y - ref) about a
 // column's reference, which is raised (O and the sums scaled down) only when a tile
-// passes it by 2^15, and is set 12 below the largest y then; fp16 holds 2^-24 to
-// 2^16 of it.  The sum of the weights themselves, 2^(y - ref) / (v scale), is kept by each
-// lane in fp32.  Two warpgroups take the tiles in turn, each with its own references, sums
-// and O, which are joined at the end of an item.
+// passes it by 2^15, and is set 2^6 below the largest then; fp16 holds 2^-24 to 2^16 of
+// it, and the last piece's rounding is at most 2^-23 of the largest weight.  The sum of the
+// weights themselves, 2^(y - ref) / (v scale), is kept by each lane in fp32.
 //
-// The tiles of all items are one list, dealt out evenly to the CTAs (one an SM): an item
-// that several CTAs share leaves its parts in the workspace, and a second kernel joins
-// them in order.
+// A CTA is one pair of softmax warpgroups (two CTAs an SM) or two pairs, which take tiles in
+// turn, each with its own references, sums and O, joined at the end of an item; a pair's
+// warpgroups take half of the columns each.  Four more warps load, issue S, issue O and plan.
+//
+// The tiles of all items are one list, dealt out evenly to the CTAs with a fixed cost for
+// each item: an item that several CTAs share leaves its parts in the workspace, and a second
+// kernel joins them in order.
+//
+// What bounds it: the cache's bytes while a row's columns are few, the softmax's instructions
+// beyond.  Of the measured copy rate it reads, with contexts that differ,
+//     256 requests x 4 rows x 4 heads a kv head, e4m3, 128:  348 us, 0.95
+//     256 requests x 8 rows x 4                              369 us, 0.90
+//     one request x 8 rows x 4, 250001 tokens                 91 us, 0.85
+//     64 requests x 16 rows x 4, bf16                        107 us, 0.75
+//     16 requests x 64 rows x 8 (512 columns)                200 us, 0.09
+// With 16, 32 and 64 columns a tile takes 1270, 1485 and 2450 cycles of an SM from L2; the
+// loads alone would be 1455 at the copy rate.  A tile is some 1500 instructions and 14.5 for each
+// column and warp of tokens, which at 64 columns fill half of the issue slots; the tensor
+// pipe is 19 % busy there.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -107,7 +122,7 @@ struct Form {
   static constexpr bool kSmall = NQ <= 32 && kP + 2 * kQ + 4 * kOperand + 2 * kScales <= 104 * 1024 && NQ + kO <= 256;
   static constexpr int kPairs = kSmall ? 1 : 2;
   // Tiles of k and of v have rings of their own: one of k is free again as soon as S is formed (with one
-  // ring a tile's loads waited for O two tiles before).  What the softmax reads, scales and the pages that
+  // ring a tile's loads waited for O two tiles before: 256 x 8 rows 415 us, with two 382).  What the softmax reads, scales and the pages that
   // are there, has a ring of kNotes: when k of tile n is loaded, S of tile n - kStagesK has been formed, so
   // S of every tile up to n - kStagesK - 3 has been read.
   static constexpr int kNotes = 8;
