@@ -77,8 +77,8 @@ __device__ __forceinline__ bool mbar_wait_paced(uint64_t* bar, uint32_t parity, 
     if (state[0]) return false;
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 7u) == 0u) {
-      const uint32_t step = (uint32_t)state[1];  // read before the counter, or it might be the later one
-      if (cycles_lo() - step > 1u << 30) return false;
+      // (signed: the other thread's step may be later than this reading of the counter)
+      if ((int32_t)(cycles_lo() - (uint32_t)state[1]) > 1 << 30) return false;
     }
   }
 }
