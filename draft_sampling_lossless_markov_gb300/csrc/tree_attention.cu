@@ -844,6 +844,9 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
         }
         if (masked && h == 0) {
           // what no row or only some see must not reach the others through 0 * NaN
+          // (the tile before is in O first: until v of tile n - kStagesV has arrived, vfull's phase is one of
+          // the same parity two back)
+          if (turn > 0) wait(&pdone[w], (turn + 1) & 1, 12);
           wait(&vfull[n % F::kStagesV], (n / F::kStagesV) & 1, 12);
           uint8_t* row = sV + n % F::kStagesV * F::kOperand + token * F::kRow;
           if (!held || pos >= base) {

@@ -454,6 +454,25 @@ def test_one_context_over_many_ctas(rows, group, D, page, dtype):
     check(c, q, offsets, base, words, call(c, q, offsets, base, words, rows))
 
 
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("rows,group,D", [(4, 4, 128), (8, 4, 128), (16, 4, 128), (16, 4, 64), (12, 12, 128)])
+def test_many_tiles_a_cta_from_memory(rows, group, D, dtype):
+    """Long runs of tiles whose loads are late: contexts out of cache, more tiles than stages for every CTA."""
+    rng = np.random.default_rng(6)
+    B, heads = 20, 8
+    base = [int(x) for x in rng.integers(0, 3500, B)]
+    c, q, offsets, words = setup(33, dtype, base, [rows] * B, heads, group, D, 128, True, fill="normal")
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    ws = T.tree_attention_workspace(B, rows, heads * group, heads, D)
+    outs = []
+    for i in range(4):
+        flush.fill_(i)
+        outs.append(call(c, q, offsets, base, words, rows, ws=ws))
+    check(c, q, offsets, base, words, outs[0])
+    for out in outs[1:]:
+        assert torch.equal(bits(out), bits(outs[0]))
+
+
 def test_two_graphs_share_a_workspace():
     """Captured calls of different sizes with one workspace, replayed in turn without a wait between them."""
     made = [setup(40, E4M3, [900, 3], [8, 5], 2, 4, 128, 32, True), setup(41, BF16, [50] * 30, [2] * 30, 2, 2, 64, 16, True)]
