@@ -178,8 +178,8 @@ struct Start {
   Request q;
 };
 // (32-bit division where the numbers allow: a 64-bit one takes some 300 cycles)
-__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
-  return (a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 // The parts of items in a CTA's share of the units, one after the other; the warps that need them walk by themselves.
 template <typename F>
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
     // ---- the parts, ahead of the softmax ----
     const auto owner = [&](int64_t unit) {  // the CTA that has it
       const int64_t wide = (each + 1) * rest;
-      return (int)(unit < wide ? quotient(unit, (int)(each + 1)) : rest + quotient(unit - wide, (int)each));
+      return (int)(unit < wide ? quotient(unit, each + 1) : rest + quotient(unit - wide, each));
     };
     for (uint32_t part = 0;; ++part) {
       const int b = part % kPlans;

@@ -644,8 +644,9 @@ DSPARK_API dspark_status dspark_token_logprobs_grad(const dspark_token_logprobs_
  * A cache is a pool of n_pages pages of page_size tokens:
  *     k, v              [n_pages, n_kv_heads, page_size, head_dim] dtype, dense
  *     k_scale, v_scale  [n_pages, n_kv_heads, page_size] f32 (DSPARK_E4M3)
- * DSPARK_E4M3: a row of head_dim codes stands for code * scale; DSPARK_BF16:
- * the values themselves, the scales NULL.  Position p of request r is slot
+ * DSPARK_E4M3: a row of head_dim codes stands for code * scale, scales being 0 or
+ * finite, positive and normal, as dspark_cache_write makes them; DSPARK_BF16: the
+ * values themselves, the scales NULL.  Position p of request r is slot
  * p % page_size of page table[r * table_ld + p / page_size].  Entries of pages
  * past a request's tokens are not looked at.  Requests may share pages that are
  * only read.  page_size is a power of two, 16 to 1024; head_dim 64 or 128; k, v
