@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           k_scale = sScale[note * 2 * kTile + token];
           v_scale = sScale[note * 2 * kTile + kTile + token];
         }
-        if (masked && h == 0) {
+        if (masked) {
           // what no row or only some see must not reach the others through 0 * NaN
           // (the tile before is in O first: until v of tile n - kStagesV has arrived, vfull's phase is one of
           // the same parity two back)
@@ -851,8 +851,12 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           uint8_t* row = sV + n % F::kStagesV * F::kOperand + token * F::kRow;
           if (!held || pos >= base) {
             uint32_t any = 0;
+            // half of the row a warpgroup, neighbouring tokens' 16-byte units in different banks
+            constexpr int kUnits = F::kParts * F::kRow / 16, kRowUnits = F::kRow / 16;
+            const int turned = (kRowUnits == 8 ? token : token >> 1) & (kRowUnits - 1);
 #pragma unroll 1
-            for (int i = 0; i < F::kParts * F::kRow / 16; ++i) {
+            for (int u = h * (kUnits / 2); u < (h + 1) * (kUnits / 2); ++u) {
+              const int i = u ^ (turned & (kUnits / 2 - 1));
               uint4* at = reinterpret_cast<uint4*>(row + i * 16 / F::kRow * F::kPart + i * 16 % F::kRow);
               if (held) {
                 const uint4 x = *at;
