@@ -33,10 +33,10 @@
 // What bounds it: the cache's bytes while a row's columns are few, the softmax's instructions
 // beyond.  Of the measured copy rate it reads, with contexts that differ,
 //     256 requests x 4 rows x 4 heads a kv head, e4m3, 128:  348 us, 0.95
-//     256 requests x 8 rows x 4                              369 us, 0.90
+//     256 requests x 8 rows x 4                              365 us, 0.91
 //     one request x 8 rows x 4, 250001 tokens                 91 us, 0.85
-//     64 requests x 16 rows x 4, bf16                        107 us, 0.75
-//     16 requests x 64 rows x 8 (512 columns)                200 us, 0.09
+//     64 requests x 16 rows x 4, bf16                        101 us, 0.80
+//     16 requests x 64 rows x 8 (512 columns)                198 us, 0.09
 // With 16, 32 and 64 columns a tile takes 1270, 1485 and 2450 cycles of an SM from L2; the
 // loads alone would be 1455 at the copy rate.  A tile is some 1500 instructions and 14.5 for each
 // column and warp of tokens, which at 64 columns fill half of the issue slots; the tensor

@@ -512,9 +512,12 @@ def _cache_rows(cache: KvCache, k, v, mark_req, mark_pos, base, n_rows) -> tuple
     pk, ldk, N, *got = _heads(k, "k", k.dtype)
     if got != [cache.n_kv_heads, cache.head_dim]:
         raise ValueError(f"k: expected [N, {cache.n_kv_heads}, {cache.head_dim}], got {tuple(k.shape)}")
-    pv, ldv, *got = _heads(v, "v", k.dtype)
     if v.shape != k.shape:
         raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    if v.dtype is k.dtype and v.is_cuda and v.stride() == k.stride():
+        pv, ldv = v.data_ptr(), ldk  # laid out as k
+    else:
+        pv, ldv, *got = _heads(v, "v", k.dtype)
     i32 = torch.int32
     return (*cache.fields, N, dt, pk, ldk, pv, ldv, _dense(mark_req, (N,), "mark_req", i32),
             _dense(mark_pos, (N,), "mark_pos", i32), _dense(base, (cache.n_req,), "base", i32),
