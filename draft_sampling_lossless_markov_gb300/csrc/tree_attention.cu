@@ -1101,10 +1101,16 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = two ? fmaf(f1[i], u[i], f0[i] * v[i]) : f0[i] * v[i];
           if (whole) {
-            const int64_t* at = &out_at[b][c0];
+            // two elements a store: even lanes take columns 0-3 of two lanes, odd ones 4-7
+            const bool odd = lane & 1;
+            const int64_t* at = &out_at[b][c0 + 4 * odd];
+            __nv_bfloat16* dst = a.out + (d & ~1);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < n) a.out[at[i] + d] = __float2bfloat16_rn(v[i]);
+            for (int i = 0; i < 4; ++i) {
+              const float mine = odd ? v[i + 4] : v[i], other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 4], 1);
+              const __nv_bfloat162 x = __floats2bfloat162_rn(odd ? other : mine, odd ? mine : other);
+              if (i + 4 * odd < n) *reinterpret_cast<__nv_bfloat162*>(dst + at[i]) = x;
+            }
           } else {
             float* at = a.part + ((int64_t)slot * NQ + c0) * D + d;
 #pragma unroll
@@ -1112,6 +1118,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
               if (i < n) at[i * D] = v[i];
           }
         }
+        __syncwarp();  // (an element may have been written by the lane beside)
         if (bad_rows && d < D)
           add_non_finite<kCodes, D, NQ>(a, now, seers[part % kPlans], out_at[b], bad_rows, wg * W, min(columns, (wg + 1) * W), d);
       }
