@@ -20,7 +20,9 @@
 // column's reference, which is raised (O and the sums scaled down) only when a tile
 // passes it by 2^15, and is set 2^6 below the largest then; fp16 holds 2^-24 to 2^16 of
 // it, and the last piece's rounding is at most 2^-23 of the largest weight.  The sum of the
-// weights themselves, 2^(y - ref) / (v scale), is kept by each lane in fp32.
+// weights themselves, 2^(y - ref) / (v scale), is kept by each lane in fp32; from a tile on in which a
+// v scale is 0 or far from 1 (rows of zeros, cleared ones), its terms are formed from the scores alone,
+// 2^(score * log2 e - a reference of the sum's own), in the branch that raises references.
 //
 // A CTA is one pair of softmax warpgroups (two CTAs an SM) or two pairs, which take tiles in
 // turn, each with its own references, sums and O, joined at the end of an item; a pair's
@@ -69,6 +71,11 @@ constexpr float kHead = kCodes ? 6.f : 0.f;
 template <bool kCodes>
 constexpr float kRaise = kCodes ? 15.f : 60.f;
 constexpr float kLog2e = 1.4426950408889634f;
+// v scales with which the sums keep the weights' reference, 2^-40 to 2^38: a term is below 2^(15 + 40), and one whose
+// weight rounds to 0 (below 2^-126) is below 2^-86 in a sum that holds one of 2^(6 - 38) or more.
+constexpr uint32_t kLeastScale = (127u - 40) << 23, kMostScale = (127u + 38) << 23;
+constexpr float kLeastNormal = 1.1754943508222875e-38f;
+constexpr float kRaiseSum = 60.f;  // the exponent that raises a sum's own reference
 
 // An item that begins in a CTA and goes on in others: where its rows and columns are, and its parts (0: there is
 // none).  first: the CTA that the item of this CTA's first part begins in, -1 if that is this one.
@@ -92,7 +99,7 @@ struct TreeArgs {
   float scale;
   WsHeader* hdr;
   Shared* meta;   // [CTAs]
-  float2* stat;   // [2 CTAs, NQ] a part's references and sums
+  float4* stat;   // [2 CTAs, NQ] a part's references, sums and the sums' references
   float* part;    // [2 CTAs, NQ, D] a part's O
 };
 
@@ -370,6 +377,52 @@ __device__ __forceinline__ void load_sum(uint32_t taddr, int apart, float (&v)[8
   }
 }
 
+// A tile's weights to sums with references of their own, of the scores alone: x are the exponents y - ref, l the sums;
+// less log2 of the v scale and by the difference of the references (at) they are the sums'.  Out of line: it is rare.
+template <int HQ>
+__device__ __noinline__ void sum_apart(uint64_t (&x)[HQ / 2], uint64_t (&l)[HQ / 2], float v_inv, float* at,
+                                       float* factor, bool* set, float (*top)[HQ], int bar) {
+  const int lane = threadIdx.x & 31, token = threadIdx.x & 127;
+  // v_inv: the scale's inverse, or the scale negated
+  const bool far = !(v_inv > 0.f), zero = far && -v_inv < kLeastNormal;
+  const float v = fabsf(v_inv), log = __log2f(zero ? kLeastNormal : v);
+  const float back = !(v == v) ? 0.f : far ? -log : log;  // (NaN is in x where the token is seen)
+  const auto exponents = [&](int i) {
+    return ptx::unpack2(ptx::add2(x[i], ptx::add2(ptx::pack2(back, back), *reinterpret_cast<const uint64_t*>(&at[2 * i]))));
+  };
+  float m = -INFINITY;  // of column `lane`
+#pragma unroll
+  for (int i = 0; i < HQ / 2; ++i) {
+    const float2 e = exponents(i);
+    const float m0 = ptx::warp_max_redux(e.x), m1 = ptx::warp_max_redux(e.y);
+    m = lane == 2 * i ? m0 : lane == 2 * i + 1 ? m1 : m;
+  }
+  if (lane < HQ) top[token / 32][lane] = m;
+  ptx::named_sync(bar, 128);
+  if (token < HQ) {
+    m = fmaxf(fmaxf(top[0][token], top[1][token]), fmaxf(top[2][token], top[3][token]));
+    const bool was = set[token];
+    const float d = (was ? m > kRaiseSum : m > -INFINITY) ? m : 0.f;
+    set[token] = was || m > -INFINITY;
+    at[token] -= d;
+    factor[token] = was ? ptx::ex2(-d) : 1.f;  // (a sum without a reference is 0 or NaN)
+  }
+  ptx::named_sync(bar, 128);
+#pragma unroll
+  for (int i = 0; i < HQ / 2; ++i) {
+    const float2 e = exponents(i);
+    l[i] = ptx::fma2(l[i], *reinterpret_cast<const uint64_t*>(&factor[2 * i]), ptx::pack2(ptx::ex2(e.x), ptx::ex2(e.y)));
+    if (zero) x[i] = ptx::pack2(-INFINITY, -INFINITY);  // codes of scale 0 are 0
+  }
+}
+
+// What turns O into the result is 2^(O's reference less the sum's) / sum, 0 where nothing was summed, as two factors:
+// neither they nor O times the first leave fp32's normal range where the result does not.
+__device__ __forceinline__ float2 inverse(float sum, float apart) {
+  const float half = sum == 0.f ? 0.f : ptx::ex2(0.5f * apart);
+  return make_float2(sum == 0.f ? 0.f : __frcp_rn(sum) * half, half);
+}
+
 // Adds the non-finite elements of v that columns c0 .. c1 see of the drafted rows `nodes` to what was
 // written for them (element d of the head).
 template <bool kCodes, int D, int NQ>
@@ -423,8 +476,12 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
   __shared__ int64_t out_at[2][NQ];
   __shared__ __align__(16) float qs[2][NQ];
   __shared__ __align__(16) float nref[kPairs][NQ], delta[kPairs][NQ], factor[kPairs][NQ];
-  __shared__ float warp_top[kSoftWarps][NQ / 2], coef[kPairs][NQ];
+  __shared__ float warp_top[kSoftWarps][NQ / 2], coef[kPairs][NQ], unit[NQ];
   __shared__ bool set[kPairs][NQ];
+  // the sums' references: whether there is one, and how far below the weights' it is (0 while they share it)
+  __shared__ bool sum_set[kPairs][NQ];
+  __shared__ __align__(16) float sum_at[kPairs][NQ];
+  __shared__ bool odd_scale[kPairs][2];  // a warpgroup has met a v scale far from 1 in this part
   volatile int* abort_flag = abort_s;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -816,7 +873,9 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       float* my_nref = &nref[w][h * HQ];
       float* my_delta = &delta[w][h * HQ];
       float* my_factor = &factor[w][h * HQ];
-      if (token < HQ) my_nref[token] = 0.f, set[w][h * HQ + token] = false;
+      float* my_sum_at = &sum_at[w][h * HQ];
+      if (token < HQ) my_nref[token] = my_sum_at[token] = 0.f, set[w][h * HQ + token] = sum_set[w][h * HQ + token] = false;
+      if (token == 0) odd_scale[w][h] = false;
       const bool got = ptx::mbar_wait_paced(&qfull[b], (part >> 1) & 1, abort_flag);
       if (!got) fail(10);
       // after a fault all leave together (q is counted as ready, and the plans are no more than they were)
@@ -828,7 +887,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       uint64_t l2[HQ / 2];
 #pragma unroll
       for (int i = 0; i < HQ / 2; ++i) l2[i] = 0;
-      bool unset = opaque(1) != 0;  // a column has no reference yet
+      bool unset = opaque(1) != 0;  // a column has no reference yet, or the sums have their own
 #pragma unroll 1
       for (int t = opaque(w); t < tiles; t += kPairs) {
         const uint32_t n = n0 + t, note = n % F::kNotes;
@@ -883,11 +942,11 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
         load_columns<L>(tS, v[0]);
         uint64_t ks2 = 0, vl2 = 0;
         if (kCodes) {
-          if (v_scale < 1.17549435e-38f) v_scale = 1.17549435e-38f;  // 0 of a cache that was cleared
-          const float v_log = __log2f(v_scale);
-          v_inv = ptx::rcp(v_scale);
-          // what is no token's scale, and NaN: then the weights of those that see it are NaN, of the others 0
-          if (masked && !(held && v_scale == v_scale)) v_inv = 1.f;
+          if (masked && !held) v_scale = 1.f;  // what is no token's scale
+          const float least = v_scale < kLeastNormal ? kLeastNormal : v_scale;  // 0 of a cache that was cleared
+          const float v_log = __log2f(least);
+          // a scale far from 1 (0 and NaN too) stands in the place of its inverse, negated
+          v_inv = __float_as_uint(v_scale) - kLeastScale > kMostScale - kLeastScale ? -v_scale : ptx::rcp(least);
           ks2 = ptx::pack2(k_scale, k_scale);
           vl2 = ptx::pack2(v_log, v_log);
         }
@@ -925,22 +984,36 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           const float2 x = ptx::unpack2(x2[i]);
           top = fmaxf(top, fmaxf(x.x, x.y));
         }
-        const bool raise = ptx::named_any(own, 128, top > kRaise<kCodes>) || unset;
+        const bool raise = ptx::named_any(own, 128, top > kRaise<kCodes> || !(v_inv > 0.f)) || unset;
         if (turn > 1) {  // the tile before is in O, and its weights have been read
           wait(&pdone[w], turn & 1, 14);
           ptx::tc_fence_after();
         }
         if (raise) {
           // the columns' largest, new references, what was summed so far brought to them
-          float m = -INFINITY;  // of column `lane`
+#pragma unroll 1
+          for (bool sums = kCodes;; sums = false) {
+            float m = -INFINITY;  // of column `lane`
 #pragma unroll
-          for (int i = 0; i < HQ / 2; ++i) {
-            const float2 x = ptx::unpack2(x2[i]);
-            const float m0 = ptx::warp_max_redux(x.x), m1 = ptx::warp_max_redux(x.y);
-            m = lane == 2 * i ? m0 : lane == 2 * i + 1 ? m1 : m;
+            for (int i = 0; i < HQ / 2; ++i) {
+              const float2 x = ptx::unpack2(x2[i]);
+              const float m0 = ptx::warp_max_redux(x.x), m1 = ptx::warp_max_redux(x.y);
+              m = lane == 2 * i ? m0 : lane == 2 * i + 1 ? m1 : m;
+            }
+            if (lane < HQ) warp_top[warp][lane] = m;
+            if (!(v_inv > 0.f)) odd_scale[w][h] = true;
+            ptx::named_sync(own, 128);
+            if (!sums || !odd_scale[w][h]) break;
+            // this tile's sums first, which changes x2
+            uint64_t x[HQ / 2], l[HQ / 2];
+#pragma unroll
+            for (int i = 0; i < HQ / 2; ++i) x[i] = x2[i], l[i] = l2[i];
+            sum_apart<HQ>(x, l, v_inv, my_sum_at, my_factor, &sum_set[w][h * HQ], &warp_top[wg * 4], own);
+#pragma unroll
+            for (int i = 0; i < HQ / 2; ++i) x2[i] = x[i], l2[i] = l[i];
+            v_inv = 0.f;
           }
-          if (lane < HQ) warp_top[warp][lane] = m;
-          ptx::named_sync(own, 128);
+          const bool apart = kCodes && odd_scale[w][h];  // the sums have references of their own
           bool none = false;
           if (token < HQ) {
             const float m = fmaxf(fmaxf(warp_top[wg * 4][token], warp_top[wg * 4 + 1][token]),
@@ -949,18 +1022,19 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
             if (set[w][h * HQ + token])
               d = fmaxf(0.f, m - kHead<kCodes>);
             else if (m > -INFINITY)
-              d = m - kHead<kCodes>, set[w][h * HQ + token] = true;
+              d = m - kHead<kCodes>, set[w][h * HQ + token] = true, sum_set[w][h * HQ + token] |= !apart;
             else
               none = true;
             my_delta[token] = -d;
             my_factor[token] = ptx::ex2(-d);
             my_nref[token] -= d;
+            if (apart) my_sum_at[token] += d;
           }
-          unset = ptx::named_any(own, 128, none);
+          unset = ptx::named_any(own, 128, none) || apart;  // (the part's later tiles all come here)
 #pragma unroll
           for (int i = 0; i < HQ / 2; ++i) {
             x2[i] = ptx::add2(x2[i], *reinterpret_cast<const uint64_t*>(&my_delta[2 * i]));
-            if (t >= kPairs) l2[i] = ptx::mul2(l2[i], *reinterpret_cast<const uint64_t*>(&my_factor[2 * i]));
+            if (t >= kPairs && !apart) l2[i] = ptx::mul2(l2[i], *reinterpret_cast<const uint64_t*>(&my_factor[2 * i]));
           }
           if (t >= kPairs) {
 #pragma unroll 1
@@ -1062,27 +1136,33 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       const bool whole = slot < 0;
       if (threadIdx.x < NQ) {
         const int c = threadIdx.x, half = c / HQ, i = c % HQ;
-        float ref[kPairs], l[kPairs];
+        float ref[kPairs], sum_ref[kPairs], l[kPairs];
 #pragma unroll
         for (int g = 0; g < kPairs; ++g) {
           const int first = (g * 2 + half) * 4;
           ref[g] = set[g][c] ? -nref[g][c] : -INFINITY;
+          sum_ref[g] = sum_set[g][c] ? -(nref[g][c] + sum_at[g][c]) : -INFINITY;
           l[g] = (warp_top[first][i] + warp_top[first + 1][i]) + (warp_top[first + 2][i] + warp_top[first + 3][i]);
         }
-        float m = ref[0], sum = l[0], f[kPairs] = {1.f};
+        float m = ref[0], sum_m = sum_ref[0], sum = l[0], f[kPairs] = {1.f};
         if constexpr (kPairs > 1) {
           f[1] = 0.f;
           if (two) {
             m = fmaxf(ref[0], ref[1]);
+            sum_m = fmaxf(sum_ref[0], sum_ref[1]);
+            sum = 0.f;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) f[g] = ref[g] == m ? 1.f : ptx::ex2(ref[g] - m);
-            sum = f[0] * l[0] + f[1] * l[1];
+            for (int g = 0; g < 2; ++g) {
+              f[g] = ref[g] == m ? 1.f : ptx::ex2(ref[g] - m);
+              sum += (sum_ref[g] == sum_m ? 1.f : ptx::ex2(sum_ref[g] - sum_m)) * l[g];
+            }
           }
         }
-        const float inv = !whole ? 1.f : sum == 0.f ? 0.f : __frcp_rn(sum);
+        const float2 inv = whole ? inverse(sum, m - sum_m) : make_float2(1.f, 1.f);
 #pragma unroll
-        for (int g = 0; g < kPairs; ++g) coef[g][c] = f[g] * inv;
-        if (!whole) a.stat[(int64_t)slot * NQ + c] = make_float2(m, sum);
+        for (int g = 0; g < kPairs; ++g) coef[g][c] = f[g] * inv.x;
+        unit[c] = inv.y;
+        if (!whole) a.stat[(int64_t)slot * NQ + c] = make_float4(m, sum, sum_m, 0.f);
       }
       ptx::named_sync(kAll, kSoft);
       // its share of the columns a warpgroup, eight at a time (a loop: straight-line code this rarely
@@ -1099,7 +1179,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           const float* f0 = &coef[0][c0];
           const float* f1 = &coef[kPairs - 1][c0];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = two ? fmaf(f1[i], u[i], f0[i] * v[i]) : f0[i] * v[i];
+          for (int i = 0; i < 8; ++i) v[i] = (two ? fmaf(f1[i], u[i], f0[i] * v[i]) : f0[i] * v[i]) * unit[c0 + i];
           if (whole) {
             // two elements a store: even lanes take columns 0-3 of two lanes, odd ones 4-7
             const bool odd = lane & 1;
@@ -1163,9 +1243,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
   if (!team) c += warp;
   if (c >= m.columns) return;
   const auto slot = [&](int p) { return (int64_t)(p ? 2 * (cta + p) : 2 * cta + 1) * NQ + c; };
-  float ref = -INFINITY;
-  for (int p = lane; p < m.parts; p += 32) ref = fmaxf(ref, a.stat[slot(p)].x);
+  float ref = -INFINITY, sum_ref = -INFINITY;
+  for (int p = lane; p < m.parts; p += 32) {
+    const float4 s = a.stat[slot(p)];
+    ref = fmaxf(ref, s.x), sum_ref = fmaxf(sum_ref, s.z);
+  }
   ref = warp_max(ref);
+  sum_ref = warp_max(sum_ref);
   float sum = 0.f, o[E] = {};
   const auto add = [&](float g, int p) {
     const float* src = a.part + slot(p) * D + lane * E;
@@ -1179,10 +1263,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
   };
   const auto factor = [&](int p) {  // of part p, whose sum is added
     if (p >= m.parts) return 0.f;
-    const float2 s = a.stat[slot(p)];
-    const float f = s.x == ref ? 1.f : exp2f(s.x - ref);
-    sum += f * s.y;
-    return f;
+    const float4 s = a.stat[slot(p)];
+    sum += (s.z == sum_ref ? 1.f : exp2f(s.z - sum_ref)) * s.y;
+    return s.x == ref ? 1.f : exp2f(s.x - ref);
   };
   if (!team) {
     const float f = factor(lane);
@@ -1214,11 +1297,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
       for (int e = 0; e < E; ++e) o[e] += os[w][lane * E + e];
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float2 inv = inverse(sum, ref - sum_ref);
   uint32_t out[E / 2];
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o[e] * inv.x * inv.y, o[e + 1] * inv.x * inv.y);
     out[e / 2] = *reinterpret_cast<const uint32_t*>(&x);
   }
   const int col = m.col0 + c, row = (int)((uint32_t)col * a.group_inv >> 32);
@@ -1244,7 +1327,7 @@ Layout layout(int max_tree, int group, int head_dim) {
   Layout l;
   l.meta = align_up(sizeof(WsHeader), 256);
   l.stat = align_up(l.meta + kMaxCtas * sizeof(Shared), 256);
-  l.part = align_up(l.stat + 2 * kMaxCtas * nq * sizeof(float2), 256);
+  l.part = align_up(l.stat + 2 * kMaxCtas * nq * sizeof(float4), 256);
   l.total = l.part + 2 * kMaxCtas * nq * head_dim * sizeof(float);
   return l;
 }
@@ -1346,7 +1429,7 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args& a, uint8_t* 
   t.hdr = reinterpret_cast<WsHeader*>(ws);
   const Layout l = layout(a.max_tree, t.group, a.cache.head_dim);
   t.meta = reinterpret_cast<Shared*>(ws + l.meta);
-  t.stat = reinterpret_cast<float2*>(ws + l.stat);
+  t.stat = reinterpret_cast<float4*>(ws + l.stat);
   t.part = reinterpret_cast<float*>(ws + l.part);
   const bool small = a.cache.head_dim == 64;
   if (a.cache.dtype == DSPARK_E4M3)
