@@ -1019,14 +1019,15 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
             const float m = fmaxf(fmaxf(warp_top[wg * 4][token], warp_top[wg * 4 + 1][token]),
                                   fmaxf(warp_top[wg * 4 + 2][token], warp_top[wg * 4 + 3][token]));
             float d = 0.f;
-            if (set[w][h * HQ + token])
+            const bool was = set[w][h * HQ + token];
+            if (was)
               d = fmaxf(0.f, m - kHead<kCodes>);
             else if (m > -INFINITY)
               d = m - kHead<kCodes>, set[w][h * HQ + token] = true, sum_set[w][h * HQ + token] |= !apart;
             else
               none = true;
             my_delta[token] = -d;
-            my_factor[token] = ptx::ex2(-d);
+            my_factor[token] = was ? ptx::ex2(-d) : 1.f;  // (nothing was summed before the first reference, however low that is)
             my_nref[token] -= d;
             if (apart) my_sum_at[token] += d;
           }

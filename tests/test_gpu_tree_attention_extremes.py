@@ -1,0 +1,64 @@
+"""GPU parity of tree_attention at the ends of its ranges.  Tolerances as in test_gpu_tree_attention.py."""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_tree_attention as A
+from draft_sampling_lossless_markov_gb300 import capi
+from draft_sampling_lossless_markov_gb300 import torch_api as T
+from gpu_common import require_gpu
+from kv_common import BF16, E4M3, i32
+
+pytestmark = pytest.mark.gpu
+
+FORMS = [(2, 2, 64), (1, 16, 128), (8, 4, 128), (4, 5, 64), (16, 4, 128), (9, 7, 64)]  # rows, heads, head size: 16, 32, 64 columns
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def set_scores(c, q, scores):
+    """q and k of request 0's tokens such that every row's score of token t is scores[t], to the rounding of k (one head)."""
+    D, page = c.head_dim, c.k.shape[2]
+    n = scores.numel()
+    q[:] = 0
+    q[..., 0] = 4.0
+    want = scores.cuda().float() * D ** 0.5 / 4
+    t = torch.arange(n, device="cuda")
+    pages, slots = c.table[0].long()[t // page], t % page
+    there = pages < c.k.shape[0]
+    pages, slots, want = pages[there], slots[there], want[there]
+    if c.k.dtype == BF16:
+        c.k[pages, 0, slots, 0] = want.to(BF16)
+    else:
+        scale = torch.where(want != 0, want.abs() / 448, torch.ones_like(want))
+        c.k_scale[pages, 0, slots] = scale
+        codes = c.k[pages, 0, slots].float()
+        codes[:, 0] = want / scale
+        c.k.view(torch.uint8)[pages, 0, slots] = codes.clamp(-448, 448).to(E4M3).view(torch.uint8)
+
+
+def call_many(c, q, base, rows, B=608):
+    """The call for so many requests like the one of c that whole items fall to a CTA; what some of them got, the workspace."""
+    many = T.KvCache(c.k, c.v, c.table.expand(B, -1).contiguous(), *(() if c.k_scale is None else (c.k_scale, c.v_scale)))
+    ws = T.tree_attention_workspace(B, rows, q.shape[1], 1, c.head_dim)
+    out = T.tree_attention(ws, many, q.repeat(B, 1, 1), i32(np.arange(B + 1) * rows), i32([base] * B), rows)
+    return [out[r * rows:(r + 1) * rows] for r in (0, 1, 2, 303, B - 1)], ws
+
+
+@pytest.mark.parametrize("dtype", [E4M3, BF16])
+@pytest.mark.parametrize("rows,group,D", FORMS)
+@pytest.mark.parametrize("missing", [1, 2, 3])
+def test_low_scores_behind_missing_pages(missing, rows, group, D, dtype):
+    """The first tiles' pages are not there, and the first scores that are seen are far below 0."""
+    base, page = 900, 128
+    c, q, offsets, _ = A.setup(1, dtype, [base], [rows], 1, group, D, page, fill="normal")
+    q = q.clone()
+    c.table[0, :missing] = 2 ** 30
+    set_scores(c, q, -110 - torch.arange(base + rows) / 500)
+    out, ws = call_many(c, q, base, rows)
+    assert ws.read_error()[0] == capi.DSPARK_BAD_INPUT
+    for o in out:
+        A.check(c, q, offsets, [base], None, o)
