@@ -65,11 +65,12 @@ namespace {
 constexpr int kTile = 128;           // tokens
 constexpr int kMaxCtas = 320;        // parts the workspace holds: two a CTA
 // A column's largest exponent when its reference is set, and the exponent that raises it: 2^15 is in
-// fp16's range, bf16 weights have room up to 2^60.
+// fp16's range; bf16 weights stay below 1, as in a softmax, so that O overflows no sooner than the sum over v
+// of weights up to 1 would.
 template <bool kCodes>
-constexpr float kHead = kCodes ? 6.f : 0.f;
+constexpr float kHead = kCodes ? 6.f : -10.f;
 template <bool kCodes>
-constexpr float kRaise = kCodes ? 15.f : 60.f;
+constexpr float kRaise = kCodes ? 15.f : 0.f;
 constexpr float kLog2e = 1.4426950408889634f;
 // v scales with which the sums keep the weights' reference, 2^-40 to 2^38: a term is below 2^(15 + 40), and one whose
 // weight rounds to 0 (below 2^-126) is below 2^-86 in a sum that holds one of 2^(6 - 38) or more.

@@ -62,3 +62,19 @@ def test_low_scores_behind_missing_pages(missing, rows, group, D, dtype):
     assert ws.read_error()[0] == capi.DSPARK_BAD_INPUT
     for o in out:
         A.check(c, q, offsets, [base], None, o)
+
+
+@pytest.mark.parametrize("rows,group,D", FORMS)
+@pytest.mark.parametrize("size", [2.0 ** 40, 2.0 ** 90, 2.0 ** 115, 2.0 ** -110])
+@pytest.mark.parametrize("rise", [0.0, 8.0, 38.0])
+def test_large_values_behind_low_scores(rise, size, rows, group, D):
+    """A bf16 cache with values of one size, and scores that rise after the first tiles, so that weights pass 1."""
+    base = 1100
+    c, q, offsets, _ = A.setup(2, BF16, [base], [rows], 1, group, D, 64, fill="normal")
+    q = q.clone()
+    set_scores(c, q, torch.where(torch.arange(base + rows) < 300, 0.0, rise))
+    c.v.mul_(size)
+    out, ws = call_many(c, q, base, rows)
+    assert ws.read_error()[0] == capi.DSPARK_OK
+    for o in out:
+        A.check(c, q, offsets, [base], None, o)
