@@ -14,12 +14,14 @@
 // into two e4m3 pieces whose sum is q exactly (8 significant bits; elements below 2^-10 of
 // the column's largest to 2^-18 of it): S = K . Q1 + K . Q2.  A weight p times its
 // token's v scale is split into three e5m2 pieces, 9 significant bits: the upper bytes of
-// its fp16 form, of what they leave, and the rounded rest.
+// its fp16 form, of 2^3 times what they leave, and the rest rounded, times 2^3 again.
 //
 // Softmax: with y = score * log2 e + log2(v scale), weights are 2^(y - ref) about a
 // column's reference, which is raised (O and the sums scaled down) only when a tile
 // passes it by 2^15, and is set 2^6 below the largest then; fp16 holds 2^-24 to 2^16 of
-// it, and the last piece's rounding is at most 2^-23 of the largest weight.  The sum of the
+// it, and the last piece's rounding is at most 2^-23, 2^-29 of the largest weight.  (e5m2 ends at 2^-16: without
+// the two factors weights below 2^-17 were lost, with them a tail of 60000 tokens 16 below a first one.  They cost
+// 1.5 %; the largest weight at 2^12 raises references so often that 256 x 8 rows take 441 us, not 369.)  The sum of the
 // weights themselves, 2^(y - ref) / (v scale), is kept by each lane in fp32; from a tile on in which a
 // v scale is 0 or far from 1 (rows of zeros, cleared ones), its terms are formed from the scores alone,
 // 2^(score * log2 e - a reference of the sum's own), in the branch that raises references.
@@ -72,6 +74,7 @@ constexpr float kHead = kCodes ? 6.f : -10.f;
 template <bool kCodes>
 constexpr float kRaise = kCodes ? 15.f : 0.f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPiece = 8.f;  // a piece's factor over the one before, which leaves less than 2^12 of less than 2^15
 // v scales with which the sums keep the weights' reference, 2^-40 to 2^38: a term is below 2^(15 + 40), and one whose
 // weight rounds to 0 (below 2^-126) is below 2^-86 in a sum that holds one of 2^(6 - 38) or more.
 constexpr uint32_t kLeastScale = (127u - 40) << 23, kMostScale = (127u + 38) << 23;
@@ -274,6 +277,10 @@ __device__ __forceinline__ uint32_t e5m2x2(uint32_t h) {
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
   return r;
 }
+// what the upper bytes of two halves leave of them, times the next piece's factor
+__device__ __forceinline__ uint32_t left_of(uint32_t h) {
+  return half2_bits(__hmul2(__hsub2(bits_half2(h), bits_half2(h & 0xFF00FF00u)), __float2half2_rn(kPiece)));
+}
 __device__ __forceinline__ uint32_t e4m3x2(uint32_t h) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
@@ -374,7 +381,7 @@ __device__ __forceinline__ void load_sum(uint32_t taddr, int apart, float (&v)[8
   for (int i = 0; i < 8; ++i) {
     v[i] = u[kPieces - 1][i];
 #pragma unroll
-    for (int p = kPieces - 2; p >= 0; --p) v[i] += u[p][i];
+    for (int p = kPieces - 2; p >= 0; --p) v[i] = fmaf(v[i], 1.f / kPiece, u[p][i]);
   }
 }
 
@@ -1070,8 +1077,8 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
             l = kCodes ? ptx::fma2(p2, vi2, l) : ptx::add2(l, p2);
             if constexpr (kCodes) {
               hh[i] = half2_bits(__floats2half2_rn(p0, p1));
-              r1[i] = half2_bits(__hsub2(bits_half2(hh[i]), bits_half2(hh[i] & 0xFF00FF00u)));
-              c3[i] = e5m2x2(half2_bits(__hsub2(bits_half2(r1[i]), bits_half2(r1[i] & 0xFF00FF00u))));
+              r1[i] = left_of(hh[i]);
+              c3[i] = e5m2x2(left_of(r1[i]));
             } else {
               const __nv_bfloat162 o = __floats2bfloat162_rn(p0, p1);
               hh[i] = *reinterpret_cast<const uint32_t*>(&o);

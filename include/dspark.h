@@ -759,10 +759,12 @@ DSPARK_API dspark_status dspark_cache_move(const dspark_cache_move_args* args, v
  * rounded once to bf16.  A row that sees nothing gets 0.  What a row does not see
  * never reaches it, NaN and infinities included; a NaN or infinite score makes its
  * row of that head NaN.  Scores and sums are fp32 (q enters them exactly, or to
- * 2^-18 of its row's largest element where smaller); a weight p enters the sum over
- * v to 2^-8 of it.  Rows from offsets[n_req] on are left as they were.  A request with
- * offsets or base out of range (0 <= offsets[r] <= offsets[r + 1] <= N, at most
- * max_tree rows, 0 <= base, base + rows <= max_pages * page_size) is skipped; the
+ * 2^-18 of its row's largest element where smaller); a weight p, times its token's
+ * scale of v in an e4m3 cache, enters the sum over v to 2^-8 of it, from an e4m3
+ * cache to 2^-28 of the row's largest such product where that is more.  Rows from
+ * offsets[n_req] on are left as they were.  A request with offsets or base out of
+ * range (0 <= offsets[r] <= offsets[r + 1] <= N, at most max_tree rows, 0 <= base,
+ * base + rows <= max_pages * page_size) is skipped; the
  * tokens of a page outside [0, n_pages) are not seen by any row; both are reported
  * (DSPARK_BAD_INPUT, detail = request).  n_q_heads is a multiple of n_kv_heads, at
  * most 65536 and 4096 times it; max_tree is 1..DSPARK_MAX_TREE; scale finite.  q, out

@@ -78,3 +78,38 @@ def test_large_values_behind_low_scores(rise, size, rows, group, D):
     assert ws.read_error()[0] == capi.DSPARK_OK
     for o in out:
         A.check(c, q, offsets, [base], None, o)
+
+
+@pytest.mark.parametrize("rows,group,D", [(1, 16, 128), (8, 4, 128), (2, 2, 64), (16, 4, 128), (9, 7, 64)])
+@pytest.mark.parametrize("n,gap", [(12000, 9), (60000, 14), (60000, 16), (250000, 16), (250000, 18)])
+def test_one_token_far_above_a_long_tail(n, gap, rows, group, D):
+    """e4m3: a first token `gap` above n others whose values have one sign, whole in a CTA's share.
+
+    Of a token's weight times its scale of v (1 here), 2^-8 may be off and 2^-28 of the row's largest; all of them may be
+    off to one side.  With T the tail's part of the softmax, u its value and f the first's, the result is
+    f + (u - f) T; besides the rounded result the error is at most (|f| (1 - T) + |u| T) 2^-8 + n 2^-28 |u| (1 - T)."""
+    page, B = 128, 304
+    pages = -(-(n + rows) // page)
+    k = torch.zeros((pages, 1, page, D), device="cuda")
+    k[0, 0, 0, 0] = 1.0
+    first = torch.tensor([0.0, 1.0, -1.0, 0.125, 16.0, 2.0 ** -6, 2.0, -4.0], device="cuda").repeat(D // 8)
+    u = torch.tensor([1.0, 1.0, 1.0, -1.0, 0.5, 0.75, -2.0, 1.5], device="cuda").repeat(D // 8)
+    v = u.expand(pages, 1, page, D).clone()
+    v[0, 0, 0] = first
+    one = torch.ones((pages, 1, page), device="cuda")
+    c = T.KvCache(k.to(E4M3), v.to(E4M3), i32(np.tile(np.arange(pages), (B, 1))), one, one.clone())
+    q = torch.zeros((B * rows, group, D), dtype=BF16, device="cuda")
+    q[..., 0] = gap
+    ws = T.tree_attention_workspace(B, rows, group, 1, D)
+    out = T.tree_attention(ws, c, q, i32(np.arange(B + 1) * rows), i32([n] * B), rows, scale=1.0)
+    assert ws.read_error()[0] == capi.DSPARK_OK
+    tail = (n + torch.arange(rows, device="cuda", dtype=torch.float64))[:, None, None] * np.exp(-float(gap))  # and the first token: 1
+    tail, first, u = tail / (1 + tail), first.double(), u.double()
+    want = first + (u - first) * tail
+    slack = (first.abs() * (1 - tail) + u.abs() * tail) * 2.0 ** -8 + (n + rows) * 2.0 ** -28 * u.abs() * (1 - tail) \
+        + 2.0 ** -8 * want.abs() + 2.0 ** -40
+    off = (out.view(B, rows, group, D).double() - want).abs()
+    assert (off <= slack).all(), (off / slack).amax((0, 1, 2))[:8].tolist()
+    if gap > 9:  # a tail of which nothing is lost: to 2^-7 of it and n 2^-28
+        off, part = off[..., 0::8], tail.squeeze(-1)[..., None]
+        assert (off <= part * 2.0 ** -7 + (n + rows) * 2.0 ** -28).all()
