@@ -757,15 +757,17 @@ DSPARK_API dspark_status dspark_cache_move(const dspark_cache_move_args* args, v
  * over what row i sees of kv head h / (n_q_heads / n_kv_heads):
  *     out[i, h] = sum_t p_t v_t,  p = softmax_t(scale * q[i, h] . k_t),
  * rounded once to bf16.  A row that sees nothing gets 0.  What a row does not see
- * never reaches it, NaN and infinities included; a NaN or infinite score makes its
- * row of that head NaN.  Scores and sums are fp32 (q enters them exactly, or to
- * 2^-18 of its row's largest element where smaller); a weight p, times its token's
+ * never reaches it, NaN and infinities included; a score that is NaN or plus
+ * infinity makes its row of that head NaN, minus infinity is a weight of 0 (all of
+ * a row's: 0, as if it saw nothing).  Scores and sums are fp32 (q enters them
+ * exactly, or to 2^-18 of its row's largest element where smaller; a term below 2^-24
+ * of what a sum over v holds already may be left out); a weight p, times its token's
  * scale of v in an e4m3 cache, enters the sum over v to 2^-8 of it, from an e4m3
- * cache to 2^-28 of the row's largest such product where that is more.  Rows from
- * offsets[n_req] on are left as they were.  A request with offsets or base out of
- * range (0 <= offsets[r] <= offsets[r + 1] <= N, at most max_tree rows, 0 <= base,
- * base + rows <= max_pages * page_size) is skipped; the
- * tokens of a page outside [0, n_pages) are not seen by any row; both are reported
+ * cache to 2^-28 of the row's largest such product where that is more.  Rows
+ * from offsets[n_req] on are left as they were.  A request with offsets or base out
+ * of range (0 <= offsets[r] <= offsets[r + 1] <= N, at most max_tree rows, 0 <= base,
+ * base + rows <= max_pages * page_size) is skipped; the tokens of a page outside
+ * [0, n_pages) are not seen by any row; both are reported
  * (DSPARK_BAD_INPUT, detail = request).  n_q_heads is a multiple of n_kv_heads, at
  * most 65536 and 4096 times it; max_tree is 1..DSPARK_MAX_TREE; scale finite.  q, out
  * 16-byte aligned, ldq and ldo multiples of 8; out must not overlap q or the cache.

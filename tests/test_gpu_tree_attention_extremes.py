@@ -113,3 +113,41 @@ def test_one_token_far_above_a_long_tail(n, gap, rows, group, D):
     if gap > 9:  # a tail of which nothing is lost: to 2^-7 of it and n 2^-28
         off, part = off[..., 0::8], tail.squeeze(-1)[..., None]
         assert (off <= part * 2.0 ** -7 + (n + rows) * 2.0 ** -28).all()
+
+
+@pytest.mark.parametrize("rows,group,D", FORMS)
+@pytest.mark.parametrize("at", [0, 130, 400, "drafted", "all"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_scores(sign, at, rows, group, D):
+    """An infinity in k of a bf16 cache: a score of plus infinity makes a row of a head NaN, minus infinity is a weight of
+    0, and a row that has no others gets 0; an element of q that is 0 there makes NaN."""
+    base, page = 500, 32
+    c, q, offsets, _ = A.setup(3, BF16, [base], [rows], 1, group, D, page, fill="normal", sharp=1.0)
+    q = q.clone()
+    q[..., 5] = 1.0
+    q[:, 1::2, 5] = -1.0
+    q[rows - 1, 0, 5] = 0.0
+    tokens = np.arange(base + rows) if at == "all" else np.array([base if at == "drafted" else at])
+    t = torch.from_numpy(tokens).cuda()
+    pages, slots = c.table[0].long()[t // page], t % page
+    c.k[pages, 0, slots, 5] = 0.0
+    ref = A.as_numpy(c)
+    c.k[pages, 0, slots, 5] = sign * float("inf")
+    got = A.np64(A.call(c, q, offsets, [base], None, rows))
+    k, v = (A.O.rows(ref, n, 0, range(base + rows))[:, 0] for n in ("k", "v"))
+    s = D ** -0.5 * np.einsum("jgd,td->jgt", A.np64(q), k)
+    direction = sign * np.sign(A.np64(q)[..., 5])
+    for j in range(rows):
+        seen = np.arange(base + rows) <= base + j
+        hit = seen & np.isin(np.arange(base + rows), tokens)
+        for g in range(group):
+            if hit.any() and direction[j, g] >= 0:
+                assert np.isnan(got[j, g]).all()
+                continue
+            use = seen & ~hit
+            if not use.any():
+                assert (got[j, g] == 0).all()
+                continue
+            e = np.exp(s[j, g, use] - s[j, g, use].max())
+            want = e @ v[use] / e.sum()
+            assert np.linalg.norm(got[j, g] - want) < A.NORM * np.linalg.norm(want)
