@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(KT) k_cache_write(const CacheRows c, const T* 
     for (int i = 0; i < KU; ++i) {
       const int u = u0 + i * G + g;
       const Unit at = unit_at(c, min(u, units - 1));
-      const T* src = (at.v ? v + (row0 + at.row) * c.ldv : k + (row0 + at.row) * c.ldk) + at.head * D + l * 8;
+      const T* src = (at.v ? v + (row0 + at.row) * c.ldv : k + (row0 + at.row) * c.ldk) + (int64_t)at.head * D + l * 8;
       x[i][0].load(src);
       x[i][1].load(src + D / 2);
     }
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(KT) k_cache_read(const CacheRows c, T* k, T* v
       const int32_t p = place[at.row];
       dst[i] = nullptr;
       if (u >= units || p < 0) continue;
-      dst[i] = (at.v ? v + (row0 + at.row) * c.ldv : k + (row0 + at.row) * c.ldk) + at.head * D + l * 8;
+      dst[i] = (at.v ? v + (row0 + at.row) * c.ldv : k + (row0 + at.row) * c.ldk) + (int64_t)at.head * D + l * 8;
       const int64_t row = (int64_t)p + ((int64_t)at.head << c.pool.shift);
       const uint8_t* pool = at.v ? c.pool.v : c.pool.k;
 #pragma unroll
