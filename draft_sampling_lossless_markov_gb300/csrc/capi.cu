@@ -482,7 +482,7 @@ dspark_status dspark_tree_attention_workspace_size(int32_t n_req, int32_t max_tr
                                                    int32_t head_dim, size_t* bytes) {
   if (!bytes) return DSPARK_INVALID_ARG;
   const dspark_status st = check_tree_sizes(n_req, max_tree, n_q_heads, n_kv_heads, head_dim);
-  if (st == DSPARK_OK) *bytes = align_up(tree_attention_ws(n_req, max_tree, n_q_heads, n_kv_heads, head_dim), 256);
+  if (st == DSPARK_OK) *bytes = align_up(tree_attention_ws(max_tree, n_q_heads, n_kv_heads, head_dim), 256);
   return st;
 }
 
@@ -499,7 +499,7 @@ dspark_status dspark_tree_attention(const dspark_tree_attention_args* a, void* w
     return DSPARK_INVALID_ARG;
   if (!a->offsets || !a->base || !aligned_to(a->offsets, 4) || !aligned_to(a->base, 4) || !aligned_to(a->tree, 8))
     return DSPARK_INVALID_ARG;
-  if (!ws_ok(workspace, workspace_bytes, tree_attention_ws(c.n_req, a->max_tree, a->n_q_heads, c.n_kv_heads, c.head_dim)))
+  if (!ws_ok(workspace, workspace_bytes, tree_attention_ws(a->max_tree, a->n_q_heads, c.n_kv_heads, c.head_dim)))
     return DSPARK_INVALID_ARG;
   if (a->N > kMaxVocabDim) return DSPARK_UNSUPPORTED;
   return launched([&] { return launch_tree_attention(*a, static_cast<uint8_t*>(workspace), (cudaStream_t)stream); });

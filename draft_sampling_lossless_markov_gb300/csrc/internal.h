@@ -139,7 +139,7 @@ cudaError_t launch_cache_write(const dspark_cache_write_args& a, WsHeader* hdr, 
 cudaError_t launch_cache_read(const dspark_cache_read_args& a, WsHeader* hdr, cudaStream_t s);
 cudaError_t launch_cache_move(const dspark_cache_move_args& a, WsHeader* hdr, cudaStream_t s);
 constexpr int kMaxTreeGroup = 4096;  // query heads a kv head
-size_t tree_attention_ws(int n_req, int max_tree, int n_q_heads, int n_kv_heads, int head_dim);
+size_t tree_attention_ws(int max_tree, int n_q_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_tree_attention(const dspark_tree_attention_args& a, uint8_t* ws, cudaStream_t s);
 
 // STS fitting (sts_fit.cu): its own workspace, after a WsHeader.

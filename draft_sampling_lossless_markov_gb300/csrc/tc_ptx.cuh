@@ -457,10 +457,6 @@ __device__ __forceinline__ void tc_mma_fp8_if(uint32_t d_tmem, uint64_t a_desc, 
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// counts as having come to it, without waiting
-__device__ __forceinline__ void named_arrive(int id, int threads) {
-  asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 // true in every thread if `p` is in one
 __device__ __forceinline__ bool named_any(int id, int threads, bool p) {
   int r;

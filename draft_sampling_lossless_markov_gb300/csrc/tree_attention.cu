@@ -96,7 +96,7 @@ struct TreeArgs {
   const int32_t* base;
   const uint64_t* tree;
   int64_t ldq, ldo;
-  int32_t N, q_heads, group, max_tree;
+  int32_t N, group, max_tree;
   // ceil(2^32 / group): c / group is c group_inv >> 32 for the columns c < 64 group + 64, as c group
   // is below 2^32 (kMaxTreeGroup)
   uint64_t group_inv;
@@ -1412,7 +1412,7 @@ cudaError_t run_columns(const dspark_kv_cache& c, const TreeArgs& t, const Dev& 
 
 }  // namespace
 
-size_t tree_attention_ws(int, int max_tree, int n_q_heads, int n_kv_heads, int head_dim) {
+size_t tree_attention_ws(int max_tree, int n_q_heads, int n_kv_heads, int head_dim) {
   return layout(max_tree, n_q_heads / n_kv_heads, head_dim).total;
 }
 
@@ -1430,7 +1430,6 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args& a, uint8_t* 
   t.ldq = a.ldq;
   t.ldo = a.ldo;
   t.N = a.N;
-  t.q_heads = a.n_q_heads;
   t.group = a.n_q_heads / a.cache.n_kv_heads;
   t.group_inv = ((1ull << 32) + t.group - 1) / t.group;
   t.max_tree = a.max_tree;
