@@ -455,7 +455,12 @@ def token_logprobs_grad(ws: Optional[Workspace], logits, tokens, row_stat, entro
 class KvCache:
     """dspark_kv_cache: k and v [n_pages, n_kv_heads, page_size, head_dim] (e4m3 with k_scale and v_scale [n_pages,
     n_kv_heads, page_size] f32, or bf16 without), table [n_req, max_pages] i32 (dense rows).  The tensors are checked
-    here, once; the calls write into them."""
+    here, once; the calls write into them.  Their contents may change (a table's entries in place), the tensors may not."""
+
+    def __setattr__(self, name, value):
+        if "fields" in self.__dict__:  # the calls would go on with the addresses of the old tensor
+            raise AttributeError(f"{name}: a KvCache keeps its tensors, make another for others")
+        super().__setattr__(name, value)
 
     def __init__(self, k, v, table, k_scale=None, v_scale=None):
         if k.dim() != 4:
