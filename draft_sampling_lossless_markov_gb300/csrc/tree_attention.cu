@@ -15,16 +15,20 @@
 // the column's largest to 2^-18 of it): S = K . Q1 + K . Q2.  A weight p times its
 // token's v scale is split into three e5m2 pieces, 9 significant bits: the upper bytes of
 // its fp16 form, of 2^3 times what they leave, and the rest rounded, times 2^3 again.
+// Against a bf16 cache a weight is rounded to bf16, as both operands of a product have one type: 0.0019 of
+// the norm off 64 bits, where weights of 32 bits leave the output's own 0.0016.
 //
 // Softmax: with y = score * log2 e + log2(v scale), weights are 2^(y - ref) about a
 // column's reference, which is raised (O and the sums scaled down) only when a tile
 // passes it by 2^15, and is set 2^6 below the largest then; fp16 holds 2^-24 to 2^16 of
-// it, and the last piece's rounding is at most 2^-23, 2^-29 of the largest weight.  (e5m2 ends at 2^-16: without
-// the two factors weights below 2^-17 were lost, with them a tail of 60000 tokens 16 below a first one.  They cost
-// 1.5 %; the largest weight at 2^12 raises references so often that 256 x 8 rows take 441 us, not 369.)  The sum of the
-// weights themselves, 2^(y - ref) / (v scale), is kept by each lane in fp32; from a tile on in which a
-// v scale is 0 or far from 1 (rows of zeros, cleared ones), its terms are formed from the scores alone,
-// 2^(score * log2 e - a reference of the sum's own), in the branch that raises references.
+// it, and the last piece's rounding is at most 2^-23, 2^-29 of the largest weight.  (e5m2
+// ends at 2^-16: without the two factors weights below 2^-17 were lost, and with them a tail
+// of 60000 tokens whose scores are 16 below a first one's.  The factors cost 1.5 %; the largest
+// weight at 2^12 instead raises references so often that 256 x 8 rows take 441 us, not 369.)
+// The sum of the weights themselves, 2^(y - ref) / (v scale), is kept by each lane in fp32;
+// from a tile on in which a v scale is 0 or far from 1 (rows of zeros, cleared ones) its terms
+// are formed from the scores alone, 2^(score * log2 e - a reference of the sum's own), in the
+// branch that raises references.
 //
 // A CTA is one pair of softmax warpgroups (two CTAs an SM) or two pairs, which take tiles in
 // turn, each with its own references, sums and O, joined at the end of an item; a pair's
@@ -36,15 +40,15 @@
 //
 // What bounds it: the cache's bytes while a row's columns are few, the softmax's instructions
 // beyond.  Of the measured copy rate it reads, with contexts that differ,
-//     256 requests x 4 rows x 4 heads a kv head, e4m3, 128:  348 us, 0.95
-//     256 requests x 8 rows x 4                              365 us, 0.91
-//     one request x 8 rows x 4, 250001 tokens                 91 us, 0.85
+//     256 requests x 4 rows x 4 heads a kv head, e4m3, 128:  342 us, 0.96
+//     256 requests x 8 rows x 4                              374 us, 0.89
+//     one request x 8 rows x 4, 250001 tokens                 93 us, 0.84
 //     64 requests x 16 rows x 4, bf16                        101 us, 0.80
-//     16 requests x 64 rows x 8 (512 columns)                198 us, 0.09
-// With 16, 32 and 64 columns a tile takes 1270, 1485 and 2450 cycles of an SM from L2; the
-// loads alone would be 1455 at the copy rate.  A tile is some 1500 instructions and 14.5 for each
-// column and warp of tokens, which at 64 columns fill half of the issue slots; the tensor
-// pipe is 19 % busy there.
+//     16 requests x 64 rows x 8 (512 columns)                203 us, 0.09
+// With 16, 32 and 64 columns a tile takes 1270, 1530 and 2490 cycles of an SM from L2; the
+// loads alone would be 1455 at the copy rate.  A tile is some 1500 instructions and 15.5 for each
+// column and warp of tokens, which at 64 columns fill 55 % of the issue slots; the tensor
+// pipe is 18 % busy there.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -110,8 +114,9 @@ struct TreeArgs {
 template <bool kCodes, int D, int NQ>
 struct Form {
   static constexpr int kColumns = NQ;
-  // What an item costs beside its tiles, in tiles (3 to 12 tried: 16 requests x 64 nodes 252, 215, 202, 202, 204 us
-  // with 3 to 7, 64 x 16 rows bf16 144, 121, 110, 108 us with 3, 6, 8, 10, 256 x 8 rows 382, 374, 378 us with 3, 4, 7)
+  // What an item costs beside its tiles, in tiles (3, 4, 5, 6, 8, 10 tried, head sizes 128 and 64, long and short contexts:
+  // 16 requests x 64 nodes 234, 209, 203, 203, 207, 213 us, 256 x 8 rows 380, 374, 376, 378, 382, 388, at head size 64
+  // 349, 342, 343, 346, 352, 358, 64 x 16 rows bf16 132, 120, 113, 109, 104, 105, at head size 64 100, 92, 86, 84, 77, 80)
   static constexpr int kItemCost = NQ < 64 ? 4 : kCodes ? 5 : 8;
   static constexpr int kElem = kCodes ? 1 : 2;
   static constexpr int kRow = D * kElem < 128 ? D * kElem : 128;  // bytes of an operand row
