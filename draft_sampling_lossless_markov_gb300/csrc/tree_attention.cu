@@ -27,8 +27,7 @@
 // weight at 2^12 instead raises references so often that 256 x 8 rows take 441 us, not 369.)
 // The sum of the weights themselves, 2^(y - ref) / (v scale), is kept by each lane in fp32;
 // from a tile on in which a v scale is 0 or far from 1 (rows of zeros, cleared ones) its terms
-// are formed from the scores alone, 2^(score * log2 e - a reference of the sum's own), in the
-// branch that raises references.
+// are formed from the scores alone, 2^(score * log2 e - a reference of the sum's own).
 //
 // A CTA is one pair of softmax warpgroups (two CTAs an SM) or two pairs, which take tiles in
 // turn, each with its own references, sums and O, joined at the end of an item; a pair's
@@ -40,11 +39,11 @@
 //
 // What bounds it: the cache's bytes while a row's columns are few, the softmax's instructions
 // beyond.  Of the measured copy rate it reads, with contexts that differ,
-//     256 requests x 4 rows x 4 heads a kv head, e4m3, 128:  342 us, 0.96
-//     256 requests x 8 rows x 4                              374 us, 0.89
-//     one request x 8 rows x 4, 250001 tokens                 93 us, 0.84
+//     256 requests x 4 rows x 4 heads a kv head, e4m3, 128:  346 us, 0.95
+//     256 requests x 8 rows x 4                              375 us, 0.89
+//     one request x 8 rows x 4, 250001 tokens                 94 us, 0.83
 //     64 requests x 16 rows x 4, bf16                        101 us, 0.80
-//     16 requests x 64 rows x 8 (512 columns)                203 us, 0.09
+//     16 requests x 64 rows x 8 (512 columns)                204 us, 0.09
 // With 16, 32 and 64 columns a tile takes 1270, 1530 and 2490 cycles of an SM from L2; the
 // loads alone would be 1455 at the copy rate.  A tile is some 1500 instructions and 15.5 for each
 // column and warp of tokens, which at 64 columns fill 55 % of the issue slots; the tensor
@@ -118,6 +117,10 @@ struct Form {
   // 16 requests x 64 nodes 234, 209, 203, 203, 207, 213 us, 256 x 8 rows 380, 374, 376, 378, 382, 388, at head size 64
   // 349, 342, 343, 346, 352, 358, 64 x 16 rows bf16 132, 120, 113, 109, 104, 105, at head size 64 100, 92, 86, 84, 77, 80)
   static constexpr int kItemCost = NQ < 64 ? 4 : kCodes ? 5 : 8;
+  // Sums with references of their own in line, where the registers do without: with a row of zeros in a thousand 256 x 8
+  // rows take 470 us, and 1340 through a function's arguments in local memory (376 us without such rows, either way);
+  // in line at 64 columns 16 x 64 nodes go from 203 to 223 us, at head size 64 256 x 8 rows from 344 to 354.
+  static constexpr bool kApartInline = kCodes && D == 128 && NQ <= 32;
   static constexpr int kElem = kCodes ? 1 : 2;
   static constexpr int kRow = D * kElem < 128 ? D * kElem : 128;  // bytes of an operand row
   static constexpr int kParts = D * kElem / kRow;                 // of a token's row
@@ -390,23 +393,50 @@ __device__ __forceinline__ void load_sum(uint32_t taddr, int apart, float (&v)[8
   }
 }
 
-// A tile's weights to sums with references of their own, of the scores alone: x are the exponents y - ref, l the sums;
-// less log2 of the v scale and by the difference of the references (at) they are the sums'.  Out of line: it is rare.
+// Sums with references of their own take the weights of the scores alone: their exponents are x = y - ref, less log2 of
+// the v scale and by the difference of the references (at).  v_inv is the scale's inverse, or the scale negated where it
+// is far from 1.
+__device__ __forceinline__ bool zero_scale(float v_inv) { return !(v_inv > 0.f) && -v_inv < kLeastNormal; }
+__device__ __forceinline__ float less_scale(float v_inv) {
+  const float v = fabsf(v_inv), log = __log2f(zero_scale(v_inv) ? kLeastNormal : v);
+  return !(v == v) ? 0.f : v_inv > 0.f ? log : -log;  // (NaN is in x where the token is seen)
+}
+__device__ __forceinline__ float2 sum_exponents(uint64_t x, float less, const float* at) {
+  return ptx::unpack2(ptx::add2(x, ptx::add2(ptx::pack2(less, less), *reinterpret_cast<const uint64_t*>(at))));
+}
 template <int HQ>
-__device__ __noinline__ void sum_apart(uint64_t (&x)[HQ / 2], uint64_t (&l)[HQ / 2], float v_inv, float* at,
-                                       float* factor, bool* set, float (*top)[HQ], int bar) {
+__device__ __forceinline__ float highest_apart(const uint64_t (&x)[HQ / 2], float v_inv, const float* at) {
+  const float less = less_scale(v_inv);
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < HQ / 2; ++i) {
+    const float2 e = sum_exponents(x[i], less, at + 2 * i);
+    top = fmaxf(top, fmaxf(e.x, e.y));
+  }
+  return top;
+}
+template <int HQ>
+__device__ __forceinline__ void add_apart(uint64_t (&x)[HQ / 2], uint64_t (&l)[HQ / 2], float v_inv, const float* at) {
+  const float less = less_scale(v_inv);
+  const bool zero = zero_scale(v_inv);
+#pragma unroll
+  for (int i = 0; i < HQ / 2; ++i) {
+    const float2 e = sum_exponents(x[i], less, at + 2 * i);
+    l[i] = ptx::add2(l[i], ptx::pack2(ptx::ex2(e.x), ptx::ex2(e.y)));
+    if (zero) x[i] = ptx::pack2(-INFINITY, -INFINITY);  // codes of scale 0 are 0
+  }
+}
+// the same with the references raised first (set: there is one; top: room for each warp's largest)
+template <int HQ>
+__device__ __forceinline__ void raise_apart(uint64_t (&x)[HQ / 2], uint64_t (&l)[HQ / 2], float v_inv, float* at,
+                                            float* factor, bool* set, float (*top)[HQ], int bar) {
   const int lane = threadIdx.x & 31, token = threadIdx.x & 127;
-  // v_inv: the scale's inverse, or the scale negated
-  const bool far = !(v_inv > 0.f), zero = far && -v_inv < kLeastNormal;
-  const float v = fabsf(v_inv), log = __log2f(zero ? kLeastNormal : v);
-  const float back = !(v == v) ? 0.f : far ? -log : log;  // (NaN is in x where the token is seen)
-  const auto exponents = [&](int i) {
-    return ptx::unpack2(ptx::add2(x[i], ptx::add2(ptx::pack2(back, back), *reinterpret_cast<const uint64_t*>(&at[2 * i]))));
-  };
+  const float less = less_scale(v_inv);
+  const bool zero = zero_scale(v_inv);
   float m = -INFINITY;  // of column `lane`
 #pragma unroll
   for (int i = 0; i < HQ / 2; ++i) {
-    const float2 e = exponents(i);
+    const float2 e = sum_exponents(x[i], less, at + 2 * i);
     const float m0 = ptx::warp_max_redux(e.x), m1 = ptx::warp_max_redux(e.y);
     m = lane == 2 * i ? m0 : lane == 2 * i + 1 ? m1 : m;
   }
@@ -423,10 +453,16 @@ __device__ __noinline__ void sum_apart(uint64_t (&x)[HQ / 2], uint64_t (&l)[HQ /
   ptx::named_sync(bar, 128);
 #pragma unroll
   for (int i = 0; i < HQ / 2; ++i) {
-    const float2 e = exponents(i);
+    const float2 e = sum_exponents(x[i], less, at + 2 * i);
     l[i] = ptx::fma2(l[i], *reinterpret_cast<const uint64_t*>(&factor[2 * i]), ptx::pack2(ptx::ex2(e.x), ptx::ex2(e.y)));
     if (zero) x[i] = ptx::pack2(-INFINITY, -INFINITY);  // codes of scale 0 are 0
   }
+}
+
+template <int HQ>
+__device__ __noinline__ void raise_apart_out_of_line(uint64_t (&x)[HQ / 2], uint64_t (&l)[HQ / 2], float v_inv, float* at,
+                                                     float* factor, bool* set, float (*top)[HQ], int bar) {
+  raise_apart<HQ>(x, l, v_inv, at, factor, set, top, bar);
 }
 
 // What turns O into the result is 2^(O's reference less the sum's) / sum, 0 where nothing was summed, as two factors:
@@ -900,7 +936,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
       uint64_t l2[HQ / 2];
 #pragma unroll
       for (int i = 0; i < HQ / 2; ++i) l2[i] = 0;
-      bool unset = opaque(1) != 0;  // a column has no reference yet, or the sums have their own
+      int mode = opaque(1);  // 1: a column has no reference yet, 2: the sums have their own
 #pragma unroll 1
       for (int t = opaque(w); t < tiles; t += kPairs) {
         const uint32_t n = n0 + t, note = n % F::kNotes;
@@ -997,12 +1033,20 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
           const float2 x = ptx::unpack2(x2[i]);
           top = fmaxf(top, fmaxf(x.x, x.y));
         }
-        const bool raise = ptx::named_any(own, 128, top > kRaise<kCodes> || !(v_inv > 0.f)) || unset;
+        const bool raise = ptx::named_any(own, 128, top > kRaise<kCodes> || !(v_inv > 0.f)) || mode;
         if (turn > 1) {  // the tile before is in O, and its weights have been read
           wait(&pdone[w], turn & 1, 14);
           ptx::tc_fence_after();
         }
-        if (raise) {
+        bool full = raise;
+        if (F::kApartInline && mode == 2) {  // most often no reference is to be raised
+          full = ptx::named_any(own, 128, top > kRaise<kCodes> || highest_apart<HQ>(x2, v_inv, my_sum_at) > kRaiseSum);
+          if (!full) {
+            add_apart<HQ>(x2, l2, v_inv, my_sum_at);
+            v_inv = 0.f;
+          }
+        }
+        if (full) {
           // the columns' largest, new references, what was summed so far brought to them
 #pragma unroll 1
           for (bool sums = kCodes;; sums = false) {
@@ -1018,12 +1062,16 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
             ptx::named_sync(own, 128);
             if (!sums || !odd_scale[w][h]) break;
             // this tile's sums first, which changes x2
-            uint64_t x[HQ / 2], l[HQ / 2];
+            if constexpr (F::kApartInline) {
+              raise_apart<HQ>(x2, l2, v_inv, my_sum_at, my_factor, &sum_set[w][h * HQ], &warp_top[wg * 4], own);
+            } else {
+              uint64_t x[HQ / 2], l[HQ / 2];
 #pragma unroll
-            for (int i = 0; i < HQ / 2; ++i) x[i] = x2[i], l[i] = l2[i];
-            sum_apart<HQ>(x, l, v_inv, my_sum_at, my_factor, &sum_set[w][h * HQ], &warp_top[wg * 4], own);
+              for (int i = 0; i < HQ / 2; ++i) x[i] = x2[i], l[i] = l2[i];
+              raise_apart_out_of_line<HQ>(x, l, v_inv, my_sum_at, my_factor, &sum_set[w][h * HQ], &warp_top[wg * 4], own);
 #pragma unroll
-            for (int i = 0; i < HQ / 2; ++i) x2[i] = x[i], l2[i] = l[i];
+              for (int i = 0; i < HQ / 2; ++i) x2[i] = x[i], l2[i] = l[i];
+            }
             v_inv = 0.f;
           }
           const bool apart = kCodes && odd_scale[w][h];  // the sums have references of their own
@@ -1044,7 +1092,7 @@ __global__ void __launch_bounds__(Form<kCodes, D, NQ>::kThreads, Form<kCodes, D,
             my_nref[token] -= d;
             if (apart) my_sum_at[token] += d;
           }
-          unset = ptx::named_any(own, 128, none) || apart;  // (the part's later tiles all come here)
+          mode = (ptx::named_any(own, 128, none) ? 1 : 0) | (apart ? 2 : 0);
 #pragma unroll
           for (int i = 0; i < HQ / 2; ++i) {
             x2[i] = ptx::add2(x2[i], *reinterpret_cast<const uint64_t*>(&my_delta[2 * i]));
